@@ -3,18 +3,23 @@ block-sparse (Splash) masked attention forward library.
 
 This module only marshals arguments: torch tensors become device pointers,
 the current torch stream becomes the cudaStream_t.  Every step of the
-computation runs in the library's CUDA kernels; there is no CPU or PyTorch
-fallback.  If the library has not been built, importing works but every call
+computation runs in the library's CUDA kernels (rope_table, a constant laid
+out once, is the exception); there is no CPU or PyTorch fallback.  If the library has not been built, importing works but every call
 raises SplashLibraryMissing.
 
     spec = MaskSpec(causal=True, window_left=4095)
     mi = build_mask_info(spec, L, L, 128, 128)
     out, lse = attention_fwd(q, k, v, mi, scale=1 / 128 ** 0.5, softcap=30.0)
 
+Serving, with positions rotated: rope_fwd / rope_bwd around the attention,
+paged_append for the keys and values of new tokens, paged_decode for their
+attention over the pages.
+
 C ABI: include/splash.h.
 """
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -86,6 +91,11 @@ def lib():
     L.splash_mask_info_set_pattern_source.argtypes = [vp, i32]
     L.splash_attention_fwd_host.argtypes = [vp, vp, vp, i32, i32, i32, i64, i64, i32, i32, vp, vp, vp, f32, f32,
                                             vp, vp, vp, vp, vp, vp, vp, vp]
+    for f in (L.splash_rope, L.splash_paged_append, L.splash_paged_decode):
+        f.argtypes = [ctypes.c_char_p, vp]  # the argument struct as packed bytes
+        f.restype = ctypes.c_int
+    L.splash_paged_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32, P(ctypes.c_size_t)]
+    L.splash_paged_decode_workspace_size.restype = ctypes.c_int
     L.splash_attention_merge.argtypes = [vp, vp, i32, i64, i32, vp, vp, vp]
     L.splash_last_device_error.argtypes = [vp]
     L.splash_debug_wait_selftest.argtypes = [ctypes.c_uint64, vp]
@@ -413,6 +423,248 @@ def shard_views(q, k, v, begin: int, end: int, out=None, lse=None, segment_ids=N
         idx = torch.arange(begin, end, device=segment_ids.device) // Hkv
         r["segment_ids"] = segment_ids.index_select(0, idx).contiguous()
     return r
+
+
+# ---- serving: rotary positions, paged append, paged decode
+
+# The argument structs of splash.h as packed bytes (native layout: the first
+# member is the size that the library compares with its own).
+_ROPE_ARGS = struct.Struct("@Q" + "Pqqq" * 4 + "PqPqq" + "8i")
+_APPEND_ARGS = struct.Struct("@Q" + "Pqqq" * 5 + "Pqqq" * 2 + "PPPqPqPqPqqq" + "12i")
+_DECODE_ARGS = struct.Struct("@Q" + "Pqqq" * 3 + "PPPqPPPPQqq" + "9i2fi")
+_NO_VIEW = (0, 0, 0, 0)
+_CACHE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+
+
+def _stream_and_device(stream, first):
+    """(cudaStream_t, device index); the tensors must be on the current device."""
+    dev = first.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors must be on the current CUDA device (got {first.device})")
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream, dev
+    return (stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)), dev
+
+
+def _new(shape, dtype, device, stream):
+    """A tensor for a call on `stream`: taken from that stream's memory, so
+    that nothing another stream still uses is overwritten, and kept until the
+    current stream's later work is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
+def _view4(name, t, shape, dev):
+    """(pointer, strides) of a bf16 [B, H, L, d] tensor with contiguous d."""
+    if t.dtype != torch.bfloat16 or t.get_device() != dev or t.shape != shape or t.stride(3) != 1:
+        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on the q / k device, contiguous in its last dimension")
+    s = t.stride()
+    return t.data_ptr(), s[0], s[1], s[2]
+
+
+def _index2(name, t, B, L, dev):
+    """(pointer, batch stride) of an int32 [B, L] or [L] tensor."""
+    if t.dtype != torch.int32 or t.get_device() != dev or t.shape[-1:] != (L,) or t.dim() > 2 \
+            or (L > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be an int32 tensor of shape [{B}, {L}] or [{L}] on the q / k device, contiguous in its last dimension")
+    if t.dim() == 1:
+        return t.data_ptr(), 0
+    if t.shape[0] != B:
+        raise ValueError(f"{name} has {t.shape[0]} rows for a batch of {B}")
+    return t.data_ptr(), t.stride(0)
+
+
+def _table2(t, dev):
+    """(pointer, rows, rot_dim) of a table made like rope_table's."""
+    if t.dtype != torch.float32 or t.get_device() != dev or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError("table must be a contiguous fp32 tensor [positions, rot_dim] on the q / k device")
+    return t.data_ptr(), t.shape[0], t.shape[1]
+
+
+def _cache4(k_cache, v_cache, k_scale, v_scale, dev):
+    """The cache's part of the argument structs, and its sizes: (k view,
+    v view, k_scale, v_scale pointers, type, pages, Hkv, page_size, dqk, dv)."""
+    kind = _CACHE_TYPES.get(k_cache.dtype)
+    if kind is None or v_cache.dtype != k_cache.dtype or k_cache.dim() != 4 or v_cache.dim() != 4 \
+            or k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise ValueError("k_cache and v_cache must be bf16 or float8_e4m3fn tensors [pages, Hkv, page_size, d] on the q / k device")
+    pages, Hkv, page, dqk = k_cache.shape
+    if v_cache.shape[:3] != k_cache.shape[:3]:
+        raise ValueError("k_cache and v_cache must have the same pages, heads and page size")
+    ks, vs = k_cache.stride(), v_cache.stride()
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError("k_cache and v_cache must be contiguous in their last dimension")
+    kp = vp = 0
+    if kind == 1:
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is None or t.dtype != torch.float32 or t.get_device() != dev or t.shape != (Hkv,) or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous fp32 tensor of shape [{Hkv}] for an e4m3 cache")
+        kp, vp = k_scale.data_ptr(), v_scale.data_ptr()
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("k_scale and v_scale belong to an e4m3 cache")
+    return ((k_cache.data_ptr(), *ks[:3]), (v_cache.data_ptr(), *vs[:3]), kp, vp, kind, pages, Hkv, page, dqk,
+            v_cache.shape[3])
+
+
+def _block_table(t, dev):
+    """(pointer, row stride, rows, columns)."""
+    if t.dtype != torch.int32 or t.get_device() != dev or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("block_table must be an int32 tensor [sequences, pages] on the q / k device, contiguous in its last dimension")
+    return t.data_ptr(), t.stride(0), t.shape[0], t.shape[1]
+
+
+def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
+    """The rotations of positions 0 .. max_positions - 1 for rope_fwd and
+    paged_append: fp32 [max_positions, rot_dim], cosines then sines of
+    position * base^(-2i / rot_dim), from 64-bit angles (far positions would
+    lose their angle in 32 bits).  Any other table of that layout will do."""
+    f = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    a = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat((a.cos(), a.sin()), 1).float()
+
+
+def _rope(what, inverse, q, k, positions, table, rot_offset, interleaved, q_out, k_out, stream):
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q and k must be 4-D")
+    s, dev = _stream_and_device(stream, q)
+    B, Hq, L, d = q.shape
+    qv = _view4("q", q, q.shape, dev)
+    kv = ko = _NO_VIEW
+    Hkv = 0
+    if q_out is None:
+        q_out = _new(q.shape, torch.bfloat16, q.device, stream)
+    if k is not None:
+        Hkv = k.shape[1]
+        kv = _view4("k", k, (B, Hkv, L, d), dev)
+        if k_out is None:
+            k_out = _new(k.shape, torch.bfloat16, q.device, stream)
+        ko = _view4("k_out", k_out, k.shape, dev)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    tp, rows, rot = _table2(table, dev)
+    args = _ROPE_ARGS.pack(_ROPE_ARGS.size, *qv, *_view4("q_out", q_out, q.shape, dev), *kv, *ko,
+                           *_index2("positions", positions, B, L, dev), tp, rows, L, B, Hq, Hkv, d, rot,
+                           int(rot_offset), int(bool(interleaved)), inverse)
+    _check(lib().splash_rope(args, s), what)
+    return q_out, k_out
+
+
+def rope_fwd(q, k, positions, table, rot_offset: int = 0, interleaved: bool = False, q_out=None, k_out=None,
+             stream=None):
+    """q [B, Hq, L, d] and k [B, Hkv, L, d] (bf16, any strides with d
+    contiguous; k may be None) rotated by positions (int32 [B, L] or [L];
+    negative: not rotated).  table: fp32 [positions, rot_dim] (rope_table); the
+    rotated dimensions start at rot_offset, pairs are half a rotation apart or
+    adjacent (interleaved).  Returns (q_out, k_out), dense unless given;
+    q_out=q rotates in place (splash_rope)."""
+    return _rope("splash_rope", 0, q, k, positions, table, rot_offset, interleaved, q_out, k_out, stream)
+
+
+def rope_bwd(dq, dk, positions, table, rot_offset: int = 0, interleaved: bool = False, dq_out=None, dk_out=None,
+             stream=None):
+    """The gradients of rope_fwd's inputs from those of its outputs (the
+    transposed rotation); arguments as rope_fwd."""
+    return _rope("splash_rope (inverse)", 1, dq, dk, positions, table, rot_offset, interleaved, dq_out, dk_out, stream)
+
+
+def paged_append(k, v, k_cache, v_cache, block_table, positions, q=None, table=None, rot_offset: int = 0,
+                 interleaved: bool = False, seq_ids=None, k_scale=None, v_scale=None, q_out=None, k_out=None,
+                 stream=None):
+    """Writes k [B, Hkv, L, dqk] and v [B, Hkv, L, dv] of new tokens into the
+    pages of their sequences, rotating k (and q) on the way when a table is
+    given (splash_paged_append).  Returns (q_out, k_out).
+
+    k_cache, v_cache: [pages, Hkv, page_size, d], bf16 or float8_e4m3fn (then
+    with k_scale, v_scale fp32 [Hkv]); pages stored token by token are passed
+    as cache.transpose(1, 2).  block_table: int32 [sequences, max_pages].
+    positions, seq_ids: int32 [B, L] or [L]; a negative position is padding
+    (nothing is stored); seq_ids is the row of block_table (default: b).
+    q [B, Hq, L, dqk] is rotated into q_out (allocated if not given); k_out
+    receives the rotated keys when given (for attention_fwd of a prompt)."""
+    if k.dim() != 4 or v.dim() != 4:
+        raise ValueError("k and v must be 4-D")
+    s, dev = _stream_and_device(stream, k)
+    kc, vc, ksp, vsp, kind, pages, Hkv, page, dqk, dv = _cache4(k_cache, v_cache, k_scale, v_scale, dev)
+    B, L = k.shape[0], k.shape[2]
+    kv = _view4("k", k, (B, Hkv, L, dqk), dev)
+    vv = _view4("v", v, (B, Hkv, L, dv), dev)
+    qv = qo = ko = _NO_VIEW
+    Hq = 0
+    if q is not None:
+        if q.dim() != 4:
+            raise ValueError("q must be 4-D")
+        Hq = q.shape[1]
+        qv = _view4("q", q, (B, Hq, L, dqk), dev)
+        if q_out is None:
+            q_out = _new(q.shape, torch.bfloat16, q.device, stream)
+        qo = _view4("q_out", q_out, q.shape, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k_out is not None:
+        ko = _view4("k_out", k_out, k.shape, dev)
+    tp, rows, rot = _table2(table, dev) if table is not None else (0, 0, 0)
+    bt, bt_stride, num_seqs, max_pages = _block_table(block_table, dev)
+    ids = _index2("seq_ids", seq_ids, B, L, dev) if seq_ids is not None else (0, 0)
+    args = _APPEND_ARGS.pack(_APPEND_ARGS.size, *qv, *qo, *kv, *ko, *vv, *kc, *vc, ksp, vsp, bt, bt_stride,
+                             *_index2("positions", positions, B, L, dev), *ids, tp, rows, L, pages, B, Hq, Hkv, dqk,
+                             dv, num_seqs, max_pages, page, kind, rot, int(rot_offset), int(bool(interleaved)))
+    _check(lib().splash_paged_append(args, s), "splash_paged_append")
+    return q_out, k_out
+
+
+def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float, softcap: float = 0.0,
+                 window_left: int = -1, k_scale=None, v_scale=None, out=None, lse=None, workspace=None, stream=None):
+    """out [B, Hq, Lq, dv] bf16 and lse [B, Hq, Lq] fp32 of the newest Lq
+    (1 .. 16) tokens of each sequence over its pages (splash_paged_decode).
+
+    q [B, Hq, Lq, dqk]: bf16, any strides with dqk contiguous.  seq_lens: int32
+    [B], cached tokens, the Lq new ones among them.  Caches, scales and
+    block_table [B, max_pages] as for paged_append.  workspace: optional uint8
+    device tensor of at least paged_decode_workspace_size(...) bytes, not
+    shared by calls that may overlap."""
+    if q.dim() != 4:
+        raise ValueError("q must be 4-D")
+    s, dev = _stream_and_device(stream, q)
+    kc, vc, ksp, vsp, kind, pages, Hkv, page, dqk, dv = _cache4(k_cache, v_cache, k_scale, v_scale, dev)
+    B, Hq, Lq, _ = q.shape
+    qv = _view4("q", q, (B, Hq, Lq, dqk), dev)
+    bt, bt_stride, num_seqs, max_pages = _block_table(block_table, dev)
+    if num_seqs != B:
+        raise ValueError(f"block_table has {num_seqs} rows for a batch of {B}")
+    if seq_lens.dtype != torch.int32 or seq_lens.get_device() != dev or seq_lens.shape != (B,) \
+            or not seq_lens.is_contiguous():
+        raise ValueError(f"seq_lens must be a contiguous int32 tensor of shape [{B}] on the q device")
+    if out is None:
+        out = _new((B, Hq, Lq, dv), torch.bfloat16, q.device, stream)
+    elif out.dtype != torch.bfloat16 or out.shape != (B, Hq, Lq, dv) or not out.is_contiguous() or out.get_device() != dev:
+        raise ValueError(f"out must be a contiguous bf16 tensor of shape {(B, Hq, Lq, dv)} on the q device")
+    if lse is None:
+        lse = _new((B, Hq, Lq), torch.float32, q.device, stream)
+    elif lse.dtype != torch.float32 or lse.shape != (B, Hq, Lq) or not lse.is_contiguous() or lse.get_device() != dev:
+        raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(B, Hq, Lq)} on the q device")
+    if workspace is None:
+        workspace = _new(paged_decode_workspace_size(B, Hq, Hkv, Lq, dv), torch.uint8, q.device, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the q device")
+    args = _DECODE_ARGS.pack(_DECODE_ARGS.size, *qv, *kc, *vc, ksp, vsp, bt, bt_stride, seq_lens.data_ptr(),
+                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), pages, int(window_left), B, Hq, Hkv, Lq,
+                             dqk, dv, max_pages, page, kind, float(scale), float(softcap), 0)
+    _check(lib().splash_paged_decode(args, s), "splash_paged_decode")
+    return out, lse
+
+
+def paged_decode_workspace_size(B: int, Hq: int, Hkv: int, Lq: int, dv: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().splash_paged_decode_workspace_size(int(B), int(Hq), int(Hkv), int(Lq), int(dv), ctypes.byref(n)),
+           "splash_paged_decode_workspace_size")
+    return int(n.value)
 
 
 def last_device_error(stream=None) -> int:

@@ -18,7 +18,8 @@ SOURCES = [("api.cu", "api", []), ("mask_info.cu", "mask_info", []),
            ("attention_fwd.cu", "attention_fwd", ["-DSPLASH_FWD_PM=0"]),
            ("attention_fwd.cu", "attention_fwd_band", ["-DSPLASH_FWD_PM=1"]),
            ("attention_fwd.cu", "attention_fwd_band_seg", ["-DSPLASH_FWD_PM=2"]),
-           ("attention_bwd.cu", "attention_bwd", []), ("host_pipeline.cu", "host_pipeline", [])]
+           ("attention_bwd.cu", "attention_bwd", []), ("host_pipeline.cu", "host_pipeline", []),
+           ("rope.cu", "rope", []), ("paged_decode.cu", "paged_decode", [])]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -388,6 +388,197 @@ splash_status splash_classify_blocks_noalloc(const splash_mask_spec *spec, int64
                                              static_cast<cudaStream_t>(cuda_stream));
 }
 
+namespace {
+
+// ---- the serving calls: rotary positions, paged append, paged decode
+
+uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+
+struct Dim {
+  int64_t size, stride;
+};
+
+// Rows of d contiguous elements (`row_align` elements are 16 bytes) at up to
+// three outer strides; the stride of a dimension of size 1 is not read.  An
+// output's rows must not overlap: with the strides in ascending order, each
+// must reach past everything the smaller ones span.
+splash_status check_rows(const void *ptr, Dim a, Dim b, Dim c, int64_t d, int64_t row_align, bool output) {
+  if (ptr == nullptr || (addr(ptr) & 15u) != 0) return SPLASH_ERR_INVALID_ARG;
+  Dim dims[3] = {a, b, c};
+  for (Dim &x : dims) {
+    if (x.size == 1) x.stride = 0;
+    if (x.stride < 0 || x.stride % row_align != 0 || x.stride > ((int64_t)1 << 40)) return SPLASH_ERR_INVALID_ARG;
+  }
+  if (!output) return SPLASH_OK;
+  std::sort(dims, dims + 3, [](const Dim &x, const Dim &y) { return x.stride < y.stride; });
+  int64_t span = d;
+  for (const Dim &x : dims) {
+    if (x.size == 1) continue;
+    if (x.stride < span) return SPLASH_ERR_INVALID_ARG;
+    // (sizes below 2^31 and strides below 2^41: the product may pass 2^63)
+    if (x.stride > 0 && x.size - 1 > (((int64_t)1 << 62) - span) / x.stride) return SPLASH_ERR_UNSUPPORTED;
+    span += (x.size - 1) * x.stride;
+  }
+  return SPLASH_OK;
+}
+
+splash_status check_view(const splash_view &v, int64_t B, int64_t H, int64_t L, int64_t d, bool output) {
+  return check_rows(v.ptr, {B, v.stride_b}, {H, v.stride_h}, {L, v.stride_l}, d, 8, output);
+}
+
+// An output that is its input's own view is written in place.
+splash_status check_out_view(const splash_view &out, const splash_view &in, int64_t B, int64_t H, int64_t L, int64_t d) {
+  const splash_status st = check_view(out, B, H, L, d, true);
+  if (st != SPLASH_OK || out.ptr != in.ptr) return st;
+  const bool same = (B == 1 || out.stride_b == in.stride_b) && (H == 1 || out.stride_h == in.stride_h) &&
+                    (L == 1 || out.stride_l == in.stride_l);
+  return same ? SPLASH_OK : SPLASH_ERR_INVALID_ARG;
+}
+
+splash_status check_cache(const splash_cache_view &v, int64_t pages, int64_t Hkv, int64_t page_size, int64_t d,
+                          int32_t type, bool output) {
+  return check_rows(v.ptr, {pages, v.stride_page}, {Hkv, v.stride_head}, {page_size, v.stride_token}, d,
+                    type == SPLASH_CACHE_E4M3 ? 16 : 8, output);
+}
+
+splash_status check_rotation(const float *table, int64_t table_rows, int32_t d, int32_t rot_dim, int32_t rot_offset,
+                             int32_t interleaved) {
+  if (table == nullptr || (addr(table) & 15u) != 0 || table_rows <= 0) return SPLASH_ERR_INVALID_ARG;
+  if (rot_dim <= 0 || rot_offset < 0 || (interleaved != 0 && interleaved != 1)) return SPLASH_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0 || rot_offset % 8 != 0) return SPLASH_ERR_UNSUPPORTED;
+  if (rot_dim > d || rot_offset > d - rot_dim) return SPLASH_ERR_SHAPE;
+  return SPLASH_OK;
+}
+
+bool valid_head_dim(int32_t d) { return d % 16 == 0 && d <= 512; }
+
+splash_status check_tokens(int32_t B, int64_t L, int64_t heads) {
+  if (L > INT32_MAX || (int64_t)B * L > INT32_MAX || heads > 65535) return SPLASH_ERR_UNSUPPORTED;
+  return SPLASH_OK;
+}
+
+splash_status check_pages(const splash_cache_view &k, const splash_cache_view &v, int64_t num_pages, int32_t Hkv,
+                          int32_t page_size, int32_t dqk, int32_t dv, int32_t type, const float *k_scale,
+                          const float *v_scale, const int32_t *block_table, int64_t block_table_stride, int64_t rows,
+                          int32_t max_pages, bool output) {
+  if (num_pages <= 0 || max_pages <= 0 || rows <= 0 || page_size <= 0 || block_table == nullptr)
+    return SPLASH_ERR_INVALID_ARG;
+  if ((addr(block_table) & 3u) != 0 || (rows > 1 && block_table_stride < 0)) return SPLASH_ERR_INVALID_ARG;
+  if (type != SPLASH_CACHE_BF16 && type != SPLASH_CACHE_E4M3) return SPLASH_ERR_INVALID_ARG;
+  if (type == SPLASH_CACHE_E4M3 &&
+      (k_scale == nullptr || v_scale == nullptr || ((addr(k_scale) | addr(v_scale)) & 3u) != 0))
+    return SPLASH_ERR_INVALID_ARG;
+  if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return SPLASH_ERR_UNSUPPORTED;
+  if (num_pages > INT32_MAX || (int64_t)max_pages * page_size > INT32_MAX) return SPLASH_ERR_UNSUPPORTED;
+  splash_status st = check_cache(k, num_pages, Hkv, page_size, dqk, type, output);
+  if (st != SPLASH_OK) return st;
+  return check_cache(v, num_pages, Hkv, page_size, dv, type, output);
+}
+
+splash_status current_error_word(uint32_t **err) {
+  int dev = 0;
+  SPLASH_CUDA_TRY(cudaGetDevice(&dev));
+  *err = splash_device_error_word(dev);
+  return *err != nullptr ? SPLASH_OK : SPLASH_ERR_CUDA;
+}
+
+}  // namespace
+
+splash_status splash_rope(const splash_rope_args *args, void *cuda_stream) {
+  if (args == nullptr || args->struct_bytes != sizeof *args) return SPLASH_ERR_INVALID_ARG;
+  const splash_rope_args &a = *args;
+  const bool has_k = a.k.ptr != nullptr;
+  if (a.B <= 0 || a.Hq <= 0 || a.L <= 0 || a.d <= 0 || (has_k && a.Hkv <= 0)) return SPLASH_ERR_INVALID_ARG;
+  if (a.positions == nullptr || (addr(a.positions) & 3u) != 0 || (a.B > 1 && a.positions_stride_b < 0))
+    return SPLASH_ERR_INVALID_ARG;
+  if (a.inverse != 0 && a.inverse != 1) return SPLASH_ERR_INVALID_ARG;
+  if (!valid_head_dim(a.d)) return SPLASH_ERR_UNSUPPORTED;
+  splash_status st = check_rotation(a.table, a.table_rows, a.d, a.rot_dim, a.rot_offset, a.interleaved);
+  if (st != SPLASH_OK) return st;
+  if ((st = check_tokens(a.B, a.L, (int64_t)a.Hq + (has_k ? a.Hkv : 0))) != SPLASH_OK) return st;
+  if ((st = check_view(a.q, a.B, a.Hq, a.L, a.d, false)) != SPLASH_OK) return st;
+  if ((st = check_out_view(a.q_out, a.q, a.B, a.Hq, a.L, a.d)) != SPLASH_OK) return st;
+  if (has_k) {
+    if ((st = check_view(a.k, a.B, a.Hkv, a.L, a.d, false)) != SPLASH_OK) return st;
+    if ((st = check_out_view(a.k_out, a.k, a.B, a.Hkv, a.L, a.d)) != SPLASH_OK) return st;
+  }
+  uint32_t *err = nullptr;
+  if ((st = current_error_word(&err)) != SPLASH_OK) return st;
+  return splash_rope_launch(a, static_cast<cudaStream_t>(cuda_stream), err);
+}
+
+splash_status splash_paged_append(const splash_paged_append_args *args, void *cuda_stream) {
+  if (args == nullptr || args->struct_bytes != sizeof *args) return SPLASH_ERR_INVALID_ARG;
+  const splash_paged_append_args &a = *args;
+  const bool has_q = a.q.ptr != nullptr;
+  if (a.B <= 0 || a.Hkv <= 0 || a.L <= 0 || a.dqk <= 0 || a.dv <= 0 || (has_q && a.Hq <= 0))
+    return SPLASH_ERR_INVALID_ARG;
+  if (a.positions == nullptr || ((addr(a.positions) | addr(a.seq_ids)) & 3u) != 0) return SPLASH_ERR_INVALID_ARG;
+  if (a.B > 1 && (a.positions_stride_b < 0 || (a.seq_ids != nullptr && a.seq_ids_stride_b < 0)))
+    return SPLASH_ERR_INVALID_ARG;
+  if (!valid_head_dim(a.dqk) || !valid_head_dim(a.dv)) return SPLASH_ERR_UNSUPPORTED;
+  if (a.seq_ids == nullptr && a.num_seqs < a.B) return SPLASH_ERR_SHAPE;
+  splash_status st = SPLASH_OK;
+  if (a.table != nullptr &&
+      (st = check_rotation(a.table, a.table_rows, a.dqk, a.rot_dim, a.rot_offset, a.interleaved)) != SPLASH_OK)
+    return st;
+  if ((st = check_tokens(a.B, a.L, (int64_t)(has_q ? a.Hq : 0) + 2 * (int64_t)a.Hkv)) != SPLASH_OK) return st;
+  if ((st = check_pages(a.k_cache, a.v_cache, a.num_pages, a.Hkv, a.page_size, a.dqk, a.dv, a.cache_type, a.k_scale,
+                        a.v_scale, a.block_table, a.block_table_stride, a.num_seqs, a.max_pages, true)) != SPLASH_OK)
+    return st;
+  if ((st = check_view(a.k, a.B, a.Hkv, a.L, a.dqk, false)) != SPLASH_OK) return st;
+  if ((st = check_view(a.v, a.B, a.Hkv, a.L, a.dv, false)) != SPLASH_OK) return st;
+  if (has_q) {
+    if ((st = check_view(a.q, a.B, a.Hq, a.L, a.dqk, false)) != SPLASH_OK) return st;
+    if ((st = check_out_view(a.q_out, a.q, a.B, a.Hq, a.L, a.dqk)) != SPLASH_OK) return st;
+  } else if (a.q_out.ptr != nullptr) {
+    return SPLASH_ERR_INVALID_ARG;
+  }
+  if (a.k_out.ptr != nullptr &&
+      (st = check_out_view(a.k_out, a.k, a.B, a.Hkv, a.L, a.dqk)) != SPLASH_OK)
+    return st;
+  uint32_t *err = nullptr;
+  if ((st = current_error_word(&err)) != SPLASH_OK) return st;
+  return splash_paged_append_launch(a, static_cast<cudaStream_t>(cuda_stream), err);
+}
+
+splash_status splash_paged_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dv,
+                                                 size_t *bytes) {
+  if (bytes == nullptr || B <= 0 || Hq <= 0 || Hkv <= 0 || Lq <= 0 || dv <= 0) return SPLASH_ERR_INVALID_ARG;
+  if (Hq % Hkv != 0) return SPLASH_ERR_SHAPE;
+  if (Lq > SPLASH_MAX_NEW_TOKENS || B > 65535 || (dv != 64 && dv != 128)) return SPLASH_ERR_UNSUPPORTED;
+  *bytes = splash_paged_decode_workspace_bytes(B, Hq, Hkv, Lq, dv);
+  return SPLASH_OK;
+}
+
+splash_status splash_paged_decode(const splash_paged_decode_args *args, void *cuda_stream) {
+  if (args == nullptr || args->struct_bytes != sizeof *args) return SPLASH_ERR_INVALID_ARG;
+  const splash_paged_decode_args &a = *args;
+  if (a.B <= 0 || a.Hq <= 0 || a.Hkv <= 0 || a.Lq <= 0 || a.dqk <= 0 || a.dv <= 0 || a.reserved != 0)
+    return SPLASH_ERR_INVALID_ARG;
+  if (a.seq_lens == nullptr || a.out == nullptr || a.lse == nullptr || a.workspace == nullptr)
+    return SPLASH_ERR_INVALID_ARG;
+  if (((addr(a.out) | addr(a.workspace)) & 15u) != 0 || ((addr(a.seq_lens) | addr(a.lse)) & 3u) != 0)
+    return SPLASH_ERR_INVALID_ARG;
+  if (!(a.scale > 0.f) || !(a.scale < INFINITY) || !(a.softcap == a.softcap) || a.softcap == INFINITY)
+    return SPLASH_ERR_INVALID_ARG;
+  if (a.window_left < -1) return SPLASH_ERR_INVALID_ARG;
+  size_t need = 0;
+  splash_status st = splash_paged_decode_workspace_size(a.B, a.Hq, a.Hkv, a.Lq, a.dv, &need);
+  if (st != SPLASH_OK) return st;
+  if (!((a.dqk == 64 && a.dv == 64) || (a.dqk == 128 && a.dv == 128) || (a.dqk == 192 && a.dv == 128)))
+    return SPLASH_ERR_UNSUPPORTED;
+  if ((int64_t)a.B * a.Hq * a.Lq > INT32_MAX || a.Hq > 65535) return SPLASH_ERR_UNSUPPORTED;
+  if (a.workspace_bytes < need) return SPLASH_ERR_INVALID_ARG;
+  if ((st = check_pages(a.k_cache, a.v_cache, a.num_pages, a.Hkv, a.page_size, a.dqk, a.dv, a.cache_type, a.k_scale,
+                        a.v_scale, a.block_table, a.block_table_stride, a.B, a.max_pages, false)) != SPLASH_OK)
+    return st;
+  if ((st = check_view(a.q, a.B, a.Hq, a.Lq, a.dqk, false)) != SPLASH_OK) return st;
+  uint32_t *err = nullptr;
+  if ((st = current_error_word(&err)) != SPLASH_OK) return st;
+  return splash_paged_decode_launch(a, static_cast<cudaStream_t>(cuda_stream), err);
+}
+
 splash_status splash_last_device_error(void *cuda_stream) {
   int dev = 0;
   SPLASH_CUDA_TRY(cudaGetDevice(&dev));

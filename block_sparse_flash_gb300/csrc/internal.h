@@ -158,6 +158,12 @@ splash_status splash_attention_fwd_host_launch(const void *q_h, const void *k_h,
 splash_status splash_wait_selftest_launch(uint64_t timeout_ns, cudaStream_t stream,
                                           uint32_t *err_word);
 
+// rope.cu, paged_decode.cu (arguments checked in api.cu)
+splash_status splash_rope_launch(const splash_rope_args &a, cudaStream_t stream, uint32_t *err_word);
+splash_status splash_paged_append_launch(const splash_paged_append_args &a, cudaStream_t stream, uint32_t *err_word);
+splash_status splash_paged_decode_launch(const splash_paged_decode_args &a, cudaStream_t stream, uint32_t *err_word);
+size_t splash_paged_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dv);
+
 // Counts kernel launches (splash_kernel_launches); call once per launch.
 void splash_count_launches(uint64_t n);
 

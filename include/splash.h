@@ -36,6 +36,7 @@
 #ifndef SPLASH_H
 #define SPLASH_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -390,6 +391,188 @@ splash_status splash_attention_bwd(const void *q, const void *k, const void *v, 
                                    splash_mask_info *mi, float scale, float softcap, void *dq,
                                    void *dk, void *dv_out, void *workspace, size_t workspace_bytes,
                                    void *cuda_stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Serving: rotary positions, a paged key/value cache, attention of new tokens
+ * ---------------------------------------------------------------------------
+ * The calls above work on contiguous keys.  The three below surround them: q
+ * and k are rotated by position before the forward (splash_rope; its inverse
+ * turns the gradients back after the backward), keys and values of served
+ * sequences are kept in pages (splash_paged_append), and new tokens attend to
+ * the pages (splash_paged_decode).  Their arguments come in one struct each;
+ * struct_bytes is sizeof the struct, so that a caller compiled against
+ * another layout is refused (INVALID_ARG).
+ *
+ * All three only queue kernels on cuda_stream and can be captured into a CUDA
+ * graph; what lives in device memory (positions, lengths, the block table)
+ * may change between replays.  Indices read on the device are checked there:
+ * one out of range touches no memory outside the tensors and is reported by
+ * splash_last_device_error as SPLASH_ERR_DEVICE_CHECK.
+ */
+
+/* A bf16 tensor [B][H][L][d]: d contiguous, the other strides in elements
+ * (multiples of 8, so that every row starts on 16 bytes; ptr 16-byte aligned).
+ * The stride of a dimension of size 1 is not read.  Inputs may repeat rows
+ * (stride 0); outputs may not overlap themselves. */
+typedef struct {
+    void *ptr;
+    int64_t stride_b, stride_h, stride_l;
+} splash_view;
+
+/* A cache tensor [num_pages][Hkv][page_size][d]: d contiguous, strides in
+ * elements, rows and ptr 16-byte aligned.  Pages stored token by token
+ * ([num_pages][page_size][Hkv][d]) are this tensor with the strides of the
+ * head and the token exchanged. */
+typedef struct {
+    void *ptr;
+    int64_t stride_page, stride_head, stride_token;
+} splash_cache_view;
+
+#define SPLASH_CACHE_BF16 0
+#define SPLASH_CACHE_E4M3 1 /* stores x / scale[kv head], rounded to nearest even, saturated at +-448 */
+
+/*
+ * splash_rope -- rotary positions.  For a token at position p and every pair
+ * (a, b) of its row's rotated dimensions, with c = table[p][i] and
+ * s = table[p][rot_dim/2 + i] for pair i:
+ *   forward (inverse = 0):  a' = a c - b s,   b' = b c + a s
+ *   gradient (inverse = 1): a' = a c + b s,   b' = b c - a s
+ * (the rotation is linear, so its gradient is the transposed rotation).  The
+ * rotated dimensions are [rot_offset, rot_offset + rot_dim); pair i is
+ * (i, i + rot_dim/2) of them, or (2i, 2i + 1) when interleaved.  The others
+ * are copied.  Computed in fp32, rounded once.
+ *
+ *   q, q_out, k, k_out  views with Hq / Hkv heads; k.ptr NULL = no k.  An
+ *               output is the input's own view (in place) or does not
+ *               overlap any input.
+ *   positions   device int32, [b][l] at positions[b * positions_stride_b + l]
+ *               (stride 0: the same for every b).  A negative position is the
+ *               identity (padding); one >= table_rows also, and is reported.
+ *   table       device fp32 [table_rows][rot_dim], cosines then sines,
+ *               16-byte aligned
+ *   d           multiple of 16, <= 512;  rot_dim a positive multiple of 16;
+ *               rot_offset a multiple of 8; rot_offset + rot_dim <= d
+ * Errors: INVALID_ARG (NULL, alignment, strides, flags), SHAPE (rotated
+ * dimensions outside d), UNSUPPORTED (sizes), CUDA.
+ */
+typedef struct {
+    uint64_t struct_bytes;
+    splash_view q, q_out, k, k_out;
+    const int32_t *positions;
+    int64_t positions_stride_b;
+    const float *table;
+    int64_t table_rows;
+    int64_t L;
+    int32_t B, Hq, Hkv, d;
+    int32_t rot_dim, rot_offset, interleaved, inverse;
+} splash_rope_args;
+splash_status splash_rope(const splash_rope_args *args, void *cuda_stream);
+
+/*
+ * splash_paged_append -- writes the keys and values of new tokens into a paged
+ * cache, rotating them on the way.  Token (b, l) of sequence
+ * s = seq_ids ? seq_ids[b][l] : b at position p = positions[b][l] goes to page
+ * block_table[s][p / page_size], row p % page_size:
+ *   k_cache[page][h][row] = rotated k[b][h][l]    v_cache[...] = v[b][h][l]
+ * (divided by k_scale[h] / v_scale[h] and rounded to e4m3 in an 8-bit cache;
+ * the rotated key is rounded once, from fp32).  Optionally also
+ *   q_out = rotated q        (q.ptr not NULL)
+ *   k_out = rotated k, bf16  (k_out.ptr not NULL: for splash_attention_fwd)
+ * With table NULL nothing is rotated.  Nothing else in the cache is written.
+ *
+ * A token with a negative position is padding: no cache row is written, its
+ * q_out / k_out rows are copies of q / k.  A position outside the table of
+ * rotations or the block table's row, a page outside [0, num_pages) or a
+ * sequence outside [0, num_seqs) is reported and treated the same way (q_out
+ * and k_out are rotated where the position has a rotation).  Two tokens of
+ * one call must not share a cache row; if they do, each of its elements is
+ * one of the two.
+ *
+ *   seq_ids     device int32 [b][l] (stride as positions) or NULL: b.  This
+ *               is how a row of packed documents is appended.
+ *   block_table device int32 [num_seqs][max_pages], row stride
+ *               block_table_stride; entries of pages not written are not read
+ *   page_size   a power of two, 16 .. 1024
+ *   dqk, dv     multiples of 16, <= 512
+ *   k_scale, v_scale  device fp32 [Hkv], both required for e4m3, else ignored
+ * The rotation's arguments and the errors are as for splash_rope.
+ */
+typedef struct {
+    uint64_t struct_bytes;
+    splash_view q, q_out, k, k_out, v;
+    splash_cache_view k_cache, v_cache;
+    const float *k_scale, *v_scale;
+    const int32_t *block_table;
+    int64_t block_table_stride;
+    const int32_t *positions;
+    int64_t positions_stride_b;
+    const int32_t *seq_ids;
+    int64_t seq_ids_stride_b;
+    const float *table;
+    int64_t table_rows;
+    int64_t L, num_pages;
+    int32_t B, Hq, Hkv, dqk, dv;
+    int32_t num_seqs, max_pages, page_size, cache_type;
+    int32_t rot_dim, rot_offset, interleaved;
+} splash_paged_append_args;
+splash_status splash_paged_append(const splash_paged_append_args *args, void *cuda_stream);
+
+/* Most new tokens per sequence in one splash_paged_decode call. */
+#define SPLASH_MAX_NEW_TOKENS 16
+
+/*
+ * splash_paged_decode -- attention of each sequence's newest Lq tokens over
+ * its paged cache (which already holds their keys).  Sequence b has
+ * n = seq_lens[b] cached tokens; its query l sits at position p = n - Lq + l
+ * and sees the keys j <= p, and with window_left >= 0 only those with
+ * p - j <= window_left.  For query head h and g = h / (Hq/Hkv):
+ *   s_j = scale * q[b,h,l,:] . k[j,:]   (times k_scale[g] for e4m3; capped as
+ *         in splash_attention_fwd when softcap > 0)
+ *   out[b,h,l,:] = sum_j exp(s_j - lse) v[j,:]   (times v_scale[g] for e4m3)
+ *   lse[b,h,l]   = ln sum_j exp(s_j)
+ * A query that sees no key (n = 0, or p < 0) gets out = 0 and lse = -inf.
+ * This equals splash_attention_fwd over the gathered keys with the mask
+ * causal from the sequence's end.  Cache rows that no query sees (past n, or
+ * before the window) are not read, nor are the block table's entries for
+ * them, so they may hold anything.
+ *
+ * A negative n counts as 0 and one above max_pages * page_size as that; a page
+ * outside [0, num_pages) reads as keys and values of zero; each is reported.
+ *
+ *   q           view [B][Hq][Lq][dqk]
+ *   out         device bf16 [B][Hq][Lq][dv] dense, 16-byte aligned
+ *   lse         device fp32 [B][Hq][Lq]
+ *   workspace   device, 16-byte aligned, at least
+ *               splash_paged_decode_workspace_size bytes for the same B, Hq,
+ *               Hkv, Lq, dv; overwritten, holds nothing between calls.  Two
+ *               calls that may run at the same time need two workspaces.
+ * Supported: (dqk, dv) in {(64, 64), (128, 128), (192, 128)}, Hq % Hkv == 0,
+ * 1 <= Lq <= SPLASH_MAX_NEW_TOKENS, page_size a power of two in 16 .. 1024,
+ * B <= 65535.  The result does not depend on timing: the same inputs give the
+ * same bits on the same GPU.
+ */
+typedef struct {
+    uint64_t struct_bytes;
+    splash_view q;
+    splash_cache_view k_cache, v_cache;
+    const float *k_scale, *v_scale;
+    const int32_t *block_table;
+    int64_t block_table_stride;
+    const int32_t *seq_lens;
+    void *out;
+    float *lse;
+    void *workspace;
+    uint64_t workspace_bytes;
+    int64_t num_pages, window_left;
+    int32_t B, Hq, Hkv, Lq, dqk, dv;
+    int32_t max_pages, page_size, cache_type;
+    float scale, softcap;
+    int32_t reserved; /* 0 */
+} splash_paged_decode_args;
+splash_status splash_paged_decode(const splash_paged_decode_args *args, void *cuda_stream);
+splash_status splash_paged_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dv,
+                                                 size_t *bytes);
 
 /*
  * splash_classify_blocks_noalloc -- the block classification of a mask

@@ -1,0 +1,232 @@
+"""Refusals of the serving calls (rope, paged_append, paged_decode) on the CPU:
+the C entry points reject invalid arguments before touching the GPU, and the
+binding rejects tensors that do not fit.  No call here reaches a launch: there
+is no device."""
+import ctypes
+
+import pytest
+import torch
+
+OK_PTR = 1 << 20  # 16-byte aligned, never read
+
+
+@pytest.fixture(scope="module")
+def splash():
+    from block_sparse_flash_gb300 import build as b
+    b.build()
+    import block_sparse_flash_gb300 as m
+    return m
+
+
+class View(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("a", "b", "c")]
+
+
+def fields(*groups):
+    out = [("struct_bytes", ctypes.c_uint64)]
+    for kind, names in groups:
+        out += [(n, kind) for n in names.split()]
+    return out
+
+
+P, I64, I32, F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = fields((View, "q q_out k k_out"), (P, "positions"), (I64, "positions_stride_b"), (P, "table"),
+                      (I64, "table_rows L"), (I32, "B Hq Hkv d rot_dim rot_offset interleaved inverse"))
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = fields((View, "q q_out k k_out v k_cache v_cache"), (P, "k_scale v_scale block_table"),
+                      (I64, "block_table_stride"), (P, "positions"), (I64, "positions_stride_b"), (P, "seq_ids"),
+                      (I64, "seq_ids_stride_b"), (P, "table"), (I64, "table_rows L num_pages"),
+                      (I32, "B Hq Hkv dqk dv num_seqs max_pages page_size cache_type rot_dim rot_offset interleaved"))
+
+
+class DecodeArgs(ctypes.Structure):
+    _fields_ = fields((View, "q k_cache v_cache"), (P, "k_scale v_scale block_table"), (I64, "block_table_stride"),
+                      (P, "seq_lens out lse workspace"), (ctypes.c_uint64, "workspace_bytes"),
+                      (I64, "num_pages window_left"), (I32, "B Hq Hkv Lq dqk dv max_pages page_size cache_type"),
+                      (F32, "scale softcap"), (I32, "reserved"))
+
+
+def dense(H, L, d):
+    return View(OK_PTR, H * L * d, L * d, d)
+
+
+def rope_args():
+    a = RopeArgs(q=dense(4, 8, 128), q_out=dense(4, 8, 128), k=dense(2, 8, 128), k_out=dense(2, 8, 128),
+                 positions=OK_PTR, positions_stride_b=8, table=OK_PTR, table_rows=8, L=8, B=2, Hq=4, Hkv=2, d=128,
+                 rot_dim=128)
+    a.struct_bytes = ctypes.sizeof(a)
+    return a
+
+
+def append_args():
+    a = AppendArgs(q=dense(4, 8, 128), q_out=dense(4, 8, 128), k=dense(2, 8, 128), v=dense(2, 8, 128),
+                   k_cache=dense(2, 16, 128), v_cache=dense(2, 16, 128), block_table=OK_PTR, block_table_stride=4,
+                   positions=OK_PTR, positions_stride_b=8, table=OK_PTR, table_rows=8, L=8, num_pages=9, B=2, Hq=4,
+                   Hkv=2, dqk=128, dv=128, num_seqs=2, max_pages=4, page_size=16, rot_dim=128)
+    a.struct_bytes = ctypes.sizeof(a)
+    return a
+
+
+def decode_args():
+    a = DecodeArgs(q=dense(4, 1, 128), k_cache=dense(2, 16, 128), v_cache=dense(2, 16, 128), block_table=OK_PTR,
+                   block_table_stride=4, seq_lens=OK_PTR, out=OK_PTR, lse=OK_PTR, workspace=OK_PTR,
+                   workspace_bytes=1 << 40, num_pages=9, window_left=-1, B=2, Hq=4, Hkv=2, Lq=1, dqk=128, dv=128,
+                   max_pages=4, page_size=16, scale=0.1)
+    a.struct_bytes = ctypes.sizeof(a)
+    return a
+
+
+def call(splash, name, a):
+    return getattr(splash.lib(), name)(bytes(a), None)
+
+
+def refused(splash, name, make, changes):
+    """Each (member, value, status): applied alone to valid arguments."""
+    for member, value, status in changes:
+        a = make()
+        where = a
+        *path, last = member.split(".")
+        for x in path:
+            where = getattr(where, x)
+        setattr(where, last, value)
+        assert call(splash, name, a) == status, (name, member, value)
+
+
+INVALID, SHAPE, UNSUPPORTED, CUDA = 1, 2, 3, 4
+
+
+def test_struct_layouts_agree(splash):
+    assert splash._ROPE_ARGS.size == ctypes.sizeof(RopeArgs)
+    assert splash._APPEND_ARGS.size == ctypes.sizeof(AppendArgs)
+    assert splash._DECODE_ARGS.size == ctypes.sizeof(DecodeArgs)
+    # the library compares struct_bytes with its own sizeof: valid arguments
+    # get past every check and fail only at the missing device
+    if not torch.cuda.is_available():
+        for name, make in (("splash_rope", rope_args), ("splash_paged_append", append_args),
+                           ("splash_paged_decode", decode_args)):
+            assert call(splash, name, make()) == CUDA
+
+
+def test_null_arguments(splash):
+    for f in (splash.lib().splash_rope, splash.lib().splash_paged_append, splash.lib().splash_paged_decode):
+        assert f(None, None) == INVALID
+
+
+COMMON_TOKENS = [("struct_bytes", 8, INVALID), ("B", 0, INVALID), ("L", 0, INVALID), ("L", -1, INVALID),
+                 ("L", 1 << 31, UNSUPPORTED), ("positions", None, INVALID), ("positions", OK_PTR + 2, INVALID),
+                 ("positions_stride_b", -8, INVALID), ("rot_dim", 0, INVALID), ("rot_dim", 24, UNSUPPORTED),
+                 ("rot_dim", 144, SHAPE), ("rot_offset", 16, SHAPE), ("rot_offset", -8, INVALID),
+                 ("rot_offset", 4, UNSUPPORTED), ("interleaved", 2, INVALID), ("table", OK_PTR + 4, INVALID),
+                 ("table_rows", 0, INVALID), ("q_out.ptr", None, INVALID), ("q_out.ptr", OK_PTR + 8, INVALID),
+                 ("q.c", 132, INVALID), ("q.a", -8, INVALID), ("q_out.b", 0, INVALID), ("q_out.c", 64, INVALID),
+                 ("q_out.c", 256, INVALID)]
+
+
+def test_rope_refusals(splash):
+    refused(splash, "splash_rope", rope_args, COMMON_TOKENS + [
+        ("Hq", 0, INVALID), ("Hkv", 0, INVALID), ("d", 0, INVALID), ("d", 120, UNSUPPORTED), ("d", 528, UNSUPPORTED),
+        ("q.ptr", None, INVALID), ("k_out.ptr", None, INVALID), ("table", None, INVALID), ("inverse", 2, INVALID),
+        ("Hq", 65534, UNSUPPORTED)])
+
+
+def test_append_refusals(splash):
+    refused(splash, "splash_paged_append", append_args, COMMON_TOKENS + [
+        ("Hkv", 0, INVALID), ("dqk", 0, INVALID), ("dv", 0, INVALID), ("dv", 72, UNSUPPORTED), ("Hq", 0, INVALID),
+        ("q.ptr", None, INVALID), ("k.ptr", None, INVALID), ("v.ptr", None, INVALID), ("v.c", 4, INVALID),
+        ("k_cache.ptr", None, INVALID), ("v_cache.ptr", OK_PTR + 8, INVALID), ("k_cache.c", 136 + 4, INVALID),
+        ("k_cache.a", 0, INVALID), ("v_cache.b", 64, INVALID), ("page_size", 0, INVALID),
+        ("page_size", 8, UNSUPPORTED), ("page_size", 24, UNSUPPORTED), ("page_size", 2048, UNSUPPORTED),
+        ("num_pages", 0, INVALID), ("max_pages", 0, INVALID), ("max_pages", 1 << 28, UNSUPPORTED),
+        ("num_seqs", 1, SHAPE), ("cache_type", 2, INVALID), ("cache_type", 1, INVALID), ("block_table", None, INVALID),
+        ("block_table_stride", -1, INVALID), ("seq_ids", OK_PTR + 1, INVALID)])
+
+
+def test_append_rows_that_would_overlap_are_refused(splash):
+    a = append_args()  # token-major pages: the same tensor with head and token strides exchanged
+    a.k_cache = View(OK_PTR, 2 * 16 * 128, 128, 2 * 128)
+    if not torch.cuda.is_available():
+        assert call(splash, "splash_paged_append", a) == CUDA  # past every check
+    a = append_args()
+    a.k_cache = View(OK_PTR, 2 * 16 * 128, 128, 128)
+    assert call(splash, "splash_paged_append", a) == INVALID
+
+
+def test_decode_refusals(splash):
+    refused(splash, "splash_paged_decode", decode_args, [
+        ("struct_bytes", 8, INVALID), ("B", 0, INVALID), ("B", 65536, UNSUPPORTED), ("Hkv", 3, SHAPE),
+        ("Lq", 0, INVALID), ("Lq", 17, UNSUPPORTED), ("dqk", 64, UNSUPPORTED), ("dv", 96, UNSUPPORTED),
+        ("seq_lens", None, INVALID), ("seq_lens", OK_PTR + 2, INVALID), ("out", None, INVALID),
+        ("out", OK_PTR + 8, INVALID), ("lse", None, INVALID), ("workspace", None, INVALID),
+        ("workspace", OK_PTR + 8, INVALID), ("workspace_bytes", 8, INVALID), ("scale", 0.0, INVALID),
+        ("scale", float("nan"), INVALID), ("scale", float("inf"), INVALID), ("softcap", float("nan"), INVALID),
+        ("softcap", float("inf"), INVALID), ("window_left", -2, INVALID), ("reserved", 1, INVALID),
+        ("q.ptr", None, INVALID), ("q.b", 4, INVALID), ("k_cache.ptr", None, INVALID), ("v_cache.c", 4, INVALID),
+        ("cache_type", 1, INVALID), ("cache_type", -1, INVALID), ("page_size", 12, UNSUPPORTED),
+        ("num_pages", 0, INVALID), ("max_pages", 0, INVALID), ("block_table", None, INVALID)])
+
+
+def test_decode_workspace_size(splash):
+    f = splash.lib().splash_paged_decode_workspace_size
+    n = ctypes.c_size_t(0)
+    assert f(4, 32, 8, 1, 128, ctypes.byref(n)) == 0 and n.value >= 16
+    assert splash.paged_decode_workspace_size(4, 32, 8, 1, 128) == n.value
+    assert f(4, 32, 8, 1, 128, None) == INVALID and f(0, 32, 8, 1, 128, ctypes.byref(n)) == INVALID
+    assert f(4, 32, 7, 1, 128, ctypes.byref(n)) == SHAPE and f(4, 32, 8, 17, 128, ctypes.byref(n)) == UNSUPPORTED
+
+
+def test_the_binding_refuses_cpu_tensors(splash, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    q = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+    pos = torch.zeros(1, 4, dtype=torch.int32)
+    t = torch.zeros(4, 64)
+    cache = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
+    bt = torch.zeros(1, 1, dtype=torch.int32)
+    for f in (lambda: splash.rope_fwd(q, q, pos, t), lambda: splash.rope_bwd(q, None, pos, t),
+              lambda: splash.paged_append(q, q, cache, cache, bt, pos),
+              lambda: splash.paged_decode(q, cache, cache, bt, pos[:, 0], 0.1)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            f()
+
+
+def test_the_binding_refuses_wrong_types_and_shapes(splash):
+    bf, dev = torch.bfloat16, -1  # CPU tensors report device -1: the checks behind the device check
+    x = torch.zeros(2, 3, 4, 64, dtype=bf)
+    assert splash._view4("x", x, x.shape, dev)[1:] == (768, 256, 64)
+    for bad in (x.float(), x[..., ::2], x.transpose(2, 3)):
+        with pytest.raises(ValueError):
+            splash._view4("x", bad, bad.shape, dev)
+    with pytest.raises(ValueError):
+        splash._view4("x", x, (2, 3, 5, 64), dev)
+    pos = torch.zeros(2, 4, dtype=torch.int32)
+    assert splash._index2("p", pos, 2, 4, dev)[1] == 4 and splash._index2("p", pos[0], 2, 4, dev)[1] == 0
+    for bad in (pos.long(), pos[:, :3], pos[:1], pos.t(), torch.zeros(2, 8, dtype=torch.int32)[:, ::2]):
+        with pytest.raises(ValueError):
+            splash._index2("p", bad, 2, 4, dev)
+    k = torch.zeros(3, 2, 16, 64, dtype=bf)
+    assert splash._cache4(k, k, None, None, dev)[4:] == (0, 3, 2, 16, 64, 64)
+    k8, s = k.to(torch.float8_e4m3fn), torch.ones(2)
+    assert splash._cache4(k8, k8, s, s, dev)[4] == 1
+    for args in ((k8, k8, None, s), (k8, k8, s, torch.ones(3)), (k8, k8, s, s.double()), (k, k, s, s), (k, k8, s, s),
+                 (k.half(), k.half(), None, None), (k, k[:2], None, None), (k[..., ::2], k, None, None)):
+        with pytest.raises(ValueError):
+            splash._cache4(*args, dev)
+    for bad in (torch.zeros(4), torch.zeros(4, 8).t(), torch.zeros(4, 8).double()):
+        with pytest.raises(ValueError):
+            splash._table2(bad, dev)
+    for bad in (pos.long(), pos[0], pos.t()):
+        with pytest.raises(ValueError):
+            splash._block_table(bad, dev)
+
+
+def test_rope_table():
+    import block_sparse_flash_gb300 as m
+    t = m.rope_table(1000, 16, base=500.0, device="cpu")
+    assert t.shape == (1000, 16) and t.dtype == torch.float32
+    a = 999 * 500.0 ** (-6 / 16)
+    assert abs(float(t[999, 3]) - torch.tensor(a, dtype=torch.float64).cos().item()) < 1e-7
+    assert abs(float(t[999, 11]) - torch.tensor(a, dtype=torch.float64).sin().item()) < 1e-7
