@@ -469,7 +469,8 @@ splash_status check_pages(const splash_cache_view &k, const splash_cache_view &v
       (k_scale == nullptr || v_scale == nullptr || ((addr(k_scale) | addr(v_scale)) & 3u) != 0))
     return SPLASH_ERR_INVALID_ARG;
   if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return SPLASH_ERR_UNSUPPORTED;
-  if (num_pages > INT32_MAX || (int64_t)max_pages * page_size > INT32_MAX) return SPLASH_ERR_UNSUPPORTED;
+  // (positions leave room for the kernels' look ahead in 32 bits)
+  if (num_pages > INT32_MAX || (int64_t)max_pages * page_size > INT32_MAX - 65535) return SPLASH_ERR_UNSUPPORTED;
   splash_status st = check_cache(k, num_pages, Hkv, page_size, dqk, type, output);
   if (st != SPLASH_OK) return st;
   return check_cache(v, num_pages, Hkv, page_size, dv, type, output);

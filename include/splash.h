@@ -493,7 +493,7 @@ splash_status splash_rope(const splash_rope_args *args, void *cuda_stream);
  *               is how a row of packed documents is appended.
  *   block_table device int32 [num_seqs][max_pages], row stride
  *               block_table_stride; entries of pages not written are not read
- *   page_size   a power of two, 16 .. 1024
+ *   page_size   a power of two, 16 .. 1024; max_pages * page_size < 2^31 - 65535
  *   dqk, dv     multiples of 16, <= 512
  *   k_scale, v_scale  device fp32 [Hkv], both required for e4m3, else ignored
  * The rotation's arguments and the errors are as for splash_rope.
@@ -549,7 +549,7 @@ splash_status splash_paged_append(const splash_paged_append_args *args, void *cu
  *               calls that may run at the same time need two workspaces.
  * Supported: (dqk, dv) in {(64, 64), (128, 128), (192, 128)}, Hq % Hkv == 0,
  * 1 <= Lq <= SPLASH_MAX_NEW_TOKENS, page_size a power of two in 16 .. 1024,
- * B <= 65535.  The result does not depend on timing: the same inputs give the
+ * max_pages * page_size < 2^31 - 65535, B <= 65535.  The result does not depend on timing: the same inputs give the
  * same bits on the same GPU.
  */
 typedef struct {
