@@ -1,0 +1,35 @@
+// dependent_launch.cuh -- launches that overlap their set-up with the end of
+// the kernel before them in the stream (programmatic dependent launch).  The
+// serving kernels take a few microseconds each and follow one another, so
+// that a launch's own latency (about 1 us) is worth hiding.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace splash {
+
+// First statement of such a kernel, before it reads or writes any memory:
+// waits until everything before it in the stream has completed, and lets the
+// next kernel's blocks be placed (they wait here in turn).
+__device__ __forceinline__ void grid_dependency() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                             const Args &...args) {
+  cudaLaunchConfig_t config = {};
+  config.gridDim = grid;
+  config.blockDim = block;
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, static_cast<Params>(args)...);
+}
+
+}  // namespace splash

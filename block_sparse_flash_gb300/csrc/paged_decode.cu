@@ -8,17 +8,18 @@
 // keep the memory system full.
 //
 //  * Work.  The keys of each (sequence, KV head, group of rows) are cut into
-//    tiles; all tiles form one list, and every CTA of a grid that fills the GPU
-//    once takes an equal, contiguous part of it.  Long and short sequences
-//    thus load every SM alike.  A (sequence, head) that one CTA covers is
-//    finished there; parts of one that several CTAs share go to the workspace
-//    as (sum, maximum, unnormalised output) and a second kernel joins them, in
-//    the order of the keys, so that the result does not depend on timing.
-//  * Loads.  Each warp takes its own keys of a tile (KW of them) and keeps its
-//    own ring of stages in shared memory, filled by 16-byte asynchronous
-//    copies: no barrier between warps in the loop.  Rows outside the keys that
-//    some query sees are filled with zeros instead of being read, so that
-//    whatever they hold cannot reach a product.
+//    steps of KW keys; all steps form one list, and every warp of a grid that
+//    fills the GPU once takes an equal, contiguous part of it.  Long and short
+//    sequences thus load every SM alike.  A (sequence, head) that one warp
+//    covers is finished there; parts of one that several warps share go to the
+//    workspace as (maximum, sum, unnormalised output) and a second kernel joins
+//    them, in the order of the keys, so that the result does not depend on
+//    timing.
+//  * Loads.  Each warp keeps a ring of stages in shared memory, filled by
+//    16-byte asynchronous copies that run ahead of the products and across the
+//    borders of sequences; there is no barrier between warps.  Rows outside the
+//    keys that some query sees are filled with zeros instead of being read, so
+//    that whatever they hold cannot reach a product.
 //  * Products.  16 rows x 16 keys per tensor instruction (mma.sync: with 4 to 32
 //    rows a tile is memory-bound many times over, and the accumulators stay in
 //    registers next to the softmax).  P goes to the second product from the
@@ -31,6 +32,7 @@
 #include <atomic>
 #include <cmath>
 
+#include "dependent_launch.cuh"
 #include "internal.h"
 #include "sm103_ptx.cuh"
 
@@ -39,7 +41,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kMaxGrid = 512;  // CTAs; the workspace holds two parts for each
+constexpr int kMaxWarps = 1216;  // of the grid; the workspace holds two parts for each
 
 // A running maximum is only moved when a score passes it by more than this
 // (in powers of two): until then exp2(s - m) stays below 2^8, which neither
@@ -58,10 +60,10 @@ struct Params {
   const int32_t *seq_lens;
   __nv_bfloat16 *out;
   float *lse;
-  float *part_o, *part_ml;  // [2 * CTAs][rows][DV], [2 * CTAs][rows][2] (maximum, sum)
-  int64_t *first_tile;      // [B + 1] tiles (of one head and row group) before each sequence
+  float *part_o, *part_ml;  // [2 * warps][part_rows][DV], [2 * warps][part_rows][2] (maximum, sum)
+  int64_t *before;          // [B + 1] list entries (of one head and row group) before each sequence
   int64_t num_pages;
-  int32_t B, Hq, Hkv, Lq, G, nrows, row_groups;  // nrows = G * Lq rows per KV head
+  int32_t B, Hkv, Lq, G, nrows, row_groups, part_rows;  // nrows = G * Lq rows per KV head
   int32_t max_pages, page_shift, window;         // window < 0: none
   float scale, cap;                              // cap <= 0: none
   uint32_t *err;
@@ -72,44 +74,69 @@ struct Config {
   static constexpr int DQK = DQK_, DV = DV_, MT = MT_, ROWS = 16 * MT_;
   static constexpr bool E4M3 = E4M3_;
   static constexpr int RK = DQK * (E4M3 ? 1 : 2), RV = DV * (E4M3 ? 1 : 2);  // bytes of a row
-  static constexpr int NB = RK + RV >= 512 ? 1 : 2;                          // 16-key blocks per warp and step
-  static constexpr int KW = 16 * NB, TILE = KW * kWarps;
+  static constexpr int NB = RK + RV >= 512 ? 1 : 2;                          // 16-key blocks per step
+  static constexpr int KW = 16 * NB;
   static constexpr int STAGE = KW * (RK + RV);
-  static constexpr int STAGES = STAGE * kWarps >= 40960 ? 2 : STAGE * kWarps >= 32768 ? 3 : 6;
-  static constexpr int RING = STAGES * STAGE;  // per warp
-  static constexpr int ODIM = DV + 4;          // floats of a row of the warps' join
-  static constexpr int QBYTES = ROWS * DQK * 2;
-  static constexpr int SMEM = kWarps * RING + QBYTES;
-  static_assert(RING >= ROWS * ODIM * 4, "the join of the warps reuses their rings");
+  static constexpr int QBYTES = MT == 1 ? 0 : ROWS * DQK * 2;  // queries of 16 rows stay in registers
+  // two CTAs per SM, if at least two stages fit
+  static constexpr int STAGES = std::max(2, (108 * 1024 / kWarps - QBYTES) / STAGE);
+  static constexpr int WARP_BYTES = STAGES * STAGE + QBYTES;
+  static constexpr int SMEM = kWarps * WARP_BYTES;
+  static constexpr int CTAS = SMEM <= 110 * 1024 ? 2 : 1;  // per SM
 };
 
-// The keys of sequence b that its queries see, in tiles.
+// The keys of sequence b that its queries see, in steps of KW.
 struct Span {
-  int32_t n, lo;      // keys [lo, n) are visible to some query
-  int32_t tile0, nt;  // tiles tile0 .. tile0 + nt - 1; at least one, so that empty rows are written too
+  int32_t n, lo;       // keys [lo, n) are visible to some query
+  int32_t step0, nst;  // steps step0 .. step0 + nst - 1; at least one, so that empty rows are written too
 };
 
-template <int TILE>
+template <int KW>
 __device__ __forceinline__ Span span_of(const Params &p, int b) {
   Span s;
   const int64_t most = (int64_t)p.max_pages << p.page_shift;
   const int32_t n = __ldg(p.seq_lens + b);
   s.n = n < 0 ? 0 : n > most ? (int32_t)most : n;
   s.lo = p.window < 0 ? 0 : max(0, s.n - p.Lq - p.window);
-  s.tile0 = s.lo / TILE;
-  s.nt = max(1, (s.n + TILE - 1) / TILE - s.tile0);
+  s.step0 = s.lo / KW;
+  s.nst = max(1, (s.n + KW - 1) / KW - s.step0);
   return s;
 }
 
-// Equal contiguous parts of T tiles: CTA c takes [part(c), part(c + 1)).
+// a / b for a >= 0, b > 0 (a 64-bit division takes some hundred instructions).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// Equal contiguous parts of T entries: warp w takes [begin(w), begin(w + 1)).
 struct Parts {
   int64_t each;
-  int32_t more;  // the first `more` CTAs take one tile more
-  __device__ __forceinline__ Parts(int64_t T, int32_t ctas) : each(T / ctas), more((int32_t)(T % ctas)) {}
-  __device__ __forceinline__ int64_t begin(int32_t c) const { return each * c + min(c, more); }
+  int32_t more;  // the first `more` warps take one entry more
+  __device__ __forceinline__ Parts(int64_t T, int32_t warps) : each(quotient(T, warps)), more((int32_t)(T - each * warps)) {}
+  __device__ __forceinline__ int64_t begin(int32_t w) const { return each * w + min(w, more); }
   __device__ __forceinline__ int32_t owner(int64_t u) const {
     const int64_t cut = (each + 1) * more;
-    return u < cut ? (int32_t)(u / (each + 1)) : more + (int32_t)((u - cut) / each);
+    return u < cut ? (int32_t)quotient(u, each + 1) : more + (int32_t)quotient(u - cut, each);
+  }
+};
+
+// A warp's place in its part of the list.
+template <int KW>
+struct Cursor {
+  int64_t u;  // list entry of the current step
+  int32_t b, seg, step;  // segment seg (head, row group) of sequence b, its step
+  Span s;
+  // returns true when the segment changed; s is that of b as long as u < end
+  __device__ __forceinline__ bool advance(const Params &p, int per_seq, int64_t end) {
+    ++u;
+    if (++step < s.nst) return false;
+    step = 0;
+    if (++seg == per_seq) {
+      seg = 0;
+      ++b;
+      if (u < end) s = span_of<KW>(p, b);
+    }
+    return true;
   }
 };
 
@@ -171,26 +198,43 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+// The larger exponent field of a word's two bf16 values, and the word as fp16
+// values over 2^(top - 127).
+__device__ __forceinline__ uint32_t exponent(uint32_t x) { return max((x >> 7) & 255u, (x >> 23) & 255u); }
+__device__ __forceinline__ uint32_t to_half(uint32_t x, uint32_t top) {
+  const float down = __uint_as_float((254u - top) << 23);
+  return pack2<true>(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down);
+}
+
 // tanh|x| = (1 - e) / (1 + e), e = exp(-2|x|)
 __device__ __forceinline__ float tanh_of(float x) {
   const float e = ex2_approx(-2.f * kLog2e * fabsf(x));
   return copysignf(__fdividef(1.f - e, 1.f + e), x);
 }
 
-// One warp's copies of its KW keys of a tile into a stage.
+// A warp's copies: the steps of its part of the list, in order.
 template <class C>
 struct Loader {
   const Params &p;
-  int b, head, lane;
-  int32_t n, lo;
+  const int lane, per_seq;
+  const int64_t end;
+  Cursor<C::KW> at;
+  const char *k, *v;  // the head's rows of page 0
   const int32_t *pages;
-  int32_t next[C::NB];  // page entries of the next step, read one step ahead
+  int32_t entry[C::NB];  // the step's page entries, read one step ahead
 
-  __device__ __forceinline__ void look(int32_t key0) {
+  __device__ __forceinline__ void enter() {
+    const int head = at.seg / p.row_groups;
+    k = p.k + head * p.k_head;
+    v = p.v + head * p.v_head;
+    pages = p.block_table + at.b * p.block_table_stride;
+  }
+
+  __device__ __forceinline__ void look() {
 #pragma unroll
     for (int i = 0; i < C::NB; ++i) {
-      const int32_t key = key0 + 16 * i;
-      next[i] = key < n && key + 16 > lo ? __ldg(pages + (key >> p.page_shift)) : 0;
+      const int32_t key = (at.s.step0 + at.step) * C::KW + 16 * i;
+      entry[i] = key < at.s.n && key + 16 > at.s.lo ? __ldg(pages + (key >> p.page_shift)) : 0;
     }
   }
 
@@ -203,31 +247,31 @@ struct Loader {
 #pragma unroll
     for (int rg = 0; rg < 16 / RPI; ++rg) {
       const int r = rg * RPI + r0;
-      const bool read = ok && key + r >= lo && key + r < n;
+      const bool read = ok && key + r >= at.s.lo && key + r < at.s.n;
 #pragma unroll
       for (int part = 0; part < ROWB / SEG; ++part)
         copy16(dst + chunk_at<ROWB>(r, part * LPS + c0), read ? src + rg * RPI * token + part * SEG : base, read);
     }
   }
 
-  // the keys key0 .. key0 + KW - 1 (pages looked up before), and the pages of
-  // the step after
-  __device__ __forceinline__ void step(uint32_t stage, int32_t key0, int32_t key_next) {
-    if (key0 < n && key0 + C::KW > lo) {
+  // the current step into a stage (nothing once the part is done), as one
+  // group of copies; then on to the next
+  __device__ __forceinline__ void step(uint32_t stage) {
+    if (at.u < end) {
 #pragma unroll
       for (int i = 0; i < C::NB; ++i) {
-        const int32_t key = key0 + 16 * i, page = next[i];
+        const int32_t key = (at.s.step0 + at.step) * C::KW + 16 * i, page = entry[i];
         const bool ok = page >= 0 && page < p.num_pages;
         if (!ok && lane == 0) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
         const int32_t slot = key & ((1 << p.page_shift) - 1);
-        const int64_t at = ok ? page : 0;
-        block<C::RK>(stage + i * 16 * C::RK, p.k + at * p.k_page + head * p.k_head + slot * p.k_token, p.k_token, key, ok);
-        block<C::RV>(stage + C::KW * C::RK + i * 16 * C::RV, p.v + at * p.v_page + head * p.v_head + slot * p.v_token,
-                     p.v_token, key, ok);
+        const int64_t pg = ok ? page : 0;
+        block<C::RK>(stage + i * 16 * C::RK, k + pg * p.k_page + slot * p.k_token, p.k_token, key, ok);
+        block<C::RV>(stage + C::KW * C::RK + i * 16 * C::RV, v + pg * p.v_page + slot * p.v_token, p.v_token, key, ok);
       }
+      if (at.advance(p, per_seq, end) && at.u < end) enter();
+      if (at.u < end) look();
     }
     copy_commit();
-    look(key_next);
   }
 };
 
@@ -236,25 +280,24 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
   constexpr int DQK = C::DQK, DV = C::DV, MT = C::MT, NB = C::NB;
   constexpr bool E4M3 = C::E4M3;
   extern __shared__ __align__(1024) char smem[];
-  __shared__ int64_t s_scan[kWarps], s_start[2];
-  __shared__ float s_factor[C::ROWS], s_ml[kWarps][C::ROWS][2];
+  __shared__ int64_t s_scan[kWarps], s_before[kWarps];
+  __shared__ int32_t s_seq[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int quad = lane >> 2, tq = lane & 3;
-  char *q_smem = smem + kWarps * C::RING;
-  char *ring = smem + warp * C::RING;
-  const uint32_t ring_u = smem_u32(ring), q_u = smem_u32(q_smem);
+  const uint32_t ring = smem_u32(smem + warp * C::WARP_BYTES);
+  const uint32_t q_u = ring + C::STAGES * C::STAGE;
+  char *q_smem = smem + warp * C::WARP_BYTES + C::STAGES * C::STAGE;
 
-  // the join may be launched; it waits for this grid before it reads
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_dependency();
 
-  // ---- this CTA's part of the list of tiles: a scan over the sequences
-  const int per_seq = p.Hkv * p.row_groups;  // entries of the list per tile of a sequence
+  // ---- the warps' parts of the list: a scan over the sequences
+  const int per_seq = p.Hkv * p.row_groups;
   int64_t T;
   {
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
     int64_t own = 0;
-    for (int b = b0; b < b1; ++b) own += span_of<C::TILE>(p, b).nt;
+    for (int b = b0; b < b1; ++b) own += span_of<C::KW>(p, b).nst;
     int64_t before = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -271,107 +314,66 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
       total += s_scan[w];
     }
     T = total * per_seq;
-    const int64_t u = Parts(T, gridDim.x).begin(blockIdx.x);
-    if (blockIdx.x == 0 || (u >= before * per_seq && u < (before + own) * per_seq)) {
+    const Parts parts(T, kWarps * gridDim.x);
+    int64_t first[kWarps];
+    bool mine = blockIdx.x == 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      first[w] = parts.begin(kWarps * blockIdx.x + w);
+      mine |= first[w] >= before * per_seq && first[w] < (before + own) * per_seq;
+    }
+    if (mine) {
       int64_t at = before;
       for (int b = b0; b < b1; ++b) {
-        const int64_t next = at + span_of<C::TILE>(p, b).nt;
-        if (u >= at * per_seq && u < next * per_seq) s_start[0] = b, s_start[1] = at;
+        const int64_t next = at + span_of<C::KW>(p, b).nst;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+          if (first[w] >= at * per_seq && first[w] < next * per_seq) s_seq[w] = b, s_before[w] = at;
         if (blockIdx.x == 0) {
-          p.first_tile[b] = at;
-          if (b == p.B - 1) p.first_tile[p.B] = next;
+          p.before[b] = at;
+          if (b == p.B - 1) p.before[p.B] = next;
+          const int32_t n = __ldg(p.seq_lens + b);
+          if (n < 0 || n > (int64_t)p.max_pages << p.page_shift) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
         }
         at = next;
       }
     }
-    if (blockIdx.x == 0)
-      for (int b = b0; b < b1; ++b) {
-        const int32_t n = p.seq_lens[b];
-        if (n < 0 || n > (int64_t)p.max_pages << p.page_shift) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
-      }
     __syncthreads();
   }
-  const Parts parts(T, gridDim.x);
-  int64_t u = parts.begin(blockIdx.x);
-  const int64_t u_begin = u, u_end = parts.begin(blockIdx.x + 1);
-  int b = (int)s_start[0];
-  int64_t seq_u = s_start[1] * per_seq;  // first list entry of sequence b
+  const int wid = kWarps * blockIdx.x + warp;
+  const Parts parts(T, kWarps * gridDim.x);
+  const int64_t end = parts.begin(wid + 1);
+  Cursor<C::KW> at;
+  at.u = parts.begin(wid);
+  if (at.u >= end) return;
+  at.b = s_seq[warp];
+  at.s = span_of<C::KW>(p, at.b);
+  {
+    const int64_t in_seq = at.u - s_before[warp] * per_seq;
+    at.seg = (int32_t)quotient(in_seq, at.s.nst);
+    at.step = (int32_t)(in_seq - (int64_t)at.seg * at.s.nst);
+  }
+  Loader<C> load{p, lane, per_seq, end, at, nullptr, nullptr, nullptr, {}};
+  load.enter();
+  load.look();
+#pragma unroll
+  for (int s = 0; s < C::STAGES - 1; ++s) load.step(ring + s * C::STAGE);
 
-  for (; u < u_end;) {
-    Span sp = span_of<C::TILE>(p, b);
-    if (u >= seq_u + (int64_t)sp.nt * per_seq) {
-      seq_u += (int64_t)sp.nt * per_seq;
-      ++b;
-      continue;
-    }
-    const int seg = (int)((u - seq_u) / sp.nt);
-    const int32_t t0 = (int32_t)((u - seq_u) % sp.nt);
-    const int32_t t1 = (int32_t)min((int64_t)sp.nt, t0 + (u_end - u));
-    const int head = seg / p.row_groups, row0 = (seg % p.row_groups) * C::ROWS;
+  int slot = 0, part = 2 * wid;
+  while (at.u < end) {
+    // ---- a segment: the rows' queries, 16 bits each.  For e4m3 they become
+    // fp16, scaled by the power of two that brings the row's largest element
+    // into [1, 2).  That is exact except for elements 2^14 times smaller (their
+    // error, 2^-25 of the largest, is below that of an fp32 sum); the factor
+    // goes to the row's scale.
+    const int head = at.seg / p.row_groups, row0 = (at.seg % p.row_groups) * C::ROWS;
     const int rows = min(C::ROWS, p.nrows - row0);
-
-    // ---- queries to shared memory, rows g * Lq + l of the KV head's group.
-    // For e4m3 they become fp16: scaled by a power of two that brings the
-    // row's largest element into [1, 2), which is exact except for elements
-    // 2^14 times smaller than it (their error, 2^-25 of the largest, is below
-    // that of an fp32 sum); the factor goes to the row's scale.
-    for (int r = warp; r < C::ROWS; r += kWarps) {
-      constexpr int W = DQK / 64;  // words (two elements) per lane
-      uint32_t x[W];
-      if (r < rows) {
-        const int g = (row0 + r) / p.Lq, l = (row0 + r) % p.Lq;
-        const char *src = p.q + b * p.q_b + (int64_t)(head * p.G + g) * p.q_h + l * p.q_l;
-#pragma unroll
-        for (int i = 0; i < W; ++i) x[i] = __ldg(reinterpret_cast<const uint32_t *>(src) + i * 32 + lane);
-      } else {
-#pragma unroll
-        for (int i = 0; i < W; ++i) x[i] = 0;
-      }
-      float f = p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e;
-      if (E4M3) {
-        uint32_t top = 0;  // exponent field of the largest element
-#pragma unroll
-        for (int i = 0; i < W; ++i) top = max(top, max((x[i] >> 7) & 255u, (x[i] >> 23) & 255u));
-        top = __reduce_max_sync(~0u, top);
-        top = top == 0 ? 1 : min(top, 253u);
-        const float down = __uint_as_float((254u - top) << 23), up = __uint_as_float(top << 23);
-#pragma unroll
-        for (int i = 0; i < W; ++i)
-          x[i] = pack2<true>(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xffff0000u) * down);
-        f *= up * __ldg(p.k_scale + head);
-      }
-      if (lane == 0) s_factor[r] = f;
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const int d = 2 * (i * 32 + lane);
-        // An ldmatrix of four e4m3 keys leaves elements 4t .. 4t+3 in the
-        // thread that the product expects to hold 2t, 2t+1, 2t+8, 2t+9 of each
-        // 16: the queries are stored in that order.
-        const int at = E4M3 ? (d & ~15) + 2 * ((d & 15) >> 2) + ((d & 2) ? 8 : 0) : d;
-        *reinterpret_cast<uint32_t *>(q_smem + chunk_at<DQK * 2>(r, at >> 3) + (at & 7) * 2) = x[i];
-      }
-    }
-
-    // ---- the keys
-    Loader<C> load{p, b, head, lane, sp.n, sp.lo, p.block_table + b * p.block_table_stride, {}};
-    const int32_t key_base = (sp.tile0 + t0) * C::TILE + warp * C::KW;
-    const int32_t steps = t1 - t0;
-    load.look(key_base);
-#pragma unroll
-    for (int s = 0; s < C::STAGES - 1; ++s) {
-      if (s < steps)
-        load.step(ring_u + s * C::STAGE, key_base + s * C::TILE, key_base + (s + 1) * C::TILE);
-      else
-        copy_commit();
-    }
-    __syncthreads();  // queries
-
+    const bool from_start = at.step == 0;
+    const Span sp = at.s;
+    const int b = at.b;
+    const char *q_head = p.q + b * p.q_b + (int64_t)head * p.G * p.q_h;
+    const float base_factor = (p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e) * (E4M3 ? __ldg(p.k_scale + head) : 1.f);
     uint32_t qa[MT == 1 ? DQK / 16 : 1][4];
-    const uint32_t q_row = (lane & 7) + ((lane >> 3) & 1) * 8;
-    if (MT == 1) {
-#pragma unroll
-      for (int kk = 0; kk < DQK / 16; ++kk) ldsm4(qa[kk], q_u + chunk_at<DQK * 2>(q_row, 2 * kk + (lane >> 4)));
-    }
     float factor[MT][2], m[MT][2], l[MT][2], o[MT][DV / 8][4];
     int32_t pos[MT][2];  // the row's position (rows past the last one see what the last query sees)
 #pragma unroll
@@ -379,34 +381,99 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = mt * 16 + quad + 8 * e;
-        factor[mt][e] = s_factor[r];
-        pos[mt][e] = sp.n - p.Lq + (r < rows ? (row0 + r) % p.Lq : p.Lq - 1);
+        const int g = (row0 + r) / p.Lq, lq = (row0 + r) - g * p.Lq;
+        factor[mt][e] = base_factor;
+        pos[mt][e] = sp.n - p.Lq + (r < rows ? lq : p.Lq - 1);
         m[mt][e] = -INFINITY;
         l[mt][e] = 0.f;
+        if (MT == 1) {
+          // An ldmatrix of e4m3 keys leaves elements 4t .. 4t+3 in the thread
+          // that the product expects to hold 2t, 2t+1, 2t+8, 2t+9 of each 16:
+          // the queries are taken in that order too.
+          const char *src = q_head + (int64_t)g * p.q_h + lq * p.q_l;
+#pragma unroll
+          for (int kk = 0; kk < DQK / 16; ++kk) {
+            uint2 x = make_uint2(0, 0);
+            if (r < rows) {
+              if (E4M3) {
+                x = __ldg(reinterpret_cast<const uint2 *>(src) + 4 * kk + tq);
+              } else {
+                x.x = __ldg(reinterpret_cast<const uint32_t *>(src) + 8 * kk + tq);
+                x.y = __ldg(reinterpret_cast<const uint32_t *>(src) + 8 * kk + tq + 4);
+              }
+            }
+            qa[kk][e] = x.x;
+            qa[kk][2 + e] = x.y;
+          }
+          if (E4M3) {
+            uint32_t top = 0;  // exponent field of the largest element
+#pragma unroll
+            for (int kk = 0; kk < DQK / 16; ++kk) top = max(top, max(exponent(qa[kk][e]), exponent(qa[kk][2 + e])));
+            top = max(top, __shfl_xor_sync(~0u, top, 1));
+            top = max(top, __shfl_xor_sync(~0u, top, 2));
+            top = min(max(top, 1u), 253u);
+#pragma unroll
+            for (int kk = 0; kk < DQK / 16; ++kk) {
+              qa[kk][e] = to_half(qa[kk][e], top);
+              qa[kk][2 + e] = to_half(qa[kk][2 + e], top);
+            }
+            factor[mt][e] *= __uint_as_float(top << 23);
+          }
+        }
       }
+    if (MT > 1) {  // more rows than the registers hold: in shared memory
+      __syncwarp();
+#pragma unroll 4
+      for (int r = 0; r < C::ROWS; ++r) {
+        constexpr int W = DQK / 64;  // words (two elements) per lane
+        const int g = (row0 + r) / p.Lq, lq = (row0 + r) - g * p.Lq;
+        uint32_t x[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          x[i] = r < rows ? __ldg(reinterpret_cast<const uint32_t *>(q_head + (int64_t)g * p.q_h + lq * p.q_l) + i * 32 + lane) : 0;
+        if (E4M3) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < W; ++i) top = max(top, exponent(x[i]));
+          top = min(max(__reduce_max_sync(~0u, top), 1u), 253u);
+#pragma unroll
+          for (int i = 0; i < W; ++i) x[i] = to_half(x[i], top);
+          if (quad == (r & 7)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (r >> 3 == 2 * mt + e) factor[mt][e] *= __uint_as_float(top << 23);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const int d = 2 * (i * 32 + lane);
+          const int to = E4M3 ? (d & ~15) + 2 * ((d & 15) >> 2) + ((d & 2) ? 8 : 0) : d;  // (the order above)
+          *reinterpret_cast<uint32_t *>(q_smem + chunk_at<DQK * 2>(r, to >> 3) + (to & 7) * 2) = x[i];
+        }
+      }
+      __syncwarp();
+    }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int j = 0; j < DV / 8; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[mt][j][i] = 0.f;
+    const uint32_t q_row = (lane & 7) + ((lane >> 3) & 1) * 8;
 
-    int slot = 0;
-    for (int32_t t = 0; t < steps; ++t) {
+    // ---- its steps
+    bool change;
+    do {
       copy_wait<C::STAGES - 2>();
       __syncwarp();
-      const int32_t key0 = key_base + t * C::TILE;
-      const uint32_t ks = ring_u + slot * C::STAGE, vs = ks + C::KW * C::RK;
-      {
-        const int32_t ahead = t + C::STAGES - 1;
-        const int into = slot == 0 ? C::STAGES - 1 : slot - 1;
-        if (ahead < steps)
-          load.step(ring_u + into * C::STAGE, key_base + ahead * C::TILE, key_base + (ahead + 1) * C::TILE);
-        else
-          copy_commit();
-      }
+      const int32_t key0 = (sp.step0 + at.step) * C::KW;
+      const uint32_t ks = ring + slot * C::STAGE, vs = ks + C::KW * C::RK;
+      load.step(ring + (slot == 0 ? C::STAGES - 1 : slot - 1) * C::STAGE);
       slot = slot == C::STAGES - 1 ? 0 : slot + 1;
-      if (key0 >= sp.n || key0 + C::KW <= sp.lo) continue;  // (the same for the whole warp)
+      change = at.advance(p, per_seq, end);
+      if (key0 >= sp.n) continue;  // no keys at all
 
       // S = Q K^T
       float s[MT][2 * NB][4];
@@ -553,12 +620,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
           }
         }
       }
-    }
+    } while (!change && at.u < end);
 
-    // ---- the warps' parts, joined through shared memory (each warp's ring
-    // holds its own)
-    copy_wait<0>();
-    __syncwarp();
+    // ---- finished rows, or this warp's part of them
+    const bool complete = from_start && change;
+    const float v_scale = E4M3 ? __ldg(p.v_scale + head) : 1.f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -567,117 +633,122 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
         float sum = l[mt][e];
         sum += __shfl_xor_sync(~0u, sum, 1);
         sum += __shfl_xor_sync(~0u, sum, 2);
-        if (tq == 0) {
-          s_ml[warp][r][0] = m[mt][e];
-          s_ml[warp][r][1] = sum;
-        }
-        float *row = reinterpret_cast<float *>(ring) + r * C::ODIM;
-        if (E4M3) {
+        if (r >= rows) continue;
+        if (complete) {
+          const float inv = sum == 0.f ? 0.f : v_scale / sum;
+          const int64_t row = ((int64_t)b * p.Hkv + head) * p.nrows + row0 + r;
+          if (tq == 0) p.lse[row] = sum == 0.f ? -INFINITY : (m[mt][e] + log2f(sum)) * kLn2;
+          char *dst = reinterpret_cast<char *>(p.out + row * DV);
+          if (E4M3) {
 #pragma unroll
-          for (int j = 0; j < DV / 16; ++j)
-            *reinterpret_cast<float4 *>(row + 16 * j + 4 * tq) = make_float4(
-                o[mt][2 * j][2 * e], o[mt][2 * j + 1][2 * e], o[mt][2 * j][2 * e + 1], o[mt][2 * j + 1][2 * e + 1]);
+            for (int j = 0; j < DV / 16; ++j)
+              *reinterpret_cast<uint2 *>(dst + 32 * j + 8 * tq) =
+                  make_uint2(pack_bf16x2(o[mt][2 * j][2 * e] * inv, o[mt][2 * j + 1][2 * e] * inv),
+                             pack_bf16x2(o[mt][2 * j][2 * e + 1] * inv, o[mt][2 * j + 1][2 * e + 1] * inv));
+          } else {
+#pragma unroll
+            for (int j = 0; j < DV / 8; ++j)
+              *reinterpret_cast<uint32_t *>(dst + 16 * j + 4 * tq) =
+                  pack_bf16x2(o[mt][j][2 * e] * inv, o[mt][j][2 * e + 1] * inv);
+          }
         } else {
+          const int64_t row = (int64_t)part * p.part_rows + r;
+          if (tq == 0) *reinterpret_cast<float2 *>(p.part_ml + 2 * row) = make_float2(m[mt][e], sum);
+          float *dst = p.part_o + row * DV;
+          if (E4M3) {
 #pragma unroll
-          for (int j = 0; j < DV / 8; ++j)
-            *reinterpret_cast<float2 *>(row + 8 * j + 2 * tq) = make_float2(o[mt][j][2 * e], o[mt][j][2 * e + 1]);
+            for (int j = 0; j < DV / 16; ++j)
+              *reinterpret_cast<float4 *>(dst + 16 * j + 4 * tq) = make_float4(
+                  o[mt][2 * j][2 * e], o[mt][2 * j + 1][2 * e], o[mt][2 * j][2 * e + 1], o[mt][2 * j + 1][2 * e + 1]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < DV / 8; ++j)
+              *reinterpret_cast<float2 *>(dst + 8 * j + 2 * tq) = make_float2(o[mt][j][2 * e], o[mt][j][2 * e + 1]);
+          }
         }
       }
-    __syncthreads();
-    const bool complete = t0 == 0 && t1 == sp.nt;
-    const int part = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
-    constexpr int LANES = DV / 4, STEP = kThreads / LANES;  // lanes per row, rows at a time
-    const int col = 4 * (threadIdx.x % LANES);
-    const float v_scale = E4M3 ? __ldg(p.v_scale + head) : 1.f;
-    for (int r = threadIdx.x / LANES; r < rows; r += STEP) {
-      float top = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][r][0]);
-      const float ref = top == -INFINITY ? 0.f : top;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2_approx(s_ml[w][r][0] - ref);
-        sum += f * s_ml[w][r][1];
-        const float4 x = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + w * C::RING) + r * C::ODIM + col);
-        acc.x += f * x.x;
-        acc.y += f * x.y;
-        acc.z += f * x.z;
-        acc.w += f * x.w;
-      }
-      if (complete) {
-        const float inv = sum == 0.f ? 0.f : v_scale / sum;
-        const int64_t row = ((int64_t)b * p.Hkv + head) * p.nrows + row0 + r;
-        *reinterpret_cast<uint2 *>(p.out + row * DV + col) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (col == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-      } else {
-        *reinterpret_cast<float4 *>(p.part_o + ((int64_t)part * C::ROWS + r) * DV + col) = acc;
-        if (col == 0) *reinterpret_cast<float2 *>(p.part_ml + ((int64_t)part * C::ROWS + r) * 2) = make_float2(top, sum);
-      }
-    }
-    __syncthreads();
-    u += t1 - t0;
+    part = 2 * wid + 1;  // what follows the first segment and is not complete is the last one
   }
+  copy_wait<0>();
 }
 
-// Joins the parts of a row that several CTAs computed: with (m_c, l_c, o_c) of
+// Joins the parts of a row that several warps computed: with (m_c, l_c, o_c) of
 // part c and m = max m_c: out = sum exp(m_c - m) o_c / sum exp(m_c - m) l_c.
 // One CTA per row, its warps taking every fourth part.
-template <int DV, int ROWS, int TILE>
-__global__ void __launch_bounds__(kThreads) paged_decode_join_kernel(const Params p, int ctas) {
+template <int DV, int ROWS>
+__global__ void __launch_bounds__(kThreads) paged_decode_join_kernel(const Params p, int warps) {
   __shared__ float s_o[kWarps][DV], s_sum[kWarps], s_top[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int PER = DV / 32;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t row = blockIdx.x;  // (b, KV head, row)
   const int head_row = (int)(row % p.nrows), head = (int)(row / p.nrows % p.Hkv), b = (int)(row / p.nrows / p.Hkv);
   const int per_seq = p.Hkv * p.row_groups;
-  const Parts parts(p.first_tile[p.B] * per_seq, ctas);
-  const int64_t nt = p.first_tile[b + 1] - p.first_tile[b];
-  const int64_t u0 = p.first_tile[b] * per_seq + nt * (head * p.row_groups + head_row / ROWS);
-  const int c0 = parts.owner(u0), c1 = parts.owner(u0 + nt - 1);
-  if (c0 == c1) return;  // written by that CTA
+  grid_dependency();
+  const Parts parts(p.before[p.B] * per_seq, warps);
+  const int64_t entries = p.before[b + 1] - p.before[b];
+  const int64_t u0 = p.before[b] * per_seq + entries * (head * p.row_groups + head_row / ROWS);
+  const int c0 = parts.owner(u0), c1 = parts.owner(u0 + entries - 1);
+  if (c0 == c1) return;  // written by that warp
   const int r = head_row % ROWS;
-  // A CTA's first part is the one its range begins with.
+  // It is the first segment of warp c0 if nothing of the one before is that warp's.
   const int64_t first = (int64_t)2 * c0 + (parts.begin(c0) >= u0 ? 0 : 1);
-  float top = -INFINITY;
-  for (int c = c0 + (int)threadIdx.x; c <= c1; c += kThreads)
-    top = fmaxf(top, p.part_ml[((c == c0 ? first : (int64_t)2 * c) * ROWS + r) * 2]);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-  if (lane == 0) s_top[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_top[w]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  float acc[PER], sum = 0.f;
+  constexpr int AHEAD = 4;  // parts read at once
+  float top = -INFINITY, sum = 0.f, acc[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-#pragma unroll 4
-  for (int c = c0 + warp; c <= c1; c += kWarps) {
-    const int64_t at = (c == c0 ? first : (int64_t)2 * c) * ROWS + r;
-    const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + at * 2);
-    const float f = ex2_approx(ml.x - ref);
-    sum += f * ml.y;
+  for (int c = c0 + warp; c <= c1; c += kWarps * AHEAD) {
+    float2 ml[AHEAD];
+    float x[AHEAD][PER];
+    float above = top;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] += f * p.part_o[at * DV + i * 32 + lane];
+    for (int a = 0; a < AHEAD; ++a) {
+      const int ca = c + a * kWarps;
+      ml[a] = make_float2(-INFINITY, 0.f);
+      if (ca <= c1) {
+        const int64_t at = (ca == c0 ? first : (int64_t)2 * ca) * p.part_rows + r;
+        ml[a] = *reinterpret_cast<const float2 *>(p.part_ml + at * 2);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) x[a][i] = p.part_o[at * DV + i * 32 + lane];
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) above = fmaxf(above, ml[a].x);
+    const float ref = above == -INFINITY ? 0.f : above, f0 = ex2_approx(top - ref);
+    sum *= f0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] *= f0;
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      if (c + a * kWarps > c1) break;
+      const float f = ex2_approx(ml[a].x - ref);
+      sum += f * ml[a].y;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] += f * x[a][i];
+    }
+    top = above;
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) s_o[warp][i * 32 + lane] = acc[i];
-  if (lane == 0) s_sum[warp] = sum;
+  if (lane == 0) s_sum[warp] = sum, s_top[warp] = top;
   __syncthreads();
+  float f[kWarps];
+  top = -INFINITY;
   sum = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) sum += s_sum[w];
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_top[w]);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    f[w] = ex2_approx(s_top[w] - (top == -INFINITY ? 0.f : top));
+    sum += f[w] * s_sum[w];
+  }
   const float v_scale = p.v_scale != nullptr ? __ldg(p.v_scale + head) : 1.f;
   const float inv = sum == 0.f ? 0.f : v_scale / sum;
   if ((int)threadIdx.x < DV / 2) {
     float x = 0.f, y = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      x += s_o[w][2 * threadIdx.x];
-      y += s_o[w][2 * threadIdx.x + 1];
+      x += f[w] * s_o[w][2 * threadIdx.x];
+      y += f[w] * s_o[w][2 * threadIdx.x + 1];
     }
     reinterpret_cast<uint32_t *>(p.out + row * DV)[threadIdx.x] = pack_bf16x2(x * inv, y * inv);
   }
@@ -700,31 +771,23 @@ splash_status launch(const splash_paged_decode_args &a, Params p, cudaStream_t s
     ready.fetch_or(bit, std::memory_order_release);
   }
   p.row_groups = (p.nrows + C::ROWS - 1) / C::ROWS;
-  // tiles that a sequence can have at most, from the row of pages and the window
-  int64_t most = (((int64_t)a.max_pages << p.page_shift) + C::TILE - 1) / C::TILE;
-  if (p.window >= 0) most = std::min(most, ((int64_t)p.window + p.Lq) / C::TILE + 2);
-  const int64_t all = std::min<int64_t>(most, kMaxGrid) * p.B * p.Hkv * p.row_groups;
-  const int ctas = (int)std::min<int64_t>({all, 2 * (int64_t)sms, kMaxGrid});
+  p.part_rows = std::min(p.nrows, C::ROWS);
+  // steps that a sequence can have at most, from the row of pages and the window
+  int64_t most = (((int64_t)a.max_pages << p.page_shift) + C::KW - 1) / C::KW;
+  if (p.window >= 0) most = std::min(most, ((int64_t)p.window + p.Lq) / C::KW + 2);
+  const int64_t all = std::min<int64_t>(most, kMaxWarps) * p.B * p.Hkv * p.row_groups;
+  const int ctas = (int)std::min<int64_t>({all, C::CTAS * (int64_t)sms, kMaxWarps / kWarps});
   char *ws = static_cast<char *>(a.workspace);
-  p.first_tile = reinterpret_cast<int64_t *>(ws);
+  p.before = reinterpret_cast<int64_t *>(ws);
   ws += align16(8 * ((int64_t)p.B + 1));
   p.part_ml = reinterpret_cast<float *>(ws);
-  ws += (int64_t)2 * kMaxGrid * C::ROWS * 2 * 4;
+  ws += (int64_t)2 * kMaxWarps * p.part_rows * 2 * 4;
   p.part_o = reinterpret_cast<float *>(ws);
-  paged_decode_kernel<C><<<ctas, kThreads, C::SMEM, stream>>>(p);
-  SPLASH_CUDA_TRY(cudaGetLastError());
+  SPLASH_CUDA_TRY(launch_dependent(paged_decode_kernel<C>, dim3(ctas), dim3(kThreads), C::SMEM, stream, p));
   splash_count_launches(1);
-  if (most <= 1) return SPLASH_OK;  // no sequence has more than one tile: nothing to join
-  cudaLaunchConfig_t config = {};
-  config.gridDim = dim3((unsigned)((int64_t)p.B * p.Hkv * p.nrows));
-  config.blockDim = dim3(kThreads);
-  config.stream = stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  config.attrs = &attr;
-  config.numAttrs = 1;
-  SPLASH_CUDA_TRY(cudaLaunchKernelEx(&config, paged_decode_join_kernel<C::DV, C::ROWS, C::TILE>, (const Params)p, ctas));
+  if (most <= 1) return SPLASH_OK;  // no sequence has more than one step: nothing to join
+  const dim3 rows((unsigned)((int64_t)p.B * p.Hkv * p.nrows));
+  SPLASH_CUDA_TRY(launch_dependent(paged_decode_join_kernel<C::DV, C::ROWS>, rows, dim3(kThreads), 0, stream, p, ctas * kWarps));
   splash_count_launches(1);
   return SPLASH_OK;
 }
@@ -742,8 +805,8 @@ splash_status pick(const splash_paged_decode_args &a, const Params &p, cudaStrea
 
 size_t splash_paged_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dv) {
   using namespace splash;
-  const int64_t rows = 16 * row_tiles((int64_t)(Hq / Hkv) * Lq);
-  return (size_t)(align16(8 * ((int64_t)B + 1)) + (int64_t)2 * kMaxGrid * rows * 4 * (dv + 2));
+  const int64_t nrows = (int64_t)(Hq / Hkv) * Lq, rows = std::min<int64_t>(nrows, 16 * row_tiles(nrows));
+  return (size_t)(align16(8 * ((int64_t)B + 1)) + (int64_t)2 * kMaxWarps * rows * 4 * (dv + 2));
 }
 
 splash_status splash_paged_decode_launch(const splash_paged_decode_args &a, cudaStream_t stream, uint32_t *err_word) {
@@ -771,7 +834,6 @@ splash_status splash_paged_decode_launch(const splash_paged_decode_args &a, cuda
   p.lse = a.lse;
   p.num_pages = a.num_pages;
   p.B = a.B;
-  p.Hq = a.Hq;
   p.Hkv = a.Hkv;
   p.Lq = a.Lq;
   p.G = a.Hq / a.Hkv;

@@ -16,6 +16,7 @@
 
 #include <algorithm>
 
+#include "dependent_launch.cuh"
 #include "internal.h"
 #include "sm103_ptx.cuh"
 
@@ -157,6 +158,7 @@ __device__ __forceinline__ uint2 to_e4m3(const float (&f)[8], float scale) {
 // one rotation.
 template <bool INTERLEAVED, bool APPEND, bool E4M3, int HEADS>
 __global__ void __launch_bounds__(256) rope_kernel(const Params p) {
+  grid_dependency();
   const int u = threadIdx.x;
   const int64_t token = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (token >= p.tokens) return;
@@ -257,11 +259,8 @@ template <bool APPEND, bool E4M3, int HEADS>
 splash_status launch_heads(const Params &p, bool interleaved, cudaStream_t stream) {
   const int ty = std::max(1, 256 / p.units);
   const dim3 block(p.units, ty), grid((p.tokens + ty - 1) / ty, (p.heads + HEADS - 1) / HEADS);
-  if (interleaved)
-    rope_kernel<true, APPEND, E4M3, HEADS><<<grid, block, 0, stream>>>(p);
-  else
-    rope_kernel<false, APPEND, E4M3, HEADS><<<grid, block, 0, stream>>>(p);
-  SPLASH_CUDA_TRY(cudaGetLastError());
+  SPLASH_CUDA_TRY(launch_dependent(interleaved ? rope_kernel<true, APPEND, E4M3, HEADS> : rope_kernel<false, APPEND, E4M3, HEADS>,
+                                   grid, block, 0, stream, p));
   splash_count_launches(1);
   return SPLASH_OK;
 }
