@@ -434,17 +434,23 @@ _ROPE_ARGS = struct.Struct("@Q" + "Pqqq" * 4 + "PqPqq" + "8i")
 _APPEND_ARGS = struct.Struct("@Q" + "Pqqq" * 5 + "Pqqq" * 2 + "PPPqPqPqPqqq" + "12i")
 _DECODE_ARGS = struct.Struct("@Q" + "Pqqq" * 3 + "PPPqPPPPQqq" + "9i2fi")
 _NO_VIEW = (0, 0, 0, 0)
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _CACHE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+
+# A serving step's kernels take a few microseconds, the time of some twenty
+# attribute reads here: the checks below read each attribute once, and the
+# current device and stream come as plain numbers.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _stream_and_device(stream, first):
     """(cudaStream_t, device index); the tensors must be on the current device."""
     dev = first.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _current_device():
         raise ValueError(f"the tensors must be on the current CUDA device (got {first.device})")
     if stream is None:
-        # the handle alone: a Stream object costs 3 us more
-        return torch._C._cuda_getCurrentRawStream(dev), dev
+        return _current_stream(dev), dev
     return (stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)), dev
 
 
@@ -464,61 +470,56 @@ def _new(shape, dtype, device, stream):
 
 def _view4(name, t, shape, dev):
     """(pointer, strides) of a bf16 [B, H, L, d] tensor with contiguous d."""
-    if t.dtype != torch.bfloat16 or t.get_device() != dev or t.shape != shape or t.stride(3) != 1:
-        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on the q / k device, contiguous in its last dimension")
     s = t.stride()
+    if t.dtype is not _BF16 or t.shape != shape or s[3] != 1 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on the current device, contiguous in its last dimension")
     return t.data_ptr(), s[0], s[1], s[2]
 
 
 def _index2(name, t, B, L, dev):
     """(pointer, batch stride) of an int32 [B, L] or [L] tensor."""
-    if t.dtype != torch.int32 or t.get_device() != dev or t.shape[-1:] != (L,) or t.dim() > 2 \
-            or (L > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must be an int32 tensor of shape [{B}, {L}] or [{L}] on the q / k device, contiguous in its last dimension")
-    if t.dim() == 1:
-        return t.data_ptr(), 0
-    if t.shape[0] != B:
-        raise ValueError(f"{name} has {t.shape[0]} rows for a batch of {B}")
-    return t.data_ptr(), t.stride(0)
+    shape, s = t.shape, t.stride()
+    if t.dtype is not _I32 or t.get_device() != dev or not (shape == (B, L) or shape == (L,)) or (L > 1 and s[-1] != 1):
+        raise ValueError(f"{name} must be an int32 tensor of shape [{B}, {L}] or [{L}] on the current device, contiguous in its last dimension")
+    return t.data_ptr(), s[0] if len(s) == 2 else 0
 
 
 def _table2(t, dev):
     """(pointer, rows, rot_dim) of a table made like rope_table's."""
-    if t.dtype != torch.float32 or t.get_device() != dev or t.dim() != 2 or not t.is_contiguous():
-        raise ValueError("table must be a contiguous fp32 tensor [positions, rot_dim] on the q / k device")
-    return t.data_ptr(), t.shape[0], t.shape[1]
+    if t.dtype is not _F32 or t.get_device() != dev or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError("table must be a contiguous fp32 tensor [positions, rot_dim] on the current device")
+    shape = t.shape
+    return t.data_ptr(), shape[0], shape[1]
 
 
-def _cache4(k_cache, v_cache, k_scale, v_scale, dev):
+def _cache4(k, v, k_scale, v_scale, dev):
     """The cache's part of the argument structs, and its sizes: (k view,
     v view, k_scale, v_scale pointers, type, pages, Hkv, page_size, dqk, dv)."""
-    kind = _CACHE_TYPES.get(k_cache.dtype)
-    if kind is None or v_cache.dtype != k_cache.dtype or k_cache.dim() != 4 or v_cache.dim() != 4 \
-            or k_cache.get_device() != dev or v_cache.get_device() != dev:
-        raise ValueError("k_cache and v_cache must be bf16 or float8_e4m3fn tensors [pages, Hkv, page_size, d] on the q / k device")
-    pages, Hkv, page, dqk = k_cache.shape
-    if v_cache.shape[:3] != k_cache.shape[:3]:
-        raise ValueError("k_cache and v_cache must have the same pages, heads and page size")
-    ks, vs = k_cache.stride(), v_cache.stride()
-    if ks[3] != 1 or vs[3] != 1:
-        raise ValueError("k_cache and v_cache must be contiguous in their last dimension")
+    dtype, shape, vshape, ks, vs = k.dtype, k.shape, v.shape, k.stride(), v.stride()
+    kind = _CACHE_TYPES.get(dtype)
+    if kind is None or v.dtype is not dtype or len(shape) != 4 or len(vshape) != 4 or shape[:3] != vshape[:3] \
+            or ks[3] != 1 or vs[3] != 1 or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("k_cache and v_cache must be bf16 or float8_e4m3fn tensors [pages, Hkv, page_size, d] on the "
+                         "current device, contiguous in the last dimension and alike in the others")
+    pages, Hkv, page, dqk = shape
     kp = vp = 0
     if kind == 1:
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if t is None or t.dtype != torch.float32 or t.get_device() != dev or t.shape != (Hkv,) or not t.is_contiguous():
+        for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if x is None or x.dtype is not _F32 or x.get_device() != dev or x.shape != (Hkv,) or not x.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous fp32 tensor of shape [{Hkv}] for an e4m3 cache")
         kp, vp = k_scale.data_ptr(), v_scale.data_ptr()
     elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale belong to an e4m3 cache")
-    return ((k_cache.data_ptr(), *ks[:3]), (v_cache.data_ptr(), *vs[:3]), kp, vp, kind, pages, Hkv, page, dqk,
-            v_cache.shape[3])
+    return ((k.data_ptr(), ks[0], ks[1], ks[2]), (v.data_ptr(), vs[0], vs[1], vs[2]), kp, vp, kind, pages, Hkv, page,
+            dqk, vshape[3])
 
 
 def _block_table(t, dev):
     """(pointer, row stride, rows, columns)."""
-    if t.dtype != torch.int32 or t.get_device() != dev or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("block_table must be an int32 tensor [sequences, pages] on the q / k device, contiguous in its last dimension")
-    return t.data_ptr(), t.stride(0), t.shape[0], t.shape[1]
+    shape, s = t.shape, t.stride()
+    if t.dtype is not _I32 or t.get_device() != dev or len(shape) != 2 or (shape[1] > 1 and s[1] != 1):
+        raise ValueError("block_table must be an int32 tensor [sequences, pages] on the current device, contiguous in its last dimension")
+    return t.data_ptr(), s[0], shape[0], shape[1]
 
 
 def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
@@ -532,25 +533,27 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="
 
 
 def _rope(what, inverse, q, k, positions, table, rot_offset, interleaved, q_out, k_out, stream):
-    if q.dim() != 4 or (k is not None and k.dim() != 4):
-        raise ValueError("q and k must be 4-D")
     s, dev = _stream_and_device(stream, q)
-    B, Hq, L, d = q.shape
-    qv = _view4("q", q, q.shape, dev)
+    shape = q.shape
+    if len(shape) != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q and k must be 4-D")
+    B, Hq, L, d = shape
+    qv = _view4("q", q, shape, dev)
     kv = ko = _NO_VIEW
     Hkv = 0
     if q_out is None:
-        q_out = _new(q.shape, torch.bfloat16, q.device, stream)
+        q_out = _new(shape, _BF16, q.device, stream)
     if k is not None:
-        Hkv = k.shape[1]
+        kshape = k.shape
+        Hkv = kshape[1]
         kv = _view4("k", k, (B, Hkv, L, d), dev)
         if k_out is None:
-            k_out = _new(k.shape, torch.bfloat16, q.device, stream)
-        ko = _view4("k_out", k_out, k.shape, dev)
+            k_out = _new(kshape, _BF16, q.device, stream)
+        ko = _view4("k_out", k_out, kshape, dev)
     elif k_out is not None:
         raise ValueError("k_out without k")
     tp, rows, rot = _table2(table, dev)
-    args = _ROPE_ARGS.pack(_ROPE_ARGS.size, *qv, *_view4("q_out", q_out, q.shape, dev), *kv, *ko,
+    args = _ROPE_ARGS.pack(_ROPE_ARGS.size, *qv, *_view4("q_out", q_out, shape, dev), *kv, *ko,
                            *_index2("positions", positions, B, L, dev), tp, rows, L, B, Hq, Hkv, d, rot,
                            int(rot_offset), int(bool(interleaved)), inverse)
     _check(lib().splash_rope(args, s), what)
@@ -589,27 +592,29 @@ def paged_append(k, v, k_cache, v_cache, block_table, positions, q=None, table=N
     (nothing is stored); seq_ids is the row of block_table (default: b).
     q [B, Hq, L, dqk] is rotated into q_out (allocated if not given); k_out
     receives the rotated keys when given (for attention_fwd of a prompt)."""
-    if k.dim() != 4 or v.dim() != 4:
-        raise ValueError("k and v must be 4-D")
     s, dev = _stream_and_device(stream, k)
     kc, vc, ksp, vsp, kind, pages, Hkv, page, dqk, dv = _cache4(k_cache, v_cache, k_scale, v_scale, dev)
-    B, L = k.shape[0], k.shape[2]
+    shape = k.shape
+    if len(shape) != 4 or v.dim() != 4:
+        raise ValueError("k and v must be 4-D")
+    B, L = shape[0], shape[2]
     kv = _view4("k", k, (B, Hkv, L, dqk), dev)
     vv = _view4("v", v, (B, Hkv, L, dv), dev)
     qv = qo = ko = _NO_VIEW
     Hq = 0
     if q is not None:
-        if q.dim() != 4:
+        qshape = q.shape
+        if len(qshape) != 4:
             raise ValueError("q must be 4-D")
-        Hq = q.shape[1]
+        Hq = qshape[1]
         qv = _view4("q", q, (B, Hq, L, dqk), dev)
         if q_out is None:
-            q_out = _new(q.shape, torch.bfloat16, q.device, stream)
-        qo = _view4("q_out", q_out, q.shape, dev)
+            q_out = _new(qshape, _BF16, k.device, stream)
+        qo = _view4("q_out", q_out, qshape, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if k_out is not None:
-        ko = _view4("k_out", k_out, k.shape, dev)
+        ko = _view4("k_out", k_out, shape, dev)
     tp, rows, rot = _table2(table, dev) if table is not None else (0, 0, 0)
     bt, bt_stride, num_seqs, max_pages = _block_table(block_table, dev)
     ids = _index2("seq_ids", seq_ids, B, L, dev) if seq_ids is not None else (0, 0)
@@ -630,34 +635,37 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float, softc
     block_table [B, max_pages] as for paged_append.  workspace: optional uint8
     device tensor of at least paged_decode_workspace_size(...) bytes, not
     shared by calls that may overlap."""
-    if q.dim() != 4:
-        raise ValueError("q must be 4-D")
     s, dev = _stream_and_device(stream, q)
     kc, vc, ksp, vsp, kind, pages, Hkv, page, dqk, dv = _cache4(k_cache, v_cache, k_scale, v_scale, dev)
-    B, Hq, Lq, _ = q.shape
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must be 4-D")
+    B, Hq, Lq, _ = shape
     qv = _view4("q", q, (B, Hq, Lq, dqk), dev)
     bt, bt_stride, num_seqs, max_pages = _block_table(block_table, dev)
     if num_seqs != B:
         raise ValueError(f"block_table has {num_seqs} rows for a batch of {B}")
-    if seq_lens.dtype != torch.int32 or seq_lens.get_device() != dev or seq_lens.shape != (B,) \
-            or not seq_lens.is_contiguous():
-        raise ValueError(f"seq_lens must be a contiguous int32 tensor of shape [{B}] on the q device")
+    if seq_lens.dtype is not _I32 or seq_lens.shape != (B,) or seq_lens.get_device() != dev or not seq_lens.is_contiguous():
+        raise ValueError(f"seq_lens must be a contiguous int32 tensor of shape [{B}] on the current device")
+    device = q.device
     if out is None:
-        out = _new((B, Hq, Lq, dv), torch.bfloat16, q.device, stream)
-    elif out.dtype != torch.bfloat16 or out.shape != (B, Hq, Lq, dv) or not out.is_contiguous() or out.get_device() != dev:
-        raise ValueError(f"out must be a contiguous bf16 tensor of shape {(B, Hq, Lq, dv)} on the q device")
+        out = _new((B, Hq, Lq, dv), _BF16, device, stream)
+    elif out.dtype is not _BF16 or out.shape != (B, Hq, Lq, dv) or not out.is_contiguous() or out.get_device() != dev:
+        raise ValueError(f"out must be a contiguous bf16 tensor of shape {(B, Hq, Lq, dv)} on the current device")
     if lse is None:
-        lse = _new((B, Hq, Lq), torch.float32, q.device, stream)
-    elif lse.dtype != torch.float32 or lse.shape != (B, Hq, Lq) or not lse.is_contiguous() or lse.get_device() != dev:
-        raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(B, Hq, Lq)} on the q device")
+        lse = _new((B, Hq, Lq), _F32, device, stream)
+    elif lse.dtype is not _F32 or lse.shape != (B, Hq, Lq) or not lse.is_contiguous() or lse.get_device() != dev:
+        raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(B, Hq, Lq)} on the current device")
     if workspace is None:
-        workspace = _new(paged_decode_workspace_size(B, Hq, Hkv, Lq, dv), torch.uint8, q.device, stream)
+        room = paged_decode_workspace_size(B, Hq, Hkv, Lq, dv)
+        workspace = _new(room, torch.uint8, device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the q device")
+        raise ValueError("workspace must be a contiguous tensor on the current device")
+    else:
+        room = workspace.numel() * workspace.element_size()
     args = _DECODE_ARGS.pack(_DECODE_ARGS.size, *qv, *kc, *vc, ksp, vsp, bt, bt_stride, seq_lens.data_ptr(),
-                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), pages, int(window_left), B, Hq, Hkv, Lq,
-                             dqk, dv, max_pages, page, kind, float(scale), float(softcap), 0)
+                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), room, pages, int(window_left), B,
+                             Hq, Hkv, Lq, dqk, dv, max_pages, page, kind, float(scale), float(softcap), 0)
     _check(lib().splash_paged_decode(args, s), "splash_paged_decode")
     return out, lse
 
