@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
   Loader<C> load{p, lane, per_seq, end, at, nullptr, nullptr, nullptr, {}};
   load.enter();
   load.look();
-#pragma unroll
+#pragma unroll 1  // (one copy of the code: its first fetch is part of a short call's time)
   for (int s = 0; s < C::STAGES - 1; ++s) load.step(ring + s * C::STAGE);
 
   int slot = 0, part = 2 * wid;
