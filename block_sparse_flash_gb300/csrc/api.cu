@@ -571,6 +571,13 @@ splash_status splash_paged_decode(const splash_paged_decode_args *args, void *cu
     return SPLASH_ERR_UNSUPPORTED;
   if ((int64_t)a.B * a.Hq * a.Lq > INT32_MAX || a.Hq > 65535) return SPLASH_ERR_UNSUPPORTED;
   if (a.workspace_bytes < need) return SPLASH_ERR_INVALID_ARG;
+  // the kernel's list: 16-key steps of every sequence, head and 16 rows, in 32 bits
+  if (a.max_pages > 0 && a.page_size > 0) {
+    int64_t steps = (int64_t)a.max_pages * a.page_size / 16 + 1;
+    if (a.window_left >= 0) steps = std::min(steps, a.window_left / 16 + 4);
+    const int64_t segments = (int64_t)a.B * a.Hkv * (((int64_t)(a.Hq / a.Hkv) * a.Lq + 15) / 16);
+    if (steps > INT32_MAX / segments) return SPLASH_ERR_UNSUPPORTED;
+  }
   if ((st = check_pages(a.k_cache, a.v_cache, a.num_pages, a.Hkv, a.page_size, a.dqk, a.dv, a.cache_type, a.k_scale,
                         a.v_scale, a.block_table, a.block_table_stride, a.B, a.max_pages, false)) != SPLASH_OK)
     return st;

@@ -61,7 +61,7 @@ struct Params {
   __nv_bfloat16 *out;
   float *lse;
   float *part_o, *part_ml;  // [2 * warps][part_rows][DV], [2 * warps][part_rows][2] (maximum, sum)
-  int64_t *before;          // [B + 1] list entries (of one head and row group) before each sequence
+  int32_t *before;          // [B + 1] list entries (of one head and row group) before each sequence
   int64_t num_pages;
   int32_t B, Hkv, Lq, G, nrows, row_groups, part_rows;  // nrows = G * Lq rows per KV head
   int32_t max_pages, page_shift, window;         // window < 0: none
@@ -103,31 +103,28 @@ __device__ __forceinline__ Span span_of(const Params &p, int b) {
   return s;
 }
 
-// a / b for a >= 0, b > 0 (a 64-bit division takes some hundred instructions).
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return (a | b) >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
 // Equal contiguous parts of T entries: warp w takes [begin(w), begin(w + 1)).
+// (The host keeps T below 2^31: with 64-bit divisions the start of a call took
+// 0.65 us longer.)
 struct Parts {
-  int64_t each;
-  int32_t more;  // the first `more` warps take one entry more
-  __device__ __forceinline__ Parts(int64_t T, int32_t warps) : each(quotient(T, warps)), more((int32_t)(T - each * warps)) {}
-  __device__ __forceinline__ int64_t begin(int32_t w) const { return each * w + min(w, more); }
-  __device__ __forceinline__ int32_t owner(int64_t u) const {
-    const int64_t cut = (each + 1) * more;
-    return u < cut ? (int32_t)quotient(u, each + 1) : more + (int32_t)quotient(u - cut, each);
+  int32_t each, more;  // the first `more` warps take one entry more
+  __device__ __forceinline__ Parts(int32_t T, int32_t warps)
+      : each((uint32_t)T / (uint32_t)warps), more(T - each * warps) {}
+  __device__ __forceinline__ int32_t begin(int32_t w) const { return each * w + min(w, more); }
+  __device__ __forceinline__ int32_t owner(int32_t u) const {
+    const int32_t cut = (each + 1) * more;
+    return u < cut ? (uint32_t)u / (uint32_t)(each + 1) : more + (uint32_t)(u - cut) / (uint32_t)each;
   }
 };
 
 // A warp's place in its part of the list.
 template <int KW>
 struct Cursor {
-  int64_t u;  // list entry of the current step
+  int32_t u;  // list entry of the current step
   int32_t b, seg, step;  // segment seg (head, row group) of sequence b, its step
   Span s;
   // returns true when the segment changed; s is that of b as long as u < end
-  __device__ __forceinline__ bool advance(const Params &p, int per_seq, int64_t end) {
+  __device__ __forceinline__ bool advance(const Params &p, int per_seq, int32_t end) {
     ++u;
     if (++step < s.nst) return false;
     step = 0;
@@ -217,7 +214,7 @@ template <class C>
 struct Loader {
   const Params &p;
   const int lane, per_seq;
-  const int64_t end;
+  const int32_t end;
   Cursor<C::KW> at;
   const char *k, *v;  // the head's rows of page 0
   const int32_t *pages;
@@ -280,8 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
   constexpr int DQK = C::DQK, DV = C::DV, MT = C::MT, NB = C::NB;
   constexpr bool E4M3 = C::E4M3;
   extern __shared__ __align__(1024) char smem[];
-  __shared__ int64_t s_scan[kWarps], s_before[kWarps];
-  __shared__ int32_t s_seq[kWarps];
+  __shared__ int32_t s_scan[kWarps], s_before[kWarps], s_seq[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int quad = lane >> 2, tq = lane & 3;
   const uint32_t ring = smem_u32(smem + warp * C::WARP_BYTES);
@@ -292,22 +288,22 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 
   // ---- the warps' parts of the list: a scan over the sequences
   const int per_seq = p.Hkv * p.row_groups;
-  int64_t T;
+  int32_t T;
   {
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
-    int64_t own = 0;
+    int32_t own = 0;
     for (int b = b0; b < b1; ++b) own += span_of<C::KW>(p, b).nst;
-    int64_t before = own;
+    int32_t before = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(~0u, before, o);
+      const int32_t y = __shfl_up_sync(~0u, before, o);
       if (lane >= o) before += y;
     }
     if (lane == 31) s_scan[warp] = before;
     before -= own;
     __syncthreads();
-    int64_t total = 0;
+    int32_t total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) before += s_scan[w];
@@ -315,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
     }
     T = total * per_seq;
     const Parts parts(T, kWarps * gridDim.x);
-    int64_t first[kWarps];
+    int32_t first[kWarps];
     bool mine = blockIdx.x == 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -323,9 +319,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
       mine |= first[w] >= before * per_seq && first[w] < (before + own) * per_seq;
     }
     if (mine) {
-      int64_t at = before;
+      int32_t at = before;
       for (int b = b0; b < b1; ++b) {
-        const int64_t next = at + span_of<C::KW>(p, b).nst;
+        const int32_t next = at + span_of<C::KW>(p, b).nst;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
           if (first[w] >= at * per_seq && first[w] < next * per_seq) s_seq[w] = b, s_before[w] = at;
@@ -342,16 +338,16 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
   }
   const int wid = kWarps * blockIdx.x + warp;
   const Parts parts(T, kWarps * gridDim.x);
-  const int64_t end = parts.begin(wid + 1);
+  const int32_t end = parts.begin(wid + 1);
   Cursor<C::KW> at;
   at.u = parts.begin(wid);
   if (at.u >= end) return;
   at.b = s_seq[warp];
   at.s = span_of<C::KW>(p, at.b);
   {
-    const int64_t in_seq = at.u - s_before[warp] * per_seq;
-    at.seg = (int32_t)quotient(in_seq, at.s.nst);
-    at.step = (int32_t)(in_seq - (int64_t)at.seg * at.s.nst);
+    const int32_t in_seq = at.u - s_before[warp] * per_seq;
+    at.seg = (uint32_t)in_seq / (uint32_t)at.s.nst;
+    at.step = in_seq - at.seg * at.s.nst;
   }
   Loader<C> load{p, lane, per_seq, end, at, nullptr, nullptr, nullptr, {}};
   load.enter();
@@ -685,8 +681,8 @@ __global__ void __launch_bounds__(kThreads) paged_decode_join_kernel(const Param
   const int per_seq = p.Hkv * p.row_groups;
   grid_dependency();
   const Parts parts(p.before[p.B] * per_seq, warps);
-  const int64_t entries = p.before[b + 1] - p.before[b];
-  const int64_t u0 = p.before[b] * per_seq + entries * (head * p.row_groups + head_row / ROWS);
+  const int32_t entries = p.before[b + 1] - p.before[b];
+  const int32_t u0 = p.before[b] * per_seq + entries * (head * p.row_groups + head_row / ROWS);
   const int c0 = parts.owner(u0), c1 = parts.owner(u0 + entries - 1);
   if (c0 == c1) return;  // written by that warp
   const int r = head_row % ROWS;
@@ -778,8 +774,8 @@ splash_status launch(const splash_paged_decode_args &a, Params p, cudaStream_t s
   const int64_t all = std::min<int64_t>(most, kMaxWarps) * p.B * p.Hkv * p.row_groups;
   const int ctas = (int)std::min<int64_t>({all, C::CTAS * (int64_t)sms, kMaxWarps / kWarps});
   char *ws = static_cast<char *>(a.workspace);
-  p.before = reinterpret_cast<int64_t *>(ws);
-  ws += align16(8 * ((int64_t)p.B + 1));
+  p.before = reinterpret_cast<int32_t *>(ws);
+  ws += align16(4 * ((int64_t)p.B + 1));
   p.part_ml = reinterpret_cast<float *>(ws);
   ws += (int64_t)2 * kMaxWarps * p.part_rows * 2 * 4;
   p.part_o = reinterpret_cast<float *>(ws);
@@ -806,7 +802,7 @@ splash_status pick(const splash_paged_decode_args &a, const Params &p, cudaStrea
 size_t splash_paged_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dv) {
   using namespace splash;
   const int64_t nrows = (int64_t)(Hq / Hkv) * Lq, rows = std::min<int64_t>(nrows, 16 * row_tiles(nrows));
-  return (size_t)(align16(8 * ((int64_t)B + 1)) + (int64_t)2 * kMaxWarps * rows * 4 * (dv + 2));
+  return (size_t)(align16(4 * ((int64_t)B + 1)) + (int64_t)2 * kMaxWarps * rows * 4 * (dv + 2));
 }
 
 splash_status splash_paged_decode_launch(const splash_paged_decode_args &a, cudaStream_t stream, uint32_t *err_word) {

@@ -549,7 +549,9 @@ splash_status splash_paged_append(const splash_paged_append_args *args, void *cu
  *               calls that may run at the same time need two workspaces.
  * Supported: (dqk, dv) in {(64, 64), (128, 128), (192, 128)}, Hq % Hkv == 0,
  * 1 <= Lq <= SPLASH_MAX_NEW_TOKENS, page_size a power of two in 16 .. 1024,
- * max_pages * page_size < 2^31 - 65535, B <= 65535.  The result does not depend on timing: the same inputs give the
+ * max_pages * page_size < 2^31 - 65535, B <= 65535, and fewer than 2^31 steps of
+ * 16 keys (at most max_pages * page_size / 16 + 1, or window_left / 16 + 4) over
+ * all sequences, KV heads and groups of 16 of the Hq/Hkv * Lq rows.  The result does not depend on timing: the same inputs give the
  * same bits on the same GPU.
  */
 typedef struct {

@@ -170,6 +170,19 @@ def test_decode_refusals(splash):
         ("num_pages", 0, INVALID), ("max_pages", 0, INVALID), ("block_table", None, INVALID)])
 
 
+def test_decode_limit_of_steps(splash):
+    """2^31 steps of 16 keys: 65535 sequences x 2 heads x 16384 pages, unless a
+    window keeps each sequence's short."""
+    a = decode_args()
+    a.B, a.max_pages = 65535, 16384
+    assert call(splash, "splash_paged_decode", a) == UNSUPPORTED
+    if not torch.cuda.is_available():
+        a.window_left = 1000
+        assert call(splash, "splash_paged_decode", a) == CUDA  # past every check
+        a.window_left, a.max_pages = -1, 16000
+        assert call(splash, "splash_paged_decode", a) == CUDA
+
+
 def test_decode_workspace_size(splash):
     f = splash.lib().splash_paged_decode_workspace_size
     n = ctypes.c_size_t(0)
