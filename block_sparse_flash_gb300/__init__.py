@@ -95,7 +95,7 @@ def lib():
     for f in (L.splash_rope, L.splash_paged_append, L.splash_paged_decode):
         f.argtypes = [ctypes.c_char_p, vp]  # the argument struct as packed bytes
         f.restype = ctypes.c_int
-    L.splash_paged_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32, P(ctypes.c_size_t)]
+    L.splash_paged_decode_workspace_size.argtypes = [i32] * 9 + [i64, P(ctypes.c_size_t)]
     L.splash_paged_decode_workspace_size.restype = ctypes.c_int
     L.splash_attention_merge.argtypes = [vp, vp, i32, i64, i32, vp, vp, vp]
     L.splash_last_device_error.argtypes = [vp]
@@ -656,26 +656,36 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float, softc
         lse = _new((B, Hq, Lq), _F32, device, stream)
     elif lse.dtype is not _F32 or lse.shape != (B, Hq, Lq) or not lse.is_contiguous() or lse.get_device() != dev:
         raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(B, Hq, Lq)} on the current device")
+    ws = 0
     if workspace is None:
-        room = paged_decode_workspace_size(B, Hq, Hkv, Lq, dv)
-        workspace = _new(room, torch.uint8, device, stream)
+        room = _paged_decode_workspace_size(B, Hq, Hkv, Lq, dqk, dv, max_pages, page, kind, int(window_left))
+        if room:
+            workspace = _new(room, torch.uint8, device, stream)
+            ws = workspace.data_ptr()
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the current device")
     else:
-        room = workspace.numel() * workspace.element_size()
+        room, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     args = _DECODE_ARGS.pack(_DECODE_ARGS.size, *qv, *kc, *vc, ksp, vsp, bt, bt_stride, seq_lens.data_ptr(),
-                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), room, pages, int(window_left), B,
+                             out.data_ptr(), lse.data_ptr(), ws, room, pages, int(window_left), B,
                              Hq, Hkv, Lq, dqk, dv, max_pages, page, kind, float(scale), float(softcap), 0)
     _check(lib().splash_paged_decode(args, s), "splash_paged_decode")
     return out, lse
 
 
 @functools.lru_cache(maxsize=256)
-def paged_decode_workspace_size(B: int, Hq: int, Hkv: int, Lq: int, dv: int) -> int:
+def _paged_decode_workspace_size(*sizes):
     n = ctypes.c_size_t(0)
-    _check(lib().splash_paged_decode_workspace_size(int(B), int(Hq), int(Hkv), int(Lq), int(dv), ctypes.byref(n)),
-           "splash_paged_decode_workspace_size")
+    _check(lib().splash_paged_decode_workspace_size(*sizes, ctypes.byref(n)), "splash_paged_decode_workspace_size")
     return int(n.value)
+
+
+def paged_decode_workspace_size(q, k_cache, v_cache, block_table, window_left: int = -1) -> int:
+    """Bytes of paged_decode's workspace for tensors of these shapes and types
+    (0 where it needs none)."""
+    return _paged_decode_workspace_size(q.shape[0], q.shape[1], k_cache.shape[1], q.shape[2], q.shape[3],
+                                        v_cache.shape[3], block_table.shape[1], k_cache.shape[2],
+                                        _CACHE_TYPES[k_cache.dtype], int(window_left))
 
 
 def last_device_error(stream=None) -> int:

@@ -457,6 +457,12 @@ splash_status check_tokens(int32_t B, int64_t L, int64_t heads) {
   return SPLASH_OK;
 }
 
+// (positions leave room for the kernels' look ahead in 32 bits)
+splash_status check_page_sizes(int32_t page_size, int32_t max_pages) {
+  if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return SPLASH_ERR_UNSUPPORTED;
+  return (int64_t)max_pages * page_size > INT32_MAX - 65535 ? SPLASH_ERR_UNSUPPORTED : SPLASH_OK;
+}
+
 splash_status check_pages(const splash_cache_view &k, const splash_cache_view &v, int64_t num_pages, int32_t Hkv,
                           int32_t page_size, int32_t dqk, int32_t dv, int32_t type, const float *k_scale,
                           const float *v_scale, const int32_t *block_table, int64_t block_table_stride, int64_t rows,
@@ -468,10 +474,10 @@ splash_status check_pages(const splash_cache_view &k, const splash_cache_view &v
   if (type == SPLASH_CACHE_E4M3 &&
       (k_scale == nullptr || v_scale == nullptr || ((addr(k_scale) | addr(v_scale)) & 3u) != 0))
     return SPLASH_ERR_INVALID_ARG;
-  if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return SPLASH_ERR_UNSUPPORTED;
-  // (positions leave room for the kernels' look ahead in 32 bits)
-  if (num_pages > INT32_MAX || (int64_t)max_pages * page_size > INT32_MAX - 65535) return SPLASH_ERR_UNSUPPORTED;
-  splash_status st = check_cache(k, num_pages, Hkv, page_size, dqk, type, output);
+  if (num_pages > INT32_MAX) return SPLASH_ERR_UNSUPPORTED;
+  splash_status st = check_page_sizes(page_size, max_pages);
+  if (st != SPLASH_OK) return st;
+  st = check_cache(k, num_pages, Hkv, page_size, dqk, type, output);
   if (st != SPLASH_OK) return st;
   return check_cache(v, num_pages, Hkv, page_size, dv, type, output);
 }
@@ -543,41 +549,40 @@ splash_status splash_paged_append(const splash_paged_append_args *args, void *cu
   return splash_paged_append_launch(a, static_cast<cudaStream_t>(cuda_stream), err);
 }
 
-splash_status splash_paged_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dv,
-                                                 size_t *bytes) {
-  if (bytes == nullptr || B <= 0 || Hq <= 0 || Hkv <= 0 || Lq <= 0 || dv <= 0) return SPLASH_ERR_INVALID_ARG;
+splash_status splash_paged_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t dv,
+                                                 int32_t max_pages, int32_t page_size, int32_t cache_type,
+                                                 int64_t window_left, size_t *bytes) {
+  if (bytes == nullptr || B <= 0 || Hq <= 0 || Hkv <= 0 || Lq <= 0 || dqk <= 0 || dv <= 0 || max_pages <= 0 ||
+      page_size <= 0 || window_left < -1 || (cache_type != SPLASH_CACHE_BF16 && cache_type != SPLASH_CACHE_E4M3))
+    return SPLASH_ERR_INVALID_ARG;
   if (Hq % Hkv != 0) return SPLASH_ERR_SHAPE;
-  if (Lq > SPLASH_MAX_NEW_TOKENS || B > 65535 || (dv != 64 && dv != 128)) return SPLASH_ERR_UNSUPPORTED;
-  *bytes = splash_paged_decode_workspace_bytes(B, Hq, Hkv, Lq, dv);
+  if (Lq > SPLASH_MAX_NEW_TOKENS || B > 65535 || Hq > 65535 || (int64_t)B * Hq * Lq > INT32_MAX)
+    return SPLASH_ERR_UNSUPPORTED;
+  if (!((dqk == 64 && dv == 64) || (dqk == 128 && dv == 128) || (dqk == 192 && dv == 128))) return SPLASH_ERR_UNSUPPORTED;
+  const splash_status st = check_page_sizes(page_size, max_pages);
+  if (st != SPLASH_OK) return st;
+  // the kernel's list: 16-key steps of every sequence, head and 16 rows, in 32 bits
+  int64_t steps = (int64_t)max_pages * page_size / 16 + 1;
+  if (window_left >= 0) steps = std::min(steps, window_left / 16 + 4);
+  const int64_t segments = (int64_t)B * Hkv * (((int64_t)(Hq / Hkv) * Lq + 15) / 16);
+  if (steps > INT32_MAX / segments) return SPLASH_ERR_UNSUPPORTED;
+  *bytes = splash_paged_decode_workspace_bytes(B, Hq, Hkv, Lq, dqk, dv, max_pages, page_size, cache_type, window_left);
   return SPLASH_OK;
 }
 
 splash_status splash_paged_decode(const splash_paged_decode_args *args, void *cuda_stream) {
   if (args == nullptr || args->struct_bytes != sizeof *args) return SPLASH_ERR_INVALID_ARG;
   const splash_paged_decode_args &a = *args;
-  if (a.B <= 0 || a.Hq <= 0 || a.Hkv <= 0 || a.Lq <= 0 || a.dqk <= 0 || a.dv <= 0 || a.reserved != 0)
-    return SPLASH_ERR_INVALID_ARG;
-  if (a.seq_lens == nullptr || a.out == nullptr || a.lse == nullptr || a.workspace == nullptr)
-    return SPLASH_ERR_INVALID_ARG;
+  if (a.seq_lens == nullptr || a.out == nullptr || a.lse == nullptr || a.reserved != 0) return SPLASH_ERR_INVALID_ARG;
   if (((addr(a.out) | addr(a.workspace)) & 15u) != 0 || ((addr(a.seq_lens) | addr(a.lse)) & 3u) != 0)
     return SPLASH_ERR_INVALID_ARG;
   if (!(a.scale > 0.f) || !(a.scale < INFINITY) || !(a.softcap == a.softcap) || a.softcap == INFINITY)
     return SPLASH_ERR_INVALID_ARG;
-  if (a.window_left < -1) return SPLASH_ERR_INVALID_ARG;
   size_t need = 0;
-  splash_status st = splash_paged_decode_workspace_size(a.B, a.Hq, a.Hkv, a.Lq, a.dv, &need);
+  splash_status st = splash_paged_decode_workspace_size(a.B, a.Hq, a.Hkv, a.Lq, a.dqk, a.dv, a.max_pages, a.page_size,
+                                                        a.cache_type, a.window_left, &need);
   if (st != SPLASH_OK) return st;
-  if (!((a.dqk == 64 && a.dv == 64) || (a.dqk == 128 && a.dv == 128) || (a.dqk == 192 && a.dv == 128)))
-    return SPLASH_ERR_UNSUPPORTED;
-  if ((int64_t)a.B * a.Hq * a.Lq > INT32_MAX || a.Hq > 65535) return SPLASH_ERR_UNSUPPORTED;
-  if (a.workspace_bytes < need) return SPLASH_ERR_INVALID_ARG;
-  // the kernel's list: 16-key steps of every sequence, head and 16 rows, in 32 bits
-  if (a.max_pages > 0 && a.page_size > 0) {
-    int64_t steps = (int64_t)a.max_pages * a.page_size / 16 + 1;
-    if (a.window_left >= 0) steps = std::min(steps, a.window_left / 16 + 4);
-    const int64_t segments = (int64_t)a.B * a.Hkv * (((int64_t)(a.Hq / a.Hkv) * a.Lq + 15) / 16);
-    if (steps > INT32_MAX / segments) return SPLASH_ERR_UNSUPPORTED;
-  }
+  if (need > 0 && (a.workspace == nullptr || a.workspace_bytes < need)) return SPLASH_ERR_INVALID_ARG;
   if ((st = check_pages(a.k_cache, a.v_cache, a.num_pages, a.Hkv, a.page_size, a.dqk, a.dv, a.cache_type, a.k_scale,
                         a.v_scale, a.block_table, a.block_table_stride, a.B, a.max_pages, false)) != SPLASH_OK)
     return st;

@@ -14,7 +14,8 @@
 //    covers is finished there; parts of one that several warps share go to the
 //    workspace as (maximum, sum, unnormalised output) and a second kernel joins
 //    them, in the order of the keys, so that the result does not depend on
-//    timing.
+//    timing.  A call of few and short segments takes one CTA for each instead:
+//    its warps share the keys and join through shared memory.
 //  * Loads.  Each warp keeps a ring of stages in shared memory, filled by
 //    16-byte asynchronous copies that run ahead of the products and across the
 //    borders of sequences; there is no barrier between warps.  Rows outside the
@@ -83,6 +84,8 @@ struct Config {
   static constexpr int WARP_BYTES = STAGES * STAGE + QBYTES;
   static constexpr int SMEM = kWarps * WARP_BYTES;
   static constexpr int CTAS = SMEM <= 110 * 1024 ? 2 : 1;  // per SM
+  static constexpr int ODIM = DV + 4;                      // floats of a row in a CTA's join
+  static_assert(WARP_BYTES >= ROWS * ODIM * 4, "the join of a CTA's warps uses their stages");
 };
 
 // The keys of sequence b that its queries see, in steps of KW.
@@ -90,6 +93,11 @@ struct Span {
   int32_t n, lo;       // keys [lo, n) are visible to some query
   int32_t step0, nst;  // steps step0 .. step0 + nst - 1; at least one, so that empty rows are written too
 };
+
+__device__ __forceinline__ void check_length(const Params &p, int b) {
+  const int32_t n = __ldg(p.seq_lens + b);
+  if (n < 0 || n > (int64_t)p.max_pages << p.page_shift) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
+}
 
 template <int KW>
 __device__ __forceinline__ Span span_of(const Params &p, int b) {
@@ -272,12 +280,29 @@ struct Loader {
   }
 };
 
+// A thread's columns of a row of the accumulators (e: the lower or upper 8 rows).
 template <class C>
+__device__ __forceinline__ void store_row(float *dst, const float (&o)[C::DV / 8][4], int e, int tq) {
+  if (C::E4M3) {
+#pragma unroll
+    for (int j = 0; j < C::DV / 16; ++j)
+      *reinterpret_cast<float4 *>(dst + 16 * j + 4 * tq) =
+          make_float4(o[2 * j][2 * e], o[2 * j + 1][2 * e], o[2 * j][2 * e + 1], o[2 * j + 1][2 * e + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < C::DV / 8; ++j)
+      *reinterpret_cast<float2 *>(dst + 8 * j + 2 * tq) = make_float2(o[j][2 * e], o[j][2 * e + 1]);
+  }
+}
+
+// TOGETHER: one CTA per segment; otherwise equal parts of the list per warp.
+template <class C, bool TOGETHER>
 __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params p) {
   constexpr int DQK = C::DQK, DV = C::DV, MT = C::MT, NB = C::NB;
   constexpr bool E4M3 = C::E4M3;
   extern __shared__ __align__(1024) char smem[];
   __shared__ int32_t s_scan[kWarps], s_before[kWarps], s_seq[kWarps];
+  __shared__ float s_ml[kWarps][C::ROWS][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int quad = lane >> 2, tq = lane & 3;
   const uint32_t ring = smem_u32(smem + warp * C::WARP_BYTES);
@@ -286,77 +311,86 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 
   grid_dependency();
 
-  // ---- the warps' parts of the list: a scan over the sequences
   const int per_seq = p.Hkv * p.row_groups;
-  int32_t T;
-  {
-    const int per = (p.B + kThreads - 1) / kThreads;
-    const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
-    int32_t own = 0;
-    for (int b = b0; b < b1; ++b) own += span_of<C::KW>(p, b).nst;
-    int32_t before = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(~0u, before, o);
-      if (lane >= o) before += y;
-    }
-    if (lane == 31) s_scan[warp] = before;
-    before -= own;
-    __syncthreads();
-    int32_t total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_scan[w];
-      total += s_scan[w];
-    }
-    T = total * per_seq;
-    const Parts parts(T, kWarps * gridDim.x);
-    int32_t first[kWarps];
-    bool mine = blockIdx.x == 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      first[w] = parts.begin(kWarps * blockIdx.x + w);
-      mine |= first[w] >= before * per_seq && first[w] < (before + own) * per_seq;
-    }
-    if (mine) {
-      int32_t at = before;
-      for (int b = b0; b < b1; ++b) {
-        const int32_t next = at + span_of<C::KW>(p, b).nst;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-          if (first[w] >= at * per_seq && first[w] < next * per_seq) s_seq[w] = b, s_before[w] = at;
-        if (blockIdx.x == 0) {
-          p.before[b] = at;
-          if (b == p.B - 1) p.before[p.B] = next;
-          const int32_t n = __ldg(p.seq_lens + b);
-          if (n < 0 || n > (int64_t)p.max_pages << p.page_shift) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
-        }
-        at = next;
-      }
-    }
-    __syncthreads();
-  }
   const int wid = kWarps * blockIdx.x + warp;
-  const Parts parts(T, kWarps * gridDim.x);
-  const int32_t end = parts.begin(wid + 1);
   Cursor<C::KW> at;
-  at.u = parts.begin(wid);
-  if (at.u >= end) return;
-  at.b = s_seq[warp];
-  at.s = span_of<C::KW>(p, at.b);
-  {
+  int32_t end;
+  if constexpr (TOGETHER) {
+    at.b = blockIdx.x / per_seq;
+    at.seg = blockIdx.x % per_seq;
+    at.s = span_of<C::KW>(p, at.b);
+    at.u = at.step = (int32_t)((int64_t)at.s.nst * warp / kWarps);
+    end = (int32_t)((int64_t)at.s.nst * (warp + 1) / kWarps);
+    if (at.seg == 0 && threadIdx.x == 0) check_length(p, at.b);
+  } else {
+    // the warps' parts of the list: a scan over the sequences
+    int32_t T;
+    {
+      const int per = (p.B + kThreads - 1) / kThreads;
+      const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+      int32_t own = 0;
+      for (int b = b0; b < b1; ++b) own += span_of<C::KW>(p, b).nst;
+      int32_t before = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(~0u, before, o);
+        if (lane >= o) before += y;
+      }
+      if (lane == 31) s_scan[warp] = before;
+      before -= own;
+      __syncthreads();
+      int32_t total = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += s_scan[w];
+        total += s_scan[w];
+      }
+      T = total * per_seq;
+      const Parts parts(T, kWarps * gridDim.x);
+      int32_t first[kWarps];
+      bool mine = blockIdx.x == 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        first[w] = parts.begin(kWarps * blockIdx.x + w);
+        mine |= first[w] >= before * per_seq && first[w] < (before + own) * per_seq;
+      }
+      if (mine) {
+        int32_t at = before;
+        for (int b = b0; b < b1; ++b) {
+          const int32_t next = at + span_of<C::KW>(p, b).nst;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w)
+            if (first[w] >= at * per_seq && first[w] < next * per_seq) s_seq[w] = b, s_before[w] = at;
+          if (blockIdx.x == 0) {
+            p.before[b] = at;
+            if (b == p.B - 1) p.before[p.B] = next;
+            check_length(p, b);
+          }
+          at = next;
+        }
+      }
+      __syncthreads();
+    }
+    const Parts parts(T, kWarps * gridDim.x);
+    at.u = parts.begin(wid);
+    end = parts.begin(wid + 1);
+    if (at.u >= end) return;
+    at.b = s_seq[warp];
+    at.s = span_of<C::KW>(p, at.b);
     const int32_t in_seq = at.u - s_before[warp] * per_seq;
     at.seg = (uint32_t)in_seq / (uint32_t)at.s.nst;
     at.step = in_seq - at.seg * at.s.nst;
   }
   Loader<C> load{p, lane, per_seq, end, at, nullptr, nullptr, nullptr, {}};
-  load.enter();
-  load.look();
+  if (at.u < end) {
+    load.enter();
+    load.look();
+  }
 #pragma unroll 1  // (one copy of the code: its first fetch is part of a short call's time)
   for (int s = 0; s < C::STAGES - 1; ++s) load.step(ring + s * C::STAGE);
 
   int slot = 0, part = 2 * wid;
-  while (at.u < end) {
+  do {
     // ---- a segment: the rows' queries, 16 bits each.  For e4m3 they become
     // fp16, scaled by the power of two that brings the row's largest element
     // into [1, 2).  That is exact except for elements 2^14 times smaller (their
@@ -460,8 +494,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
     const uint32_t q_row = (lane & 7) + ((lane >> 3) & 1) * 8;
 
     // ---- its steps
-    bool change;
-    do {
+    bool change = false;
+    while (!change && at.u < end) {
       copy_wait<C::STAGES - 2>();
       __syncwarp();
       const int32_t key0 = (sp.step0 + at.step) * C::KW;
@@ -616,7 +650,51 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
           }
         }
       }
-    } while (!change && at.u < end);
+    }
+
+    if constexpr (TOGETHER) {
+      copy_wait<0>();
+      __syncwarp();
+      float *own = reinterpret_cast<float *>(smem + warp * C::WARP_BYTES);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = mt * 16 + quad + 8 * e;
+          float sum = l[mt][e];
+          sum += __shfl_xor_sync(~0u, sum, 1);
+          sum += __shfl_xor_sync(~0u, sum, 2);
+          if (r >= rows) continue;
+          if (tq == 0) s_ml[warp][r][0] = m[mt][e], s_ml[warp][r][1] = sum;
+          store_row<C>(own + r * C::ODIM, o[mt], e, tq);
+        }
+      __syncthreads();
+      constexpr int LANES = DV / 4;
+      const int col = 4 * (threadIdx.x % LANES);
+      const float v_scale = E4M3 ? __ldg(p.v_scale + head) : 1.f;
+      for (int r = threadIdx.x / LANES; r < rows; r += kThreads / LANES) {
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][r][0]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2_approx(s_ml[w][r][0] - (top == -INFINITY ? 0.f : top));
+          const float4 x = *reinterpret_cast<const float4 *>(smem + w * C::WARP_BYTES + 4 * (r * C::ODIM + col));
+          sum += f * s_ml[w][r][1];
+          acc.x += f * x.x;
+          acc.y += f * x.y;
+          acc.z += f * x.z;
+          acc.w += f * x.w;
+        }
+        const float inv = sum == 0.f ? 0.f : v_scale / sum;
+        const int64_t row = ((int64_t)b * p.Hkv + head) * p.nrows + row0 + r;
+        *reinterpret_cast<uint2 *>(p.out + row * DV + col) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (col == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+      }
+      return;
+    }
 
     // ---- finished rows, or this warp's part of them
     const bool complete = from_start && change;
@@ -650,21 +728,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
         } else {
           const int64_t row = (int64_t)part * p.part_rows + r;
           if (tq == 0) *reinterpret_cast<float2 *>(p.part_ml + 2 * row) = make_float2(m[mt][e], sum);
-          float *dst = p.part_o + row * DV;
-          if (E4M3) {
-#pragma unroll
-            for (int j = 0; j < DV / 16; ++j)
-              *reinterpret_cast<float4 *>(dst + 16 * j + 4 * tq) = make_float4(
-                  o[mt][2 * j][2 * e], o[mt][2 * j + 1][2 * e], o[mt][2 * j][2 * e + 1], o[mt][2 * j + 1][2 * e + 1]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < DV / 8; ++j)
-              *reinterpret_cast<float2 *>(dst + 8 * j + 2 * tq) = make_float2(o[mt][j][2 * e], o[mt][j][2 * e + 1]);
-          }
+          store_row<C>(p.part_o + row * DV, o[mt], e, tq);
         }
       }
     part = 2 * wid + 1;  // what follows the first segment and is not complete is the last one
-  }
+  } while (at.u < end);
   copy_wait<0>();
 }
 
@@ -753,35 +821,65 @@ __global__ void __launch_bounds__(kThreads) paged_decode_join_kernel(const Param
 
 int64_t align16(int64_t x) { return (x + 15) & ~(int64_t)15; }
 
-int row_tiles(int64_t nrows) { return nrows <= 16 ? 1 : 2; }
+// What the sizes of a call decide.
+struct Plan {
+  int row_tiles;        // 16 rows each, 1 or 2
+  int64_t most;         // steps that a sequence can have, from its row of pages and the window
+  int64_t segments;
+  bool together;        // one CTA per segment
+  size_t workspace;
+};
 
-template <class C>
-splash_status launch(const splash_paged_decode_args &a, Params p, cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  SPLASH_CUDA_TRY(cudaGetDevice(&dev));
-  SPLASH_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+constexpr int kTogetherSteps = 8;  // per warp
+
+Plan plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t dv, int32_t max_pages, int32_t page_size,
+          int32_t type, int64_t window) {
+  Plan x;
+  const int64_t nrows = (int64_t)(Hq / Hkv) * Lq;
+  x.row_tiles = nrows <= 16 ? 1 : 2;
+  const int64_t kw = (dqk + dv) * (type == SPLASH_CACHE_E4M3 ? 1 : 2) >= 512 ? 16 : 32;  // (Config::KW)
+  x.most = ((int64_t)max_pages * page_size + kw - 1) / kw;
+  if (window >= 0) x.most = std::min(x.most, window / kw + 4);
+  x.segments = (int64_t)B * Hkv * ((nrows + 16 * x.row_tiles - 1) / (16 * x.row_tiles));
+  x.together = x.most <= kTogetherSteps * kWarps && x.segments <= kMaxWarps / kWarps;
+  const int64_t rows = std::min<int64_t>(nrows, 16 * x.row_tiles);
+  x.workspace = x.together ? 0 : (size_t)(align16(4 * ((int64_t)B + 1)) + (int64_t)2 * kMaxWarps * rows * 4 * (dv + 2));
+  return x;
+}
+
+template <class C, bool TOGETHER>
+splash_status launch_kernel(int ctas, const Params &p, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};  // devices that allow this kernel its shared memory
+  int dev = 0;
+  SPLASH_CUDA_TRY(cudaGetDevice(&dev));
   const uint64_t bit = (uint64_t)1 << (dev & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
-    SPLASH_CUDA_TRY(cudaFuncSetAttribute(paged_decode_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+    SPLASH_CUDA_TRY(cudaFuncSetAttribute(paged_decode_kernel<C, TOGETHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
     ready.fetch_or(bit, std::memory_order_release);
   }
+  SPLASH_CUDA_TRY(launch_dependent(paged_decode_kernel<C, TOGETHER>, dim3(ctas), dim3(kThreads), C::SMEM, stream, p));
+  splash_count_launches(1);
+  return SPLASH_OK;
+}
+
+template <class C>
+splash_status launch(const Plan &x, void *workspace, Params p, cudaStream_t stream) {
   p.row_groups = (p.nrows + C::ROWS - 1) / C::ROWS;
   p.part_rows = std::min(p.nrows, C::ROWS);
-  // steps that a sequence can have at most, from the row of pages and the window
-  int64_t most = (((int64_t)a.max_pages << p.page_shift) + C::KW - 1) / C::KW;
-  if (p.window >= 0) most = std::min(most, ((int64_t)p.window + p.Lq) / C::KW + 2);
-  const int64_t all = std::min<int64_t>(most, kMaxWarps) * p.B * p.Hkv * p.row_groups;
-  const int ctas = (int)std::min<int64_t>({all, C::CTAS * (int64_t)sms, kMaxWarps / kWarps});
-  char *ws = static_cast<char *>(a.workspace);
+  if (x.together) return launch_kernel<C, true>((int)x.segments, p, stream);
+  char *ws = static_cast<char *>(workspace);
   p.before = reinterpret_cast<int32_t *>(ws);
   ws += align16(4 * ((int64_t)p.B + 1));
   p.part_ml = reinterpret_cast<float *>(ws);
   ws += (int64_t)2 * kMaxWarps * p.part_rows * 2 * 4;
   p.part_o = reinterpret_cast<float *>(ws);
-  SPLASH_CUDA_TRY(launch_dependent(paged_decode_kernel<C>, dim3(ctas), dim3(kThreads), C::SMEM, stream, p));
-  splash_count_launches(1);
-  if (most <= 1) return SPLASH_OK;  // no sequence has more than one step: nothing to join
+  int dev = 0, sms = 0;
+  SPLASH_CUDA_TRY(cudaGetDevice(&dev));
+  SPLASH_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  const int ctas = (int)std::min<int64_t>({std::min<int64_t>(x.most, kMaxWarps) * x.segments, C::CTAS * (int64_t)sms,
+                                           kMaxWarps / kWarps});
+  const splash_status st = launch_kernel<C, false>(ctas, p, stream);
+  if (st != SPLASH_OK || x.most <= 1) return st;  // (no segment has more than one step: nothing to join)
   const dim3 rows((unsigned)((int64_t)p.B * p.Hkv * p.nrows));
   SPLASH_CUDA_TRY(launch_dependent(paged_decode_join_kernel<C::DV, C::ROWS>, rows, dim3(kThreads), 0, stream, p, ctas * kWarps));
   splash_count_launches(1);
@@ -790,19 +888,20 @@ splash_status launch(const splash_paged_decode_args &a, Params p, cudaStream_t s
 
 template <int DQK, int DV>
 splash_status pick(const splash_paged_decode_args &a, const Params &p, cudaStream_t stream) {
-  const bool one = row_tiles(p.nrows) == 1;
+  const Plan x = plan(a.B, a.Hq, a.Hkv, a.Lq, a.dqk, a.dv, a.max_pages, a.page_size, a.cache_type, a.window_left);
   if (a.cache_type == SPLASH_CACHE_E4M3)
-    return one ? launch<Config<DQK, DV, true, 1>>(a, p, stream) : launch<Config<DQK, DV, true, 2>>(a, p, stream);
-  return one ? launch<Config<DQK, DV, false, 1>>(a, p, stream) : launch<Config<DQK, DV, false, 2>>(a, p, stream);
+    return x.row_tiles == 1 ? launch<Config<DQK, DV, true, 1>>(x, a.workspace, p, stream)
+                            : launch<Config<DQK, DV, true, 2>>(x, a.workspace, p, stream);
+  return x.row_tiles == 1 ? launch<Config<DQK, DV, false, 1>>(x, a.workspace, p, stream)
+                          : launch<Config<DQK, DV, false, 2>>(x, a.workspace, p, stream);
 }
 
 }  // namespace
 }  // namespace splash
 
-size_t splash_paged_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dv) {
-  using namespace splash;
-  const int64_t nrows = (int64_t)(Hq / Hkv) * Lq, rows = std::min<int64_t>(nrows, 16 * row_tiles(nrows));
-  return (size_t)(align16(4 * ((int64_t)B + 1)) + (int64_t)2 * kMaxWarps * rows * 4 * (dv + 2));
+size_t splash_paged_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t dv,
+                                           int32_t max_pages, int32_t page_size, int32_t type, int64_t window) {
+  return splash::plan(B, Hq, Hkv, Lq, dqk, dv, max_pages, page_size, type, window).workspace;
 }
 
 splash_status splash_paged_decode_launch(const splash_paged_decode_args &a, cudaStream_t stream, uint32_t *err_word) {

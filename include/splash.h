@@ -544,9 +544,9 @@ splash_status splash_paged_append(const splash_paged_append_args *args, void *cu
  *   out         device bf16 [B][Hq][Lq][dv] dense, 16-byte aligned
  *   lse         device fp32 [B][Hq][Lq]
  *   workspace   device, 16-byte aligned, at least
- *               splash_paged_decode_workspace_size bytes for the same B, Hq,
- *               Hkv, Lq, dv; overwritten, holds nothing between calls.  Two
- *               calls that may run at the same time need two workspaces.
+ *               splash_paged_decode_workspace_size bytes for the same sizes;
+ *               overwritten, holds nothing between calls.  Two calls that may
+ *               run at the same time need two workspaces.
  * Supported: (dqk, dv) in {(64, 64), (128, 128), (192, 128)}, Hq % Hkv == 0,
  * 1 <= Lq <= SPLASH_MAX_NEW_TOKENS, page_size a power of two in 16 .. 1024,
  * max_pages * page_size < 2^31 - 65535, B <= 65535, and fewer than 2^31 steps of
@@ -573,8 +573,11 @@ typedef struct {
     int32_t reserved; /* 0 */
 } splash_paged_decode_args;
 splash_status splash_paged_decode(const splash_paged_decode_args *args, void *cuda_stream);
-splash_status splash_paged_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dv,
-                                                 size_t *bytes);
+/* *bytes = the workspace of a call with these sizes (0: none, workspace may be
+ * NULL): INVALID_ARG, SHAPE or UNSUPPORTED where the call itself would be. */
+splash_status splash_paged_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t dv,
+                                                 int32_t max_pages, int32_t page_size, int32_t cache_type,
+                                                 int64_t window_left, size_t *bytes);
 
 /*
  * splash_classify_blocks_noalloc -- the block classification of a mask

@@ -104,10 +104,14 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("long_rows", [False, True], ids=["short", "long"])
 @pytest.mark.parametrize("case", CASES, ids=str)
-def test_decode_matches_the_reference(splash, case):
+def test_decode_matches_the_reference(splash, case, long_rows):
+    """With rows of pages that hold little more than the lengths, and with rows
+    that allow over 1024 keys (the keys are then split over the whole GPU)."""
     lens, Lq, Hq, Hkv, dqk, dv, page, kind, layout, window, cap = case
-    x = make(lens, Lq, Hq, Hkv, dqk, dv, page, kind, layout, seed=100 + CASES.index(case))
+    x = make(lens, Lq, Hq, Hkv, dqk, dv, page, kind, layout, seed=100 + CASES.index(case),
+             extra_cols=1 + 1100 // page if long_rows else 0)
     q, kc, vc, bt, n, ks, vs = x
     scale = 1 / math.sqrt(dqk)
     got = splash.paged_decode(q, kc, vc, bt, n, scale, softcap=cap, window_left=window, k_scale=ks, v_scale=vs)
@@ -143,7 +147,7 @@ def test_rows_before_the_window_are_not_read(splash):
     """Pages that have left the window may be gone: their entries point
     nowhere, their rows hold NaN."""
     n, page, window = 500, 16, 100
-    q, kc, vc, bt, lens, _, _ = make([n], 2, 4, 2, 128, 128, page, seed=70)
+    q, kc, vc, bt, lens, _, _ = make([n], 2, 4, 2, 128, 128, page, seed=70, extra_cols=100)
     want = bounds(q, kc, vc, bt, lens, 0.1, 0.0, window)
     lo = n - 2 - window  # first key of the earliest query
     for c in range(lo // page):
@@ -160,7 +164,7 @@ def test_rows_before_the_window_are_not_read(splash):
 
 def test_strided_queries_shared_pages_and_given_outputs(splash):
     lens, Hq, Hkv, d = [100, 100, 37], 8, 2, 128
-    q, kc, vc, bt, n, _, _ = make(lens, 1, Hq, Hkv, d, d, 16, seed=80)
+    q, kc, vc, bt, n, _, _ = make(lens, 1, Hq, Hkv, d, d, 16, seed=80, extra_cols=60)
     bt[1, :6] = bt[0, :6]  # a shared prefix
     wide = torch.zeros(3, 1, Hq + 5, d, dtype=torch.bfloat16, device="cuda")
     wide[:, :, 2:2 + Hq] = q.transpose(1, 2)
@@ -168,7 +172,7 @@ def test_strided_queries_shared_pages_and_given_outputs(splash):
     kv = torch.stack((kc, vc), 1)  # K and V of a page side by side
     out = torch.full((3, Hq, 1, d), 7.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.empty(3, Hq, 1, device="cuda")
-    size = splash.paged_decode_workspace_size(3, Hq, Hkv, 1, d)
+    size = splash.paged_decode_workspace_size(view, kc, vc, bt)
     ws = torch.full((size + 64,), 0xA5, dtype=torch.uint8, device="cuda")
     got = splash.paged_decode(view, kv[:, 0], kv[:, 1], bt, n, 0.1, out=out, lse=lse, workspace=ws[:size])
     assert got[0] is out and got[1] is lse

@@ -122,13 +122,14 @@ def step(splash, tok, kc, vc, bt, lens, table, q_out, out, lse, ws):
     splash.paged_decode(q_out, kc, vc, bt, lens, 0.1, out=out, lse=lse, workspace=ws)
 
 
-def test_a_captured_step_replays_with_growing_lengths(splash):
-    tok, kc, vc, bt, lens = decode_state()
+@pytest.mark.parametrize("per", [12, 40], ids=["short rows of pages", "long rows of pages"])
+def test_a_captured_step_replays_with_growing_lengths(splash, per):
+    tok, kc, vc, bt, lens = decode_state(per=per)
     table = splash.rope_table(256, 128)
     B, Hq, Hkv, d = 3, 8, 2, 128
     q_out, out = torch.empty_like(tok[0]), torch.empty(B, Hq, 1, d, dtype=torch.bfloat16, device="cuda")
     lse = torch.empty(B, Hq, 1, device="cuda")
-    ws = torch.empty(splash.paged_decode_workspace_size(B, Hq, Hkv, 1, d), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(splash.paged_decode_workspace_size(tok[0], kc, vc, bt), dtype=torch.uint8, device="cuda")
     eager = [kc.clone(), vc.clone(), bt, lens.clone()]
     eo, el, eq = torch.empty_like(out), torch.empty_like(lse), torch.empty_like(q_out)
     side = torch.cuda.Stream()
@@ -150,7 +151,7 @@ def test_a_captured_step_replays_with_growing_lengths(splash):
 
 
 def test_calls_on_another_stream_and_two_at_once(splash):
-    tok, kc, vc, bt, lens = decode_state()
+    tok, kc, vc, bt, lens = decode_state(per=40)
     table = splash.rope_table(256, 128)
     pos = lens[:, None].contiguous()
     q1, _ = splash.paged_append(tok[1], tok[2], kc, vc, bt, pos, q=tok[0], table=table)

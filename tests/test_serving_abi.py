@@ -81,6 +81,11 @@ def decode_args():
     return a
 
 
+def with_pages(a, n):
+    a.max_pages = n
+    return a
+
+
 def call(splash, name, a):
     return getattr(splash.lib(), name)(bytes(a), None)
 
@@ -157,7 +162,8 @@ def test_append_rows_that_would_overlap_are_refused(splash):
 
 
 def test_decode_refusals(splash):
-    refused(splash, "splash_paged_decode", decode_args, [
+    long = lambda: with_pages(decode_args(), 256)  # noqa: E731  (a call that needs a workspace)
+    refused(splash, "splash_paged_decode", long, [
         ("struct_bytes", 8, INVALID), ("B", 0, INVALID), ("B", 65536, UNSUPPORTED), ("Hkv", 3, SHAPE),
         ("Lq", 0, INVALID), ("Lq", 17, UNSUPPORTED), ("dqk", 64, UNSUPPORTED), ("dv", 96, UNSUPPORTED),
         ("seq_lens", None, INVALID), ("seq_lens", OK_PTR + 2, INVALID), ("out", None, INVALID),
@@ -184,12 +190,24 @@ def test_decode_limit_of_steps(splash):
 
 
 def test_decode_workspace_size(splash):
-    f = splash.lib().splash_paged_decode_workspace_size
     n = ctypes.c_size_t(0)
-    assert f(4, 32, 8, 1, 128, ctypes.byref(n)) == 0 and n.value >= 16
-    assert splash.paged_decode_workspace_size(4, 32, 8, 1, 128) == n.value
-    assert f(4, 32, 8, 1, 128, None) == INVALID and f(0, 32, 8, 1, 128, ctypes.byref(n)) == INVALID
-    assert f(4, 32, 7, 1, 128, ctypes.byref(n)) == SHAPE and f(4, 32, 8, 17, 128, ctypes.byref(n)) == UNSUPPORTED
+
+    def size(B=4, Hq=32, Hkv=8, Lq=1, dqk=128, dv=128, max_pages=256, page=16, kind=0, window=-1):
+        return splash.lib().splash_paged_decode_workspace_size(B, Hq, Hkv, Lq, dqk, dv, max_pages, page, kind, window,
+                                                               ctypes.byref(n))
+    assert size() == 0 and n.value > 0
+    q = torch.zeros(4, 32, 1, 128)
+    cache = torch.zeros(2, 8, 16, 128, dtype=torch.bfloat16)
+    assert splash.paged_decode_workspace_size(q, cache, cache, torch.zeros(4, 256)) == n.value
+    # few and short sequences need none; many, or longer ones, do
+    assert size(max_pages=32) == 0 and n.value == 0
+    assert size(window=100) == 0 and n.value == 0
+    assert size(max_pages=33) == 0 and n.value > 0
+    assert size(B=64, max_pages=4) == 0 and n.value > 0
+    assert size(B=0) == INVALID and size(kind=2) == INVALID and size(window=-2) == INVALID and size(page=0) == INVALID
+    assert size(Hkv=7) == SHAPE and size(Lq=17) == UNSUPPORTED and size(dqk=64) == UNSUPPORTED
+    assert size(page=20) == UNSUPPORTED and size(max_pages=1 << 28) == UNSUPPORTED
+    assert splash.lib().splash_paged_decode_workspace_size(4, 32, 8, 1, 128, 128, 256, 16, 0, -1, None) == INVALID
 
 
 def test_the_binding_refuses_cpu_tensors(splash):
