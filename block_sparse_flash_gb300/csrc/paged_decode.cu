@@ -14,8 +14,10 @@
 //    covers is finished there; parts of one that several warps share go to the
 //    workspace as (maximum, sum, unnormalised output) and a second kernel joins
 //    them, in the order of the keys, so that the result does not depend on
-//    timing.  A call of few and short segments takes one CTA for each instead:
-//    its warps share the keys and join through shared memory.
+//    timing.  Where there are too few segments to fill the GPU and none can be
+//    very long, each takes a cluster of CTAs instead: their warps share the keys
+//    equally and join through distributed shared memory, which saves the scan,
+//    the workspace and the second kernel.
 //  * Loads.  Each warp keeps a ring of stages in shared memory, filled by
 //    16-byte asynchronous copies that run ahead of the products and across the
 //    borders of sequences; there is no barrier between warps.  Rows outside the
@@ -155,6 +157,9 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
 __device__ __forceinline__ void copy16(uint32_t dst, const char *src, bool read) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const char *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -244,18 +249,26 @@ struct Loader {
   }
 
   template <int ROWB>
-  __device__ __forceinline__ void block(uint32_t dst, const char *base, int64_t token, int32_t key, bool ok) const {
+  __device__ __forceinline__ void block(uint32_t dst, const char *base, int64_t token, int32_t key, bool ok, bool whole) const {
     constexpr int SEG = ROWB % 128 == 0 ? 128 : 64;  // a row's contiguous bytes per instruction
     constexpr int LPS = SEG / 16, RPI = 32 / LPS;
     const int r0 = lane / LPS, c0 = lane % LPS;
     const char *src = base + r0 * token + c0 * 16;
+    if (whole) {
 #pragma unroll
-    for (int rg = 0; rg < 16 / RPI; ++rg) {
-      const int r = rg * RPI + r0;
-      const bool read = ok && key + r >= at.s.lo && key + r < at.s.n;
+      for (int rg = 0; rg < 16 / RPI; ++rg)
 #pragma unroll
-      for (int part = 0; part < ROWB / SEG; ++part)
-        copy16(dst + chunk_at<ROWB>(r, part * LPS + c0), read ? src + rg * RPI * token + part * SEG : base, read);
+        for (int part = 0; part < ROWB / SEG; ++part)
+          copy16(dst + chunk_at<ROWB>(rg * RPI + r0, part * LPS + c0), src + rg * RPI * token + part * SEG);
+    } else {
+#pragma unroll 1
+      for (int rg = 0; rg < 16 / RPI; ++rg) {
+        const int r = rg * RPI + r0;
+        const bool read = ok && key + r >= at.s.lo && key + r < at.s.n;
+#pragma unroll
+        for (int part = 0; part < ROWB / SEG; ++part)
+          copy16(dst + chunk_at<ROWB>(r, part * LPS + c0), read ? src + rg * RPI * token + part * SEG : base, read);
+      }
     }
   }
 
@@ -270,8 +283,9 @@ struct Loader {
         if (!ok && lane == 0) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
         const int32_t slot = key & ((1 << p.page_shift) - 1);
         const int64_t pg = ok ? page : 0;
-        block<C::RK>(stage + i * 16 * C::RK, k + pg * p.k_page + slot * p.k_token, p.k_token, key, ok);
-        block<C::RV>(stage + C::KW * C::RK + i * 16 * C::RV, v + pg * p.v_page + slot * p.v_token, p.v_token, key, ok);
+        const bool whole = ok && key >= at.s.lo && key + 16 <= at.s.n;
+        block<C::RK>(stage + i * 16 * C::RK, k + pg * p.k_page + slot * p.k_token, p.k_token, key, ok, whole);
+        block<C::RV>(stage + C::KW * C::RK + i * 16 * C::RV, v + pg * p.v_page + slot * p.v_token, p.v_token, key, ok, whole);
       }
       if (at.advance(p, per_seq, end) && at.u < end) enter();
       if (at.u < end) look();
@@ -295,14 +309,59 @@ __device__ __forceinline__ void store_row(float *dst, const float (&o)[C::DV / 8
   }
 }
 
-// TOGETHER: one CTA per segment; otherwise equal parts of the list per warp.
+// acc and sum += a part (maximum, sum, x), both taken relative to `high`.
+__device__ __forceinline__ void add_part(float4 &acc, float &sum, float high, float2 ml, float4 x) {
+  const float f = ex2_approx(ml.x - (high == -INFINITY ? 0.f : high));
+  sum += f * ml.y;
+  acc.x += f * x.x;
+  acc.y += f * x.y;
+  acc.z += f * x.z;
+  acc.w += f * x.w;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t n;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return n;
+}
+// Every thread of every CTA of the cluster arrives and waits.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// The same shared memory address in another CTA of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(addr)
+               : "memory");
+  return x;
+}
+__device__ __forceinline__ float2 load_cluster2(uint32_t addr) {
+  float2 x;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(addr) : "memory");
+  return x;
+}
+
+// TOGETHER: a cluster of CTAs per segment; otherwise equal parts of the list per warp.
 template <class C, bool TOGETHER>
 __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params p) {
   constexpr int DQK = C::DQK, DV = C::DV, MT = C::MT, NB = C::NB;
   constexpr bool E4M3 = C::E4M3;
   extern __shared__ __align__(1024) char smem[];
   __shared__ int32_t s_scan[kWarps], s_before[kWarps], s_seq[kWarps];
-  __shared__ float s_ml[kWarps][C::ROWS][2];
+  __shared__ float2 s_ml[kWarps][C::ROWS], s_cta[C::ROWS];  // (maximum, sum) of the rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int quad = lane >> 2, tq = lane & 3;
   const uint32_t ring = smem_u32(smem + warp * C::WARP_BYTES);
@@ -316,12 +375,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
   Cursor<C::KW> at;
   int32_t end;
   if constexpr (TOGETHER) {
-    at.b = blockIdx.x / per_seq;
-    at.seg = blockIdx.x % per_seq;
+    const uint32_t ctas = cluster_size(), rank = cluster_rank(), segment = blockIdx.x / ctas;
+    at.b = segment / per_seq;
+    at.seg = segment % per_seq;
     at.s = span_of<C::KW>(p, at.b);
-    at.u = at.step = (int32_t)((int64_t)at.s.nst * warp / kWarps);
-    end = (int32_t)((int64_t)at.s.nst * (warp + 1) / kWarps);
-    if (at.seg == 0 && threadIdx.x == 0) check_length(p, at.b);
+    const Parts parts(at.s.nst, kWarps * ctas);
+    at.u = at.step = parts.begin(rank * kWarps + warp);
+    end = parts.begin(rank * kWarps + warp + 1);
+    if (at.seg == 0 && rank == 0 && threadIdx.x == 0) check_length(p, at.b);
   } else {
     // the warps' parts of the list: a scan over the sequences
     int32_t T;
@@ -556,39 +617,55 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 
       // scores in powers of two; masked where some row does not see some key
       const bool whole = key0 + C::KW <= sp.n - p.Lq + 1 && (p.window < 0 || key0 >= sp.n - 1 - p.window);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 2 * NB; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[mt][j][i] *= factor[mt][i >> 1];
+      if (p.cap > 0.f) {
+        const float cap = p.cap * kLog2e;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < 2 * NB; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[mt][j][i] = cap * tanh_of(s[mt][j][i]);
+      }
+      if (!whole) {
+        const uint32_t reach = p.window < 0 ? 0x7fffffffu : (uint32_t)p.window;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < 2 * NB; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // (as unsigned, a key ahead of the query is out of reach too)
+              const uint32_t behind = (uint32_t)(pos[mt][i >> 1] - (key0 + 8 * j + 2 * tq + (i & 1)));
+              if (behind > reach) s[mt][j][i] = -INFINITY;
+            }
+      }
+      float top[MT][2];
       bool move = false;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float top = -INFINITY;
+          top[mt][e] = fmaxf(s[mt][0][2 * e], s[mt][0][2 * e + 1]);
 #pragma unroll
-          for (int j = 0; j < 2 * NB; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float y = s[mt][j][2 * e + i] * factor[mt][e];
-              if (p.cap > 0.f) y = p.cap * kLog2e * tanh_of(y);
-              if (!whole) {
-                const int32_t behind = pos[mt][e] - (key0 + 8 * j + 2 * tq + i);
-                if (behind < 0 || (p.window >= 0 && behind > p.window)) y = -INFINITY;
-              }
-              s[mt][j][2 * e + i] = y;
-              top = fmaxf(top, y);
-            }
-          move |= top > m[mt][e] + kSlack;
+          for (int j = 1; j < 2 * NB; ++j) top[mt][e] = fmax3(top[mt][e], s[mt][j][2 * e], s[mt][j][2 * e + 1]);
+          move |= top[mt][e] > m[mt][e] + kSlack;
         }
       if (__any_sync(~0u, move)) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = m[mt][e];
-#pragma unroll
-            for (int j = 0; j < 2 * NB; ++j) top = fmax3(top, s[mt][j][2 * e], s[mt][j][2 * e + 1]);
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            const float alpha = top == -INFINITY ? 1.f : ex2_approx(m[mt][e] - top);
-            m[mt][e] = top;
+            float high = fmaxf(top[mt][e], m[mt][e]);
+            high = fmaxf(high, __shfl_xor_sync(~0u, high, 1));
+            high = fmaxf(high, __shfl_xor_sync(~0u, high, 2));
+            const float alpha = high == -INFINITY ? 1.f : ex2_approx(m[mt][e] - high);
+            m[mt][e] = high;
             l[mt][e] *= alpha;
 #pragma unroll
             for (int j = 0; j < DV / 8; ++j) {
@@ -665,34 +742,47 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
           sum += __shfl_xor_sync(~0u, sum, 1);
           sum += __shfl_xor_sync(~0u, sum, 2);
           if (r >= rows) continue;
-          if (tq == 0) s_ml[warp][r][0] = m[mt][e], s_ml[warp][r][1] = sum;
+          if (tq == 0) s_ml[warp][r] = make_float2(m[mt][e], sum);
           store_row<C>(own + r * C::ODIM, o[mt], e, tq);
         }
       __syncthreads();
+      // the CTA's rows, where the first warp's were
       constexpr int LANES = DV / 4;
       const int col = 4 * (threadIdx.x % LANES);
-      const float v_scale = E4M3 ? __ldg(p.v_scale + head) : 1.f;
       for (int r = threadIdx.x / LANES; r < rows; r += kThreads / LANES) {
-        float top = -INFINITY, sum = 0.f;
+        float high = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][r][0]);
+        for (int w = 0; w < kWarps; ++w) high = fmaxf(high, s_ml[w][r].x);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = ex2_approx(s_ml[w][r][0] - (top == -INFINITY ? 0.f : top));
-          const float4 x = *reinterpret_cast<const float4 *>(smem + w * C::WARP_BYTES + 4 * (r * C::ODIM + col));
-          sum += f * s_ml[w][r][1];
-          acc.x += f * x.x;
-          acc.y += f * x.y;
-          acc.z += f * x.z;
-          acc.w += f * x.w;
-        }
+        for (int w = 0; w < kWarps; ++w)
+          add_part(acc, sum, high, s_ml[w][r], *reinterpret_cast<const float4 *>(smem + w * C::WARP_BYTES + 4 * (r * C::ODIM + col)));
+        *reinterpret_cast<float4 *>(smem + 4 * (r * C::ODIM + col)) = acc;
+        if (col == 0) s_cta[r] = make_float2(high, sum);
+      }
+      // the cluster's: every CTA finishes some of the segment's columns
+      const uint32_t ctas = cluster_size();
+      if (ctas > 1)
+        cluster_sync();
+      else
+        __syncthreads();
+      const float v_scale = E4M3 ? __ldg(p.v_scale + head) : 1.f;
+      for (int i = cluster_rank() * kThreads + threadIdx.x; i < rows * LANES; i += ctas * kThreads) {
+        const int r = i / LANES, c = 4 * (i % LANES);
+        const uint32_t ml = smem_u32(&s_cta[r]), from = smem_u32(smem) + 4 * (r * C::ODIM + c);
+        float high = -INFINITY, sum = 0.f;
+        for (uint32_t k = 0; k < ctas; ++k) high = fmaxf(high, load_cluster2(in_cta(ml, k)).x);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (uint32_t k = 0; k < ctas; ++k)
+          add_part(acc, sum, high, load_cluster2(in_cta(ml, k)), load_cluster4(in_cta(from, k)));
         const float inv = sum == 0.f ? 0.f : v_scale / sum;
         const int64_t row = ((int64_t)b * p.Hkv + head) * p.nrows + row0 + r;
-        *reinterpret_cast<uint2 *>(p.out + row * DV + col) =
+        *reinterpret_cast<uint2 *>(p.out + row * DV + c) =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (col == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        if (c == 0) p.lse[row] = sum == 0.f ? -INFINITY : (high + log2f(sum)) * kLn2;
       }
+      if (ctas > 1) cluster_sync();  // (no CTA ends while another reads its shared memory)
       return;
     }
 
@@ -826,11 +916,22 @@ struct Plan {
   int row_tiles;        // 16 rows each, 1 or 2
   int64_t most;         // steps that a sequence can have, from its row of pages and the window
   int64_t segments;
-  bool together;        // one CTA per segment
+  int cluster;          // CTAs per segment, 0: the list
   size_t workspace;
 };
 
-constexpr int kTogetherSteps = 8;  // per warp
+// Clusters or the list.  A cluster call has no scan and no second kernel, the
+// list loads every SM alike however the lengths differ.  Measured (32 query, 8
+// KV heads of 128, bf16; list -> clusters, us): 1 sequence of 64 keys
+// 5.6 -> 3.3, 2048 keys 12.4 -> 6.8, 16384 keys 20.6 -> 17.6; 8 sequences of
+// 2048 keys 14.3 -> 10.9, of 8192 keys 48.2 -> 43.4; 16 sequences through a
+// window of 4096 keys 48.8 -> 42.8; 8 sequences of 1023 .. 8191 keys 33.1 ->
+// 32.5.  A sequence much longer than the others keeps its clusters running
+// alone (2048 keys take a CTA 23 us), so the keys that a CTA may get are
+// limited: 2048, and the ends of a window of that size per CTA.
+constexpr int kSlots = kMaxWarps / kWarps;  // CTAs that fill the GPU
+constexpr int kMaxCluster = 16;             // (8 without opting in: 16384 keys of 1 sequence 25.2 us)
+constexpr int kClusterKeys = 2304;          // per CTA, at most
 
 Plan plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t dv, int32_t max_pages, int32_t page_size,
           int32_t type, int64_t window) {
@@ -841,23 +942,26 @@ Plan plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t d
   x.most = ((int64_t)max_pages * page_size + kw - 1) / kw;
   if (window >= 0) x.most = std::min(x.most, window / kw + 4);
   x.segments = (int64_t)B * Hkv * ((nrows + 16 * x.row_tiles - 1) / (16 * x.row_tiles));
-  x.together = x.most <= kTogetherSteps * kWarps && x.segments <= kMaxWarps / kWarps;
+  x.cluster = x.segments <= kSlots ? 1 : 0;
+  while (x.cluster > 0 && x.cluster < kMaxCluster && 2 * x.cluster * x.segments <= kSlots && x.cluster * kWarps < x.most) x.cluster *= 2;
+  if (x.most * kw > (int64_t)kClusterKeys * x.cluster) x.cluster = 0;
   const int64_t rows = std::min<int64_t>(nrows, 16 * x.row_tiles);
-  x.workspace = x.together ? 0 : (size_t)(align16(4 * ((int64_t)B + 1)) + (int64_t)2 * kMaxWarps * rows * 4 * (dv + 2));
+  x.workspace = x.cluster > 0 ? 0 : (size_t)(align16(4 * ((int64_t)B + 1)) + (int64_t)2 * kMaxWarps * rows * 4 * (dv + 2));
   return x;
 }
 
 template <class C, bool TOGETHER>
-splash_status launch_kernel(int ctas, const Params &p, cudaStream_t stream) {
+splash_status launch_kernel(int ctas, int cluster, const Params &p, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};  // devices that allow this kernel its shared memory
   int dev = 0;
   SPLASH_CUDA_TRY(cudaGetDevice(&dev));
   const uint64_t bit = (uint64_t)1 << (dev & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
     SPLASH_CUDA_TRY(cudaFuncSetAttribute(paged_decode_kernel<C, TOGETHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+    if (TOGETHER) SPLASH_CUDA_TRY(cudaFuncSetAttribute(paged_decode_kernel<C, TOGETHER>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     ready.fetch_or(bit, std::memory_order_release);
   }
-  SPLASH_CUDA_TRY(launch_dependent(paged_decode_kernel<C, TOGETHER>, dim3(ctas), dim3(kThreads), C::SMEM, stream, p));
+  SPLASH_CUDA_TRY(launch_dependent(paged_decode_kernel<C, TOGETHER>, dim3(ctas), dim3(kThreads), C::SMEM, cluster, stream, p));
   splash_count_launches(1);
   return SPLASH_OK;
 }
@@ -866,7 +970,7 @@ template <class C>
 splash_status launch(const Plan &x, void *workspace, Params p, cudaStream_t stream) {
   p.row_groups = (p.nrows + C::ROWS - 1) / C::ROWS;
   p.part_rows = std::min(p.nrows, C::ROWS);
-  if (x.together) return launch_kernel<C, true>((int)x.segments, p, stream);
+  if (x.cluster > 0) return launch_kernel<C, true>((int)x.segments * x.cluster, x.cluster, p, stream);
   char *ws = static_cast<char *>(workspace);
   p.before = reinterpret_cast<int32_t *>(ws);
   ws += align16(4 * ((int64_t)p.B + 1));
@@ -878,10 +982,10 @@ splash_status launch(const Plan &x, void *workspace, Params p, cudaStream_t stre
   SPLASH_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   const int ctas = (int)std::min<int64_t>({std::min<int64_t>(x.most, kMaxWarps) * x.segments, C::CTAS * (int64_t)sms,
                                            kMaxWarps / kWarps});
-  const splash_status st = launch_kernel<C, false>(ctas, p, stream);
+  const splash_status st = launch_kernel<C, false>(ctas, 1, p, stream);
   if (st != SPLASH_OK || x.most <= 1) return st;  // (no segment has more than one step: nothing to join)
   const dim3 rows((unsigned)((int64_t)p.B * p.Hkv * p.nrows));
-  SPLASH_CUDA_TRY(launch_dependent(paged_decode_join_kernel<C::DV, C::ROWS>, rows, dim3(kThreads), 0, stream, p, ctas * kWarps));
+  SPLASH_CUDA_TRY(launch_dependent(paged_decode_join_kernel<C::DV, C::ROWS>, rows, dim3(kThreads), 0, 1, stream, p, ctas * kWarps));
   splash_count_launches(1);
   return SPLASH_OK;
 }

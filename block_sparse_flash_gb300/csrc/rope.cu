@@ -261,7 +261,7 @@ splash_status launch_heads(const Params &p, bool interleaved, cudaStream_t strea
   const int ty = std::max(1, 128 / p.units);
   const dim3 block(p.units, ty), grid((p.tokens + ty - 1) / ty, (p.heads + HEADS - 1) / HEADS);
   SPLASH_CUDA_TRY(launch_dependent(interleaved ? rope_kernel<true, APPEND, E4M3, HEADS> : rope_kernel<false, APPEND, E4M3, HEADS>,
-                                   grid, block, 0, stream, p));
+                                   grid, block, 0, 1, stream, p));
   splash_count_launches(1);
   return SPLASH_OK;
 }

@@ -107,11 +107,12 @@ CASES = [
 @pytest.mark.parametrize("long_rows", [False, True], ids=["short", "long"])
 @pytest.mark.parametrize("case", CASES, ids=str)
 def test_decode_matches_the_reference(splash, case, long_rows):
-    """With rows of pages that hold little more than the lengths, and with rows
-    that allow over 1024 keys (the keys are then split over the whole GPU)."""
+    """With rows of pages that hold little more than the lengths (a cluster per
+    sequence and head), and with rows that allow 40000 keys (the keys are then
+    split over the whole GPU)."""
     lens, Lq, Hq, Hkv, dqk, dv, page, kind, layout, window, cap = case
     x = make(lens, Lq, Hq, Hkv, dqk, dv, page, kind, layout, seed=100 + CASES.index(case),
-             extra_cols=1 + 1100 // page if long_rows else 0)
+             extra_cols=1 + 40000 // page if long_rows else 0)
     q, kc, vc, bt, n, ks, vs = x
     scale = 1 / math.sqrt(dqk)
     got = splash.paged_decode(q, kc, vc, bt, n, scale, softcap=cap, window_left=window, k_scale=ks, v_scale=vs)
@@ -121,7 +122,7 @@ def test_decode_matches_the_reference(splash, case, long_rows):
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
 
 
-@pytest.mark.parametrize("B", [1, 130, 300])
+@pytest.mark.parametrize("B", [1, 130, 300, 700])
 def test_many_sequences_of_mixed_lengths(splash, B):
     g = torch.Generator().manual_seed(B)
     lens = torch.randint(0, 200, (B,), generator=g).tolist()
@@ -164,7 +165,7 @@ def test_rows_before_the_window_are_not_read(splash):
 
 def test_strided_queries_shared_pages_and_given_outputs(splash):
     lens, Hq, Hkv, d = [100, 100, 37], 8, 2, 128
-    q, kc, vc, bt, n, _, _ = make(lens, 1, Hq, Hkv, d, d, 16, seed=80, extra_cols=60)
+    q, kc, vc, bt, n, _, _ = make(lens, 1, Hq, Hkv, d, d, 16, seed=80, extra_cols=2600)
     bt[1, :6] = bt[0, :6]  # a shared prefix
     wide = torch.zeros(3, 1, Hq + 5, d, dtype=torch.bfloat16, device="cuda")
     wide[:, :, 2:2 + Hq] = q.transpose(1, 2)

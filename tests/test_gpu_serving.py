@@ -122,7 +122,7 @@ def step(splash, tok, kc, vc, bt, lens, table, q_out, out, lse, ws):
     splash.paged_decode(q_out, kc, vc, bt, lens, 0.1, out=out, lse=lse, workspace=ws)
 
 
-@pytest.mark.parametrize("per", [12, 40], ids=["short rows of pages", "long rows of pages"])
+@pytest.mark.parametrize("per", [12, 2600], ids=["short rows of pages", "long rows of pages"])
 def test_a_captured_step_replays_with_growing_lengths(splash, per):
     tok, kc, vc, bt, lens = decode_state(per=per)
     table = splash.rope_table(256, 128)
@@ -151,7 +151,7 @@ def test_a_captured_step_replays_with_growing_lengths(splash, per):
 
 
 def test_calls_on_another_stream_and_two_at_once(splash):
-    tok, kc, vc, bt, lens = decode_state(per=40)
+    tok, kc, vc, bt, lens = decode_state(per=2600)
     table = splash.rope_table(256, 128)
     pos = lens[:, None].contiguous()
     q1, _ = splash.paged_append(tok[1], tok[2], kc, vc, bt, pos, q=tok[0], table=table)

@@ -162,7 +162,7 @@ def test_append_rows_that_would_overlap_are_refused(splash):
 
 
 def test_decode_refusals(splash):
-    long = lambda: with_pages(decode_args(), 256)  # noqa: E731  (a call that needs a workspace)
+    long = lambda: with_pages(decode_args(), 8192)  # noqa: E731  (a call that needs a workspace)
     refused(splash, "splash_paged_decode", long, [
         ("struct_bytes", 8, INVALID), ("B", 0, INVALID), ("B", 65536, UNSUPPORTED), ("Hkv", 3, SHAPE),
         ("Lq", 0, INVALID), ("Lq", 17, UNSUPPORTED), ("dqk", 64, UNSUPPORTED), ("dv", 96, UNSUPPORTED),
@@ -192,22 +192,21 @@ def test_decode_limit_of_steps(splash):
 def test_decode_workspace_size(splash):
     n = ctypes.c_size_t(0)
 
-    def size(B=4, Hq=32, Hkv=8, Lq=1, dqk=128, dv=128, max_pages=256, page=16, kind=0, window=-1):
+    def size(B=4, Hq=32, Hkv=8, Lq=1, dqk=128, dv=128, max_pages=8192, page=16, kind=0, window=-1):
         return splash.lib().splash_paged_decode_workspace_size(B, Hq, Hkv, Lq, dqk, dv, max_pages, page, kind, window,
                                                                ctypes.byref(n))
     assert size() == 0 and n.value > 0
     q = torch.zeros(4, 32, 1, 128)
     cache = torch.zeros(2, 8, 16, 128, dtype=torch.bfloat16)
-    assert splash.paged_decode_workspace_size(q, cache, cache, torch.zeros(4, 256)) == n.value
+    assert splash.paged_decode_workspace_size(q, cache, cache, torch.zeros(4, 8192)) == n.value
     # few and short sequences need none; many, or longer ones, do
     assert size(max_pages=32) == 0 and n.value == 0
     assert size(window=100) == 0 and n.value == 0
-    assert size(max_pages=33) == 0 and n.value > 0
     assert size(B=64, max_pages=4) == 0 and n.value > 0
     assert size(B=0) == INVALID and size(kind=2) == INVALID and size(window=-2) == INVALID and size(page=0) == INVALID
     assert size(Hkv=7) == SHAPE and size(Lq=17) == UNSUPPORTED and size(dqk=64) == UNSUPPORTED
     assert size(page=20) == UNSUPPORTED and size(max_pages=1 << 28) == UNSUPPORTED
-    assert splash.lib().splash_paged_decode_workspace_size(4, 32, 8, 1, 128, 128, 256, 16, 0, -1, None) == INVALID
+    assert splash.lib().splash_paged_decode_workspace_size(4, 32, 8, 1, 128, 128, 8192, 16, 0, -1, None) == INVALID
 
 
 def test_the_binding_refuses_cpu_tensors(splash):
