@@ -72,13 +72,20 @@ struct Params {
   uint32_t *err;
 };
 
-template <int DQK_, int DV_, bool E4M3_, int MT_>
+// Keys of a step, from the bytes of a key and its value: 8 KB or so per step.
+constexpr int keys_per_step(int bytes) { return bytes >= 512 ? 16 : 32; }
+
+// ROWS: query rows of a tile, 8, 16 or 32.  Eight rows (up to 8 query heads per
+// KV head, one new token) leave half of each 16-row product free: for a bf16
+// cache it takes what rounding P to bf16 loses, see below.
+template <int DQK_, int DV_, bool E4M3_, int ROWS_>
 struct Config {
-  static constexpr int DQK = DQK_, DV = DV_, MT = MT_, ROWS = 16 * MT_;
+  static constexpr int DQK = DQK_, DV = DV_, ROWS = ROWS_;
+  static constexpr int MT = ROWS <= 16 ? 1 : 2;  // products of 16 rows
+  static constexpr int E = ROWS == 8 ? 1 : 2;    // halves of them that hold rows
   static constexpr bool E4M3 = E4M3_;
   static constexpr int RK = DQK * (E4M3 ? 1 : 2), RV = DV * (E4M3 ? 1 : 2);  // bytes of a row
-  static constexpr int NB = RK + RV >= 512 ? 1 : 2;                          // 16-key blocks per step
-  static constexpr int KW = 16 * NB;
+  static constexpr int KW = keys_per_step(RK + RV), NB = KW / 16;            // keys and 16-key blocks of a step
   static constexpr int STAGE = KW * (RK + RV);
   static constexpr int QBYTES = MT == 1 ? 0 : ROWS * DQK * 2;  // queries of 16 rows stay in registers
   // two CTAs per SM, if at least two stages fit
@@ -357,7 +364,7 @@ __device__ __forceinline__ float2 load_cluster2(uint32_t addr) {
 // TOGETHER: a cluster of CTAs per segment; otherwise equal parts of the list per warp.
 template <class C, bool TOGETHER>
 __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params p) {
-  constexpr int DQK = C::DQK, DV = C::DV, MT = C::MT, NB = C::NB;
+  constexpr int DQK = C::DQK, DV = C::DV, MT = C::MT, NB = C::NB, E = C::E;
   constexpr bool E4M3 = C::E4M3;
   extern __shared__ __align__(1024) char smem[];
   __shared__ int32_t s_scan[kWarps], s_before[kWarps], s_seq[kWarps];
@@ -465,12 +472,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
     const char *q_head = p.q + b * p.q_b + (int64_t)head * p.G * p.q_h;
     const float base_factor = (p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e) * (E4M3 ? __ldg(p.k_scale + head) : 1.f);
     uint32_t qa[MT == 1 ? DQK / 16 : 1][4];
-    float factor[MT][2], m[MT][2], l[MT][2], o[MT][DV / 8][4];
-    int32_t pos[MT][2];  // the row's position (rows past the last one see what the last query sees)
+    float factor[MT][E], m[MT][E], l[MT][E], o[MT][DV / 8][4];
+    int32_t pos[MT][E];  // the row's position (rows past the last one see what the last query sees)
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < E; ++e) {
         const int r = mt * 16 + quad + 8 * e;
         const int g = (row0 + r) / p.Lq, lq = (row0 + r) - g * p.Lq;
         factor[mt][e] = base_factor;
@@ -495,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
             }
             qa[kk][e] = x.x;
             qa[kk][2 + e] = x.y;
+            if (E == 1) qa[kk][1] = qa[kk][3] = 0;
           }
           if (E4M3) {
             uint32_t top = 0;  // exponent field of the largest element
@@ -533,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
+              for (int e = 0; e < E; ++e)
                 if (r >> 3 == 2 * mt + e) factor[mt][e] *= __uint_as_float(top << 23);
           }
         }
@@ -622,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll
         for (int j = 0; j < 2 * NB; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[mt][j][i] *= factor[mt][i >> 1];
+          for (int i = 0; i < 2 * E; ++i) s[mt][j][i] *= factor[mt][i >> 1];
       if (p.cap > 0.f) {
         const float cap = p.cap * kLog2e;
 #pragma unroll
@@ -630,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll
           for (int j = 0; j < 2 * NB; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[mt][j][i] = cap * tanh_of(s[mt][j][i]);
+            for (int i = 0; i < 2 * E; ++i) s[mt][j][i] = cap * tanh_of(s[mt][j][i]);
       }
       if (!whole) {
         const uint32_t reach = p.window < 0 ? 0x7fffffffu : (uint32_t)p.window;
@@ -639,18 +647,18 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll
           for (int j = 0; j < 2 * NB; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2 * E; ++i) {
               // (as unsigned, a key ahead of the query is out of reach too)
               const uint32_t behind = (uint32_t)(pos[mt][i >> 1] - (key0 + 8 * j + 2 * tq + (i & 1)));
               if (behind > reach) s[mt][j][i] = -INFINITY;
             }
       }
-      float top[MT][2];
+      float top[MT][E];
       bool move = false;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < E; ++e) {
           top[mt][e] = fmaxf(s[mt][0][2 * e], s[mt][0][2 * e + 1]);
 #pragma unroll
           for (int j = 1; j < 2 * NB; ++j) top[mt][e] = fmax3(top[mt][e], s[mt][j][2 * e], s[mt][j][2 * e + 1]);
@@ -660,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < E; ++e) {
             float high = fmaxf(top[mt][e], m[mt][e]);
             high = fmaxf(high, __shfl_xor_sync(~0u, high, 1));
             high = fmaxf(high, __shfl_xor_sync(~0u, high, 2));
@@ -671,16 +679,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
             for (int j = 0; j < DV / 8; ++j) {
               o[mt][j][2 * e] *= alpha;
               o[mt][j][2 * e + 1] *= alpha;
+              if (E == 1) o[mt][j][2] *= alpha, o[mt][j][3] *= alpha;
             }
           }
       }
 
-      // P (rounded to 16 bits for the product; its sum is taken before), O += P V
+      // P, O += P V.  The product takes P in 16 bits (its sum is taken before):
+      // fp16, 2^-12, for an e4m3 cache; bf16, 2^-9, as the forward's.  With
+      // eight rows the free half of the product takes the rest, P - bf16(P),
+      // and the result carries one bf16 rounding, its own.  (With more rows
+      // that would be a second product: measured 1 to 6 % slower.)
       uint32_t pa[MT][NB][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < E; ++e) {
           const float ref = m[mt][e] == -INFINITY ? 0.f : m[mt][e];
 #pragma unroll
           for (int j = 0; j < 2 * NB; ++j)
@@ -694,8 +707,16 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            pa[mt][nb][i] = pack2<E4M3>(s[mt][2 * nb + (i >> 1)][2 * (i & 1)], s[mt][2 * nb + (i >> 1)][2 * (i & 1) + 1]);
+          for (int i = 0; i < 4; ++i) {
+            const float *y = &s[mt][2 * nb + (i >> 1)][E == 1 ? 0 : 2 * (i & 1)];
+            if (E == 2 || (i & 1) == 0)
+              pa[mt][nb][i] = pack2<E4M3>(y[0], y[1]);
+            else if (E4M3)
+              pa[mt][nb][i] = 0;
+            else
+              pa[mt][nb][i] = pack_bf16x2(y[0] - __uint_as_float(pa[mt][nb][i - 1] << 16),
+                                          y[1] - __uint_as_float(pa[mt][nb][i - 1] & 0xffff0000u));
+          }
       }
       const int v_row = (lane & 7) + ((lane >> 3) & 1) * 8, v_chunk = lane >> 4;
 #pragma unroll
@@ -729,6 +750,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
       }
     }
 
+    if (E == 1) {
+#pragma unroll
+      for (int j = 0; j < DV / 8; ++j) o[0][j][0] += o[0][j][2], o[0][j][1] += o[0][j][3];
+    }
     if constexpr (TOGETHER) {
       copy_wait<0>();
       __syncwarp();
@@ -736,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < E; ++e) {
           const int r = mt * 16 + quad + 8 * e;
           float sum = l[mt][e];
           sum += __shfl_xor_sync(~0u, sum, 1);
@@ -792,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < E; ++e) {
         const int r = mt * 16 + quad + 8 * e;
         float sum = l[mt][e];
         sum += __shfl_xor_sync(~0u, sum, 1);
@@ -913,7 +938,7 @@ int64_t align16(int64_t x) { return (x + 15) & ~(int64_t)15; }
 
 // What the sizes of a call decide.
 struct Plan {
-  int row_tiles;        // 16 rows each, 1 or 2
+  int rows;             // of a tile: 8, 16 or 32
   int64_t most;         // steps that a sequence can have, from its row of pages and the window
   int64_t segments;
   int cluster;          // CTAs per segment, 0: the list
@@ -937,15 +962,15 @@ Plan plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t d
           int32_t type, int64_t window) {
   Plan x;
   const int64_t nrows = (int64_t)(Hq / Hkv) * Lq;
-  x.row_tiles = nrows <= 16 ? 1 : 2;
-  const int64_t kw = (dqk + dv) * (type == SPLASH_CACHE_E4M3 ? 1 : 2) >= 512 ? 16 : 32;  // (Config::KW)
+  x.rows = nrows <= 8 ? 8 : nrows <= 16 ? 16 : 32;
+  const int64_t kw = keys_per_step((dqk + dv) * (type == SPLASH_CACHE_E4M3 ? 1 : 2));
   x.most = ((int64_t)max_pages * page_size + kw - 1) / kw;
   if (window >= 0) x.most = std::min(x.most, window / kw + 4);
-  x.segments = (int64_t)B * Hkv * ((nrows + 16 * x.row_tiles - 1) / (16 * x.row_tiles));
+  x.segments = (int64_t)B * Hkv * ((nrows + x.rows - 1) / x.rows);
   x.cluster = x.segments <= kSlots ? 1 : 0;
   while (x.cluster > 0 && x.cluster < kMaxCluster && 2 * x.cluster * x.segments <= kSlots && x.cluster * kWarps < x.most) x.cluster *= 2;
   if (x.most * kw > (int64_t)kClusterKeys * x.cluster) x.cluster = 0;
-  const int64_t rows = std::min<int64_t>(nrows, 16 * x.row_tiles);
+  const int64_t rows = std::min<int64_t>(nrows, x.rows);
   x.workspace = x.cluster > 0 ? 0 : (size_t)(align16(4 * ((int64_t)B + 1)) + (int64_t)2 * kMaxWarps * rows * 4 * (dv + 2));
   return x;
 }
@@ -990,14 +1015,18 @@ splash_status launch(const Plan &x, void *workspace, Params p, cudaStream_t stre
   return SPLASH_OK;
 }
 
+template <int DQK, int DV, bool E4M3>
+splash_status pick_rows(const Plan &x, void *workspace, const Params &p, cudaStream_t stream) {
+  if (x.rows == 8) return launch<Config<DQK, DV, E4M3, 8>>(x, workspace, p, stream);
+  if (x.rows == 16) return launch<Config<DQK, DV, E4M3, 16>>(x, workspace, p, stream);
+  return launch<Config<DQK, DV, E4M3, 32>>(x, workspace, p, stream);
+}
+
 template <int DQK, int DV>
 splash_status pick(const splash_paged_decode_args &a, const Params &p, cudaStream_t stream) {
   const Plan x = plan(a.B, a.Hq, a.Hkv, a.Lq, a.dqk, a.dv, a.max_pages, a.page_size, a.cache_type, a.window_left);
-  if (a.cache_type == SPLASH_CACHE_E4M3)
-    return x.row_tiles == 1 ? launch<Config<DQK, DV, true, 1>>(x, a.workspace, p, stream)
-                            : launch<Config<DQK, DV, true, 2>>(x, a.workspace, p, stream);
-  return x.row_tiles == 1 ? launch<Config<DQK, DV, false, 1>>(x, a.workspace, p, stream)
-                          : launch<Config<DQK, DV, false, 2>>(x, a.workspace, p, stream);
+  return a.cache_type == SPLASH_CACHE_E4M3 ? pick_rows<DQK, DV, true>(x, a.workspace, p, stream)
+                                           : pick_rows<DQK, DV, false>(x, a.workspace, p, stream);
 }
 
 }  // namespace
