@@ -13,13 +13,15 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libsplash.so")
 # (source, object, defines): attention_fwd.cu is compiled once per pattern
-# mode, so that its kernel instantiations build in parallel
+# mode and paged_decode.cu once per cache type, so that their kernel
+# instantiations build in parallel
 SOURCES = [("api.cu", "api", []), ("mask_info.cu", "mask_info", []),
            ("attention_fwd.cu", "attention_fwd", ["-DSPLASH_FWD_PM=0"]),
            ("attention_fwd.cu", "attention_fwd_band", ["-DSPLASH_FWD_PM=1"]),
            ("attention_fwd.cu", "attention_fwd_band_seg", ["-DSPLASH_FWD_PM=2"]),
            ("attention_bwd.cu", "attention_bwd", []), ("host_pipeline.cu", "host_pipeline", []),
-           ("rope.cu", "rope", []), ("paged_decode.cu", "paged_decode", [])]
+           ("rope.cu", "rope", []), ("paged_decode.cu", "paged_decode_bf16", ["-DSPLASH_DECODE_E4M3=0"]),
+           ("paged_decode.cu", "paged_decode_e4m3", ["-DSPLASH_DECODE_E4M3=1"])]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

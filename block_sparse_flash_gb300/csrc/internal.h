@@ -162,6 +162,8 @@ splash_status splash_wait_selftest_launch(uint64_t timeout_ns, cudaStream_t stre
 splash_status splash_rope_launch(const splash_rope_args &a, cudaStream_t stream, uint32_t *err_word);
 splash_status splash_paged_append_launch(const splash_paged_append_args &a, cudaStream_t stream, uint32_t *err_word);
 splash_status splash_paged_decode_launch(const splash_paged_decode_args &a, cudaStream_t stream, uint32_t *err_word);
+splash_status splash_paged_decode_launch_bf16(const splash_paged_decode_args &a, cudaStream_t stream, uint32_t *err_word);
+splash_status splash_paged_decode_launch_e4m3(const splash_paged_decode_args &a, cudaStream_t stream, uint32_t *err_word);
 size_t splash_paged_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t dv,
                                            int32_t max_pages, int32_t page_size, int32_t type, int64_t window);
 

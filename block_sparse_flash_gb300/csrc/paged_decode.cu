@@ -1,5 +1,6 @@
 // paged_decode.cu -- attention of new tokens over a paged key/value cache
-// (splash_paged_decode in splash.h).
+// (splash_paged_decode in splash.h).  Compiled once for each cache type
+// (SPLASH_DECODE_E4M3 = 0, 1), so that the instantiations build in parallel.
 //
 // For a query row: s_j = scale q.k_j, m = max s_j, l = sum exp(s_j - m),
 // out = sum exp(s_j - m) v_j / l, lse = m + ln l, in one pass over the keys.
@@ -78,9 +79,10 @@ constexpr int keys_per_step(int bytes) { return bytes >= 512 ? 16 : 32; }
 // ROWS: query rows of a tile, 8, 16 or 32.  Eight rows (up to 8 query heads per
 // KV head, one new token) leave half of each 16-row product free: for a bf16
 // cache it takes what rounding P to bf16 loses, see below.
-template <int DQK_, int DV_, bool E4M3_, int ROWS_>
+template <int DQK_, int DV_, bool E4M3_, int ROWS_, bool MULTI_>
 struct Config {
   static constexpr int DQK = DQK_, DV = DV_, ROWS = ROWS_;
+  static constexpr bool MULTI = MULTI_;          // more than one query per sequence and head
   static constexpr int MT = ROWS <= 16 ? 1 : 2;  // products of 16 rows
   static constexpr int E = ROWS == 8 ? 1 : 2;    // halves of them that hold rows
   static constexpr bool E4M3 = E4M3_;
@@ -361,11 +363,73 @@ __device__ __forceinline__ float2 load_cluster2(uint32_t addr) {
   return x;
 }
 
+// The pairs of keys of a step that a query sees (2 tq, 2 tq + 1 and the same + 8
+// of each 16), as masks of the value's pairs, and which of a thread's rows are
+// that query's.
+template <class C>
+struct Seen {
+  uint32_t keys[C::NB][2];
+  bool row[C::MT][C::E];
+};
+
+template <class C, bool MASKED>
+__device__ __forceinline__ void add_product(float (&o)[4], const uint32_t (&pa)[4], uint32_t b0, uint32_t b1,
+                                            const bool (&row)[C::E]) {
+  if (!MASKED) {
+    mma<C::E4M3>(o, pa, b0, b1);
+  } else {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    mma<C::E4M3>(x, pa, b0, b1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (row[C::E == 1 ? 0 : i >> 1]) o[i] += x[i];
+  }
+}
+
+// O += P V for the step whose values are at vs; with MASKED only the rows and
+// keys of `seen`.
+template <class C, bool MASKED>
+__device__ __forceinline__ void add_values(float (&o)[C::MT][C::DV / 8][4], const uint32_t (&pa)[C::MT][C::NB][4], uint32_t vs,
+                                           int lane, const Seen<C> &seen) {
+  const int v_row = (lane & 7) + ((lane >> 3) & 1) * 8, v_chunk = lane >> 4;
+#pragma unroll
+  for (int nb = 0; nb < C::NB; ++nb) {
+    const uint32_t m0 = MASKED ? seen.keys[nb][0] : ~0u, m1 = MASKED ? seen.keys[nb][1] : ~0u;
+#pragma unroll
+    for (int j = 0; j < C::DV / 16; j += C::E4M3 ? 2 : 1) {
+      uint32_t vb[4];
+      ldsm4_trans(vb, vs + nb * 16 * C::RV + chunk_at<C::RV>(v_row, (C::E4M3 ? j : 2 * j) + v_chunk));
+      if (C::E4M3) {
+        // Each word holds two neighbouring columns of two keys: the even
+        // columns of 16 go to one product, the odd ones to the next.
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t b0, b1, c0, c1;
+          widen(__byte_perm(vb[2 * x], 0, 0x3120), b0, c0);
+          widen(__byte_perm(vb[2 * x + 1], 0, 0x3120), b1, c1);
+#pragma unroll
+          for (int mt = 0; mt < C::MT; ++mt) {
+            add_product<C, MASKED>(o[mt][2 * (j + (C::E4M3 ? x : 0))], pa[mt][nb], b0 & m0, b1 & m1, seen.row[mt]);
+            add_product<C, MASKED>(o[mt][2 * (j + (C::E4M3 ? x : 0)) + 1], pa[mt][nb], c0 & m0, c1 & m1, seen.row[mt]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int mt = 0; mt < C::MT; ++mt) {
+          add_product<C, MASKED>(o[mt][2 * j], pa[mt][nb], vb[0] & m0, vb[1] & m1, seen.row[mt]);
+          add_product<C, MASKED>(o[mt][2 * j + 1], pa[mt][nb], vb[2] & m0, vb[3] & m1, seen.row[mt]);
+        }
+      }
+    }
+  }
+}
+
 // TOGETHER: a cluster of CTAs per segment; otherwise equal parts of the list per warp.
 template <class C, bool TOGETHER>
 __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params p) {
   constexpr int DQK = C::DQK, DV = C::DV, MT = C::MT, NB = C::NB, E = C::E;
   constexpr bool E4M3 = C::E4M3;
+  const int Lq = C::MULTI ? p.Lq : 1;
   extern __shared__ __align__(1024) char smem[];
   __shared__ int32_t s_scan[kWarps], s_before[kWarps], s_seq[kWarps];
   __shared__ float2 s_ml[kWarps][C::ROWS], s_cta[C::ROWS];  // (maximum, sum) of the rows
@@ -479,9 +543,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int r = mt * 16 + quad + 8 * e;
-        const int g = (row0 + r) / p.Lq, lq = (row0 + r) - g * p.Lq;
+        const int g = (row0 + r) / Lq, lq = (row0 + r) - g * Lq;
         factor[mt][e] = base_factor;
-        pos[mt][e] = sp.n - p.Lq + (r < rows ? lq : p.Lq - 1);
+        pos[mt][e] = sp.n - Lq + (r < rows ? lq : Lq - 1);
         m[mt][e] = -INFINITY;
         l[mt][e] = 0.f;
         if (MT == 1) {
@@ -525,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll 4
       for (int r = 0; r < C::ROWS; ++r) {
         constexpr int W = DQK / 64;  // words (two elements) per lane
-        const int g = (row0 + r) / p.Lq, lq = (row0 + r) - g * p.Lq;
+        const int g = (row0 + r) / Lq, lq = (row0 + r) - g * Lq;
         uint32_t x[W];
 #pragma unroll
         for (int i = 0; i < W; ++i)
@@ -624,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
       }
 
       // scores in powers of two; masked where some row does not see some key
-      const bool whole = key0 + C::KW <= sp.n - p.Lq + 1 && (p.window < 0 || key0 >= sp.n - 1 - p.window);
+      const bool whole = key0 + C::KW <= sp.n - Lq + 1 && (p.window < 0 || key0 >= sp.n - 1 - p.window);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -685,10 +749,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
       }
 
       // P, O += P V.  The product takes P in 16 bits (its sum is taken before):
-      // fp16, 2^-12, for an e4m3 cache; bf16, 2^-9, as the forward's.  With
-      // eight rows the free half of the product takes the rest, P - bf16(P),
-      // and the result carries one bf16 rounding, its own.  (With more rows
-      // that would be a second product: measured 1 to 6 % slower.)
+      // fp16, 2^-11 of each p, for an e4m3 cache; bf16, 2^-8, as the forward's.
+      // With eight rows the free half of the product takes the rest, P -
+      // bf16(P), and the result carries one bf16 rounding, its own.  (With more
+      // rows that would be a second product: measured 1 to 6 % slower.)
       uint32_t pa[MT][NB][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -718,34 +782,29 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
                                           y[1] - __uint_as_float(pa[mt][nb][i - 1] & 0xffff0000u));
           }
       }
-      const int v_row = (lane & 7) + ((lane >> 3) & 1) * 8, v_chunk = lane >> 4;
+      if (!C::MULTI || whole) {
+        add_values<C, false>(o, pa, vs, lane, Seen<C>());
+      } else if constexpr (C::MULTI) {
+        // Some of the step's values are one query's and not another's: a
+        // product for each query, with zeros in the place of the values that
+        // it does not see, whatever they are (0 x infinity is not 0).
+#pragma unroll 1
+        for (int lq = 0; lq < Lq; ++lq) {
+          const int32_t last = sp.n - Lq + lq;
+          const uint32_t reach = p.window < 0 ? 0x7fffffffu : (uint32_t)p.window;
+          Seen<C> seen;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int j = 0; j < DV / 16; j += E4M3 ? 2 : 1) {
-          uint32_t vb[4];
-          ldsm4_trans(vb, vs + nb * 16 * C::RV + chunk_at<C::RV>(v_row, (E4M3 ? j : 2 * j) + v_chunk));
-          if (E4M3) {
-            // Each word holds two neighbouring columns of two keys: the even
-            // columns of 16 go to one product, the odd ones to the next.
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t b0, b1, c0, c1;
-              widen(__byte_perm(vb[2 * x], 0, 0x3120), b0, c0);
-              widen(__byte_perm(vb[2 * x + 1], 0, 0x3120), b1, c1);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma<true>(o[mt][2 * (j + (E4M3 ? x : 0))], pa[mt][nb], b0, b1);
-                mma<true>(o[mt][2 * (j + (E4M3 ? x : 0)) + 1], pa[mt][nb], c0, c1);
-              }
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t behind = (uint32_t)(last - (key0 + 16 * nb + 8 * i + 2 * tq));
+              seen.keys[nb][i] = (behind <= reach ? 0xffffu : 0u) | (behind - 1u <= reach ? 0xffff0000u : 0u);
             }
-          } else {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma<false>(o[mt][2 * j], pa[mt][nb], vb[0], vb[1]);
-              mma<false>(o[mt][2 * j + 1], pa[mt][nb], vb[2], vb[3]);
-            }
-          }
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < E; ++e) seen.row[mt][e] = pos[mt][e] == last;
+          add_values<C, true>(o, pa, vs, lane, seen);
         }
       }
     }
@@ -1015,29 +1074,41 @@ splash_status launch(const Plan &x, void *workspace, Params p, cudaStream_t stre
   return SPLASH_OK;
 }
 
-template <int DQK, int DV, bool E4M3>
-splash_status pick_rows(const Plan &x, void *workspace, const Params &p, cudaStream_t stream) {
-  if (x.rows == 8) return launch<Config<DQK, DV, E4M3, 8>>(x, workspace, p, stream);
-  if (x.rows == 16) return launch<Config<DQK, DV, E4M3, 16>>(x, workspace, p, stream);
-  return launch<Config<DQK, DV, E4M3, 32>>(x, workspace, p, stream);
+template <int DQK, int DV, int ROWS>
+splash_status pick_queries(const Plan &x, void *workspace, const Params &p, cudaStream_t stream) {
+  constexpr bool E4M3 = SPLASH_DECODE_E4M3 != 0;
+  return p.Lq == 1 ? launch<Config<DQK, DV, E4M3, ROWS, false>>(x, workspace, p, stream)
+                   : launch<Config<DQK, DV, E4M3, ROWS, true>>(x, workspace, p, stream);
 }
 
 template <int DQK, int DV>
 splash_status pick(const splash_paged_decode_args &a, const Params &p, cudaStream_t stream) {
   const Plan x = plan(a.B, a.Hq, a.Hkv, a.Lq, a.dqk, a.dv, a.max_pages, a.page_size, a.cache_type, a.window_left);
-  return a.cache_type == SPLASH_CACHE_E4M3 ? pick_rows<DQK, DV, true>(x, a.workspace, p, stream)
-                                           : pick_rows<DQK, DV, false>(x, a.workspace, p, stream);
+  if (x.rows == 8) return pick_queries<DQK, DV, 8>(x, a.workspace, p, stream);
+  if (x.rows == 16) return pick_queries<DQK, DV, 16>(x, a.workspace, p, stream);
+  return pick_queries<DQK, DV, 32>(x, a.workspace, p, stream);
 }
 
 }  // namespace
 }  // namespace splash
 
+#if !SPLASH_DECODE_E4M3
 size_t splash_paged_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t dv,
                                            int32_t max_pages, int32_t page_size, int32_t type, int64_t window) {
   return splash::plan(B, Hq, Hkv, Lq, dqk, dv, max_pages, page_size, type, window).workspace;
 }
 
 splash_status splash_paged_decode_launch(const splash_paged_decode_args &a, cudaStream_t stream, uint32_t *err_word) {
+  return a.cache_type == SPLASH_CACHE_E4M3 ? splash_paged_decode_launch_e4m3(a, stream, err_word)
+                                           : splash_paged_decode_launch_bf16(a, stream, err_word);
+}
+#endif
+
+#if SPLASH_DECODE_E4M3
+splash_status splash_paged_decode_launch_e4m3(const splash_paged_decode_args &a, cudaStream_t stream, uint32_t *err_word) {
+#else
+splash_status splash_paged_decode_launch_bf16(const splash_paged_decode_args &a, cudaStream_t stream, uint32_t *err_word) {
+#endif
   using namespace splash;
   const int64_t size = a.cache_type == SPLASH_CACHE_E4M3 ? 1 : 2;
   Params p = {};

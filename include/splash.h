@@ -535,7 +535,8 @@ splash_status splash_paged_append(const splash_paged_append_args *args, void *cu
  * This equals splash_attention_fwd over the gathered keys with the mask
  * causal from the sequence's end.  Cache rows that no query sees (past n, or
  * before the window) are not read, nor are the block table's entries for
- * them, so they may hold anything.
+ * them, so they may hold anything; rows that only some of the queries see do
+ * not reach the others, whatever they hold.
  *
  * A negative n counts as 0 and one above max_pages * page_size as that; a page
  * outside [0, num_pages) reads as keys and values of zero; each is reported.

@@ -48,7 +48,7 @@ def make(lens, Lq, Hq, Hkv, dqk, dv, page, kind="bf16", layout="heads", seed=0, 
         if kind == "e4m3":
             s = torch.linspace(0.01, 0.02, Hkv) * (1 + i)
             scales[i] = s.cuda()
-            x = x / s[:, None, None]
+            x = (x / s[:, None, None]).clamp(-448, 448)  # as append stores it (torch's conversion gives NaN beyond)
         x = x.masked_fill(~used[:, None, :, None], float("nan"))
         x = x.to(torch.float8_e4m3fn if kind == "e4m3" else torch.bfloat16).cuda()
         if layout == "tokens":
@@ -161,6 +161,36 @@ def test_rows_before_the_window_are_not_read(splash):
     got = splash.paged_decode(q, kc, vc, bt, lens, 0.1, window_left=window)
     splash.check_device_error()
     check(got, want)
+
+
+@pytest.mark.parametrize("long_rows", [False, True], ids=["short", "long"])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq, Lq, window", [(2, 4, -1), (8, 3, 70), (16, 5, 9), (2, 16, 16)])
+def test_values_that_only_some_queries_see(splash, kind, Hq, Lq, window, long_rows):
+    """Keys after a query, and keys before its window, do not reach it, NaN
+    and infinities among them; a query that sees one has it in its result."""
+    n, d = 150, 64
+    q, kc, vc, bt, lens, ks, vs = make([n, 40], Lq, Hq, 1, d, d, 16, kind, seed=85,
+                                       extra_cols=2600 if long_rows else 1)
+    want = bounds(q, kc, vc, bt, lens, 0.125, 0.0, window, ks, vs)
+    nan = torch.tensor(float("nan"), device="cuda").to(kc.dtype)
+    for b, total in enumerate((n, 40)):  # the newest key: the last query's alone
+        at = total - 1
+        kc[bt[b, at // 16], :, at % 16] = nan
+        vc[bt[b, at // 16], :, at % 16] = nan if kind == "e4m3" else float("-inf")
+        if window >= 0 and total - Lq - window >= 0:  # the earliest: the first query's alone
+            at = total - Lq - window
+            vc[bt[b, at // 16], :, at % 16] = nan
+    got = splash.paged_decode(q, kc, vc, bt, lens, 0.125, window_left=window, k_scale=ks, v_scale=vs)
+    splash.check_device_error()
+    o, l = got[0].double().cpu().numpy(), got[1].double().cpu().numpy()
+    for b, total in enumerate((n, 40)):
+        first = 1 if window >= 0 and total - Lq - window >= 0 else 0
+        clear = slice(first, Lq - 1)
+        assert (np.abs(o - want[0]) <= want[2])[b, :, clear].all() and (np.abs(l - want[1]) <= want[3])[b, :, clear].all()
+        assert np.isnan(o[b, :, Lq - 1]).all() and np.isnan(l[b, :, Lq - 1]).all()
+        if first:
+            assert np.isnan(o[b, :, 0]).all() and (np.abs(l - want[1]) <= want[3])[b, :, 0].all()
 
 
 def test_strided_queries_shared_pages_and_given_outputs(splash):
