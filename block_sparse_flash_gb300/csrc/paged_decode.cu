@@ -6,7 +6,11 @@
 // out = sum exp(s_j - m) v_j / l, lse = m + ln l, in one pass over the keys.
 // Every key and value is used by the Hq/Hkv * Lq rows of its head only, a few
 // FLOP per byte: reading the cache bounds the call, so the kernel is built to
-// keep the memory system full.
+// keep the memory system full.  64 requests of 64 .. 4096 tokens (32 query, 8 KV
+// heads of 128, bf16) take 90 us, 6.1 TB/s with the launches; 64 requests of up
+// to 32768 tokens with an e4m3 cache 316 us, 6.9 TB/s; DRAM reads are the
+// cache's bytes (546 MB of 546 for the first).  One request of 300 tokens takes
+// 4.7 us: the launch, three dependent reads (length, page, keys) and the join.
 //
 //  * Work.  The keys of each (sequence, KV head, group of rows) are cut into
 //    steps of KW keys; all steps form one list, and every warp of a grid that
@@ -21,7 +25,9 @@
 //    the workspace and the second kernel.
 //  * Loads.  Each warp keeps a ring of stages in shared memory, filled by
 //    16-byte asynchronous copies that run ahead of the products and across the
-//    borders of sequences; there is no barrier between warps.  Rows outside the
+//    borders of sequences; there is no barrier between warps.  Two CTAs of four
+//    warps with 2 or 3 stages of 8 KB per SM saturate DRAM; more in flight
+//    (prefetching into L2) measured slower.  Rows outside the
 //    keys that some query sees are filled with zeros instead of being read, so
 //    that whatever they hold cannot reach a product.
 //  * Products.  16 rows x 16 keys per tensor instruction (mma.sync: with 4 to 32
@@ -50,7 +56,7 @@ constexpr int kMaxWarps = 1216;  // of the grid; the workspace holds two parts f
 // A running maximum is only moved when a score passes it by more than this
 // (in powers of two): until then exp2(s - m) stays below 2^8, which neither
 // the sums (fp32) nor P's 16-bit types mind, and no shuffles or rescaling of
-// the output are needed.
+// the output are needed (4 tokens of 8 requests 32.6 us, against 33.4 without).
 constexpr float kSlack = 8.f;
 
 struct Params {
@@ -1007,14 +1013,14 @@ struct Plan {
 // Clusters or the list.  A cluster call has no scan and no second kernel, the
 // list loads every SM alike however the lengths differ.  Measured (32 query, 8
 // KV heads of 128, bf16; list -> clusters, us): 1 sequence of 64 keys
-// 5.6 -> 3.3, 2048 keys 12.4 -> 6.8, 16384 keys 20.6 -> 17.6; 8 sequences of
-// 2048 keys 14.3 -> 10.9, of 8192 keys 48.2 -> 43.4; 16 sequences through a
-// window of 4096 keys 48.8 -> 42.8; 8 sequences of 1023 .. 8191 keys 33.1 ->
-// 32.5.  A sequence much longer than the others keeps its clusters running
-// alone (2048 keys take a CTA 23 us), so the keys that a CTA may get are
-// limited: 2048, and the ends of a window of that size per CTA.
+// 5.4 -> 3.1, 2048 keys 12.3 -> 6.6, 16384 keys 19.6 -> 17.2; 8 sequences of
+// 2048 keys 13.9 -> 10.6, of 8192 keys 47.4 -> 42.9; 16 sequences through a
+// window of 4096 keys 48.0 -> 42.7; 8 sequences of 1023 .. 8191 keys, 4 tokens
+// each, 33.4 -> 32.6.  A sequence much longer than the others keeps its
+// clusters running alone (2048 keys take a CTA 23 us), so the keys that a CTA may
+// get are limited: 2048, and the ends of a window of that size per CTA.
 constexpr int kSlots = kMaxWarps / kWarps;  // CTAs that fill the GPU
-constexpr int kMaxCluster = 16;             // (8 without opting in: 16384 keys of 1 sequence 25.2 us)
+constexpr int kMaxCluster = 16;             // (with at most 8, 16384 keys of 1 sequence take 24.8 us)
 constexpr int kClusterKeys = 2304;          // per CTA, at most
 
 Plan plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t dv, int32_t max_pages, int32_t page_size,

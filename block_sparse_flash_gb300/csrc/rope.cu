@@ -4,7 +4,11 @@
 // A pair (a, b) at position p turns by the angle whose cosine c and sine s
 // are in the table: a' = a c - b s, b' = b c + a s; the transposed rotation
 // (the gradient) has -s.  Both are 2 multiplications and 1 addition per
-// element on data that is read once and written once, so HBM bounds them.
+// element on data that is read once and written once, so HBM bounds them:
+// q and k of 2 x 4096 tokens (32 + 8 heads of 128) take 27.5 us, 6.2 TB/s, the
+// gradient of 128 + 128 heads of 192 dimensions 117 us, 6.9 TB/s, a packed
+// prompt of 32768 tokens (16 + 8 + 8 heads, K and V to the cache) 98 us, 6.2 TB/s.
+// The next token of one request is a launch, 1.9 us.
 //
 // One thread takes 16 elements of a row as two 16-byte chunks: for rotated
 // dimensions the chunks that hold 8 whole pairs (8 a's and the 8 b's half a
@@ -269,11 +273,11 @@ splash_status launch_heads(const Params &p, bool interleaved, cudaStream_t strea
 template <bool APPEND, bool E4M3>
 splash_status launch(const Params &p, bool interleaved, cudaStream_t stream) {
   // Four rows per thread where that still gives every SM 1024 threads (152 x
-  // 1024): dense q and k of 2 x 4096 tokens 28.5 us against 29.5 with one row,
-  // 128 heads of 192 dimensions 120 against 130 (fewer reads of the rotations
-  // per row); 257 tokens of 4 heads 3.1 against 2.2 us (blocks of 256 threads).
-  // Appending always takes one: a prompt of 32768 tokens 103 us against 106,
-  // the next token of 256 requests 3.4 against 5.7.
+  // 1024): q and k of 2 x 4096 tokens 27.8 us against 28.3 with one row, 128
+  // heads of 192 dimensions 117.6 against 129 (fewer reads of the rotations per
+  // row); 257 tokens of 4 heads 2.2 against 1.7 us.  Appending always takes
+  // one: a prompt of 32768 tokens 99.2 us against 98.0 with four, the next token
+  // of 256 requests 3.0 against 5.1.
   if constexpr (!APPEND) {
     if ((int64_t)p.tokens * p.units * ((p.heads + 3) / 4) >= 152 * 1024)
       return launch_heads<APPEND, E4M3, 4>(p, interleaved, stream);
