@@ -440,8 +440,9 @@ _CACHE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
 # A serving step's kernels take a few microseconds, the time of some twenty
 # attribute reads here: the checks below read each attribute once, and the
 # current device and stream come as plain numbers.
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _stream_and_device(stream, first):
@@ -532,29 +533,40 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="
     return torch.cat((a.cos(), a.sin()), 1).float()
 
 
+def _out4(name, out, like, shape, dev, stream):
+    """(tensor, its view): the given output, or a new dense one."""
+    if out is not None:
+        return out, _view4(name, out, shape, dev)
+    if stream is None and like.is_contiguous():
+        out = torch.empty_like(like)
+    else:
+        out = _new(shape, _BF16, like.device, stream)
+    L, d = shape[2], shape[3]
+    return out, (out.data_ptr(), shape[1] * L * d, L * d, d)
+
+
 def _rope(what, inverse, q, k, positions, table, rot_offset, interleaved, q_out, k_out, stream):
     s, dev = _stream_and_device(stream, q)
     shape = q.shape
-    if len(shape) != 4 or (k is not None and k.dim() != 4):
-        raise ValueError("q and k must be 4-D")
+    if len(shape) != 4:
+        raise ValueError("q must be 4-D")
     B, Hq, L, d = shape
     qv = _view4("q", q, shape, dev)
-    kv = ko = _NO_VIEW
-    Hkv = 0
-    if q_out is None:
-        q_out = _new(shape, _BF16, q.device, stream)
+    tp, rows, rot = _table2(table, dev)
+    pos, pos_stride = _index2("positions", positions, B, L, dev)
     if k is not None:
         kshape = k.shape
+        if len(kshape) != 4:
+            raise ValueError("k must be 4-D")
         Hkv = kshape[1]
         kv = _view4("k", k, (B, Hkv, L, d), dev)
-        if k_out is None:
-            k_out = _new(kshape, _BF16, q.device, stream)
-        ko = _view4("k_out", k_out, kshape, dev)
+        k_out, ko = _out4("k_out", k_out, k, kshape, dev, stream)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    tp, rows, rot = _table2(table, dev)
-    args = _ROPE_ARGS.pack(_ROPE_ARGS.size, *qv, *_view4("q_out", q_out, shape, dev), *kv, *ko,
-                           *_index2("positions", positions, B, L, dev), tp, rows, L, B, Hq, Hkv, d, rot,
+    else:
+        Hkv, kv, ko = 0, _NO_VIEW, _NO_VIEW
+    q_out, qo = _out4("q_out", q_out, q, shape, dev, stream)
+    args = _ROPE_ARGS.pack(_ROPE_ARGS.size, *qv, *qo, *kv, *ko, pos, pos_stride, tp, rows, L, B, Hq, Hkv, d, rot,
                            int(rot_offset), int(bool(interleaved)), inverse)
     _check(lib().splash_rope(args, s), what)
     return q_out, k_out
@@ -608,9 +620,7 @@ def paged_append(k, v, k_cache, v_cache, block_table, positions, q=None, table=N
             raise ValueError("q must be 4-D")
         Hq = qshape[1]
         qv = _view4("q", q, (B, Hq, L, dqk), dev)
-        if q_out is None:
-            q_out = _new(qshape, _BF16, k.device, stream)
-        qo = _view4("q_out", q_out, qshape, dev)
+        q_out, qo = _out4("q_out", q_out, q, qshape, dev, stream)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if k_out is not None:

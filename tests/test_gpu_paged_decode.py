@@ -1,7 +1,8 @@
 """paged_decode on the GPU against the float64 reference.
 
 Bounds.  With A = sum_j p_j |v_j| and u the rounding of the probabilities to
-the tensor cores' input type (bf16: 2^-8, e4m3 caches use fp16: 2^-11, and its
+the tensor cores' input type (bf16: 2^-8, or 2^-16 with up to 8 rows per KV head,
+whose remainder is rounded a second time; e4m3 caches use fp16: 2^-11, and its
 smallest step 2^-25 on each of n keys):
   |out - exact| <= (u + 2 e) A + 2^-8 |exact| + n 2^-25 max|v|
   |lse - exact| <= e + 2^-20 + 2^-22 |exact|
@@ -63,7 +64,8 @@ def bounds(q, kc, vc, bt, lens, scale, cap=0.0, window=-1, ks=None, vs=None):
     out, lse, A, reach = ref.decode(n(q), n(kc), n(vc), bt.cpu().numpy(), lens.cpu().numpy(), scale, cap, window,
                                     n(ks), n(vs))
     e = (q.shape[3] + 8) * 2.0 ** -23 * reach + (cap * 2.0 ** -20 if cap > 0 else 0)
-    u = 2.0 ** -8 if ks is None else 2.0 ** -11
+    rows = q.shape[1] // kc.shape[1] * q.shape[2]
+    u = 2.0 ** -11 if ks is not None else 2.0 ** -16 if rows <= 8 else 2.0 ** -8
     vmax = np.nanmax(np.abs(n(vc))) * (1 if vs is None else n(vs).max())
     small = 0 if ks is None else int(lens.max()) * 2.0 ** -25 * vmax
     return out, lse, (u + 2 * e[..., None]) * A + 2.0 ** -8 * np.abs(out) + small, \
@@ -120,6 +122,19 @@ def test_decode_matches_the_reference(splash, case, long_rows):
     check(got, bounds(q, kc, vc, bt, n, scale, cap, window, ks, vs))
     again = splash.paged_decode(q, kc, vc, bt, n, scale, softcap=cap, window_left=window, k_scale=ks, v_scale=vs)
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("long_rows", [False, True], ids=["short", "long"])
+@pytest.mark.parametrize("Lq", [1, 2])
+@pytest.mark.parametrize("rows", [6, 14, 22, 40])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dqk, dv", [(64, 64), (128, 128), (192, 128)])
+def test_every_tile_of_rows(splash, dqk, dv, kind, rows, Lq, long_rows):
+    q, kc, vc, bt, n, ks, vs = make([77, 150, 3], Lq, 2 * rows // Lq, 2, dqk, dv, 32, kind, seed=rows + dqk,
+                                    extra_cols=1300 if long_rows else 0)
+    got = splash.paged_decode(q, kc, vc, bt, n, dqk ** -0.5, k_scale=ks, v_scale=vs)
+    splash.check_device_error()
+    check(got, bounds(q, kc, vc, bt, n, dqk ** -0.5, 0.0, -1, ks, vs))
 
 
 @pytest.mark.parametrize("B", [1, 130, 300, 700])
