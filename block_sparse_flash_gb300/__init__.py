@@ -1,8 +1,9 @@
 """block_sparse_flash_gb300 -- Python binding of libsplash.so, the sm_103a
 block-sparse (Splash) masked attention forward library.
 
-This module only marshals arguments: torch tensors become device pointers,
-the current torch stream becomes the cudaStream_t.  Every step of the
+This module only marshals arguments, through ctypes and for the serving calls
+through a compiled module (csrc/binding.cpp): torch tensors become device
+pointers, the current torch stream becomes the cudaStream_t.  Every step of the
 computation runs in the library's CUDA kernels (rope_table, a constant laid
 out once, is the exception); there is no CPU or PyTorch fallback.  If the library has not been built, importing works but every call
 raises SplashLibraryMissing.
@@ -19,8 +20,8 @@ C ABI: include/splash.h.
 """
 import ctypes
 import functools
+import importlib.util
 import os
-import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -92,9 +93,6 @@ def lib():
     L.splash_mask_info_set_pattern_source.argtypes = [vp, i32]
     L.splash_attention_fwd_host.argtypes = [vp, vp, vp, i32, i32, i32, i64, i64, i32, i32, vp, vp, vp, f32, f32,
                                             vp, vp, vp, vp, vp, vp, vp, vp]
-    for f in (L.splash_rope, L.splash_paged_append, L.splash_paged_decode):
-        f.argtypes = [ctypes.c_char_p, vp]  # the argument struct as packed bytes
-        f.restype = ctypes.c_int
     L.splash_paged_decode_workspace_size.argtypes = [i32] * 9 + [i64, P(ctypes.c_size_t)]
     L.splash_paged_decode_workspace_size.restype = ctypes.c_int
     L.splash_attention_merge.argtypes = [vp, vp, i32, i64, i32, vp, vp, vp]
@@ -428,99 +426,45 @@ def shard_views(q, k, v, begin: int, end: int, out=None, lse=None, segment_ids=N
 
 # ---- serving: rotary positions, paged append, paged decode
 
-# The argument structs of splash.h as packed bytes (native layout: the first
-# member is the size that the library compares with its own).
-_ROPE_ARGS = struct.Struct("@Q" + "Pqqq" * 4 + "PqPqq" + "8i")
-_APPEND_ARGS = struct.Struct("@Q" + "Pqqq" * 5 + "Pqqq" * 2 + "PPPqPqPqPqqq" + "12i")
-_DECODE_ARGS = struct.Struct("@Q" + "Pqqq" * 3 + "PPPqPPPPQqq" + "9i2fi")
-_NO_VIEW = (0, 0, 0, 0)
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _CACHE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
-
-# A serving step's kernels take a few microseconds, the time of some twenty
-# attribute reads here: the checks below read each attribute once, and the
-# current device and stream come as plain numbers.
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_binding = None
 
 
-def _stream_and_device(stream, first):
-    """(cudaStream_t, device index); the tensors must be on the current device."""
-    dev = first.get_device()
-    if dev < 0 or dev != _current_device():
-        raise ValueError(f"the tensors must be on the current CUDA device (got {first.device})")
-    if stream is None:
-        return _current_stream(dev), dev
-    return (stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)), dev
+def _native():
+    """The compiled part of the binding (csrc/binding.cpp): the serving calls,
+    whose kernels take a few microseconds, as long as reading their tensors'
+    attributes from Python would.  Raises SplashLibraryMissing."""
+    global _binding
+    if _binding is None:
+        from .build import binding_path
+        lib()
+        path = binding_path()
+        if not os.path.exists(path):
+            raise SplashLibraryMissing(
+                f"{path} is missing: build it with block_sparse_flash_gb300.build.build() "
+                "(there is no fallback implementation)")
+        spec = importlib.util.spec_from_file_location("_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_error(SplashError)
+        _binding = module
+    return _binding
+
+
+def _handle(stream) -> int:
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _new(shape, dtype, device, stream):
     """A tensor for a call on `stream`: taken from that stream's memory, so
     that nothing another stream still uses is overwritten, and kept until the
     current stream's later work is done with it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
     current = torch.cuda.current_stream()
     with torch.cuda.stream(s):
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(current)
     return t
-
-
-def _view4(name, t, shape, dev):
-    """(pointer, strides) of a bf16 [B, H, L, d] tensor with contiguous d."""
-    s = t.stride()
-    if t.dtype is not _BF16 or t.shape != shape or s[3] != 1 or t.get_device() != dev:
-        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on the current device, contiguous in its last dimension")
-    return t.data_ptr(), s[0], s[1], s[2]
-
-
-def _index2(name, t, B, L, dev):
-    """(pointer, batch stride) of an int32 [B, L] or [L] tensor."""
-    shape, s = t.shape, t.stride()
-    if t.dtype is not _I32 or t.get_device() != dev or not (shape == (B, L) or shape == (L,)) or (L > 1 and s[-1] != 1):
-        raise ValueError(f"{name} must be an int32 tensor of shape [{B}, {L}] or [{L}] on the current device, contiguous in its last dimension")
-    return t.data_ptr(), s[0] if len(s) == 2 else 0
-
-
-def _table2(t, dev):
-    """(pointer, rows, rot_dim) of a table made like rope_table's."""
-    if t.dtype is not _F32 or t.get_device() != dev or t.dim() != 2 or not t.is_contiguous():
-        raise ValueError("table must be a contiguous fp32 tensor [positions, rot_dim] on the current device")
-    shape = t.shape
-    return t.data_ptr(), shape[0], shape[1]
-
-
-def _cache4(k, v, k_scale, v_scale, dev):
-    """The cache's part of the argument structs, and its sizes: (k view,
-    v view, k_scale, v_scale pointers, type, pages, Hkv, page_size, dqk, dv)."""
-    dtype, shape, vshape, ks, vs = k.dtype, k.shape, v.shape, k.stride(), v.stride()
-    kind = _CACHE_TYPES.get(dtype)
-    if kind is None or v.dtype is not dtype or len(shape) != 4 or len(vshape) != 4 or shape[:3] != vshape[:3] \
-            or ks[3] != 1 or vs[3] != 1 or k.get_device() != dev or v.get_device() != dev:
-        raise ValueError("k_cache and v_cache must be bf16 or float8_e4m3fn tensors [pages, Hkv, page_size, d] on the "
-                         "current device, contiguous in the last dimension and alike in the others")
-    pages, Hkv, page, dqk = shape
-    kp = vp = 0
-    if kind == 1:
-        for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if x is None or x.dtype is not _F32 or x.get_device() != dev or x.shape != (Hkv,) or not x.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous fp32 tensor of shape [{Hkv}] for an e4m3 cache")
-        kp, vp = k_scale.data_ptr(), v_scale.data_ptr()
-    elif k_scale is not None or v_scale is not None:
-        raise ValueError("k_scale and v_scale belong to an e4m3 cache")
-    return ((k.data_ptr(), ks[0], ks[1], ks[2]), (v.data_ptr(), vs[0], vs[1], vs[2]), kp, vp, kind, pages, Hkv, page,
-            dqk, vshape[3])
-
-
-def _block_table(t, dev):
-    """(pointer, row stride, rows, columns)."""
-    shape, s = t.shape, t.stride()
-    if t.dtype is not _I32 or t.get_device() != dev or len(shape) != 2 or (shape[1] > 1 and s[1] != 1):
-        raise ValueError("block_table must be an int32 tensor [sequences, pages] on the current device, contiguous in its last dimension")
-    return t.data_ptr(), s[0], shape[0], shape[1]
 
 
 def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
@@ -533,43 +477,14 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="
     return torch.cat((a.cos(), a.sin()), 1).float()
 
 
-def _out4(name, out, like, shape, dev, stream):
-    """(tensor, its view): the given output, or a new dense one."""
-    if out is not None:
-        return out, _view4(name, out, shape, dev)
-    if stream is None and like.is_contiguous():
-        out = torch.empty_like(like)
-    else:
-        out = _new(shape, _BF16, like.device, stream)
-    L, d = shape[2], shape[3]
-    return out, (out.data_ptr(), shape[1] * L * d, L * d, d)
-
-
-def _rope(what, inverse, q, k, positions, table, rot_offset, interleaved, q_out, k_out, stream):
-    s, dev = _stream_and_device(stream, q)
-    shape = q.shape
-    if len(shape) != 4:
-        raise ValueError("q must be 4-D")
-    B, Hq, L, d = shape
-    qv = _view4("q", q, shape, dev)
-    tp, rows, rot = _table2(table, dev)
-    pos, pos_stride = _index2("positions", positions, B, L, dev)
-    if k is not None:
-        kshape = k.shape
-        if len(kshape) != 4:
-            raise ValueError("k must be 4-D")
-        Hkv = kshape[1]
-        kv = _view4("k", k, (B, Hkv, L, d), dev)
-        k_out, ko = _out4("k_out", k_out, k, kshape, dev, stream)
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    else:
-        Hkv, kv, ko = 0, _NO_VIEW, _NO_VIEW
-    q_out, qo = _out4("q_out", q_out, q, shape, dev, stream)
-    args = _ROPE_ARGS.pack(_ROPE_ARGS.size, *qv, *qo, *kv, *ko, pos, pos_stride, tp, rows, L, B, Hq, Hkv, d, rot,
-                           int(rot_offset), int(bool(interleaved)), inverse)
-    _check(lib().splash_rope(args, s), what)
-    return q_out, k_out
+def _rope(inverse, q, k, positions, table, rot_offset, interleaved, q_out, k_out, stream):
+    if stream is not None:
+        if q_out is None:
+            q_out = _new(q.shape, torch.bfloat16, q.device, stream)
+        if k is not None and k_out is None:
+            k_out = _new(k.shape, torch.bfloat16, q.device, stream)
+        stream = _handle(stream)
+    return (_binding or _native()).rope(q, k, positions, table, rot_offset, interleaved, inverse, q_out, k_out, stream)
 
 
 def rope_fwd(q, k, positions, table, rot_offset: int = 0, interleaved: bool = False, q_out=None, k_out=None,
@@ -580,14 +495,14 @@ def rope_fwd(q, k, positions, table, rot_offset: int = 0, interleaved: bool = Fa
     rotated dimensions start at rot_offset, pairs are half a rotation apart or
     adjacent (interleaved).  Returns (q_out, k_out), dense unless given;
     q_out=q rotates in place (splash_rope)."""
-    return _rope("splash_rope", 0, q, k, positions, table, rot_offset, interleaved, q_out, k_out, stream)
+    return _rope(0, q, k, positions, table, rot_offset, interleaved, q_out, k_out, stream)
 
 
 def rope_bwd(dq, dk, positions, table, rot_offset: int = 0, interleaved: bool = False, dq_out=None, dk_out=None,
              stream=None):
     """The gradients of rope_fwd's inputs from those of its outputs (the
     transposed rotation); arguments as rope_fwd."""
-    return _rope("splash_rope (inverse)", 1, dq, dk, positions, table, rot_offset, interleaved, dq_out, dk_out, stream)
+    return _rope(1, dq, dk, positions, table, rot_offset, interleaved, dq_out, dk_out, stream)
 
 
 def paged_append(k, v, k_cache, v_cache, block_table, positions, q=None, table=None, rot_offset: int = 0,
@@ -604,35 +519,12 @@ def paged_append(k, v, k_cache, v_cache, block_table, positions, q=None, table=N
     (nothing is stored); seq_ids is the row of block_table (default: b).
     q [B, Hq, L, dqk] is rotated into q_out (allocated if not given); k_out
     receives the rotated keys when given (for attention_fwd of a prompt)."""
-    s, dev = _stream_and_device(stream, k)
-    kc, vc, ksp, vsp, kind, pages, Hkv, page, dqk, dv = _cache4(k_cache, v_cache, k_scale, v_scale, dev)
-    shape = k.shape
-    if len(shape) != 4 or v.dim() != 4:
-        raise ValueError("k and v must be 4-D")
-    B, L = shape[0], shape[2]
-    kv = _view4("k", k, (B, Hkv, L, dqk), dev)
-    vv = _view4("v", v, (B, Hkv, L, dv), dev)
-    qv = qo = ko = _NO_VIEW
-    Hq = 0
-    if q is not None:
-        qshape = q.shape
-        if len(qshape) != 4:
-            raise ValueError("q must be 4-D")
-        Hq = qshape[1]
-        qv = _view4("q", q, (B, Hq, L, dqk), dev)
-        q_out, qo = _out4("q_out", q_out, q, qshape, dev, stream)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    if k_out is not None:
-        ko = _view4("k_out", k_out, shape, dev)
-    tp, rows, rot = _table2(table, dev) if table is not None else (0, 0, 0)
-    bt, bt_stride, num_seqs, max_pages = _block_table(block_table, dev)
-    ids = _index2("seq_ids", seq_ids, B, L, dev) if seq_ids is not None else (0, 0)
-    args = _APPEND_ARGS.pack(_APPEND_ARGS.size, *qv, *qo, *kv, *ko, *vv, *kc, *vc, ksp, vsp, bt, bt_stride,
-                             *_index2("positions", positions, B, L, dev), *ids, tp, rows, L, pages, B, Hq, Hkv, dqk,
-                             dv, num_seqs, max_pages, page, kind, rot, int(rot_offset), int(bool(interleaved)))
-    _check(lib().splash_paged_append(args, s), "splash_paged_append")
-    return q_out, k_out
+    if stream is not None:
+        if q is not None and q_out is None:
+            q_out = _new(q.shape, torch.bfloat16, k.device, stream)
+        stream = _handle(stream)
+    return (_binding or _native()).paged_append(k, v, k_cache, v_cache, block_table, positions, q, table, rot_offset,
+                                                interleaved, seq_ids, k_scale, v_scale, q_out, k_out, stream)
 
 
 def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float, softcap: float = 0.0,
@@ -645,42 +537,18 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float, softc
     block_table [B, max_pages] as for paged_append.  workspace: optional uint8
     device tensor of at least paged_decode_workspace_size(...) bytes, not
     shared by calls that may overlap."""
-    s, dev = _stream_and_device(stream, q)
-    kc, vc, ksp, vsp, kind, pages, Hkv, page, dqk, dv = _cache4(k_cache, v_cache, k_scale, v_scale, dev)
-    shape = q.shape
-    if len(shape) != 4:
-        raise ValueError("q must be 4-D")
-    B, Hq, Lq, _ = shape
-    qv = _view4("q", q, (B, Hq, Lq, dqk), dev)
-    bt, bt_stride, num_seqs, max_pages = _block_table(block_table, dev)
-    if num_seqs != B:
-        raise ValueError(f"block_table has {num_seqs} rows for a batch of {B}")
-    if seq_lens.dtype is not _I32 or seq_lens.shape != (B,) or seq_lens.get_device() != dev or not seq_lens.is_contiguous():
-        raise ValueError(f"seq_lens must be a contiguous int32 tensor of shape [{B}] on the current device")
-    device = q.device
-    if out is None:
-        out = _new((B, Hq, Lq, dv), _BF16, device, stream)
-    elif out.dtype is not _BF16 or out.shape != (B, Hq, Lq, dv) or not out.is_contiguous() or out.get_device() != dev:
-        raise ValueError(f"out must be a contiguous bf16 tensor of shape {(B, Hq, Lq, dv)} on the current device")
-    if lse is None:
-        lse = _new((B, Hq, Lq), _F32, device, stream)
-    elif lse.dtype is not _F32 or lse.shape != (B, Hq, Lq) or not lse.is_contiguous() or lse.get_device() != dev:
-        raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(B, Hq, Lq)} on the current device")
-    ws = 0
-    if workspace is None:
-        room = _paged_decode_workspace_size(B, Hq, Hkv, Lq, dqk, dv, max_pages, page, kind, int(window_left))
-        if room:
-            workspace = _new(room, torch.uint8, device, stream)
-            ws = workspace.data_ptr()
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the current device")
-    else:
-        room, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
-    args = _DECODE_ARGS.pack(_DECODE_ARGS.size, *qv, *kc, *vc, ksp, vsp, bt, bt_stride, seq_lens.data_ptr(),
-                             out.data_ptr(), lse.data_ptr(), ws, room, pages, int(window_left), B,
-                             Hq, Hkv, Lq, dqk, dv, max_pages, page, kind, float(scale), float(softcap), 0)
-    _check(lib().splash_paged_decode(args, s), "splash_paged_decode")
-    return out, lse
+    if stream is not None:
+        shape = q.shape[:3]
+        if out is None:
+            out = _new((*shape, v_cache.shape[3]), torch.bfloat16, q.device, stream)
+        if lse is None:
+            lse = _new(shape, torch.float32, q.device, stream)
+        if workspace is None:
+            room = paged_decode_workspace_size(q, k_cache, v_cache, block_table, window_left)
+            workspace = _new(room, torch.uint8, q.device, stream) if room else None
+        stream = _handle(stream)
+    return (_binding or _native()).paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, softcap,
+                                                window_left, k_scale, v_scale, out, lse, workspace, stream)
 
 
 @functools.lru_cache(maxsize=256)

@@ -1,9 +1,11 @@
 """Builds libsplash.so in-tree (block_sparse_flash_gb300/_build/) with nvcc for
-sm_103a.  Translation units are compiled in parallel and linked into one
-shared library; nothing is installed outside the repository."""
+sm_103a, and the compiled part of the Python binding with g++.  Translation
+units are compiled in parallel and linked into one shared library; nothing is
+installed outside the repository."""
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +25,15 @@ SOURCES = [("api.cu", "api", []), ("mask_info.cu", "mask_info", []),
            ("rope.cu", "rope", []), ("paged_decode.cu", "paged_decode_bf16", ["-DSPLASH_DECODE_E4M3=0"]),
            ("paged_decode.cu", "paged_decode_e4m3", ["-DSPLASH_DECODE_E4M3=1"])]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+# the compiled part of the Python binding, for this Python and this torch
+BINDING_SOURCE = "binding.cpp"
+
+
+def binding_path() -> str:
+    import torch
+    return os.path.join(OUT_DIR, f"_binding.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.so")
+
+
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
 
@@ -37,10 +48,41 @@ def _newest_input():
     return max(os.path.getmtime(f) for f in files)
 
 
+def _torch_root():
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding() -> str:
+    import torch
+    root, obj = _torch_root(), os.path.join(OUT_DIR, "binding.o")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+          "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+          "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+          "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj], f"g++ failed for {BINDING_SOURCE}")
+    return obj
+
+
+def _link_binding(obj: str, path: str) -> None:
+    libs, tmp = os.path.join(_torch_root(), "lib"), path + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-lsplash", "-L", libs, "-ltorch_python", "-ltorch",
+          "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"], "link of the binding failed")
+    os.replace(tmp, path)
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Compiles (if stale) and returns the path of libsplash.so."""
     os.makedirs(OUT_DIR, exist_ok=True)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
+    binding = binding_path()
+    if not force and all(os.path.exists(x) and os.path.getmtime(x) >= _newest_input() for x in (LIB, binding)):
         return LIB
     nvcc = _nvcc()
 
@@ -55,7 +97,8 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding_obj = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
@@ -63,6 +106,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj.result(), binding)
     return LIB
 
 

@@ -105,16 +105,14 @@ def refused(splash, name, make, changes):
 INVALID, SHAPE, UNSUPPORTED, CUDA = 1, 2, 3, 4
 
 
-def test_struct_layouts_agree(splash):
-    assert splash._ROPE_ARGS.size == ctypes.sizeof(RopeArgs)
-    assert splash._APPEND_ARGS.size == ctypes.sizeof(AppendArgs)
-    assert splash._DECODE_ARGS.size == ctypes.sizeof(DecodeArgs)
-    # the library compares struct_bytes with its own sizeof: valid arguments
-    # get past every check and fail only at the missing device
-    if not torch.cuda.is_available():
-        for name, make in (("splash_rope", rope_args), ("splash_paged_append", append_args),
-                           ("splash_paged_decode", decode_args)):
-            assert call(splash, name, make()) == CUDA
+def test_valid_arguments_reach_the_device(splash):
+    """The library compares struct_bytes with its own sizeof: valid arguments
+    get past every check and fail only at the missing device."""
+    if torch.cuda.is_available():
+        pytest.skip("a device is present")
+    for name, make in (("splash_rope", rope_args), ("splash_paged_append", append_args),
+                       ("splash_paged_decode", decode_args)):
+        assert call(splash, name, make()) == CUDA
 
 
 def test_null_arguments(splash):
@@ -209,47 +207,93 @@ def test_decode_workspace_size(splash):
     assert splash.lib().splash_paged_decode_workspace_size(4, 32, 8, 1, 128, 128, 8192, 16, 0, -1, None) == INVALID
 
 
-def test_the_binding_refuses_cpu_tensors(splash):
-    q = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
-    pos = torch.zeros(1, 4, dtype=torch.int32)
-    t = torch.zeros(4, 64)
-    cache = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
-    bt = torch.zeros(1, 1, dtype=torch.int32)
-    for f in (lambda: splash.rope_fwd(q, q, pos, t), lambda: splash.rope_bwd(q, None, pos, t),
-              lambda: splash.paged_append(q, q, cache, cache, bt, pos),
-              lambda: splash.paged_decode(q, cache, cache, bt, pos[:, 0], 0.1)):
-        with pytest.raises(ValueError, match="current CUDA device"):
-            f()
+def bf16(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
 
 
-def test_the_binding_refuses_wrong_types_and_shapes(splash):
-    bf, dev = torch.bfloat16, -1  # CPU tensors report device -1: the checks behind the device check
-    x = torch.zeros(2, 3, 4, 64, dtype=bf)
-    assert splash._view4("x", x, x.shape, dev)[1:] == (768, 256, 64)
-    for bad in (x.float(), x[..., ::2], x.transpose(2, 3)):
-        with pytest.raises(ValueError):
-            splash._view4("x", bad, bad.shape, dev)
+def i32(*shape):
+    return torch.zeros(*shape, dtype=torch.int32)
+
+
+def rope_call():
+    return dict(q=bf16(2, 4, 8, 64), k=bf16(2, 2, 8, 64), positions=i32(2, 8), table=torch.zeros(8, 64))
+
+
+def append_call():
+    return dict(k=bf16(2, 2, 8, 64), v=bf16(2, 2, 8, 64), k_cache=bf16(5, 2, 16, 64), v_cache=bf16(5, 2, 16, 64),
+                block_table=i32(2, 3), positions=i32(2, 8), q=bf16(2, 4, 8, 64), table=torch.zeros(8, 64))
+
+
+def decode_call():
+    return dict(q=bf16(2, 4, 1, 64), k_cache=bf16(5, 2, 16, 64), v_cache=bf16(5, 2, 16, 64), block_table=i32(2, 3),
+                seq_lens=i32(2), scale=0.125)
+
+
+def e4m3(call):
+    x = call()
+    x.update({n: x[n].to(torch.float8_e4m3fn) for n in ("k_cache", "v_cache")})
+    x.update(k_scale=torch.ones(2), v_scale=torch.ones(2))
+    return x
+
+
+BAD_TOKENS = [("q", bf16(2, 4, 8, 64).float()), ("q", bf16(2, 4, 8, 128)[..., ::2]), ("q", bf16(2, 4, 64)),
+              ("k", bf16(2, 2, 9, 64)), ("k", bf16(2, 2, 64)), ("k", bf16(2, 2, 8, 64).half()),
+              ("positions", i32(2, 8).long()), ("positions", i32(2, 7)), ("positions", i32(3, 8)),
+              ("positions", i32(8, 2).t()), ("positions", i32(2, 16)[:, ::2]), ("positions", i32(1)),
+              ("table", torch.zeros(8, 64).double()), ("table", torch.zeros(64, 8).t()), ("table", torch.zeros(64)),
+              ("q_out", bf16(2, 4, 8, 32)), ("k_out", bf16(2, 4, 8, 64)), ("positions", None)]
+BAD_CACHE = [("k_cache", bf16(5, 2, 16, 64).half()), ("k_cache", bf16(4, 2, 16, 64)), ("v_cache", bf16(5, 2, 16)),
+             ("v_cache", bf16(5, 2, 16, 128)[..., ::2]), ("v_cache", bf16(5, 2, 16, 64).to(torch.float8_e4m3fn)),
+             ("k_scale", torch.ones(2)), ("block_table", i32(2, 3).long()), ("block_table", i32(3)),
+             ("block_table", i32(3, 2).t()), ("block_table", [0])]
+BAD_SCALES = [("k_scale", None), ("v_scale", torch.ones(3)), ("k_scale", torch.ones(2).double()),
+              ("v_scale", torch.ones(4)[::2])]
+BINDING = [
+    ("rope_fwd", rope_call, BAD_TOKENS),
+    ("paged_append", append_call, BAD_TOKENS + BAD_CACHE + [("v", bf16(2, 2, 8, 32)), ("seq_ids", i32(2, 9))]),
+    ("paged_append", lambda: e4m3(append_call), BAD_SCALES),
+    ("paged_decode", decode_call, BAD_CACHE + [
+        ("q", bf16(2, 4, 1, 128)), ("q", bf16(2, 4, 64)), ("block_table", i32(3, 3)), ("seq_lens", i32(3)),
+        ("seq_lens", i32(2).long()), ("seq_lens", i32(4)[::2]), ("out", bf16(2, 4, 1, 32)),
+        ("out", bf16(2, 4, 1, 64).float()), ("lse", torch.zeros(2, 4)), ("lse", bf16(2, 4, 1)),
+        ("workspace", torch.zeros(64, 2, dtype=torch.uint8)[:, 0])]),
+    ("paged_decode", lambda: e4m3(decode_call), BAD_SCALES),
+]
+
+
+@pytest.mark.parametrize("name, make, bad", BINDING, ids=[f"{i}-{x[0]}" for i, x in enumerate(BINDING)])
+def test_the_binding_refuses_wrong_tensors(splash, name, make, bad):
+    f = getattr(splash, name)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        f(**make())  # CPU tensors: all else is right
+    for member, value in bad:
+        x = make()
+        x[member] = value
+        with pytest.raises(ValueError) as e:
+            f(**x)
+        assert "current CUDA device" not in str(e.value), (member, str(e.value))
+
+
+def test_the_binding_refuses_outputs_without_inputs(splash):
+    x = rope_call()
+    with pytest.raises(ValueError, match="k_out without k"):
+        splash.rope_bwd(x["q"], None, x["positions"], x["table"], dk_out=x["k"])
+    x = append_call()
+    q = x.pop("q")
+    with pytest.raises(ValueError, match="q_out without q"):
+        splash.paged_append(**x, q_out=q)
+    with pytest.raises(TypeError):
+        splash.paged_decode(**{**decode_call(), "scale": "large"})
     with pytest.raises(ValueError):
-        splash._view4("x", x, (2, 3, 5, 64), dev)
-    pos = torch.zeros(2, 4, dtype=torch.int32)
-    assert splash._index2("p", pos, 2, 4, dev)[1] == 4 and splash._index2("p", pos[0], 2, 4, dev)[1] == 0
-    for bad in (pos.long(), pos[:, :3], pos[:1], pos.t(), torch.zeros(2, 8, dtype=torch.int32)[:, ::2]):
-        with pytest.raises(ValueError):
-            splash._index2("p", bad, 2, 4, dev)
-    k = torch.zeros(3, 2, 16, 64, dtype=bf)
-    assert splash._cache4(k, k, None, None, dev)[4:] == (0, 3, 2, 16, 64, 64)
-    k8, s = k.to(torch.float8_e4m3fn), torch.ones(2)
-    assert splash._cache4(k8, k8, s, s, dev)[4] == 1
-    for args in ((k8, k8, None, s), (k8, k8, s, torch.ones(3)), (k8, k8, s, s.double()), (k, k, s, s), (k, k8, s, s),
-                 (k.half(), k.half(), None, None), (k, k[:2], None, None), (k[..., ::2], k, None, None)):
-        with pytest.raises(ValueError):
-            splash._cache4(*args, dev)
-    for bad in (torch.zeros(4), torch.zeros(4, 8).t(), torch.zeros(4, 8).double()):
-        with pytest.raises(ValueError):
-            splash._table2(bad, dev)
-    for bad in (pos.long(), pos[0], pos.t()):
-        with pytest.raises(ValueError):
-            splash._block_table(bad, dev)
+        splash.rope_fwd(**rope_call(), rot_offset=1 << 40)
+
+
+def test_the_binding_fails_loudly_when_it_is_missing(splash, monkeypatch):
+    from block_sparse_flash_gb300 import build
+    monkeypatch.setattr(splash, "_binding", None)
+    monkeypatch.setattr(build, "binding_path", lambda: "/nonexistent/_binding.so")
+    with pytest.raises(splash.SplashLibraryMissing):
+        splash.rope_fwd(**rope_call())
 
 
 def test_rope_table():
