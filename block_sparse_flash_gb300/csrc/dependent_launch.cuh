@@ -10,7 +10,10 @@ namespace splash {
 
 // First statement of such a kernel, before it reads or writes any memory:
 // waits until everything before it in the stream has completed, and lets the
-// next kernel's blocks be placed (they wait here in turn).
+// next kernel's blocks be placed (they wait here in turn).  What follows reads
+// global memory with ordinary loads: the kernel before may have written it
+// while this one was already resident, so that it is not constant for this
+// kernel's lifetime (ld.global.nc may be moved above the wait).
 __device__ __forceinline__ void grid_dependency() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

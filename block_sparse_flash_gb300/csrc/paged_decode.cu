@@ -112,7 +112,7 @@ struct Span {
 };
 
 __device__ __forceinline__ void check_length(const Params &p, int b) {
-  const int32_t n = __ldg(p.seq_lens + b);
+  const int32_t n = p.seq_lens[b];
   if (n < 0 || n > (int64_t)p.max_pages << p.page_shift) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
 }
 
@@ -120,7 +120,7 @@ template <int KW>
 __device__ __forceinline__ Span span_of(const Params &p, int b) {
   Span s;
   const int64_t most = (int64_t)p.max_pages << p.page_shift;
-  const int32_t n = __ldg(p.seq_lens + b);
+  const int32_t n = p.seq_lens[b];
   s.n = n < 0 ? 0 : n > most ? (int32_t)most : n;
   s.lo = p.window < 0 ? 0 : max(0, s.n - p.Lq - p.window);
   s.step0 = s.lo / KW;
@@ -259,7 +259,7 @@ struct Loader {
 #pragma unroll
     for (int i = 0; i < C::NB; ++i) {
       const int32_t key = (at.s.step0 + at.step) * C::KW + 16 * i;
-      entry[i] = key < at.s.n && key + 16 > at.s.lo ? __ldg(pages + (key >> p.page_shift)) : 0;
+      entry[i] = key < at.s.n && key + 16 > at.s.lo ? pages[key >> p.page_shift] : 0;
     }
   }
 
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
     const Span sp = at.s;
     const int b = at.b;
     const char *q_head = p.q + b * p.q_b + (int64_t)head * p.G * p.q_h;
-    const float base_factor = (p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e) * (E4M3 ? __ldg(p.k_scale + head) : 1.f);
+    const float base_factor = (p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e) * (E4M3 ? p.k_scale[head] : 1.f);
     uint32_t qa[MT == 1 ? DQK / 16 : 1][4];
     float factor[MT][E], m[MT][E], l[MT][E], o[MT][DV / 8][4];
     int32_t pos[MT][E];  // the row's position (rows past the last one see what the last query sees)
@@ -564,10 +564,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
             uint2 x = make_uint2(0, 0);
             if (r < rows) {
               if (E4M3) {
-                x = __ldg(reinterpret_cast<const uint2 *>(src) + 4 * kk + tq);
+                x = reinterpret_cast<const uint2 *>(src)[4 * kk + tq];
               } else {
-                x.x = __ldg(reinterpret_cast<const uint32_t *>(src) + 8 * kk + tq);
-                x.y = __ldg(reinterpret_cast<const uint32_t *>(src) + 8 * kk + tq + 4);
+                x.x = reinterpret_cast<const uint32_t *>(src)[8 * kk + tq];
+                x.y = reinterpret_cast<const uint32_t *>(src)[8 * kk + tq + 4];
               }
             }
             qa[kk][e] = x.x;
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
         uint32_t x[W];
 #pragma unroll
         for (int i = 0; i < W; ++i)
-          x[i] = r < rows ? __ldg(reinterpret_cast<const uint32_t *>(q_head + (int64_t)g * p.q_h + lq * p.q_l) + i * 32 + lane) : 0;
+          x[i] = r < rows ? reinterpret_cast<const uint32_t *>(q_head + (int64_t)g * p.q_h + lq * p.q_l)[i * 32 + lane] : 0;
         if (E4M3) {
           uint32_t top = 0;
 #pragma unroll
@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
         cluster_sync();
       else
         __syncthreads();
-      const float v_scale = E4M3 ? __ldg(p.v_scale + head) : 1.f;
+      const float v_scale = E4M3 ? p.v_scale[head] : 1.f;
       for (int i = cluster_rank() * kThreads + threadIdx.x; i < rows * LANES; i += ctas * kThreads) {
         const int r = i / LANES, c = 4 * (i % LANES);
         const uint32_t ml = smem_u32(&s_cta[r]), from = smem_u32(smem) + 4 * (r * C::ODIM + c);
@@ -878,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 
     // ---- finished rows, or this warp's part of them
     const bool complete = from_start && change;
-    const float v_scale = E4M3 ? __ldg(p.v_scale + head) : 1.f;
+    const float v_scale = E4M3 ? p.v_scale[head] : 1.f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -985,7 +985,7 @@ __global__ void __launch_bounds__(kThreads) paged_decode_join_kernel(const Param
     f[w] = ex2_approx(s_top[w] - (top == -INFINITY ? 0.f : top));
     sum += f[w] * s_sum[w];
   }
-  const float v_scale = p.v_scale != nullptr ? __ldg(p.v_scale + head) : 1.f;
+  const float v_scale = p.v_scale != nullptr ? p.v_scale[head] : 1.f;
   const float inv = sum == 0.f ? 0.f : v_scale / sum;
   if ((int)threadIdx.x < DV / 2) {
     float x = 0.f, y = 0.f;

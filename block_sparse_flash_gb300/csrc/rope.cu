@@ -105,9 +105,9 @@ struct Turn {
 
 __device__ __forceinline__ void load_turn(const Params &p, int64_t position, int pair, Turn &t) {
   const float *row = p.table + position * p.rot + pair;
-  const float4 c0 = __ldg(reinterpret_cast<const float4 *>(row)), c1 = __ldg(reinterpret_cast<const float4 *>(row + 4));
+  const float4 c0 = reinterpret_cast<const float4 *>(row)[0], c1 = reinterpret_cast<const float4 *>(row)[1];
   const float *srow = row + p.rot / 2;
-  const float4 s0 = __ldg(reinterpret_cast<const float4 *>(srow)), s1 = __ldg(reinterpret_cast<const float4 *>(srow + 4));
+  const float4 s0 = reinterpret_cast<const float4 *>(srow)[0], s1 = reinterpret_cast<const float4 *>(srow)[1];
   const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
   const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
@@ -170,9 +170,12 @@ __global__ void __launch_bounds__(128) rope_kernel(const Params p) {
   const int h0 = blockIdx.y * HEADS;
   const Chunks c = chunks_of<INTERLEAVED>(p, u), cv = {16 * u, 16 * u + 8, -1};
   Data x[HEADS];
+  float scale[HEADS];
 #pragma unroll
   for (int i = 0; i < HEADS; ++i) {
     const int h = h0 + i;
+    if (APPEND && E4M3 && h >= p.Hq && h < p.heads)
+      scale[i] = h < p.Hq + p.Hkv ? p.k_scale[h - p.Hq] : p.v_scale[h - p.Hq - p.Hkv];
     if (h < p.Hq + p.Hkv) {
       const View &in = h < p.Hq ? p.q : p.k;
       if (u < p.units_qk) x[i] = load(in.ptr + b * in.b + (h < p.Hq ? h : h - p.Hq) * in.h + l * in.l, c);
@@ -180,16 +183,16 @@ __global__ void __launch_bounds__(128) rope_kernel(const Params p) {
       x[i] = load(p.v.ptr + b * p.v.b + (h - p.Hq - p.Hkv) * p.v.h + l * p.v.l, cv);
     }
   }
-  const int64_t pos = __ldg(p.positions + b * p.positions_stride + l);
+  const int64_t pos = p.positions[b * p.positions_stride + l];
   bool bad = false;
   bool rotate = p.table != nullptr && pos >= 0;
   if (rotate && pos >= p.table_rows) rotate = false, bad = true;
   int64_t page = -1;
   if (APPEND && pos >= 0) {
-    const int64_t seq = p.seq_ids != nullptr ? __ldg(p.seq_ids + b * p.seq_ids_stride + l) : b;
+    const int64_t seq = p.seq_ids != nullptr ? p.seq_ids[b * p.seq_ids_stride + l] : b;
     const int64_t col = pos >> p.page_shift;
     if (seq >= 0 && seq < p.num_seqs && col < p.max_pages && !bad) {
-      page = __ldg(p.block_table + seq * p.block_table_stride + col);
+      page = p.block_table[seq * p.block_table_stride + col];
       if (page < 0 || page >= p.num_pages) page = -1;
     }
     bad = bad || page < 0;
@@ -227,9 +230,8 @@ __global__ void __launch_bounds__(128) rope_kernel(const Params p) {
       if (APPEND && !is_q && page >= 0) {
         char *row = p.kc.ptr + page * p.kc.page + hh * p.kc.head + slot * p.kc.token;
         if (E4M3) {
-          const float sc = __ldg(p.k_scale + hh);
-          *reinterpret_cast<uint2 *>(row + c.c0) = to_e4m3(y0, sc);
-          *reinterpret_cast<uint2 *>(row + c.c1) = to_e4m3(y1, sc);
+          *reinterpret_cast<uint2 *>(row + c.c0) = to_e4m3(y0, scale[i]);
+          *reinterpret_cast<uint2 *>(row + c.c1) = to_e4m3(y1, scale[i]);
         } else {
           *reinterpret_cast<uint4 *>(row + 2 * c.c0) = o0;
           *reinterpret_cast<uint4 *>(row + 2 * c.c1) = o1;
@@ -242,8 +244,7 @@ __global__ void __launch_bounds__(128) rope_kernel(const Params p) {
         float y0[8], y1[8];
         unpack(x[i].x0, y0);
         unpack(x[i].x1, y1);
-        const float sc = __ldg(p.v_scale + hh);
-        const uint2 e0 = to_e4m3(y0, sc), e1 = to_e4m3(y1, sc);
+        const uint2 e0 = to_e4m3(y0, scale[i]), e1 = to_e4m3(y1, scale[i]);
         *reinterpret_cast<uint4 *>(row + 16 * u) = make_uint4(e0.x, e0.y, e1.x, e1.y);
       } else {
         *reinterpret_cast<uint4 *>(row + 2 * cv.c0) = x[i].x0;
