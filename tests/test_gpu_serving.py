@@ -150,6 +150,42 @@ def test_a_captured_step_replays_with_growing_lengths(splash, per):
     assert splash.last_device_error() == 0
 
 
+def test_two_captured_steps_replayed_at_once(splash):
+    """Two graphs, each with a cache and a workspace of its own, replayed on two
+    streams at the same time: both paths of the decode, bit for bit."""
+    table = splash.rope_table(256, 128)
+    runs = []
+    for i, per in enumerate((12, 2600, 2600)):
+        tok, kc, vc, bt, lens = decode_state(per=per, seed=500 + 10 * i)
+        runs.append([tok, kc, vc, bt, lens, torch.empty_like(tok[0]), torch.empty_like(tok[0]),
+                     torch.empty(3, 8, 1, device="cuda"), torch.cuda.CUDAGraph(), torch.cuda.Stream()])
+    def one(r):
+        splash.paged_append(r[0][1], r[0][2], r[1], r[2], r[3], r[4][:, None], q=r[0][0], table=table, q_out=r[5])
+        r[4] += 1
+        splash.paged_decode(r[5], r[1], r[2], r[3], r[4], 0.1, out=r[6], lse=r[7])  # (its own workspace)
+    want = []
+    for r in runs:
+        keep = [x.clone() for x in (r[1], r[2], r[4])]
+        for _ in range(5):
+            one(r)
+        want.append([r[i].clone() for i in (1, 2, 4, 6, 7)])
+        for x, y in zip((r[1], r[2], r[4]), keep):
+            x.copy_(y)
+    torch.cuda.synchronize()
+    for r in runs:
+        with torch.cuda.graph(r[8]):
+            one(r)
+    for _ in range(5):
+        for r in runs:
+            with torch.cuda.stream(r[9]):
+                r[8].replay()
+    torch.cuda.synchronize()
+    for r, w in zip(runs, want):
+        for i, x in zip((1, 2, 4, 6, 7), w):
+            assert torch.equal(r[i], x)
+    assert splash.last_device_error() == 0
+
+
 def test_calls_on_another_stream_and_two_at_once(splash):
     tok, kc, vc, bt, lens = decode_state(per=2600)
     table = splash.rope_table(256, 128)
