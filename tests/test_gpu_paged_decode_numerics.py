@@ -1,0 +1,72 @@
+"""paged_decode on the GPU where the numbers are far from ordinary: soft caps
+of any size.  References in float64; the bounds are derived at each test."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import workloads
+from oracle import serving_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def splash():
+    from block_sparse_flash_gb300 import build as b
+    b.build()
+    import block_sparse_flash_gb300 as m
+    return m
+
+
+def make(lens, Lq, Hq, Hkv, dqk, dv, page, kind="bf16", cols=0, seed=0):
+    """Caches, a shuffled block table of at least `cols` columns, queries."""
+    g = torch.Generator().manual_seed(seed)
+    need = [-(-n // page) for n in lens]
+    order = torch.randperm(sum(need), generator=g).tolist()
+    bt = torch.full((len(lens), max(need + [cols, 1])), -1, dtype=torch.int32)
+    for b, m in enumerate(need):
+        for c in range(m):
+            bt[b, c] = order.pop()
+    caches, scales = [], [None, None]
+    for i, d in enumerate((dqk, dv)):
+        x = workloads.normal_bf16((max(1, sum(need)), Hkv, page, d), seed + 1 + i).float()
+        if kind == "e4m3":
+            s = torch.linspace(0.01, 0.02, Hkv) * (1 + i)
+            scales[i] = s.cuda()
+            x = (x / s[:, None, None]).clamp(-448, 448)
+        caches.append(x.to(torch.float8_e4m3fn if kind == "e4m3" else torch.bfloat16).cuda())
+    q = workloads.normal_bf16((len(lens), Hq, Lq, dqk), seed + 3).cuda()
+    return q, caches[0], caches[1], bt.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), scales[0], scales[1]
+
+
+def reference(x, scale, cap=0.0, window=-1):
+    q, kc, vc, bt, lens, ks, vs = (None if t is None else t.cpu() for t in x)
+    n = lambda t: None if t is None else t.double().numpy()  # noqa: E731
+    return ref.decode(n(q), n(kc), n(vc), bt.numpy(), lens.numpy(), scale, cap, window, n(ks), n(vs))
+
+
+@pytest.mark.parametrize("kind, Lq, Hq, Hkv, dqk, dv, cols", [
+    ("bf16", 1, 4, 2, 64, 64, 0), ("bf16", 1, 4, 2, 128, 128, 2600), ("bf16", 3, 10, 2, 128, 128, 0),
+    ("bf16", 2, 24, 2, 192, 128, 2600), ("e4m3", 1, 4, 2, 64, 64, 2600), ("e4m3", 4, 8, 2, 192, 128, 0),
+    ("e4m3", 2, 24, 2, 128, 128, 0)])
+@pytest.mark.parametrize("cap", [3.0, 50.0, 1e3, 1e4, 1e6])
+def test_soft_caps_of_any_size(splash, cap, kind, Lq, Hq, Hkv, dqk, dv, cols):
+    """The cap's own error is relative to the score, however large the cap.
+    For |t| <= 1/4 the fit of tanh(t)/t is off by 4.8e-7 and four fp32
+    operations by 4 * 2^-24; above it 1 - 2 / (1 + e^2t) is off by at most
+    3e-7, which is 2^-19.6 of tanh(1/4): 2^-19 |s| bounds both.  The scores
+    before it: dqk products summed in fp32, (dqk + 8) 2^-23 of the sum of their
+    absolute values (`reach`), which bounds |s| too."""
+    x = make([300, 41], Lq, Hq, Hkv, dqk, dv, 16, kind, cols, seed=500)
+    scale = 2 / math.sqrt(dqk)
+    out, lse, A, reach = reference(x, scale, cap)
+    got = splash.paged_decode(*x[:5], scale, softcap=cap, k_scale=x[5], v_scale=x[6])
+    splash.check_device_error()
+    o, l = got[0].double().cpu().numpy(), got[1].double().cpu().numpy()
+    e = ((dqk + 8) * 2.0 ** -23 + 2.0 ** -19) * reach
+    assert (np.abs(l - lse) <= e + 2.0 ** -20 + 2.0 ** -22 * np.abs(lse)).all(), np.abs(l - lse).max()
+    rows = Hq // Hkv * Lq
+    u = 2.0 ** -11 if kind == "e4m3" else 2.0 ** -16 if rows <= 8 else 2.0 ** -8
+    assert (np.abs(o - out) <= (u + 2 * e[..., None]) * A + 2.0 ** -8 * np.abs(out) + 300 * 2.0 ** -25 * 12).all()
