@@ -60,6 +60,14 @@ constexpr int kMaxWarps = 1216;  // of the grid; the workspace holds two parts f
 // the output are needed (4 tokens of 8 requests 32.6 us, against 33.4 without).
 constexpr float kSlack = 8.f;
 
+// For an e4m3 cache the reference is this much below the maximum, so that
+// probabilities use fp16 from the top: 2^7 for the largest key, below 2^15 with
+// the slack (fp16 ends at 65504).  At the bottom fp16 steps by 2^-24, which is
+// 2^-31 of the largest key: what is dropped below half of that stays under the
+// output's own rounding (2^-9) up to 2^23 keys in one warp, where a reference
+// at the maximum itself stopped at 2^16.  bf16 has fp32's range.
+constexpr float kBelowTop = 7.f;
+
 struct Params {
   const char *q;
   int64_t q_b, q_h, q_l;  // byte strides
@@ -757,6 +765,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
           top[mt][e] = fmaxf(s[mt][0][2 * e], s[mt][0][2 * e + 1]);
 #pragma unroll
           for (int j = 1; j < 2 * NB; ++j) top[mt][e] = fmax3(top[mt][e], s[mt][j][2 * e], s[mt][j][2 * e + 1]);
+          if (E4M3) top[mt][e] -= kBelowTop;
           move |= top[mt][e] > m[mt][e] + kSlack;
         }
       if (__any_sync(~0u, move)) {

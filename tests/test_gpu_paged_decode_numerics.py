@@ -1,5 +1,5 @@
 """paged_decode on the GPU where the numbers are far from ordinary: soft caps
-of any size.  References in float64; the bounds are derived at each test."""
+of any size, one key far above very many.  References in float64; the bounds are derived at each test."""
 import math
 
 import numpy as np
@@ -70,3 +70,39 @@ def test_soft_caps_of_any_size(splash, cap, kind, Lq, Hq, Hkv, dqk, dv, cols):
     rows = Hq // Hkv * Lq
     u = 2.0 ** -11 if kind == "e4m3" else 2.0 ** -16 if rows <= 8 else 2.0 ** -8
     assert (np.abs(o - out) <= (u + 2 * e[..., None]) * A + 2.0 ** -8 * np.abs(out) + 300 * 2.0 ** -25 * 12).all()
+
+
+@pytest.mark.parametrize("Hq", [1, 12, 24])
+def test_one_key_far_above_very_many(splash, Hq):
+    """One key 2^26 times as probable as each of the 2^17 - 1 others of an e4m3
+    cache, all in the same warp (as many sequences as the GPU has warps, all on
+    the same pages): together the others carry 2^-9 of the result, and it is
+    they that have a value.
+
+    Probabilities are fp16 in the second product: 2^-11 of each, and at the
+    bottom of its range half a step of 2^-32 of the largest key's, on each of
+    n keys.  The scores are exact but for the rounding of ln 2 (2^-24 of 26).
+    What remains are the fp32 sums of n terms, n 2^-24 of their value."""
+    n, d, page = 1 << 17, 64, 1024
+    B = 4 * 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    k = torch.zeros(n // page, 1, page, d)
+    k[0, 0, 5, 0] = 26.0
+    v = torch.zeros_like(k)
+    v[..., 1] = 1.0
+    v[..., 2] = torch.tensor([1.0, -0.5]).repeat(n // 2).view(-1, 1, page)
+    v[0, 0, 5] = 0.0
+    x = [t.to(torch.float8_e4m3fn).cuda() for t in (k, v)]
+    q = torch.zeros(B, Hq, 1, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    bt = torch.arange(n // page, dtype=torch.int32, device="cuda").expand(B, -1)
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    one = torch.ones(1, device="cuda")
+    out, lse = splash.paged_decode(q, x[0], x[1], bt, lens, math.log(2.0), k_scale=one, v_scale=one)
+    splash.check_device_error()
+    z = 1 + (n - 1) * 2.0 ** -26
+    exact = torch.zeros(d, dtype=torch.float64)
+    exact[1] = (n - 1) * 2.0 ** -26 / z
+    exact[2] = (n / 2 * 0.5 - (-0.5 if 5 % 2 else 1.0)) * 2.0 ** -26 / z
+    room = (2.0 ** -11 + 2.0 ** -8 + n * 2.0 ** -24 + 2.0 ** -18) * exact[1] + n * 2.0 ** -32
+    assert (out.double().cpu() - exact).abs().max().item() <= room
+    assert (lse.double().cpu() - (26 * math.log(2.0) + math.log(z))).abs().max().item() <= n * 2.0 ** -24 + 2.0 ** -18
