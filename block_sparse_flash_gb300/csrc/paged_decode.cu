@@ -64,7 +64,7 @@ constexpr float kSlack = 8.f;
 // probabilities use fp16 from the top: 2^7 for the largest key, below 2^15 with
 // the slack (fp16 ends at 65504).  At the bottom fp16 steps by 2^-24, which is
 // 2^-31 of the largest key: what is dropped below half of that stays under the
-// output's own rounding (2^-9) up to 2^23 keys in one warp, where a reference
+// output's own rounding (2^-8) up to 2^23 keys in one warp, where a reference
 // at the maximum itself stopped at 2^16.  bf16 has fp32's range.
 constexpr float kBelowTop = 7.f;
 
@@ -231,6 +231,15 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+// Two positive numbers cut off to bf16, and what that leaves of them.
+__device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+__device__ __forceinline__ float rest_of(float x) {
+  return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xffff0000u), __uint_as_float(0x00800000u));
+}
+__device__ __forceinline__ uint32_t rest_bf16x2(float lo, float hi) { return pack_bf16x2(rest_of(lo), rest_of(hi)); }
 
 // The larger exponent field of a word's two bf16 values, and the word as fp16
 // values over 2^(top - 127).
@@ -792,7 +801,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
       // fp16, 2^-11 of each p, for an e4m3 cache; bf16, 2^-8, as the forward's.
       // With eight rows the free half of the product takes the rest, P -
       // bf16(P), and the result carries one bf16 rounding, its own.  (With more
-      // rows that would be a second product: measured 1 to 6 % slower.)
+      // rows that would be a second product: measured 1 to 6 % slower.)  There
+      // bf16(P) is P cut off and the rest is kept above 0: an infinite value
+      // times either part then has its sign, and their sum is that infinity
+      // (0 x infinity and infinity - infinity are NaN).  The rest's floor, the
+      // smallest normal number, adds less than 2^-126 of a value.
       uint32_t pa[MT][NB][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -813,13 +826,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float *y = &s[mt][2 * nb + (i >> 1)][E == 1 ? 0 : 2 * (i & 1)];
-            if (E == 2 || (i & 1) == 0)
+            if (E == 1 && !E4M3) {
+              pa[mt][nb][i] = (i & 1) == 0 ? cut_bf16x2(y[0], y[1]) : rest_bf16x2(y[0], y[1]);
+            } else if (E == 2 || (i & 1) == 0) {
               pa[mt][nb][i] = pack2<E4M3>(y[0], y[1]);
-            else if (E4M3)
+            } else {
               pa[mt][nb][i] = 0;
-            else
-              pa[mt][nb][i] = pack_bf16x2(y[0] - __uint_as_float(pa[mt][nb][i - 1] << 16),
-                                          y[1] - __uint_as_float(pa[mt][nb][i - 1] & 0xffff0000u));
+            }
           }
       }
       if (!C::MULTI || whole) {

@@ -1,5 +1,6 @@
 """paged_decode on the GPU where the numbers are far from ordinary: soft caps
-of any size, one key far above very many.  References in float64; the bounds are derived at each test."""
+of any size, one key far above very many, infinite values.  References in
+float64; the bounds are derived at each test."""
 import math
 
 import numpy as np
@@ -106,3 +107,56 @@ def test_one_key_far_above_very_many(splash, Hq):
     room = (2.0 ** -11 + 2.0 ** -8 + n * 2.0 ** -24 + 2.0 ** -18) * exact[1] + n * 2.0 ** -32
     assert (out.double().cpu() - exact).abs().max().item() <= room
     assert (lse.double().cpu() - (26 * math.log(2.0) + math.log(z))).abs().max().item() <= n * 2.0 ** -24 + 2.0 ** -18
+
+
+@pytest.mark.filterwarnings("ignore:invalid value encountered")  # (the reference's infinity - infinity)
+@pytest.mark.parametrize("cols", [0, 2600], ids=["short", "long"])
+@pytest.mark.parametrize("Hq, Lq", [(1, 1), (8, 1), (2, 3), (4, 4), (12, 2), (40, 1)])
+def test_infinite_values_reach_the_result_as_they_are(splash, Hq, Lq, cols):
+    """An infinite value of a finite key: its column of every query that sees
+    it is that infinity (every probability is positive), the others are as
+    without it; both infinities in one column give NaN."""
+    n, d = 150, 64
+    x = make([n, 70], Lq, Hq, 1, d, d, 16, cols=cols, seed=600)
+    q, kc, vc, bt, lens = x[:5]
+    inf = float("inf")
+
+    def put(j, col, value):
+        for b in range(2):
+            vc[bt[b, j // 16], 0, j % 16, col] = value
+    plain = reference(x, 0.125)
+    clean = splash.paged_decode(q, kc, vc, bt, lens, 0.125)
+    for j in range(66):
+        put(j, j % 32, inf if j % 3 else -inf)
+    for b, total in enumerate((n, 70)):  # the newest key: the last query's alone
+        at = total - 1
+        vc[bt[b, at // 16], 0, at % 16, 63] = -inf
+    got = splash.paged_decode(q, kc, vc, bt, lens, 0.125)
+    splash.check_device_error()
+    want = reference(x, 0.125)[0]
+    o = got[0].double().cpu().numpy()
+    assert np.array_equal(np.isnan(o), np.isnan(want))
+    assert np.array_equal(np.isposinf(o), np.isposinf(want)) and np.array_equal(np.isneginf(o), np.isneginf(want))
+    fine = np.isfinite(want)
+    assert fine[..., 32:63].all() and not fine[..., :32].any()
+    assert np.array_equal(o[fine], clean[0].double().cpu().numpy()[fine]) and torch.equal(got[1], clean[1])
+    assert np.abs(clean[1].double().cpu().numpy() - plain[1]).max() <= 1e-4
+
+
+@pytest.mark.parametrize("Hq", [1, 8, 16, 24])
+def test_an_infinite_value_of_the_largest_key(splash, Hq):
+    """The key whose probability is exactly 1 has infinite values."""
+    d, n = 64, 40
+    kc = torch.zeros(3, 1, 16, d, dtype=torch.bfloat16, device="cuda")
+    vc = workloads.normal_bf16((3, 1, 16, d), 620).cuda()
+    kc[1, 0, 4] = 1.0
+    vc[1, 0, 4, 0], vc[1, 0, 4, 1] = float("inf"), float("-inf")
+    q = torch.ones(1, Hq, 1, d, dtype=torch.bfloat16, device="cuda")
+    bt = torch.arange(3, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    for cols in (3, 2600):
+        table = torch.nn.functional.pad(bt, (0, cols - 3), value=-1).contiguous()
+        out, lse = splash.paged_decode(q, kc, vc, table, lens, 0.125)
+        splash.check_device_error()
+        assert torch.isposinf(out[..., 0]).all() and torch.isneginf(out[..., 1]).all()
+        assert torch.isfinite(out[..., 2:]).all() and torch.isfinite(lse).all()
