@@ -232,15 +232,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-// Two positive numbers cut off to bf16, and what that leaves of them.
-__device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
-  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
-}
-__device__ __forceinline__ float rest_of(float x) {
-  return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xffff0000u), __uint_as_float(0x00800000u));
-}
-__device__ __forceinline__ uint32_t rest_bf16x2(float lo, float hi) { return pack_bf16x2(rest_of(lo), rest_of(hi)); }
-
 // The larger exponent field of a word's two bf16 values, and the word as fp16
 // values over 2^(top - 127).
 __device__ __forceinline__ uint32_t exponent(uint32_t x) { return max((x >> 7) & 255u, (x >> 23) & 255u); }
@@ -801,11 +792,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
       // fp16, 2^-11 of each p, for an e4m3 cache; bf16, 2^-8, as the forward's.
       // With eight rows the free half of the product takes the rest, P -
       // bf16(P), and the result carries one bf16 rounding, its own.  (With more
-      // rows that would be a second product: measured 1 to 6 % slower.)  There
-      // bf16(P) is P cut off and the rest is kept above 0: an infinite value
-      // times either part then has its sign, and their sum is that infinity
-      // (0 x infinity and infinity - infinity are NaN).  The rest's floor, the
-      // smallest normal number, adds less than 2^-126 of a value.
+      // rows that would be a second product: measured 1 to 6 % slower.)
       uint32_t pa[MT][NB][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -826,13 +813,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float *y = &s[mt][2 * nb + (i >> 1)][E == 1 ? 0 : 2 * (i & 1)];
-            if (E == 1 && !E4M3) {
-              pa[mt][nb][i] = (i & 1) == 0 ? cut_bf16x2(y[0], y[1]) : rest_bf16x2(y[0], y[1]);
-            } else if (E == 2 || (i & 1) == 0) {
+            if (E == 2 || (i & 1) == 0)
               pa[mt][nb][i] = pack2<E4M3>(y[0], y[1]);
-            } else {
+            else if (E4M3)
               pa[mt][nb][i] = 0;
-            }
+            else
+              pa[mt][nb][i] = pack_bf16x2(y[0] - __uint_as_float(pa[mt][nb][i - 1] << 16),
+                                          y[1] - __uint_as_float(pa[mt][nb][i - 1] & 0xffff0000u));
           }
       }
       if (!C::MULTI || whole) {
@@ -863,8 +850,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
     }
 
     if (E == 1) {
+      // The halves' sum.  The rest of a P is 0 or negative too: an infinite value
+      // times it is NaN or the other infinity, so that a sum which is not finite
+      // stays as bf16(P) made it.
 #pragma unroll
-      for (int j = 0; j < DV / 8; ++j) o[0][j][0] += o[0][j][2], o[0][j][1] += o[0][j][3];
+      for (int j = 0; j < DV / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (fabsf(o[0][j][i]) < INFINITY) o[0][j][i] += o[0][j][i + 2];
     }
     if constexpr (TOGETHER) {
       copy_wait<0>();
