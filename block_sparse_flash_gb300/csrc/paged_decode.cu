@@ -93,7 +93,8 @@ constexpr int keys_per_step(int bytes) { return bytes >= 512 ? 16 : 32; }
 
 // ROWS: query rows of a tile, 8, 16 or 32.  Eight rows (up to 8 query heads per
 // KV head, one new token) leave half of each 16-row product free: for a bf16
-// cache it takes what rounding P to bf16 loses, see below.
+// cache it takes what rounding P to bf16 loses, which with more rows has a product
+// of its own (REST), see below.
 template <int DQK_, int DV_, bool E4M3_, int ROWS_, bool MULTI_>
 struct Config {
   static constexpr int DQK = DQK_, DV = DV_, ROWS = ROWS_;
@@ -101,6 +102,7 @@ struct Config {
   static constexpr int MT = ROWS <= 16 ? 1 : 2;  // products of 16 rows
   static constexpr int E = ROWS == 8 ? 1 : 2;    // halves of them that hold rows
   static constexpr bool E4M3 = E4M3_;
+  static constexpr bool REST = !E4M3 && E == 2;  // what rounding P loses has a product of its own
   static constexpr int RK = DQK * (E4M3 ? 1 : 2), RV = DV * (E4M3 ? 1 : 2);  // bytes of a row
   static constexpr int KW = keys_per_step(RK + RV), NB = KW / 16;            // keys and 16-key blocks of a step
   static constexpr int STAGE = KW * (RK + RV);
@@ -231,6 +233,15 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+// Two positive numbers cut off to bf16, and what that leaves of them.
+__device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+__device__ __forceinline__ float rest_of(float x) {
+  return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xffff0000u), __uint_as_float(0x00800000u));
+}
+__device__ __forceinline__ uint32_t rest_bf16x2(float lo, float hi) { return pack_bf16x2(rest_of(lo), rest_of(hi)); }
 
 // The larger exponent field of a word's two bf16 values, and the word as fp16
 // values over 2^(top - 127).
@@ -392,14 +403,22 @@ struct Seen {
   bool row[C::MT][C::E];
 };
 
+// P in 16 bits as the product takes it, with its rest where that has a product
+// of its own.
+template <class C>
+struct Weights {
+  uint32_t p[C::MT][C::NB][4], rest[C::REST ? C::MT : 1][C::REST ? C::NB : 1][4];
+};
+
 template <class C, bool MASKED>
-__device__ __forceinline__ void add_product(float (&o)[4], const uint32_t (&pa)[4], uint32_t b0, uint32_t b1,
+__device__ __forceinline__ void add_product(float (&o)[4], const Weights<C> &w, int mt, int nb, uint32_t b0, uint32_t b1,
                                             const bool (&row)[C::E]) {
-  if (!MASKED) {
-    mma<C::E4M3>(o, pa, b0, b1);
+  if constexpr (!MASKED) {
+    mma<C::E4M3>(o, w.p[mt][nb], b0, b1);
   } else {
     float x[4] = {0.f, 0.f, 0.f, 0.f};
-    mma<C::E4M3>(x, pa, b0, b1);
+    mma<C::E4M3>(x, w.p[mt][nb], b0, b1);
+    if constexpr (C::REST) mma<C::E4M3>(x, w.rest[mt][nb], b0, b1);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (row[C::E == 1 ? 0 : i >> 1]) o[i] += x[i];
@@ -409,8 +428,8 @@ __device__ __forceinline__ void add_product(float (&o)[4], const uint32_t (&pa)[
 // O += P V for the step whose values are at vs; with MASKED only the rows and
 // keys of `seen`.
 template <class C, bool MASKED>
-__device__ __forceinline__ void add_values(float (&o)[C::MT][C::DV / 8][4], const uint32_t (&pa)[C::MT][C::NB][4], uint32_t vs,
-                                           int lane, const Seen<C> &seen) {
+__device__ __forceinline__ void add_values(float (&o)[C::MT][C::DV / 8][4], const Weights<C> &w, uint32_t vs, int lane,
+                                           const Seen<C> &seen) {
   const int v_row = (lane & 7) + ((lane >> 3) & 1) * 8, v_chunk = lane >> 4;
 #pragma unroll
   for (int nb = 0; nb < C::NB; ++nb) {
@@ -429,15 +448,22 @@ __device__ __forceinline__ void add_values(float (&o)[C::MT][C::DV / 8][4], cons
           widen(__byte_perm(vb[2 * x + 1], 0, 0x3120), b1, c1);
 #pragma unroll
           for (int mt = 0; mt < C::MT; ++mt) {
-            add_product<C, MASKED>(o[mt][2 * (j + (C::E4M3 ? x : 0))], pa[mt][nb], b0 & m0, b1 & m1, seen.row[mt]);
-            add_product<C, MASKED>(o[mt][2 * (j + (C::E4M3 ? x : 0)) + 1], pa[mt][nb], c0 & m0, c1 & m1, seen.row[mt]);
+            add_product<C, MASKED>(o[mt][2 * (j + (C::E4M3 ? x : 0))], w, mt, nb, b0 & m0, b1 & m1, seen.row[mt]);
+            add_product<C, MASKED>(o[mt][2 * (j + (C::E4M3 ? x : 0)) + 1], w, mt, nb, c0 & m0, c1 & m1, seen.row[mt]);
           }
         }
       } else {
 #pragma unroll
         for (int mt = 0; mt < C::MT; ++mt) {
-          add_product<C, MASKED>(o[mt][2 * j], pa[mt][nb], vb[0] & m0, vb[1] & m1, seen.row[mt]);
-          add_product<C, MASKED>(o[mt][2 * j + 1], pa[mt][nb], vb[2] & m0, vb[3] & m1, seen.row[mt]);
+          add_product<C, MASKED>(o[mt][2 * j], w, mt, nb, vb[0] & m0, vb[1] & m1, seen.row[mt]);
+          add_product<C, MASKED>(o[mt][2 * j + 1], w, mt, nb, vb[2] & m0, vb[3] & m1, seen.row[mt]);
+        }
+        if constexpr (C::REST && !MASKED) {  // (after the tiles' other products, which it would wait for)
+#pragma unroll
+          for (int mt = 0; mt < C::MT; ++mt) {
+            mma<false>(o[mt][2 * j], w.rest[mt][nb], vb[0], vb[1]);
+            mma<false>(o[mt][2 * j + 1], w.rest[mt][nb], vb[2], vb[3]);
+          }
         }
       }
     }
@@ -788,12 +814,20 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
           }
       }
 
-      // P, O += P V.  The product takes P in 16 bits (its sum is taken before):
-      // fp16, 2^-11 of each p, for an e4m3 cache; bf16, 2^-8, as the forward's.
-      // With eight rows the free half of the product takes the rest, P -
-      // bf16(P), and the result carries one bf16 rounding, its own.  (With more
-      // rows that would be a second product: measured 1 to 6 % slower.)
-      uint32_t pa[MT][NB][4];
+      // P, O += P V.  The product takes P in 16 bits (its sum is taken before).
+      // For an e4m3 cache that is fp16, 2^-11 of each p.  bf16 would be 2^-8 of
+      // it, as much as the rounding of the result, so that what it loses is
+      // multiplied too and the result carries one bf16 rounding, its own.
+      //  * Eight rows: the free half of the product takes P - bf16(P); the halves
+      //    are added at the end.
+      //  * More: the rest has a product of its own into the same sums (4 tokens of
+      //    64 requests take 107.1 us, 104.3 without, of 8 requests 36.1 and 33.8, 32
+      //    rows of 192-wide heads 79.2 and 71.8; errors 1.7e-3 and 2.3e-3).  There P
+      //    is cut off to bf16 and the rest kept above 0: an infinite value times
+      //    either has its sign, and the sum is that infinity (0 x infinity and
+      //    infinity - infinity are NaN).  The rest's floor, the smallest normal
+      //    number, adds 2^-126 of a value.
+      Weights<C> w;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -813,17 +847,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float *y = &s[mt][2 * nb + (i >> 1)][E == 1 ? 0 : 2 * (i & 1)];
-            if (E == 2 || (i & 1) == 0)
-              pa[mt][nb][i] = pack2<E4M3>(y[0], y[1]);
-            else if (E4M3)
-              pa[mt][nb][i] = 0;
-            else
-              pa[mt][nb][i] = pack_bf16x2(y[0] - __uint_as_float(pa[mt][nb][i - 1] << 16),
-                                          y[1] - __uint_as_float(pa[mt][nb][i - 1] & 0xffff0000u));
+            if constexpr (C::REST) {
+              w.p[mt][nb][i] = cut_bf16x2(y[0], y[1]);
+              w.rest[mt][nb][i] = rest_bf16x2(y[0], y[1]);
+            } else if (E == 2 || (i & 1) == 0) {
+              w.p[mt][nb][i] = pack2<E4M3>(y[0], y[1]);
+            } else if (E4M3) {
+              w.p[mt][nb][i] = 0;
+            } else {
+              w.p[mt][nb][i] = pack_bf16x2(y[0] - __uint_as_float(w.p[mt][nb][i - 1] << 16),
+                                           y[1] - __uint_as_float(w.p[mt][nb][i - 1] & 0xffff0000u));
+            }
           }
       }
       if (!C::MULTI || whole) {
-        add_values<C, false>(o, pa, vs, lane, Seen<C>());
+        add_values<C, false>(o, w, vs, lane, Seen<C>());
       } else if constexpr (C::MULTI) {
         // Some of the step's values are one query's and not another's: a
         // product for each query, with zeros in the place of the values that
@@ -844,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int e = 0; e < E; ++e) seen.row[mt][e] = pos[mt][e] == last;
-          add_values<C, true>(o, pa, vs, lane, seen);
+          add_values<C, true>(o, w, vs, lane, seen);
         }
       }
     }

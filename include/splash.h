@@ -554,6 +554,11 @@ splash_status splash_paged_append(const splash_paged_append_args *args, void *cu
  * 16 keys (at most max_pages * page_size / 16 + 1, or window_left / 16 + 4) over
  * all sequences, KV heads and groups of 16 of the Hq/Hkv * Lq rows.  The result does not depend on timing: the same inputs give the
  * same bits on the same GPU.
+ *
+ * Precision: scores, softmax statistics and sums are fp32, out is rounded once.
+ * The product with the values takes each probability to 2^-16 of it for a bf16
+ * cache and to 2^-11 for an e4m3 one, where those below 2^-32 of the largest
+ * count in lse but not in out (below out's own rounding up to 2^23 such keys).
  */
 typedef struct {
     uint64_t struct_bytes;

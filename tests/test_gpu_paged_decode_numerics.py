@@ -1,6 +1,6 @@
 """paged_decode on the GPU where the numbers are far from ordinary: soft caps
-of any size, one key far above very many, infinite values.  References in
-float64; the bounds are derived at each test."""
+of any size, one key far above very many, infinite values; and that a result
+carries no rounding but its own, in every tile of rows.  References in float64; the bounds are derived at each test."""
 import math
 
 import numpy as np
@@ -160,3 +160,21 @@ def test_an_infinite_value_of_the_largest_key(splash, Hq):
         splash.check_device_error()
         assert torch.isposinf(out[..., 0]).all() and torch.isneginf(out[..., 1]).all()
         assert torch.isfinite(out[..., 2:]).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("cols", [0, 2600], ids=["short", "long"])
+@pytest.mark.parametrize("dqk, dv", [(64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("Lq", [1, 2])
+@pytest.mark.parametrize("rows", [6, 14, 22, 40])
+def test_every_tile_of_rows_rounds_its_result_once(splash, rows, Lq, dqk, dv, cols):
+    """A bf16 cache: the probabilities reach the product to 2^-16 of each
+    (cut off to bf16, and the rest in bf16), the result is rounded to bf16, 2^-8
+    of it.  Scores as above."""
+    x = make([700, 333], Lq, 2 * rows // Lq, 2, dqk, dv, 32, cols=cols // 2, seed=700 + rows + dqk)
+    out, lse, A, reach = reference(x, dqk ** -0.5)
+    o, l = splash.paged_decode(*x[:5], dqk ** -0.5)
+    splash.check_device_error()
+    e = (dqk + 8) * 2.0 ** -23 * reach
+    off = np.abs(o.double().cpu().numpy() - out)
+    assert (off <= (2.0 ** -16 + 2 * e[..., None]) * A + 2.0 ** -8 * np.abs(out)).all(), off.max()
+    assert (np.abs(l.double().cpu().numpy() - lse) <= e + 2.0 ** -20 + 2.0 ** -22 * np.abs(lse)).all()
