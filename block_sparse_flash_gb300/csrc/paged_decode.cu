@@ -92,9 +92,9 @@ struct Params {
 constexpr int keys_per_step(int bytes) { return bytes >= 512 ? 16 : 32; }
 
 // ROWS: query rows of a tile, 8, 16 or 32.  Eight rows (up to 8 query heads per
-// KV head, one new token) leave half of each 16-row product free: for a bf16
-// cache it takes what rounding P to bf16 loses, which with more rows has a product
-// of its own (REST), see below.
+// KV head, one new token) leave half of each 16-row product free: it takes what
+// rounding P to 16 bits loses.  With more rows that has a product of its own for a
+// bf16 cache (REST), see below.
 template <int DQK_, int DV_, bool E4M3_, int ROWS_, bool MULTI_>
 struct Config {
   static constexpr int DQK = DQK_, DV = DV_, ROWS = ROWS_;
@@ -814,13 +814,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
           }
       }
 
-      // P, O += P V.  The product takes P in 16 bits (its sum is taken before).
-      // For an e4m3 cache that is fp16, 2^-11 of each p.  bf16 would be 2^-8 of
-      // it, as much as the rounding of the result, so that what it loses is
-      // multiplied too and the result carries one bf16 rounding, its own.
-      //  * Eight rows: the free half of the product takes P - bf16(P); the halves
-      //    are added at the end.
-      //  * More: the rest has a product of its own into the same sums (4 tokens of
+      // P, O += P V.  The product takes P in 16 bits (its sum is taken before):
+      // fp16 for an e4m3 cache, 2^-11 of each p, or bf16, 2^-8, which is as much as
+      // the rounding of the result.
+      //  * Eight rows: the free half of the product takes the rest, P - bf16(P) or
+      //    P - fp16(P); the halves are added at the end, and the result carries
+      //    one bf16 rounding, its own.  (e4m3: 8 requests of 1023 .. 8191 tokens
+      //    27.0 us, 26.5 without, longer ones as before; bf16: no difference.)
+      //  * More: bf16's rest has a product of its own into the same sums (4 tokens of
       //    64 requests take 107.1 us, 104.3 without, of 8 requests 36.1 and 33.8, 32
       //    rows of 192-wide heads 79.2 and 71.8; errors 1.7e-3 and 2.3e-3).  There P
       //    is cut off to bf16 and the rest kept above 0: an infinite value times
@@ -853,7 +854,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
             } else if (E == 2 || (i & 1) == 0) {
               w.p[mt][nb][i] = pack2<E4M3>(y[0], y[1]);
             } else if (E4M3) {
-              w.p[mt][nb][i] = 0;
+              const uint32_t h = w.p[mt][nb][i - 1];
+              const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+              w.p[mt][nb][i] = pack2<true>(y[0] - f.x, y[1] - f.y);
             } else {
               w.p[mt][nb][i] = pack_bf16x2(y[0] - __uint_as_float(w.p[mt][nb][i - 1] << 16),
                                            y[1] - __uint_as_float(w.p[mt][nb][i - 1] & 0xffff0000u));

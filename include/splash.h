@@ -557,8 +557,9 @@ splash_status splash_paged_append(const splash_paged_append_args *args, void *cu
  *
  * Precision: scores, softmax statistics and sums are fp32, out is rounded once.
  * The product with the values takes each probability to 2^-16 of it for a bf16
- * cache and to 2^-11 for an e4m3 one, where those below 2^-32 of the largest
- * count in lse but not in out (below out's own rounding up to 2^23 such keys).
+ * cache; for an e4m3 one to 2^-11, or 2^-22 with at most 8 of the Hq/Hkv * Lq
+ * rows, and those below 2^-32 of the largest count in lse but not in out (below
+ * out's own rounding up to 2^23 such keys).
  */
 typedef struct {
     uint64_t struct_bytes;

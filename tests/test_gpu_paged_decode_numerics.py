@@ -1,6 +1,7 @@
 """paged_decode on the GPU where the numbers are far from ordinary: soft caps
 of any size, one key far above very many, infinite values; and that a result
-carries no rounding but its own, in every tile of rows.  References in float64; the bounds are derived at each test."""
+carries no rounding but its own.  References in float64; the bounds are derived
+at each test."""
 import math
 
 import numpy as np
@@ -178,3 +179,39 @@ def test_every_tile_of_rows_rounds_its_result_once(splash, rows, Lq, dqk, dv, co
     off = np.abs(o.double().cpu().numpy() - out)
     assert (off <= (2.0 ** -16 + 2 * e[..., None]) * A + 2.0 ** -8 * np.abs(out)).all(), off.max()
     assert (np.abs(l.double().cpu().numpy() - lse) <= e + 2.0 ** -20 + 2.0 ** -22 * np.abs(lse)).all()
+
+
+@pytest.mark.parametrize("cols", [0, 2600], ids=["short", "long"])
+@pytest.mark.parametrize("kind, Hq, d", [("e4m3", 1, 64), ("e4m3", 8, 128), ("bf16", 1, 64), ("bf16", 8, 128), ("bf16", 16, 64),
+                                         ("bf16", 40, 128)])
+def test_probabilities_whose_errors_add_up(splash, kind, Hq, d, cols):
+    """Three keys of probability 1/3 and value 1 for each one of probability 1
+    and value -1 (over their sum): the result is nearly 0, and what rounding
+    1/3 loses adds up over all keys.  It reaches the product as two parts, to
+    2^-16 of it for a bf16 cache and 2^-22 for an e4m3 one.  The scores are one
+    fp32 product, ln 3 rounded (2^-24 of it), and exp2 is off by 2^-22: 2^-20
+    for all of them and the sums' rounding of n terms of like size, 2^-24 each
+    at most and random, below 2^-20 too."""
+    n = 700
+    k = torch.zeros(44, 1, 16, d)
+    v = torch.zeros_like(k)
+    j = torch.arange(44 * 16).view(44, 16)
+    k[:, 0, :, 0] = (j % 4 == 3).float()
+    v[:, 0, :, 1] = torch.where(j % 4 == 3, -1.0, 1.0)
+    dtype = torch.float8_e4m3fn if kind == "e4m3" else torch.bfloat16
+    one = torch.ones(1, device="cuda") if kind == "e4m3" else None
+    q = torch.zeros(1, Hq, 1, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    bt = torch.arange(44, dtype=torch.int32)[None]
+    bt = torch.nn.functional.pad(bt, (0, max(0, cols - 44)), value=-1).cuda()
+    scale = float(torch.tensor(math.log(3.0)))
+    out, lse = splash.paged_decode(q, k.to(dtype).cuda(), v.to(dtype).cuda(), bt, torch.tensor([n], dtype=torch.int32, device="cuda"),
+                                   scale, k_scale=one, v_scale=one)
+    splash.check_device_error()
+    p = math.exp(-scale)
+    exact = (3 * p - 1) / (3 * p + 1)
+    room = 2.0 ** -16 if kind == "bf16" else 2.0 ** -22
+    o = out.double().cpu()
+    assert (o[..., 1] - exact).abs().max().item() <= room + 2.0 ** -19 + 2.0 ** -8 * abs(exact)
+    assert not o[..., 2:].any() and not o[..., 0].any()
+    assert (lse.double().cpu() - (scale + math.log(n / 4 * (3 * p + 1)))).abs().max().item() <= 2.0 ** -19
