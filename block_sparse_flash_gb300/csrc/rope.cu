@@ -264,7 +264,8 @@ template <bool APPEND, bool E4M3, int HEADS>
 splash_status launch_heads(const Params &p, bool interleaved, cudaStream_t stream) {
   // 128 threads: a packed prompt of 32768 tokens 98 us, against 104 with 256 and 133 with 64
   const int ty = std::max(1, 128 / p.units);
-  const dim3 block(p.units, ty), grid((p.tokens + ty - 1) / ty, (p.heads + HEADS - 1) / HEADS);
+  // (a call may have 2^31 - 1 tokens: adding to that would overflow)
+  const dim3 block(p.units, ty), grid((p.tokens - 1) / ty + 1, (p.heads + HEADS - 1) / HEADS);
   SPLASH_CUDA_TRY(launch_dependent(interleaved ? rope_kernel<true, APPEND, E4M3, HEADS> : rope_kernel<false, APPEND, E4M3, HEADS>,
                                    grid, block, 0, 1, stream, p));
   splash_count_launches(1);
