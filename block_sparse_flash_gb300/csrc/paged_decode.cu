@@ -1100,9 +1100,14 @@ struct Plan {
 // each, 33.4 -> 32.6.  A sequence much longer than the others keeps its
 // clusters running alone (2048 keys take a CTA 23 us), so the keys that a CTA may
 // get are limited: 2048, and the ends of a window of that size per CTA.
-constexpr int kSlots = kMaxWarps / kWarps;  // CTAs that fill the GPU
+constexpr int kSlots = kMaxWarps / kWarps;  // CTAs that fill the GPU at two per SM
 constexpr int kMaxCluster = 16;             // (with at most 8, 16384 keys of 1 sequence take 24.8 us)
 constexpr int kClusterKeys = 2304;          // per CTA, at most
+// The 32-row tile of 192-wide heads has one CTA per SM, so that its clusters may
+// come in two waves.  That is better for sequences of mixed lengths (us, one wave
+// or the list -> two waves: 20 sequences of 204 .. 4096 keys and 2 KV heads 47.7 ->
+// 38.3, 100 of 20 .. 2048 67.7 -> 63.1) and worse for equal ones (50 of 2048 keys
+// 47.9 -> 59.1, 100 of them 76.8 -> 93.7); the limit is the same for all tiles.
 
 Plan plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t dv, int32_t max_pages, int32_t page_size,
           int32_t type, int64_t window) {
@@ -1121,18 +1126,52 @@ Plan plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t d
   return x;
 }
 
+// The largest cluster, of `want` CTAs at most, that the current device can place.
+// More than 8 need not fit (a part of a GPU, say, may not have 16 SMs next to one
+// another); a smaller one does the same with more keys per CTA.
+template <class C>
+splash_status placeable(int want, int *cluster) {
+  *cluster = want;
+  while (*cluster > 1) {
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(*cluster);
+    config.blockDim = dim3(kThreads);
+    config.dynamicSmemBytes = C::SMEM;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)*cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    config.attrs = &attr;
+    config.numAttrs = 1;
+    int clusters = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, paged_decode_kernel<C, true>, &config);
+    if (e != cudaSuccess && e != cudaErrorInvalidClusterSize) return SPLASH_ERR_CUDA;
+    if (e == cudaSuccess && clusters > 0) break;
+    (void)cudaGetLastError();
+    *cluster /= 2;
+  }
+  return SPLASH_OK;
+}
+
+// grid clusters of `cluster` CTAs each, or of fewer where that has no room.
 template <class C, bool TOGETHER>
-splash_status launch_kernel(int ctas, int cluster, const Params &p, cudaStream_t stream) {
-  static std::atomic<uint64_t> ready{0};  // devices that allow this kernel its shared memory
+splash_status launch_kernel(int grid, int cluster, const Params &p, cudaStream_t stream) {
+  static std::atomic<int8_t> most[64];  // per device: CTAs of a cluster that fits, 0: this kernel has not run there
   int dev = 0;
   SPLASH_CUDA_TRY(cudaGetDevice(&dev));
-  const uint64_t bit = (uint64_t)1 << (dev & 63);
-  if (!(ready.load(std::memory_order_acquire) & bit)) {
+  std::atomic<int8_t> &fits = most[dev & 63];
+  if (fits.load(std::memory_order_acquire) == 0) {
     SPLASH_CUDA_TRY(cudaFuncSetAttribute(paged_decode_kernel<C, TOGETHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
-    if (TOGETHER) SPLASH_CUDA_TRY(cudaFuncSetAttribute(paged_decode_kernel<C, TOGETHER>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
-    ready.fetch_or(bit, std::memory_order_release);
+    int room = 1;
+    if constexpr (TOGETHER) {
+      SPLASH_CUDA_TRY(cudaFuncSetAttribute(paged_decode_kernel<C, TOGETHER>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+      const splash_status st = placeable<C>(kMaxCluster, &room);
+      if (st != SPLASH_OK) return st;
+    }
+    fits.store((int8_t)room, std::memory_order_release);
   }
-  SPLASH_CUDA_TRY(launch_dependent(paged_decode_kernel<C, TOGETHER>, dim3(ctas), dim3(kThreads), C::SMEM, cluster, stream, p));
+  cluster = std::min<int>(cluster, fits.load(std::memory_order_relaxed));
+  SPLASH_CUDA_TRY(launch_dependent(paged_decode_kernel<C, TOGETHER>, dim3(grid * cluster), dim3(kThreads), C::SMEM, cluster, stream, p));
   splash_count_launches(1);
   return SPLASH_OK;
 }
@@ -1141,7 +1180,7 @@ template <class C>
 splash_status launch(const Plan &x, void *workspace, Params p, cudaStream_t stream) {
   p.row_groups = (p.nrows + C::ROWS - 1) / C::ROWS;
   p.part_rows = std::min(p.nrows, C::ROWS);
-  if (x.cluster > 0) return launch_kernel<C, true>((int)x.segments * x.cluster, x.cluster, p, stream);
+  if (x.cluster > 0) return launch_kernel<C, true>((int)x.segments, x.cluster, p, stream);
   char *ws = static_cast<char *>(workspace);
   p.before = reinterpret_cast<int32_t *>(ws);
   ws += align16(4 * ((int64_t)p.B + 1));
