@@ -451,20 +451,13 @@ def _native():
     return _binding
 
 
-def _handle(stream) -> int:
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-
-
-def _new(shape, dtype, device, stream):
-    """A tensor for a call on `stream`: taken from that stream's memory, so
-    that nothing another stream still uses is overwritten, and kept until the
-    current stream's later work is done with it."""
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    current = torch.cuda.current_stream()
-    with torch.cuda.stream(s):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(current)
-    return t
+def _handle(stream):
+    """The handle of a call's stream; None: torch's current one."""
+    if not isinstance(stream, torch.cuda.Stream):
+        return None if stream is None else int(stream)
+    if stream.device_index != torch.cuda.current_device():
+        raise ValueError(f"the stream must be on the current CUDA device (got one of cuda:{stream.device_index})")
+    return stream.cuda_stream
 
 
 def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
@@ -478,13 +471,8 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="
 
 
 def _rope(inverse, q, k, positions, table, rot_offset, interleaved, q_out, k_out, stream):
-    if stream is not None:
-        if q_out is None:
-            q_out = _new(q.shape, torch.bfloat16, q.device, stream)
-        if k is not None and k_out is None:
-            k_out = _new(k.shape, torch.bfloat16, q.device, stream)
-        stream = _handle(stream)
-    return (_binding or _native()).rope(q, k, positions, table, rot_offset, interleaved, inverse, q_out, k_out, stream)
+    return (_binding or _native()).rope(q, k, positions, table, rot_offset, interleaved, inverse, q_out, k_out,
+                                        _handle(stream))
 
 
 def rope_fwd(q, k, positions, table, rot_offset: int = 0, interleaved: bool = False, q_out=None, k_out=None,
@@ -519,12 +507,8 @@ def paged_append(k, v, k_cache, v_cache, block_table, positions, q=None, table=N
     (nothing is stored); seq_ids is the row of block_table (default: b).
     q [B, Hq, L, dqk] is rotated into q_out (allocated if not given); k_out
     receives the rotated keys when given (for attention_fwd of a prompt)."""
-    if stream is not None:
-        if q is not None and q_out is None:
-            q_out = _new(q.shape, torch.bfloat16, k.device, stream)
-        stream = _handle(stream)
     return (_binding or _native()).paged_append(k, v, k_cache, v_cache, block_table, positions, q, table, rot_offset,
-                                                interleaved, seq_ids, k_scale, v_scale, q_out, k_out, stream)
+                                                interleaved, seq_ids, k_scale, v_scale, q_out, k_out, _handle(stream))
 
 
 def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float, softcap: float = 0.0,
@@ -537,18 +521,8 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float, softc
     block_table [B, max_pages] as for paged_append.  workspace: optional uint8
     device tensor of at least paged_decode_workspace_size(...) bytes, not
     shared by calls that may overlap."""
-    if stream is not None:
-        shape = q.shape[:3]
-        if out is None:
-            out = _new((*shape, v_cache.shape[3]), torch.bfloat16, q.device, stream)
-        if lse is None:
-            lse = _new(shape, torch.float32, q.device, stream)
-        if workspace is None:
-            room = paged_decode_workspace_size(q, k_cache, v_cache, block_table, window_left)
-            workspace = _new(room, torch.uint8, q.device, stream) if room else None
-        stream = _handle(stream)
     return (_binding or _native()).paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, softcap,
-                                                window_left, k_scale, v_scale, out, lse, workspace, stream)
+                                                window_left, k_scale, v_scale, out, lse, workspace, _handle(stream))
 
 
 @functools.lru_cache(maxsize=256)
@@ -561,6 +535,10 @@ def _paged_decode_workspace_size(*sizes):
 def paged_decode_workspace_size(q, k_cache, v_cache, block_table, window_left: int = -1) -> int:
     """Bytes of paged_decode's workspace for tensors of these shapes and types
     (0 where it needs none)."""
+    if q.dim() != 4 or k_cache.dim() != 4 or v_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q, k_cache and v_cache must be 4-D and block_table 2-D")
+    if k_cache.dtype not in _CACHE_TYPES:
+        raise ValueError("k_cache and v_cache must be bf16 or float8_e4m3fn tensors")
     return _paged_decode_workspace_size(q.shape[0], q.shape[1], k_cache.shape[1], q.shape[2], q.shape[3],
                                         v_cache.shape[3], block_table.shape[1], k_cache.shape[2],
                                         _CACHE_TYPES[k_cache.dtype], int(window_left))

@@ -14,6 +14,7 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include "splash.h"
@@ -180,20 +181,35 @@ struct Output {
   }
 };
 
-at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like) {
-  return at::empty(shape, like.options().dtype(type), at::MemoryFormat::Contiguous);
-}
+// The stream of a call: torch's current one, or a given handle.
+struct Stream {
+  c10::cuda::CUDAStream current, used;
 
-cudaStream_t stream_of(PyObject *x) {
-  if (x == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
-  return reinterpret_cast<cudaStream_t>((uintptr_t)integer(x));
-}
+  // after check_device
+  explicit Stream(PyObject *x)
+      : current(c10::cuda::getCurrentCUDAStream()),
+        used(x == Py_None ? current
+                          : c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>((uintptr_t)integer(x)),
+                                                             current.device_index())) {}
+
+  // A new tensor of the call, from the memory of its stream, so that nothing
+  // another stream still uses is overwritten; kept until the current stream's
+  // later work is done with it.
+  at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like) const {
+    const auto options = like.options().dtype(type);
+    if (used == current) return at::empty(shape, options, at::MemoryFormat::Contiguous);
+    const c10::cuda::CUDAStreamGuard guard(used);
+    at::Tensor t = at::empty(shape, options, at::MemoryFormat::Contiguous);
+    t.record_stream(current.unwrap());
+    return t;
+  }
+};
 
 template <class Args>
-void run(splash_status (*f)(const Args *, void *), const Args &a, cudaStream_t stream, const char *what) {
+void run(splash_status (*f)(const Args *, void *), const Args &a, const Stream &stream, const char *what) {
   splash_status st;
   Py_BEGIN_ALLOW_THREADS;
-  st = f(&a, stream);
+  st = f(&a, stream.used.stream());
   Py_END_ALLOW_THREADS;
   if (st == SPLASH_OK) return;
   PyObject *e = PyObject_CallFunction(g_error, "is", (int)st, what);
@@ -252,16 +268,17 @@ PyObject *rope(PyObject *const *x, Py_ssize_t n) {
   if (qo.object != nullptr) a.q_out = c.view(tensor(x[7], "q_out"), "q_out", shape);
   if (has_k && ko.object != nullptr) a.k_out = c.view(tensor(x[8], "k_out"), "k_out", k->sizes());
   c.check_device();
+  const Stream stream(x[9]);
   const int64_t row = shape[3], head = shape[2] * row;
   if (qo.object == nullptr) {
-    qo.made = make(shape, at::kBFloat16, q);
+    qo.made = stream.make(shape, at::kBFloat16, q);
     a.q_out = {qo.made.data_ptr(), shape[1] * head, head, row};
   }
   if (ko.object == nullptr) {
-    ko.made = make(k->sizes(), at::kBFloat16, q);
+    ko.made = stream.make(k->sizes(), at::kBFloat16, q);
     a.k_out = {ko.made.data_ptr(), k->size(1) * head, head, row};
   }
-  run(splash_rope, a, stream_of(x[9]), "splash_rope");
+  run(splash_rope, a, stream, "splash_rope");
   return pair(qo, ko);
 }
 
@@ -300,11 +317,12 @@ PyObject *paged_append(PyObject *const *x, Py_ssize_t n) {
   }
   if (x[14] != Py_None) a.k_out = c.view(tensor(x[14], "k_out"), "k_out", k.sizes());
   c.check_device();
+  const Stream stream(x[15]);
   if (qo.object == nullptr) {
-    qo.made = make(q->sizes(), at::kBFloat16, k);
+    qo.made = stream.make(q->sizes(), at::kBFloat16, k);
     a.q_out = {qo.made.data_ptr(), q->size(1) * L * a.dqk, L * a.dqk, a.dqk};
   }
-  run(splash_paged_append, a, stream_of(x[15]), "splash_paged_append");
+  run(splash_paged_append, a, stream, "splash_paged_append");
   return pair(qo, ko);
 }
 
@@ -353,26 +371,27 @@ PyObject *paged_decode(PyObject *const *x, Py_ssize_t n) {
     a.workspace_bytes = t.nbytes();
   }
   c.check_device();
+  const Stream stream(x[13]);
   at::Tensor workspace;
   if (x[12] == Py_None) {
     size_t bytes = 0;  // (an error here is the call's own: it is reported there)
     splash_paged_decode_workspace_size(a.B, a.Hq, a.Hkv, a.Lq, a.dqk, a.dv, a.max_pages, a.page_size, a.cache_type,
                                        a.window_left, &bytes);
     if (bytes > 0) {
-      workspace = make({(int64_t)bytes}, at::kByte, q);
+      workspace = stream.make({(int64_t)bytes}, at::kByte, q);
       a.workspace = workspace.data_ptr();
       a.workspace_bytes = bytes;
     }
   }
   if (out.object == nullptr) {
-    out.made = make(full, at::kBFloat16, q);
+    out.made = stream.make(full, at::kBFloat16, q);
     a.out = out.made.data_ptr();
   }
   if (lse.object == nullptr) {
-    lse.made = make(rows, at::kFloat, q);
+    lse.made = stream.make(rows, at::kFloat, q);
     a.lse = static_cast<float *>(lse.made.data_ptr());
   }
-  run(splash_paged_decode, a, stream_of(x[13]), "splash_paged_decode");
+  run(splash_paged_decode, a, stream, "splash_paged_decode");
   return pair(out, lse);
 }
 
