@@ -2,10 +2,12 @@
 sm_103a, and the compiled part of the Python binding with g++.  Translation
 units are compiled in parallel and linked into one shared library; nothing is
 installed outside the repository."""
+import contextlib
 import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,10 +44,10 @@ def _nvcc():
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _newest_input():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "splash.h"),
-                                                               os.path.abspath(__file__)]
-    return max(os.path.getmtime(f) for f in files)
+def _stale(output, sources):
+    """Whether output is older than one of its sources, the interface or this file."""
+    files = [os.path.join(CSRC, f) for f in sources] + [os.path.join(INCLUDE, "splash.h"), os.path.abspath(__file__)]
+    return not os.path.exists(output) or os.path.getmtime(output) < max(os.path.getmtime(f) for f in files)
 
 
 def _torch_root():
@@ -79,11 +81,36 @@ def _link_binding(obj: str, path: str) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compiles (if stale) and returns the path of libsplash.so."""
+    """Compiles what is stale and returns the path of libsplash.so.
+
+    The library needs nvcc and its host compiler.  The binding also needs the
+    headers of Python and torch: where it cannot be built, that is a warning,
+    and only the serving calls are missing (they raise SplashLibraryMissing)."""
     os.makedirs(OUT_DIR, exist_ok=True)
-    binding = binding_path()
-    if not force and all(os.path.exists(x) and os.path.getmtime(x) >= _newest_input() for x in (LIB, binding)):
-        return LIB
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_binding_object, force)  # (while nvcc compiles)
+        if force or _stale(LIB, [f for f in os.listdir(CSRC) if f != BINDING_SOURCE]):
+            _build_library(ex, verbose, extra)
+    try:
+        path, obj = binding.result()
+        if obj is not None:
+            _link_binding(obj, path)
+    except Exception as e:
+        warnings.warn(f"the serving calls are not available: {e}", RuntimeWarning, stacklevel=2)
+    return LIB
+
+
+def _binding_object(force):
+    """(path of the binding, its new object or None where it is up to date)."""
+    path = binding_path()
+    if not force and not _stale(path, [BINDING_SOURCE]):
+        return path, None
+    with contextlib.suppress(FileNotFoundError):
+        os.remove(path)  # (not left behind if it no longer builds)
+    return path, _compile_binding()
+
+
+def _build_library(ex, verbose, extra):
     nvcc = _nvcc()
 
     def compile_one(entry):
@@ -97,17 +124,10 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding_obj = ex.submit(_compile_binding)
-        objs = list(ex.map(compile_one, SOURCES))
+    objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], "link failed")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj.result(), binding)
-    return LIB
 
 
 if __name__ == "__main__":
