@@ -1268,7 +1268,9 @@ splash_status splash_paged_decode_launch_bf16(const splash_paged_decode_args &a,
   // (differences of positions stay below 2^31 - 64)
   p.window = a.window_left < 0 ? -1 : (int32_t)std::min<int64_t>(a.window_left, INT32_MAX - 64);
   p.scale = a.scale;
-  p.cap = a.softcap;
+  // (cap log2 e would overflow next to fp32's end; from 2^100 on tanh leaves every
+  // score below 2^88 as it is)
+  p.cap = a.softcap < 0x1p100f ? a.softcap : 0.f;
   p.err = err_word;
   if (a.dqk == 64) return pick<64, 64>(a, p, stream);
   if (a.dqk == 128) return pick<128, 128>(a, p, stream);

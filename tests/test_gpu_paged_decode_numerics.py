@@ -74,6 +74,20 @@ def test_soft_caps_of_any_size(splash, cap, kind, Lq, Hq, Hkv, dqk, dv, cols):
     assert (np.abs(o - out) <= (u + 2 * e[..., None]) * A + 2.0 ** -8 * np.abs(out) + 300 * 2.0 ** -25 * 12).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("cap", [1e20, 1e30, 2.4e38, 3.4e38])
+def test_soft_caps_next_to_the_end_of_fp32(splash, cap, kind):
+    """A cap that no score comes near is none: tanh(t) = t in fp32.  Both sides
+    differ by the roundings of scale / cap and of cap log2 e, 2^-22 of a score
+    below 16 together."""
+    x = make([300, 41], 1, 4, 2, 64, 64, 16, kind, seed=520)
+    got = splash.paged_decode(*x[:5], 0.125, softcap=cap, k_scale=x[5], v_scale=x[6])
+    want = splash.paged_decode(*x[:5], 0.125, k_scale=x[5], v_scale=x[6])
+    splash.check_device_error()
+    assert (got[1] - want[1]).abs().max().item() <= 16 * 2.0 ** -22 + 2.0 ** -20
+    assert (got[0].float() - want[0].float()).abs().max().item() <= 2.0 ** -7 * want[0].float().abs().max().item()
+
+
 @pytest.mark.parametrize("Hq", [1, 12, 24])
 def test_one_key_far_above_very_many(splash, Hq):
     """One key 2^26 times as probable as each of the 2^17 - 1 others of an e4m3
