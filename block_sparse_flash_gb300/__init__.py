@@ -5,8 +5,9 @@ This module only marshals arguments, through ctypes and for the serving calls
 through a compiled module (csrc/binding.cpp): torch tensors become device
 pointers, the current torch stream becomes the cudaStream_t.  Every step of the
 computation runs in the library's CUDA kernels (rope_table, a constant laid
-out once, is the exception); there is no CPU or PyTorch fallback.  If the library has not been built, importing works but every call
-raises SplashLibraryMissing.
+out once, is the exception); there is no CPU or PyTorch fallback.  If the
+library has not been built, importing works but every call raises
+SplashLibraryMissing; so do the serving calls without the compiled module.
 
     spec = MaskSpec(causal=True, window_left=4095)
     mi = build_mask_info(spec, L, L, 128, 128)

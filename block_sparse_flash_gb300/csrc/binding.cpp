@@ -4,8 +4,8 @@
 // The rest of the library is called through ctypes.  A serving step's kernels
 // take 2 to 5 us each, and reading some forty tensor attributes from Python
 // took 8 to 10 us a call; here it takes half a microsecond.  Host time of a
-// call: append 10.7 -> 3.0 us, a short rope 13.2 -> 5.2 us, a short decode
-// 13.8 -> 5.4 us, most of it the launch and the outputs' allocation.
+// call: append 10.7 -> 3.0 .. 3.6 us, a short rope 13.2 -> 5.2 .. 6.0, a short
+// decode 13.8 -> 5.4 .. 6.4, most of it the launch and the outputs' allocation.
 //
 // Shapes and types are checked before the device, so that the refusals can be
 // tested without one.  Nothing here computes.

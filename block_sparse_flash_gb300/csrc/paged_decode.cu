@@ -7,10 +7,13 @@
 // Every key and value is used by the Hq/Hkv * Lq rows of its head only, a few
 // FLOP per byte: reading the cache bounds the call, so the kernel is built to
 // keep the memory system full.  64 requests of 64 .. 4096 tokens (32 query, 8 KV
-// heads of 128, bf16) take 90 us, 6.1 TB/s with the launches; 64 requests of up
-// to 32768 tokens with an e4m3 cache 316 us, 6.9 TB/s; DRAM reads are the
-// cache's bytes (546 MB of 546 for the first).  One request of 300 tokens takes
-// 4.7 us: the launch, three dependent reads (length, page, keys) and the join.
+// heads of 128, bf16) take 89 .. 91 us (box to box), 6.1 TB/s with the launches;
+// 64 requests of up to 32768 tokens with an e4m3 cache 316 .. 323 us, 6.8 .. 6.9
+// TB/s; DRAM reads are the cache's bytes (546 MB of 546 for the first).  One
+// request of 300 tokens takes 4.7 us: the launch, three dependent reads (length,
+// page, keys) and the join.  Up to 32 rows share a reading; 64 rows read the cache
+// twice and take twice the time (64 requests of up to 4096 tokens, 64 / 8 heads: 4
+// tokens each 223 us, 8 tokens 465), as their products, not DRAM, bound them.
 //
 //  * Work.  The keys of each (sequence, KV head, group of rows) are cut into
 //    steps of KW keys; all steps form one list, and every warp of a grid that
@@ -26,14 +29,17 @@
 //  * Loads.  Each warp keeps a ring of stages in shared memory, filled by
 //    16-byte asynchronous copies that run ahead of the products and across the
 //    borders of sequences; there is no barrier between warps.  Two CTAs of four
-//    warps with 2 or 3 stages of 8 KB per SM saturate DRAM; more in flight
-//    (prefetching into L2) measured slower.  Rows outside the
-//    keys that some query sees are filled with zeros instead of being read, so
-//    that whatever they hold cannot reach a product.
+//    warps per SM with 2 to 6 stages of 4 to 10 KB saturate DRAM (the 32-row tile of
+//    192-wide heads has room for one CTA); more in flight (prefetching into L2)
+//    measured slower.  Rows outside the keys that some query sees are filled with
+//    zeros instead of being read, so that whatever they hold cannot reach a
+//    product.
 //  * Products.  16 rows x 16 keys per tensor instruction (mma.sync: with 4 to 32
 //    rows a tile is memory-bound many times over, and the accumulators stay in
 //    registers next to the softmax).  P goes to the second product from the
-//    registers that the first one left it in.
+//    registers that the first one left it in.  With two CTAs of 128 threads per
+//    SM a thread has 255 registers: the tiles of 32 rows, and those of several
+//    queries with up to 8 rows, need up to 88 bytes more, which spill.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -1099,7 +1105,9 @@ struct Plan {
 // window of 4096 keys 48.0 -> 42.7; 8 sequences of 1023 .. 8191 keys, 4 tokens
 // each, 33.4 -> 32.6.  A sequence much longer than the others keeps its
 // clusters running alone (2048 keys take a CTA 23 us), so the keys that a CTA may
-// get are limited: 2048, and the ends of a window of that size per CTA.
+// get are limited: 2048, and the ends of a window of that size per CTA.  (Each
+// side was timed with the other one switched off in a copy of this file, for this
+// head layout; other head sizes and e4m3 caches take the same limit.)
 constexpr int kSlots = kMaxWarps / kWarps;  // CTAs that fill the GPU at two per SM
 constexpr int kMaxCluster = 16;             // (with at most 8, 16384 keys of 1 sequence take 24.8 us)
 constexpr int kClusterKeys = 2304;          // per CTA, at most

@@ -7,7 +7,9 @@
 // element on data that is read once and written once, so HBM bounds them:
 // q and k of 2 x 4096 tokens (32 + 8 heads of 128) take 27.5 us, 6.2 TB/s, the
 // gradient of 128 + 128 heads of 192 dimensions 117 us, 6.9 TB/s, a packed
-// prompt of 32768 tokens (16 + 8 + 8 heads, K and V to the cache) 98 us, 6.2 TB/s.
+// prompt of 32768 tokens (16 + 8 + 8 heads, K and V to the cache) 99 us, 6.1 TB/s;
+// the same with an e4m3 cache 133 us, 4.1 TB/s (a division per element and 8-byte
+// stores of the keys).
 // The next token of one request is a launch, 1.9 us.
 //
 // One thread takes 16 elements of a row as two 16-byte chunks: for rotated

@@ -552,8 +552,9 @@ splash_status splash_paged_append(const splash_paged_append_args *args, void *cu
  * 1 <= Lq <= SPLASH_MAX_NEW_TOKENS, page_size a power of two in 16 .. 1024,
  * max_pages * page_size < 2^31 - 65535, B <= 65535, and fewer than 2^31 steps of
  * 16 keys (at most max_pages * page_size / 16 + 1, or window_left / 16 + 4) over
- * all sequences, KV heads and groups of 16 of the Hq/Hkv * Lq rows.  The result does not depend on timing: the same inputs give the
- * same bits on the same GPU.
+ * all sequences, KV heads and groups of 16 of the Hq/Hkv * Lq rows.  The result
+ * does not depend on timing: the same inputs give the same bits on the same GPU.
+ * The cache is read once for every 32 of the Hq/Hkv * Lq rows.
  *
  * Precision: scores, softmax statistics and sums are fp32, out is rounded once.
  * The product with the values takes each probability to 2^-16 of it for a bf16
