@@ -1105,9 +1105,12 @@ struct Plan {
 // window of 4096 keys 48.0 -> 42.7; 8 sequences of 1023 .. 8191 keys, 4 tokens
 // each, 33.4 -> 32.6.  A sequence much longer than the others keeps its
 // clusters running alone (2048 keys take a CTA 23 us), so the keys that a CTA may
-// get are limited: 2048, and the ends of a window of that size per CTA.  (Each
-// side was timed with the other one switched off in a copy of this file, for this
-// head layout; other head sizes and e4m3 caches take the same limit.)
+// get are limited: 2048, and the ends of a window of that size per CTA.  (A block
+// table with more columns takes the list.)  Other layouts take the same limits:
+// 16 / 16 heads of 192: 1 sequence of 2048 keys 12.7 -> 11.5, of 16384 35.0 -> 43.3;
+// 4 / 2 of 64: 7.5 -> 4.6, 24.7 -> 10.3; 4 tokens of 8 / 1 heads of 128: 20.9 -> 16.2,
+// 96.2 -> 31.5; 32 / 8 heads of 128 in e4m3: 9.9 -> 6.7, 20.7 -> 16.3, but 8 sequences
+// of 1023 .. 8191 keys 19.4 -> 24.7.
 constexpr int kSlots = kMaxWarps / kWarps;  // CTAs that fill the GPU at two per SM
 constexpr int kMaxCluster = 16;             // (with at most 8, 16384 keys of 1 sequence take 24.8 us)
 constexpr int kClusterKeys = 2304;          // per CTA, at most
