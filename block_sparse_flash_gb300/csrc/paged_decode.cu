@@ -51,7 +51,6 @@
 #include "dependent_launch.cuh"
 #include "internal.h"
 #include "sm103_ptx.cuh"
-#include "softcap.cuh"
 
 namespace splash {
 namespace {
@@ -257,8 +256,13 @@ __device__ __forceinline__ uint32_t to_half(uint32_t x, uint32_t top) {
   return pack2<true>(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down);
 }
 
-// tanh: by the series up to kTanhSeriesLimit, whose error is relative to x;
-// above it tanh|x| = (1 - e) / (1 + e), e = exp(-2|x|).
+// tanh for the soft cap.  Up to 0.25 the forward's polynomial (attention_fwd.cu):
+// t (1 + u (c1 + c2 u)), u = t^2, a minimax fit of tanh(t)/t with a relative error
+// of 4.8e-7, so that cap * tanh(s / cap) keeps the score's low bits however large
+// the cap; above it tanh|x| = (1 - e) / (1 + e), e = exp(-2|x|), whose error is
+// absolute.
+constexpr float kTanhC1 = -0.33324610f, kTanhC2 = 0.12877172f, kTanhSeriesLimit = 0.25f;
+
 __device__ __forceinline__ float tanh_series(float x) {
   const float u = x * x;
   return fmaf(x * u, fmaf(u, kTanhC2, kTanhC1), x);
@@ -1137,31 +1141,28 @@ Plan plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t d
   return x;
 }
 
-// The largest cluster, of `want` CTAs at most, that the current device can place.
-// More than 8 need not fit (a part of a GPU, say, may not have 16 SMs next to one
-// another); a smaller one does the same with more keys per CTA.
+// The largest cluster that the current device can place.  More than 8 CTAs need
+// not fit (a part of a GPU, say, may not have 16 SMs next to one another); a
+// smaller one does the same with more keys per CTA.
 template <class C>
-splash_status placeable(int want, int *cluster) {
-  *cluster = want;
-  while (*cluster > 1) {
+int placeable() {
+  int cluster = kMaxCluster;
+  for (; cluster > 1; cluster /= 2) {
     cudaLaunchConfig_t config = {};
-    config.gridDim = dim3(*cluster);
+    config.gridDim = dim3(cluster);
     config.blockDim = dim3(kThreads);
     config.dynamicSmemBytes = C::SMEM;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)*cluster;
+    attr.val.clusterDim.x = (unsigned)cluster;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     config.attrs = &attr;
     config.numAttrs = 1;
     int clusters = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, paged_decode_kernel<C, true>, &config);
-    if (e != cudaSuccess && e != cudaErrorInvalidClusterSize) return SPLASH_ERR_CUDA;
-    if (e == cudaSuccess && clusters > 0) break;
-    (void)cudaGetLastError();
-    *cluster /= 2;
+    if (cudaOccupancyMaxActiveClusters(&clusters, paged_decode_kernel<C, true>, &config) == cudaSuccess && clusters > 0) break;
+    (void)cudaGetLastError();  // (what else is wrong shows at the launch)
   }
-  return SPLASH_OK;
+  return cluster;
 }
 
 // grid clusters of `cluster` CTAs each, or of fewer where that has no room.
@@ -1176,8 +1177,7 @@ splash_status launch_kernel(int grid, int cluster, const Params &p, cudaStream_t
     int room = 1;
     if constexpr (TOGETHER) {
       SPLASH_CUDA_TRY(cudaFuncSetAttribute(paged_decode_kernel<C, TOGETHER>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
-      const splash_status st = placeable<C>(kMaxCluster, &room);
-      if (st != SPLASH_OK) return st;
+      room = placeable<C>();
     }
     fits.store((int8_t)room, std::memory_order_release);
   }
