@@ -15,7 +15,9 @@ SplashLibraryMissing; so do the serving calls without the compiled module.
 
 Serving, with positions rotated: rope_fwd / rope_bwd around the attention,
 paged_append for the keys and values of new tokens, paged_decode for their
-attention over the pages.
+attention over the pages.  rope_axes_fwd / rope_axes_bwd / paged_append_axes
+take several position axes, paged_tree_decode a tree of drafted tokens,
+paged_compact, paged_remap and paged_copy keep the pages in order.
 
 C ABI: include/splash.h.
 """
@@ -96,6 +98,10 @@ def lib():
                                             vp, vp, vp, vp, vp, vp, vp, vp]
     L.splash_paged_decode_workspace_size.argtypes = [i32] * 9 + [i64, P(ctypes.c_size_t)]
     L.splash_paged_decode_workspace_size.restype = ctypes.c_int
+    L.splash_paged_tree_decode_workspace_size.argtypes = [i32] * 9 + [i64, P(ctypes.c_size_t)]
+    L.splash_paged_tree_decode_workspace_size.restype = ctypes.c_int
+    L.splash_paged_remap_workspace_size.argtypes = [i64, i32, P(ctypes.c_size_t)]
+    L.splash_paged_remap_workspace_size.restype = ctypes.c_int
     L.splash_attention_merge.argtypes = [vp, vp, i32, i64, i32, vp, vp, vp]
     L.splash_last_device_error.argtypes = [vp]
     L.splash_debug_wait_selftest.argtypes = [ctypes.c_uint64, vp]
@@ -527,22 +533,139 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float, softc
 
 
 @functools.lru_cache(maxsize=256)
-def _paged_decode_workspace_size(*sizes):
+def _decode_workspace_size(name, *sizes):
     n = ctypes.c_size_t(0)
-    _check(lib().splash_paged_decode_workspace_size(*sizes, ctypes.byref(n)), "splash_paged_decode_workspace_size")
+    _check(getattr(lib(), name)(*sizes, ctypes.byref(n)), name)
     return int(n.value)
+
+
+def _workspace_of(name, q, k_cache, v_cache, block_table, window_left):
+    if q.dim() != 4 or k_cache.dim() != 4 or v_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q, k_cache and v_cache must be 4-D and block_table 2-D")
+    if k_cache.dtype not in _CACHE_TYPES:
+        raise ValueError("k_cache and v_cache must be bf16 or float8_e4m3fn tensors")
+    return _decode_workspace_size(name, q.shape[0], q.shape[1], k_cache.shape[1], q.shape[2], q.shape[3],
+                                  v_cache.shape[3], block_table.shape[1], k_cache.shape[2],
+                                  _CACHE_TYPES[k_cache.dtype], int(window_left))
 
 
 def paged_decode_workspace_size(q, k_cache, v_cache, block_table, window_left: int = -1) -> int:
     """Bytes of paged_decode's workspace for tensors of these shapes and types
     (0 where it needs none)."""
-    if q.dim() != 4 or k_cache.dim() != 4 or v_cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("q, k_cache and v_cache must be 4-D and block_table 2-D")
-    if k_cache.dtype not in _CACHE_TYPES:
-        raise ValueError("k_cache and v_cache must be bf16 or float8_e4m3fn tensors")
-    return _paged_decode_workspace_size(q.shape[0], q.shape[1], k_cache.shape[1], q.shape[2], q.shape[3],
-                                        v_cache.shape[3], block_table.shape[1], k_cache.shape[2],
-                                        _CACHE_TYPES[k_cache.dtype], int(window_left))
+    return _workspace_of("splash_paged_decode_workspace_size", q, k_cache, v_cache, block_table, window_left)
+
+
+# ---- several position axes, trees of drafted tokens, upkeep of the paged cache
+
+
+def rope_axis_map(sections, cycled: bool = False) -> bytes:
+    """The `axes` argument of rope_axes_fwd and paged_append_axes: which axis
+    each rotated pair turns by.  sections: pairs of each axis, e.g. (16, 24, 24)
+    for time, height and width; in a row, or (cycled) taking turns from pair to
+    pair until each is used up.  Laid out once."""
+    left = [int(n) for n in sections]
+    if not left or min(left) < 0 or len(left) > 255:
+        raise ValueError("sections must be a pair count for each axis")
+    if not cycled:
+        return bytes(a for a, n in enumerate(left) for _ in range(n))
+    return bytes(a for i in range(max(left)) for a, n in enumerate(left) if i < n)
+
+
+def _rope_axes(inverse, q, k, positions, table, axes, rot_offset, interleaved, q_out, k_out, stream):
+    return (_binding or _native()).rope_axes(q, k, positions, table, axes, rot_offset, interleaved, inverse, q_out, k_out,
+                                             _handle(stream))
+
+
+def rope_axes_fwd(q, k, positions, table, axes, rot_offset: int = 0, interleaved: bool = False, q_out=None, k_out=None,
+                  stream=None):
+    """rope_fwd with several position axes (time, height, width of images and
+    video; splash_rope_axes): pair i turns by positions[axes[i]].  positions:
+    int32 [axes, B, L], up to 4 axes; axes: bytes, one for each pair
+    (rope_axis_map); the others as rope_fwd."""
+    return _rope_axes(0, q, k, positions, table, axes, rot_offset, interleaved, q_out, k_out, stream)
+
+
+def rope_axes_bwd(dq, dk, positions, table, axes, rot_offset: int = 0, interleaved: bool = False, dq_out=None,
+                  dk_out=None, stream=None):
+    """The gradients of rope_axes_fwd's inputs from those of its outputs (the
+    transposed rotation); arguments as rope_axes_fwd."""
+    return _rope_axes(1, dq, dk, positions, table, axes, rot_offset, interleaved, dq_out, dk_out, stream)
+
+
+def paged_append_axes(k, v, k_cache, v_cache, block_table, positions, rot_positions, table, axes, q=None,
+                      rot_offset: int = 0, interleaved: bool = False, seq_ids=None, k_scale=None, v_scale=None,
+                      q_out=None, k_out=None, stream=None):
+    """paged_append where a token's slot and its rotation are apart
+    (splash_paged_append_axes): it is stored at positions [B, L] and turned by
+    rot_positions (int32 [axes, B, L]) as in rope_axes_fwd.  With one axis
+    (axes = rope_axis_map([rot_dim // 2])) this stores a tree of drafts: slots
+    in a row, rotations by depth.  The others as paged_append."""
+    return (_binding or _native()).paged_append_axes(k, v, k_cache, v_cache, block_table, positions, q, table, rot_offset,
+                                                     interleaved, seq_ids, k_scale, v_scale, q_out, k_out,
+                                                     _handle(stream), rot_positions, axes)
+
+
+def paged_tree_decode(q, k_cache, v_cache, block_table, seq_lens, parents, scale: float, softcap: float = 0.0,
+                      window_left: int = -1, k_scale=None, v_scale=None, out=None, lse=None, workspace=None, stream=None):
+    """out [B, Hq, T, dv] bf16 and lse [B, Hq, T] fp32 of a tree of T (1 .. 64)
+    drafted tokens of each sequence, whose keys and values are its newest T
+    cached tokens (splash_paged_tree_decode).
+
+    parents: int32 [B, T] or [T]: the earlier token of the tree that each
+    continues, -1 for the context, below -1 for padding.  A token sees the
+    context, its ancestors and itself.  q [B, Hq, T, dqk]; the others as
+    paged_decode; the workspace is of paged_tree_decode_workspace_size(...)
+    bytes."""
+    return (_binding or _native()).paged_tree_decode(q, k_cache, v_cache, block_table, seq_lens, scale, softcap,
+                                                     window_left, k_scale, v_scale, out, lse, workspace,
+                                                     _handle(stream), parents)
+
+
+def paged_tree_decode_workspace_size(q, k_cache, v_cache, block_table, window_left: int = -1) -> int:
+    """Bytes of paged_tree_decode's workspace for tensors of these shapes and
+    types (0 where it needs none)."""
+    return _workspace_of("splash_paged_tree_decode_workspace_size", q, k_cache, v_cache, block_table, window_left)
+
+
+def paged_compact(k_cache, v_cache, block_table, src, start, stream=None):
+    """Moves tokens inside their sequences (splash_paged_compact): the one at
+    position src[b, m] becomes the one at start[b] + m.  src: int32 [B, moves],
+    ascending, src[b, m] >= start[b] + m, a negative entry ends a row's list;
+    start: int32 [B].  Keeps the accepted branch of a tree of drafts (start =
+    the context's length), or what an eviction leaves.  Caches and block_table
+    as for paged_append (e4m3 without scales: values move as they are)."""
+    (_binding or _native()).paged_compact(k_cache, v_cache, block_table, src, start, _handle(stream))
+
+
+def paged_remap(block_table, parents, keep, room, refs, page_size: int, new_table=None, refs_out=None, copies=None,
+                short=None, workspace=None, stream=None):
+    """(new_table, refs_out, copies, short): forks, extends, truncates, frees
+    and admits sequences (splash_paged_remap).
+
+    Row i of the new table takes over the first keep[i] tokens of row
+    parents[i] of block_table (int32 [rows, max_pages], unused entries -1;
+    negative parent: none) and has pages for max(keep[i], room[i]) tokens.
+    refs: int32 [pages], uses of each page (0: free).  Whole pages are shared;
+    a page kept in part is copied unless the row alone has it.  copies: int32
+    [new rows, 3], to be given to paged_copy for every layer's cache.  short:
+    int32 [1], pages that were missing (then use none of the results)."""
+    return (_binding or _native()).paged_remap(block_table, parents, keep, room, refs, page_size, new_table, refs_out,
+                                               copies, short, workspace, _handle(stream))
+
+
+def paged_remap_workspace_size(num_pages: int, new_rows: int) -> int:
+    """Bytes of paged_remap's workspace."""
+    n = ctypes.c_size_t(0)
+    _check(lib().splash_paged_remap_workspace_size(int(num_pages), int(new_rows), ctypes.byref(n)),
+           "splash_paged_remap_workspace_size")
+    return int(n.value)
+
+
+def paged_copy(k_cache, v_cache, copies, stream=None):
+    """Copies rows between pages (splash_paged_copy): for each (source page,
+    destination page, n) of copies, int32 [count, 3], the first n rows of every
+    head.  Entries of -1 are skipped."""
+    (_binding or _native()).paged_copy(k_cache, v_cache, copies, _handle(stream))
 
 
 def last_device_error(stream=None) -> int:

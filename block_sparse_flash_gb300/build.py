@@ -24,7 +24,8 @@ SOURCES = [("api.cu", "api", []), ("mask_info.cu", "mask_info", []),
            ("attention_fwd.cu", "attention_fwd_band", ["-DSPLASH_FWD_PM=1"]),
            ("attention_fwd.cu", "attention_fwd_band_seg", ["-DSPLASH_FWD_PM=2"]),
            ("attention_bwd.cu", "attention_bwd", []), ("host_pipeline.cu", "host_pipeline", []),
-           ("rope.cu", "rope", []), ("paged_decode.cu", "paged_decode_bf16", ["-DSPLASH_DECODE_E4M3=0"]),
+           ("rope.cu", "rope", []), ("pages.cu", "pages", []), ("tree_decode.cu", "tree_decode", []),
+           ("paged_decode.cu", "paged_decode_bf16", ["-DSPLASH_DECODE_E4M3=0"]),
            ("paged_decode.cu", "paged_decode_e4m3", ["-DSPLASH_DECODE_E4M3=1"])]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # the compiled part of the Python binding, for this Python and this torch

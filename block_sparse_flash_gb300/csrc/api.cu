@@ -482,18 +482,7 @@ splash_status check_pages(const splash_cache_view &k, const splash_cache_view &v
   return check_cache(v, num_pages, Hkv, page_size, dv, type, output);
 }
 
-splash_status current_error_word(uint32_t **err) {
-  int dev = 0;
-  SPLASH_CUDA_TRY(cudaGetDevice(&dev));
-  *err = splash_device_error_word(dev);
-  return *err != nullptr ? SPLASH_OK : SPLASH_ERR_CUDA;
-}
-
-}  // namespace
-
-splash_status splash_rope(const splash_rope_args *args, void *cuda_stream) {
-  if (args == nullptr || args->struct_bytes != sizeof *args) return SPLASH_ERR_INVALID_ARG;
-  const splash_rope_args &a = *args;
+splash_status check_rope(const splash_rope_args &a) {
   const bool has_k = a.k.ptr != nullptr;
   if (a.B <= 0 || a.Hq <= 0 || a.L <= 0 || a.d <= 0 || (has_k && a.Hkv <= 0)) return SPLASH_ERR_INVALID_ARG;
   if (a.positions == nullptr || (addr(a.positions) & 3u) != 0 || (a.B > 1 && a.positions_stride_b < 0))
@@ -509,14 +498,10 @@ splash_status splash_rope(const splash_rope_args *args, void *cuda_stream) {
     if ((st = check_view(a.k, a.B, a.Hkv, a.L, a.d, false)) != SPLASH_OK) return st;
     if ((st = check_out_view(a.k_out, a.k, a.B, a.Hkv, a.L, a.d)) != SPLASH_OK) return st;
   }
-  uint32_t *err = nullptr;
-  if ((st = current_error_word(&err)) != SPLASH_OK) return st;
-  return splash_rope_launch(a, static_cast<cudaStream_t>(cuda_stream), err);
+  return SPLASH_OK;
 }
 
-splash_status splash_paged_append(const splash_paged_append_args *args, void *cuda_stream) {
-  if (args == nullptr || args->struct_bytes != sizeof *args) return SPLASH_ERR_INVALID_ARG;
-  const splash_paged_append_args &a = *args;
+splash_status check_append(const splash_paged_append_args &a) {
   const bool has_q = a.q.ptr != nullptr;
   if (a.B <= 0 || a.Hkv <= 0 || a.L <= 0 || a.dqk <= 0 || a.dv <= 0 || (has_q && a.Hq <= 0))
     return SPLASH_ERR_INVALID_ARG;
@@ -544,28 +529,117 @@ splash_status splash_paged_append(const splash_paged_append_args *args, void *cu
   if (a.k_out.ptr != nullptr &&
       (st = check_out_view(a.k_out, a.k, a.B, a.Hkv, a.L, a.dqk)) != SPLASH_OK)
     return st;
-  uint32_t *err = nullptr;
-  if ((st = current_error_word(&err)) != SPLASH_OK) return st;
-  return splash_paged_append_launch(a, static_cast<cudaStream_t>(cuda_stream), err);
+  return SPLASH_OK;
 }
 
-splash_status splash_paged_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t dv,
-                                                 int32_t max_pages, int32_t page_size, int32_t cache_type,
-                                                 int64_t window_left, size_t *bytes) {
-  if (bytes == nullptr || B <= 0 || Hq <= 0 || Hkv <= 0 || Lq <= 0 || dqk <= 0 || dv <= 0 || max_pages <= 0 ||
-      page_size <= 0 || window_left < -1 || (cache_type != SPLASH_CACHE_BF16 && cache_type != SPLASH_CACHE_E4M3))
+splash_status check_axes(const uint8_t *axes, int32_t num_axes, int32_t rot_dim, const int32_t *positions, int64_t stride_a,
+                         int64_t stride_b, int32_t B, int32_t reserved) {
+  if (axes == nullptr || num_axes <= 0 || reserved != 0 || positions == nullptr || (addr(positions) & 3u) != 0)
+    return SPLASH_ERR_INVALID_ARG;
+  if ((num_axes > 1 && stride_a < 0) || (B > 1 && stride_b < 0)) return SPLASH_ERR_INVALID_ARG;
+  if (num_axes > SPLASH_MAX_AXES) return SPLASH_ERR_UNSUPPORTED;
+  for (int32_t i = 0; i < rot_dim / 2; ++i)
+    if (axes[i] >= num_axes) return SPLASH_ERR_INVALID_ARG;
+  return SPLASH_OK;
+}
+
+// What the attention calls over a paged cache have in common; most: new tokens per sequence.
+splash_status check_decode_sizes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t most, int32_t dqk, int32_t dv,
+                                 int32_t max_pages, int32_t page_size, int32_t cache_type, int64_t window_left) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Lq <= 0 || dqk <= 0 || dv <= 0 || max_pages <= 0 || page_size <= 0 ||
+      window_left < -1 || (cache_type != SPLASH_CACHE_BF16 && cache_type != SPLASH_CACHE_E4M3))
     return SPLASH_ERR_INVALID_ARG;
   if (Hq % Hkv != 0) return SPLASH_ERR_SHAPE;
-  if (Lq > SPLASH_MAX_NEW_TOKENS || B > 65535 || Hq > 65535 || (int64_t)B * Hq * Lq > INT32_MAX)
-    return SPLASH_ERR_UNSUPPORTED;
+  if (Lq > most || B > 65535 || Hq > 65535 || (int64_t)B * Hq * Lq > INT32_MAX) return SPLASH_ERR_UNSUPPORTED;
   if (!((dqk == 64 && dv == 64) || (dqk == 128 && dv == 128) || (dqk == 192 && dv == 128))) return SPLASH_ERR_UNSUPPORTED;
   const splash_status st = check_page_sizes(page_size, max_pages);
   if (st != SPLASH_OK) return st;
   // the kernel's list: 16-key steps of every sequence, head and 16 rows, in 32 bits
   int64_t steps = (int64_t)max_pages * page_size / 16 + 1;
-  if (window_left >= 0) steps = std::min(steps, window_left / 16 + 4);
+  if (window_left >= 0) steps = std::min(steps, window_left / 16 + 4 + (Lq > SPLASH_MAX_NEW_TOKENS ? Lq / 16 : 0));
   const int64_t segments = (int64_t)B * Hkv * (((int64_t)(Hq / Hkv) * Lq + 15) / 16);
-  if (steps > INT32_MAX / segments) return SPLASH_ERR_UNSUPPORTED;
+  return steps > INT32_MAX / segments ? SPLASH_ERR_UNSUPPORTED : SPLASH_OK;
+}
+
+// need: bytes of workspace.
+splash_status check_decode(const splash_paged_decode_args &a, size_t need) {
+  if (need > 0 && (a.workspace == nullptr || a.workspace_bytes < need)) return SPLASH_ERR_INVALID_ARG;
+  const splash_status st =
+      check_pages(a.k_cache, a.v_cache, a.num_pages, a.Hkv, a.page_size, a.dqk, a.dv, a.cache_type, a.k_scale, a.v_scale,
+                  a.block_table, a.block_table_stride, a.B, a.max_pages, false);
+  if (st != SPLASH_OK) return st;
+  return check_view(a.q, a.B, a.Hq, a.Lq, a.dqk, false);
+}
+
+splash_status check_decode_values(const splash_paged_decode_args &a) {
+  if (a.seq_lens == nullptr || a.out == nullptr || a.lse == nullptr || a.reserved != 0) return SPLASH_ERR_INVALID_ARG;
+  if (((addr(a.out) | addr(a.workspace)) & 15u) != 0 || ((addr(a.seq_lens) | addr(a.lse)) & 3u) != 0)
+    return SPLASH_ERR_INVALID_ARG;
+  if (!(a.scale > 0.f) || !(a.scale < INFINITY) || !(a.softcap == a.softcap) || a.softcap == INFINITY)
+    return SPLASH_ERR_INVALID_ARG;
+  return SPLASH_OK;
+}
+
+splash_status current_error_word(uint32_t **err) {
+  int dev = 0;
+  SPLASH_CUDA_TRY(cudaGetDevice(&dev));
+  *err = splash_device_error_word(dev);
+  return *err != nullptr ? SPLASH_OK : SPLASH_ERR_CUDA;
+}
+
+}  // namespace
+
+splash_status splash_rope(const splash_rope_args *args, void *cuda_stream) {
+  if (args == nullptr || args->struct_bytes != sizeof *args) return SPLASH_ERR_INVALID_ARG;
+  splash_status st = check_rope(*args);
+  if (st != SPLASH_OK) return st;
+  uint32_t *err = nullptr;
+  if ((st = current_error_word(&err)) != SPLASH_OK) return st;
+  return splash_rope_launch(*args, static_cast<cudaStream_t>(cuda_stream), err);
+}
+
+splash_status splash_paged_append(const splash_paged_append_args *args, void *cuda_stream) {
+  if (args == nullptr || args->struct_bytes != sizeof *args) return SPLASH_ERR_INVALID_ARG;
+  splash_status st = check_append(*args);
+  if (st != SPLASH_OK) return st;
+  uint32_t *err = nullptr;
+  if ((st = current_error_word(&err)) != SPLASH_OK) return st;
+  return splash_paged_append_launch(*args, static_cast<cudaStream_t>(cuda_stream), err);
+}
+
+splash_status splash_rope_axes(const splash_rope_axes_args *args, void *cuda_stream) {
+  if (args == nullptr || args->struct_bytes != sizeof *args || args->rope.struct_bytes != sizeof args->rope)
+    return SPLASH_ERR_INVALID_ARG;
+  splash_status st = check_rope(args->rope);
+  if (st != SPLASH_OK) return st;
+  st = check_axes(args->axes, args->num_axes, args->rope.rot_dim, args->rope.positions, args->positions_stride_a,
+                  args->rope.positions_stride_b, args->rope.B, args->reserved);
+  if (st != SPLASH_OK) return st;
+  uint32_t *err = nullptr;
+  if ((st = current_error_word(&err)) != SPLASH_OK) return st;
+  return splash_rope_axes_launch(*args, static_cast<cudaStream_t>(cuda_stream), err);
+}
+
+splash_status splash_paged_append_axes(const splash_paged_append_axes_args *args, void *cuda_stream) {
+  if (args == nullptr || args->struct_bytes != sizeof *args || args->append.struct_bytes != sizeof args->append ||
+      args->append.table == nullptr)
+    return SPLASH_ERR_INVALID_ARG;
+  splash_status st = check_append(args->append);
+  if (st != SPLASH_OK) return st;
+  st = check_axes(args->axes, args->num_axes, args->append.rot_dim, args->rot_positions, args->rot_positions_stride_a,
+                  args->rot_positions_stride_b, args->append.B, args->reserved);
+  if (st != SPLASH_OK) return st;
+  uint32_t *err = nullptr;
+  if ((st = current_error_word(&err)) != SPLASH_OK) return st;
+  return splash_paged_append_axes_launch(*args, static_cast<cudaStream_t>(cuda_stream), err);
+}
+
+splash_status splash_paged_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t dv,
+                                                 int32_t max_pages, int32_t page_size, int32_t cache_type,
+                                                 int64_t window_left, size_t *bytes) {
+  if (bytes == nullptr) return SPLASH_ERR_INVALID_ARG;
+  const splash_status st = check_decode_sizes(B, Hq, Hkv, Lq, SPLASH_MAX_NEW_TOKENS, dqk, dv, max_pages, page_size, cache_type, window_left);
+  if (st != SPLASH_OK) return st;
   *bytes = splash_paged_decode_workspace_bytes(B, Hq, Hkv, Lq, dqk, dv, max_pages, page_size, cache_type, window_left);
   return SPLASH_OK;
 }
@@ -573,23 +647,108 @@ splash_status splash_paged_decode_workspace_size(int32_t B, int32_t Hq, int32_t 
 splash_status splash_paged_decode(const splash_paged_decode_args *args, void *cuda_stream) {
   if (args == nullptr || args->struct_bytes != sizeof *args) return SPLASH_ERR_INVALID_ARG;
   const splash_paged_decode_args &a = *args;
-  if (a.seq_lens == nullptr || a.out == nullptr || a.lse == nullptr || a.reserved != 0) return SPLASH_ERR_INVALID_ARG;
-  if (((addr(a.out) | addr(a.workspace)) & 15u) != 0 || ((addr(a.seq_lens) | addr(a.lse)) & 3u) != 0)
-    return SPLASH_ERR_INVALID_ARG;
-  if (!(a.scale > 0.f) || !(a.scale < INFINITY) || !(a.softcap == a.softcap) || a.softcap == INFINITY)
-    return SPLASH_ERR_INVALID_ARG;
-  size_t need = 0;
-  splash_status st = splash_paged_decode_workspace_size(a.B, a.Hq, a.Hkv, a.Lq, a.dqk, a.dv, a.max_pages, a.page_size,
-                                                        a.cache_type, a.window_left, &need);
+  splash_status st = check_decode_values(a);
   if (st != SPLASH_OK) return st;
-  if (need > 0 && (a.workspace == nullptr || a.workspace_bytes < need)) return SPLASH_ERR_INVALID_ARG;
-  if ((st = check_pages(a.k_cache, a.v_cache, a.num_pages, a.Hkv, a.page_size, a.dqk, a.dv, a.cache_type, a.k_scale,
-                        a.v_scale, a.block_table, a.block_table_stride, a.B, a.max_pages, false)) != SPLASH_OK)
-    return st;
-  if ((st = check_view(a.q, a.B, a.Hq, a.Lq, a.dqk, false)) != SPLASH_OK) return st;
+  size_t need = 0;
+  st = splash_paged_decode_workspace_size(a.B, a.Hq, a.Hkv, a.Lq, a.dqk, a.dv, a.max_pages, a.page_size, a.cache_type,
+                                          a.window_left, &need);
+  if (st != SPLASH_OK) return st;
+  if ((st = check_decode(a, need)) != SPLASH_OK) return st;
   uint32_t *err = nullptr;
   if ((st = current_error_word(&err)) != SPLASH_OK) return st;
   return splash_paged_decode_launch(a, static_cast<cudaStream_t>(cuda_stream), err);
+}
+
+splash_status splash_paged_tree_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t dqk, int32_t dv,
+                                                      int32_t max_pages, int32_t page_size, int32_t cache_type,
+                                                      int64_t window_left, size_t *bytes) {
+  if (bytes == nullptr) return SPLASH_ERR_INVALID_ARG;
+  const splash_status st = check_decode_sizes(B, Hq, Hkv, T, SPLASH_MAX_TREE_TOKENS, dqk, dv, max_pages, page_size, cache_type, window_left);
+  if (st != SPLASH_OK) return st;
+  *bytes = splash_paged_tree_decode_workspace_bytes(B, Hq, Hkv, T, dqk, dv, max_pages, page_size, cache_type, window_left);
+  return SPLASH_OK;
+}
+
+splash_status splash_paged_tree_decode(const splash_paged_tree_decode_args *args, void *cuda_stream) {
+  if (args == nullptr || args->struct_bytes != sizeof *args || args->decode.struct_bytes != sizeof args->decode)
+    return SPLASH_ERR_INVALID_ARG;
+  const splash_paged_decode_args &a = args->decode;
+  splash_status st = check_decode_values(a);
+  if (st != SPLASH_OK) return st;
+  if (args->parents == nullptr || (addr(args->parents) & 3u) != 0 || (a.B > 1 && args->parents_stride_b < 0))
+    return SPLASH_ERR_INVALID_ARG;
+  size_t need = 0;
+  st = splash_paged_tree_decode_workspace_size(a.B, a.Hq, a.Hkv, a.Lq, a.dqk, a.dv, a.max_pages, a.page_size, a.cache_type,
+                                               a.window_left, &need);
+  if (st != SPLASH_OK) return st;
+  if ((st = check_decode(a, need)) != SPLASH_OK) return st;
+  uint32_t *err = nullptr;
+  if ((st = current_error_word(&err)) != SPLASH_OK) return st;
+  return splash_paged_tree_decode_launch(*args, static_cast<cudaStream_t>(cuda_stream), err);
+}
+
+splash_status splash_paged_compact(const splash_paged_compact_args *args, void *cuda_stream) {
+  if (args == nullptr || args->struct_bytes != sizeof *args) return SPLASH_ERR_INVALID_ARG;
+  const splash_paged_compact_args &a = *args;
+  if (a.B <= 0 || a.Hkv <= 0 || a.dqk <= 0 || a.dv <= 0 || a.moves <= 0 || a.reserved != 0) return SPLASH_ERR_INVALID_ARG;
+  if (a.src == nullptr || a.start == nullptr || ((addr(a.src) | addr(a.start)) & 3u) != 0 || (a.B > 1 && a.src_stride < 0))
+    return SPLASH_ERR_INVALID_ARG;
+  if (!valid_head_dim(a.dqk) || !valid_head_dim(a.dv) || a.Hkv > 65535 || a.moves > INT32_MAX) return SPLASH_ERR_UNSUPPORTED;
+  // (the scales are not used: values move as they are)
+  const float *scale = reinterpret_cast<const float *>(a.src);
+  splash_status st = check_pages(a.k_cache, a.v_cache, a.num_pages, a.Hkv, a.page_size, a.dqk, a.dv, a.cache_type, scale, scale,
+                                 a.block_table, a.block_table_stride, a.B, a.max_pages, true);
+  if (st != SPLASH_OK) return st;
+  uint32_t *err = nullptr;
+  if ((st = current_error_word(&err)) != SPLASH_OK) return st;
+  return splash_paged_compact_launch(a, static_cast<cudaStream_t>(cuda_stream), err);
+}
+
+splash_status splash_paged_remap_workspace_size(int64_t num_pages, int32_t new_rows, size_t *bytes) {
+  if (bytes == nullptr || num_pages <= 0 || new_rows <= 0) return SPLASH_ERR_INVALID_ARG;
+  if (num_pages > INT32_MAX) return SPLASH_ERR_UNSUPPORTED;
+  *bytes = splash_paged_remap_workspace_bytes(num_pages, new_rows);
+  return SPLASH_OK;
+}
+
+splash_status splash_paged_remap(const splash_paged_remap_args *args, void *cuda_stream) {
+  if (args == nullptr || args->struct_bytes != sizeof *args) return SPLASH_ERR_INVALID_ARG;
+  const splash_paged_remap_args &a = *args;
+  if (a.num_rows < 0 || a.new_rows <= 0 || a.max_pages <= 0 || a.page_size <= 0 || a.num_pages <= 0) return SPLASH_ERR_INVALID_ARG;
+  if ((a.num_rows > 0 && a.block_table == nullptr) || a.new_table == nullptr || a.parents == nullptr || a.keep == nullptr ||
+      a.room == nullptr || a.refs == nullptr || a.refs_out == nullptr || a.copies == nullptr || a.short_pages == nullptr ||
+      a.workspace == nullptr)
+    return SPLASH_ERR_INVALID_ARG;
+  if (((addr(a.block_table) | addr(a.new_table) | addr(a.parents) | addr(a.keep) | addr(a.room) | addr(a.refs) | addr(a.refs_out) |
+        addr(a.copies) | addr(a.short_pages)) & 3u) != 0 ||
+      (addr(a.workspace) & 15u) != 0)
+    return SPLASH_ERR_INVALID_ARG;
+  if ((a.num_rows > 1 && a.block_table_stride < 0) || (a.new_rows > 1 && a.new_table_stride < a.max_pages))
+    return SPLASH_ERR_INVALID_ARG;
+  splash_status st = check_page_sizes(a.page_size, a.max_pages);
+  if (st != SPLASH_OK) return st;
+  if ((int64_t)a.num_rows * a.max_pages > INT32_MAX || (int64_t)a.new_rows * a.max_pages > INT32_MAX) return SPLASH_ERR_UNSUPPORTED;
+  size_t need = 0;
+  if ((st = splash_paged_remap_workspace_size(a.num_pages, a.new_rows, &need)) != SPLASH_OK) return st;
+  if (a.workspace_bytes < need) return SPLASH_ERR_INVALID_ARG;
+  uint32_t *err = nullptr;
+  if ((st = current_error_word(&err)) != SPLASH_OK) return st;
+  return splash_paged_remap_launch(a, static_cast<cudaStream_t>(cuda_stream), err);
+}
+
+splash_status splash_paged_copy(const splash_paged_copy_args *args, void *cuda_stream) {
+  if (args == nullptr || args->struct_bytes != sizeof *args) return SPLASH_ERR_INVALID_ARG;
+  const splash_paged_copy_args &a = *args;
+  if (a.count <= 0 || a.Hkv <= 0 || a.dqk <= 0 || a.dv <= 0 || a.copies == nullptr || (addr(a.copies) & 3u) != 0)
+    return SPLASH_ERR_INVALID_ARG;
+  if (!valid_head_dim(a.dqk) || !valid_head_dim(a.dv) || a.Hkv > 65535) return SPLASH_ERR_UNSUPPORTED;
+  const float *scale = reinterpret_cast<const float *>(a.copies);  // (not used)
+  splash_status st = check_pages(a.k_cache, a.v_cache, a.num_pages, a.Hkv, a.page_size, a.dqk, a.dv, a.cache_type, scale, scale,
+                                 a.copies, 0, 1, 1, true);
+  if (st != SPLASH_OK) return st;
+  uint32_t *err = nullptr;
+  if ((st = current_error_word(&err)) != SPLASH_OK) return st;
+  return splash_paged_copy_launch(a, static_cast<cudaStream_t>(cuda_stream), err);
 }
 
 splash_status splash_last_device_error(void *cuda_stream) {

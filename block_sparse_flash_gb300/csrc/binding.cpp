@@ -94,6 +94,25 @@ struct Call {
     return {t.data_ptr(), s[0], s[1], s[2]};
   }
 
+  // int32 [axes, B, L]
+  const int32_t *axis_index(PyObject *x, const char *name, int64_t B, int64_t L, int64_t *axes, int64_t *stride_a, int64_t *stride_b) {
+    const at::Tensor &t = tensor(x, name);
+    if (t.scalar_type() != at::kInt || t.dim() != 3 || t.size(0) < 1 || t.size(1) != B || t.size(2) != L || (L > 1 && t.stride(2) != 1))
+      value_error(std::string(name) + " must be an int32 tensor [axes, " + std::to_string(B) + ", " + std::to_string(L) +
+                  "], contiguous in its last dimension (got " + text(t.sizes()) + ")");
+    *axes = t.size(0);
+    *stride_a = t.stride(0);
+    *stride_b = t.stride(1);
+    return static_cast<const int32_t *>(take(t).data_ptr());
+  }
+
+  // A contiguous int32 tensor of a shape.
+  int32_t *ints(const at::Tensor &t, const char *name, at::IntArrayRef shape) {
+    if (t.scalar_type() != at::kInt || t.sizes() != shape || !t.is_contiguous())
+      value_error(std::string(name) + " must be a contiguous int32 tensor of shape " + text(shape) + " (got " + text(t.sizes()) + ")");
+    return static_cast<int32_t *>(take(t).data_ptr());
+  }
+
   // int32 [B, L] or [L]
   const int32_t *index(PyObject *x, const char *name, int64_t B, int64_t L, int64_t *stride) {
     const at::Tensor &t = tensor(x, name);
@@ -123,9 +142,9 @@ struct Call {
     value_error(std::string(name) + " must be a contiguous fp32 tensor of shape " + text({heads}) + " for an e4m3 cache");
   }
 
-  // The caches' part of an argument struct.
+  // The caches of an argument struct; returns whether they are e4m3.
   template <class Args>
-  void caches(Args &a, PyObject *kx, PyObject *vx, PyObject *ks, PyObject *vs) {
+  bool cache_pair(Args &a, PyObject *kx, PyObject *vx) {
     const at::Tensor &k = tensor(kx, "k_cache"), &v = tensor(vx, "v_cache");
     const auto type = k.scalar_type();
     const bool e4m3 = type == at::kFloat8_e4m3fn;
@@ -144,9 +163,15 @@ struct Call {
     a.dqk = (int32_t)shape[3];
     a.dv = (int32_t)v.size(3);
     a.cache_type = e4m3 ? SPLASH_CACHE_E4M3 : SPLASH_CACHE_BF16;
-    if (e4m3) {
-      a.k_scale = scale(ks, "k_scale", shape[1]);
-      a.v_scale = scale(vs, "v_scale", shape[1]);
+    return e4m3;
+  }
+
+  // The same with their scales.
+  template <class Args>
+  void caches(Args &a, PyObject *kx, PyObject *vx, PyObject *ks, PyObject *vs) {
+    if (cache_pair(a, kx, vx)) {
+      a.k_scale = scale(ks, "k_scale", a.Hkv);
+      a.v_scale = scale(vs, "v_scale", a.Hkv);
     } else if (ks != Py_None || vs != Py_None) {
       value_error("k_scale and v_scale belong to an e4m3 cache");
     }
@@ -168,6 +193,17 @@ struct Call {
 int32_t size32(int64_t v, const char *name) {
   if (v > INT32_MAX) value_error(std::string(name) + " is too large");
   return (int32_t)v;
+}
+
+// The axis of each rotated pair, as bytes; the library checks their values.
+const uint8_t *axis_map(PyObject *x, int64_t rot) {
+  char *p = nullptr;
+  Py_ssize_t n = 0;
+  if (!PyBytes_Check(x) || PyBytes_AsStringAndSize(x, &p, &n) != 0 || n != rot / 2) {
+    PyErr_Clear();
+    value_error("axes must be bytes, an axis for each of the table's " + std::to_string(rot / 2) + " pairs (rope_axis_map)");
+  }
+  return reinterpret_cast<const uint8_t *>(p);
 }
 
 // A new tensor of the call, or the given one.
@@ -235,11 +271,16 @@ void count(Py_ssize_t n, Py_ssize_t want) {
   }
 }
 
-// rope(q, k, positions, table, rot_offset, interleaved, inverse, q_out, k_out, stream)
+// rope(q, k, positions, table, rot_offset, interleaved, inverse, q_out, k_out, stream), with `axes` after the table
+// for several of them
+template <bool AXES>
 PyObject *rope(PyObject *const *x, Py_ssize_t n) {
-  count(n, 10);
+  count(n, AXES ? 11 : 10);
+  PyObject *const *y = AXES ? x + 1 : x;  // the arguments behind the table
   Call c;
-  splash_rope_args a = {};
+  splash_rope_axes_args all = {};
+  all.struct_bytes = sizeof all;
+  splash_rope_args &a = all.rope;
   a.struct_bytes = sizeof a;
   const at::Tensor &q = tensor(x[0], "q");
   if (q.dim() != 4) value_error("q must be 4-D");
@@ -256,19 +297,25 @@ PyObject *rope(PyObject *const *x, Py_ssize_t n) {
     if (k->dim() != 4) value_error("k must be 4-D");
     a.Hkv = size32(k->size(1), "Hkv");
     a.k = c.view(*k, "k", {shape[0], k->size(1), shape[2], shape[3]});
-  } else if (x[8] != Py_None) {
+  } else if (y[8] != Py_None) {
     value_error("k_out without k");
   }
-  a.positions = c.index(x[2], "positions", shape[0], shape[2], &a.positions_stride_b);
+  int64_t axes = 0;
+  a.positions = AXES ? c.axis_index(x[2], "positions", shape[0], shape[2], &axes, &all.positions_stride_a, &a.positions_stride_b)
+                     : c.index(x[2], "positions", shape[0], shape[2], &a.positions_stride_b);
   a.table = c.table(x[3], &a.table_rows, &a.rot_dim);
-  a.rot_offset = integer32(x[4], "rot_offset");
-  a.interleaved = truth(x[5]);
-  a.inverse = truth(x[6]);
-  Output qo{x[7] != Py_None ? x[7] : nullptr, {}}, ko{x[8] != Py_None || !has_k ? x[8] : nullptr, {}};
-  if (qo.object != nullptr) a.q_out = c.view(tensor(x[7], "q_out"), "q_out", shape);
-  if (has_k && ko.object != nullptr) a.k_out = c.view(tensor(x[8], "k_out"), "k_out", k->sizes());
+  if (AXES) {
+    all.axes = axis_map(x[4], a.rot_dim);
+    all.num_axes = size32(axes, "positions");
+  }
+  a.rot_offset = integer32(y[4], "rot_offset");
+  a.interleaved = truth(y[5]);
+  a.inverse = truth(y[6]);
+  Output qo{y[7] != Py_None ? y[7] : nullptr, {}}, ko{y[8] != Py_None || !has_k ? y[8] : nullptr, {}};
+  if (qo.object != nullptr) a.q_out = c.view(tensor(y[7], "q_out"), "q_out", shape);
+  if (has_k && ko.object != nullptr) a.k_out = c.view(tensor(y[8], "k_out"), "k_out", k->sizes());
   c.check_device();
-  const Stream stream(x[9]);
+  const Stream stream(y[9]);
   const int64_t row = shape[3], head = shape[2] * row;
   if (qo.object == nullptr) {
     qo.made = stream.make(shape, at::kBFloat16, q);
@@ -278,16 +325,22 @@ PyObject *rope(PyObject *const *x, Py_ssize_t n) {
     ko.made = stream.make(k->sizes(), at::kBFloat16, q);
     a.k_out = {ko.made.data_ptr(), k->size(1) * head, head, row};
   }
-  run(splash_rope, a, stream, "splash_rope");
+  if (AXES)
+    run(splash_rope_axes, all, stream, "splash_rope_axes");
+  else
+    run(splash_rope, a, stream, "splash_rope");
   return pair(qo, ko);
 }
 
 // paged_append(k, v, k_cache, v_cache, block_table, positions, q, table, rot_offset, interleaved, seq_ids,
-//              k_scale, v_scale, q_out, k_out, stream)
+//              k_scale, v_scale, q_out, k_out, stream), with `rot_positions, axes` at the end for several axes
+template <bool AXES>
 PyObject *paged_append(PyObject *const *x, Py_ssize_t n) {
-  count(n, 16);
+  count(n, AXES ? 18 : 16);
   Call c;
-  splash_paged_append_args a = {};
+  splash_paged_append_axes_args all = {};
+  all.struct_bytes = sizeof all;
+  splash_paged_append_args &a = all.append;
   a.struct_bytes = sizeof a;
   c.caches(a, x[2], x[3], x[11], x[12]);
   const at::Tensor &k = tensor(x[0], "k"), &v = tensor(x[1], "v");
@@ -300,7 +353,13 @@ PyObject *paged_append(PyObject *const *x, Py_ssize_t n) {
   a.num_seqs = (int32_t)c.block_table(a, x[4]);
   a.positions = c.index(x[5], "positions", B, L, &a.positions_stride_b);
   if (x[10] != Py_None) a.seq_ids = c.index(x[10], "seq_ids", B, L, &a.seq_ids_stride_b);
-  if (x[7] != Py_None) a.table = c.table(x[7], &a.table_rows, &a.rot_dim);
+  if (AXES || x[7] != Py_None) a.table = c.table(x[7], &a.table_rows, &a.rot_dim);
+  if (AXES) {
+    int64_t axes = 0;
+    all.rot_positions = c.axis_index(x[16], "rot_positions", B, L, &axes, &all.rot_positions_stride_a, &all.rot_positions_stride_b);
+    all.axes = axis_map(x[17], a.rot_dim);
+    all.num_axes = size32(axes, "rot_positions");
+  }
   a.rot_offset = integer32(x[8], "rot_offset");
   a.interleaved = truth(x[9]);
   const bool has_q = x[6] != Py_None;
@@ -322,16 +381,22 @@ PyObject *paged_append(PyObject *const *x, Py_ssize_t n) {
     qo.made = stream.make(q->sizes(), at::kBFloat16, k);
     a.q_out = {qo.made.data_ptr(), q->size(1) * L * a.dqk, L * a.dqk, a.dqk};
   }
-  run(splash_paged_append, a, stream, "splash_paged_append");
+  if (AXES)
+    run(splash_paged_append_axes, all, stream, "splash_paged_append_axes");
+  else
+    run(splash_paged_append, a, stream, "splash_paged_append");
   return pair(qo, ko);
 }
 
 // paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, softcap, window_left, k_scale, v_scale,
-//              out, lse, workspace, stream)
+//              out, lse, workspace, stream), with `parents` at the end for a tree
+template <bool TREE>
 PyObject *paged_decode(PyObject *const *x, Py_ssize_t n) {
-  count(n, 14);
+  count(n, TREE ? 15 : 14);
   Call c;
-  splash_paged_decode_args a = {};
+  splash_paged_tree_decode_args all = {};
+  all.struct_bytes = sizeof all;
+  splash_paged_decode_args &a = all.decode;
   a.struct_bytes = sizeof a;
   c.caches(a, x[1], x[2], x[8], x[9]);
   const at::Tensor &q = tensor(x[0], "q");
@@ -346,6 +411,7 @@ PyObject *paged_decode(PyObject *const *x, Py_ssize_t n) {
   if (lens.scalar_type() != at::kInt || lens.dim() != 1 || lens.size(0) != B || !lens.is_contiguous())
     value_error("seq_lens must be a contiguous int32 tensor of shape " + text({B}));
   a.seq_lens = static_cast<const int32_t *>(c.take(lens).data_ptr());
+  if (TREE) all.parents = c.index(x[14], "parents", B, Lq, &all.parents_stride_b);
   a.scale = number(x[5]);
   a.softcap = number(x[6]);
   a.window_left = integer(x[7]);
@@ -375,8 +441,8 @@ PyObject *paged_decode(PyObject *const *x, Py_ssize_t n) {
   at::Tensor workspace;
   if (x[12] == Py_None) {
     size_t bytes = 0;  // (an error here is the call's own: it is reported there)
-    splash_paged_decode_workspace_size(a.B, a.Hq, a.Hkv, a.Lq, a.dqk, a.dv, a.max_pages, a.page_size, a.cache_type,
-                                       a.window_left, &bytes);
+    const auto size = TREE ? splash_paged_tree_decode_workspace_size : splash_paged_decode_workspace_size;
+    size(a.B, a.Hq, a.Hkv, a.Lq, a.dqk, a.dv, a.max_pages, a.page_size, a.cache_type, a.window_left, &bytes);
     if (bytes > 0) {
       workspace = stream.make({(int64_t)bytes}, at::kByte, q);
       a.workspace = workspace.data_ptr();
@@ -391,8 +457,112 @@ PyObject *paged_decode(PyObject *const *x, Py_ssize_t n) {
     lse.made = stream.make(rows, at::kFloat, q);
     a.lse = static_cast<float *>(lse.made.data_ptr());
   }
-  run(splash_paged_decode, a, stream, "splash_paged_decode");
+  if (TREE)
+    run(splash_paged_tree_decode, all, stream, "splash_paged_tree_decode");
+  else
+    run(splash_paged_decode, a, stream, "splash_paged_decode");
   return pair(out, lse);
+}
+
+// paged_compact(k_cache, v_cache, block_table, src, start, stream)
+PyObject *paged_compact(PyObject *const *x, Py_ssize_t n) {
+  count(n, 6);
+  Call c;
+  splash_paged_compact_args a = {};
+  a.struct_bytes = sizeof a;
+  c.cache_pair(a, x[0], x[1]);
+  const int64_t B = c.block_table(a, x[2]);
+  a.B = size32(B, "B");
+  const at::Tensor &src = tensor(x[3], "src");
+  if (src.scalar_type() != at::kInt || src.dim() != 2 || src.size(0) != B || (src.size(1) > 1 && src.stride(1) != 1))
+    value_error("src must be an int32 tensor [" + std::to_string(B) + ", moves], contiguous in its last dimension (got " +
+                text(src.sizes()) + ")");
+  a.src = static_cast<const int32_t *>(c.take(src).data_ptr());
+  a.src_stride = src.stride(0);
+  a.moves = src.size(1);
+  a.start = c.ints(tensor(x[4], "start"), "start", {B});
+  c.check_device();
+  const Stream stream(x[5]);
+  run(splash_paged_compact, a, stream, "splash_paged_compact");
+  Py_RETURN_NONE;
+}
+
+// paged_copy(k_cache, v_cache, copies, stream)
+PyObject *paged_copy(PyObject *const *x, Py_ssize_t n) {
+  count(n, 4);
+  Call c;
+  splash_paged_copy_args a = {};
+  a.struct_bytes = sizeof a;
+  c.cache_pair(a, x[0], x[1]);
+  const at::Tensor &copies = tensor(x[2], "copies");
+  const int64_t rows = copies.dim() == 2 ? copies.size(0) : 0;
+  a.copies = c.ints(copies, "copies", {rows, 3});
+  a.count = size32(rows, "copies");
+  c.check_device();
+  const Stream stream(x[3]);
+  run(splash_paged_copy, a, stream, "splash_paged_copy");
+  Py_RETURN_NONE;
+}
+
+// paged_remap(block_table, parents, keep, room, refs, page_size, new_table, refs_out, copies, short, workspace, stream)
+PyObject *paged_remap(PyObject *const *x, Py_ssize_t n) {
+  count(n, 12);
+  Call c;
+  splash_paged_remap_args a = {};
+  a.struct_bytes = sizeof a;
+  a.num_rows = (int32_t)c.block_table(a, x[0]);
+  const at::Tensor &parents = tensor(x[1], "parents"), &refs = tensor(x[4], "refs");
+  if (parents.dim() != 1) value_error("parents must be 1-D");
+  if (refs.dim() != 1) value_error("refs must be 1-D");
+  const int64_t rows = parents.size(0), pages = refs.size(0);
+  a.new_rows = size32(rows, "parents");
+  a.num_pages = pages;
+  a.parents = c.ints(parents, "parents", {rows});
+  a.keep = c.ints(tensor(x[2], "keep"), "keep", {rows});
+  a.room = c.ints(tensor(x[3], "room"), "room", {rows});
+  a.refs = c.ints(refs, "refs", {pages});
+  a.page_size = integer32(x[5], "page_size");
+  Output made[4];
+  const int64_t shapes[4][2] = {{rows, a.max_pages}, {pages, 0}, {rows, 3}, {1, 0}};
+  const char *const names[4] = {"new_table", "refs_out", "copies", "short"};
+  int32_t **const ptrs[4] = {&a.new_table, &a.refs_out, &a.copies, &a.short_pages};
+  for (int i = 0; i < 4; ++i) {
+    made[i].object = x[6 + i] != Py_None ? x[6 + i] : nullptr;
+    if (made[i].object != nullptr) *ptrs[i] = c.ints(tensor(x[6 + i], names[i]), names[i], at::IntArrayRef(shapes[i], i % 2 ? 1 : 2));
+  }
+  if (x[10] != Py_None) {
+    const at::Tensor &t = tensor(x[10], "workspace");
+    if (!t.is_contiguous()) value_error("workspace must be contiguous");
+    a.workspace = c.take(t).data_ptr();
+    a.workspace_bytes = t.nbytes();
+  }
+  c.check_device();
+  a.new_table_stride = a.max_pages;
+  const Stream stream(x[11]);
+  at::Tensor workspace;
+  if (x[10] == Py_None) {
+    size_t bytes = 0;  // (an error here is the call's own: it is reported there)
+    splash_paged_remap_workspace_size(a.num_pages, a.new_rows, &bytes);
+    workspace = stream.make({(int64_t)bytes}, at::kByte, refs);
+    a.workspace = workspace.data_ptr();
+    a.workspace_bytes = bytes;
+  }
+  for (int i = 0; i < 4; ++i) {
+    if (made[i].object != nullptr) continue;
+    made[i].made = stream.make(at::IntArrayRef(shapes[i], i % 2 ? 1 : 2), at::kInt, refs);
+    *ptrs[i] = static_cast<int32_t *>(made[i].made.data_ptr());
+  }
+  run(splash_paged_remap, a, stream, "splash_paged_remap");
+  PyObject *t = PyTuple_New(4);
+  for (int i = 0; t != nullptr && i < 4; ++i) {
+    PyObject *o = made[i].python();
+    if (o == nullptr) {
+      Py_DECREF(t);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(t, i, o);
+  }
+  return t;
 }
 
 // No C++ exception reaches Python's frames: torch's become its Python errors.
@@ -419,9 +589,15 @@ PyCFunction entry() {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&guarded<F>));
 }
 
-PyMethodDef methods[] = {{"rope", entry<rope>(), METH_FASTCALL, nullptr},
-                         {"paged_append", entry<paged_append>(), METH_FASTCALL, nullptr},
-                         {"paged_decode", entry<paged_decode>(), METH_FASTCALL, nullptr},
+PyMethodDef methods[] = {{"rope", entry<rope<false>>(), METH_FASTCALL, nullptr},
+                         {"rope_axes", entry<rope<true>>(), METH_FASTCALL, nullptr},
+                         {"paged_append", entry<paged_append<false>>(), METH_FASTCALL, nullptr},
+                         {"paged_append_axes", entry<paged_append<true>>(), METH_FASTCALL, nullptr},
+                         {"paged_decode", entry<paged_decode<false>>(), METH_FASTCALL, nullptr},
+                         {"paged_tree_decode", entry<paged_decode<true>>(), METH_FASTCALL, nullptr},
+                         {"paged_compact", entry<paged_compact>(), METH_FASTCALL, nullptr},
+                         {"paged_copy", entry<paged_copy>(), METH_FASTCALL, nullptr},
+                         {"paged_remap", entry<paged_remap>(), METH_FASTCALL, nullptr},
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

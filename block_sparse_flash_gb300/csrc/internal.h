@@ -167,6 +167,18 @@ splash_status splash_paged_decode_launch_e4m3(const splash_paged_decode_args &a,
 size_t splash_paged_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t dv,
                                            int32_t max_pages, int32_t page_size, int32_t type, int64_t window);
 
+splash_status splash_rope_axes_launch(const splash_rope_axes_args &a, cudaStream_t stream, uint32_t *err_word);
+splash_status splash_paged_append_axes_launch(const splash_paged_append_axes_args &a, cudaStream_t stream, uint32_t *err_word);
+
+// tree_decode.cu, pages.cu (arguments checked in api.cu)
+splash_status splash_paged_tree_decode_launch(const splash_paged_tree_decode_args &a, cudaStream_t stream, uint32_t *err_word);
+size_t splash_paged_tree_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t dqk, int32_t dv,
+                                                int32_t max_pages, int32_t page_size, int32_t type, int64_t window);
+splash_status splash_paged_compact_launch(const splash_paged_compact_args &a, cudaStream_t stream, uint32_t *err_word);
+splash_status splash_paged_remap_launch(const splash_paged_remap_args &a, cudaStream_t stream, uint32_t *err_word);
+size_t splash_paged_remap_workspace_bytes(int64_t num_pages, int32_t new_rows);
+splash_status splash_paged_copy_launch(const splash_paged_copy_args &a, cudaStream_t stream, uint32_t *err_word);
+
 // Counts kernel launches (splash_kernel_launches); call once per launch.
 void splash_count_launches(uint64_t n);
 

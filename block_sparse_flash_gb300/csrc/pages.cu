@@ -1,0 +1,491 @@
+// pages.cu -- the upkeep of a paged cache: remapping block tables (forks,
+// growth, truncation, release), copying pages and compacting sequences
+// (splash_paged_remap, splash_paged_copy and splash_paged_compact in splash.h).
+//
+// None of them computes; they read and write each byte once, so HBM bounds the
+// large ones and the chain of dependent reads the small ones.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "dependent_launch.cuh"
+#include "internal.h"
+
+namespace splash {
+namespace {
+
+struct Cache {
+  char *ptr;
+  int64_t page, head, token;  // byte strides
+  int32_t chunks;             // 16-byte chunks of a row
+};
+
+Cache cache(const splash_cache_view &v, int64_t size, int32_t d) {
+  return {static_cast<char *>(v.ptr), size * v.stride_page, size * v.stride_head, size * v.stride_token, (int32_t)(d * size / 16)};
+}
+
+// ------------------------------------------------------------------ compact
+constexpr int kMoveThreads = 256, kMoveRows = 256;  // most tokens of a batch
+constexpr int kMovesEach = 4;                       // chunks that a thread has in flight
+
+struct CompactParams {
+  Cache k, v;
+  int32_t k_slices, v_slices;  // groups of up to 8 chunk columns (128 bytes)
+  const int32_t *block_table, *src, *start;
+  int64_t block_table_stride, src_stride, num_pages;
+  int64_t moves;
+  int32_t max_pages, page_shift;
+  uint32_t *err;
+};
+
+// A move's places: byte offsets of the rows, from < 0: nothing to do.
+struct Move {
+  int64_t from, to;
+};
+
+// CTA (sequence, head, slice): the slice's columns of all moves in order, in
+// batches.  A batch is read into registers before any of it is written; what it
+// overwrites (start + m <= src[m]) was read in it or before, and what later
+// batches read (src > src[m]) is not overwritten by it, so that one barrier per
+// batch is enough.  The places of the next batch (three dependent reads) are
+// looked up while this one's data is on the way.
+__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactParams p) {
+  __shared__ Move s_move[2][kMoveRows];
+  __shared__ int s_end[2];
+  grid_dependency();
+  const int tid = threadIdx.x, head = blockIdx.y;
+  const int64_t b = blockIdx.x;
+  const bool is_v = (int)blockIdx.z >= p.k_slices;
+  const Cache &c = is_v ? p.v : p.k;
+  const int slices = is_v ? p.v_slices : p.k_slices, slice = is_v ? blockIdx.z - p.k_slices : blockIdx.z;
+  const int width = (c.chunks + slices - 1) / slices;  // columns of a slice
+  const int column = slice * width + tid % width, lane = tid / width, lanes = kMoveThreads / width;
+  const int batch = min(kMovesEach * lanes, kMoveRows);
+  const bool works = lane < lanes && column < c.chunks;
+  char *base = c.ptr + head * c.head + column * 16;
+  const int32_t *src = p.src + b * p.src_stride, *pages = p.block_table + b * p.block_table_stride;
+  const int64_t first = p.start[b], limit = (int64_t)p.max_pages << p.page_shift;
+  const int32_t in_page = (1 << p.page_shift) - 1;
+  const bool reports = head == 0 && blockIdx.z == 0;
+
+  // Move m of the list; *stop: the list ends here, *bad: for a reason that is reported.
+  auto place = [&](int64_t m, bool *stop, bool *bad) {
+    Move x = {-1, -1};
+    *stop = true;
+    *bad = false;
+    const int32_t s = src[m];
+    if (s < 0) return x;
+    const int64_t d = first + m;
+    *bad = first < 0 || s < d || s >= limit || (m > 0 && src[m - 1] >= s);
+    if (*bad) return x;
+    const int64_t from = pages[s >> p.page_shift], to = pages[d >> p.page_shift];
+    *bad = from < 0 || from >= p.num_pages || to < 0 || to >= p.num_pages;
+    if (*bad) return x;
+    *stop = false;
+    if (s == d) return x;
+    x.from = from * c.page + (s & in_page) * c.token;
+    x.to = to * c.page + (d & in_page) * c.token;
+    return x;
+  };
+  // The places of batch [m0, m0 + batch) into s_move[half]; s_end[half]: the list's end in it.
+  auto look = [&](int64_t m0, int half) {
+    if (tid >= batch || m0 + tid >= p.moves) return;
+    bool stop, bad;
+    const Move x = place(m0 + tid, &stop, &bad);
+    s_move[half][tid] = x;
+    if (stop) {
+      // (an entry behind the list's end is not reported: the first one that ends it is)
+      const int before = atomicMin(&s_end[half], 2 * tid + (bad ? 1 : 0));
+      (void)before;
+    }
+  };
+
+  if (tid < 2) s_end[tid] = INT_MAX;
+  __syncthreads();
+  look(0, 0);
+  __syncthreads();
+  int half = 0;
+  for (int64_t m0 = 0; m0 < p.moves; m0 += batch) {
+    const int end = s_end[half];  // 2 * index + reported, INT_MAX: none
+    const int n = (int)min((int64_t)batch, p.moves - m0);
+    const int count = end == INT_MAX ? n : end >> 1;
+    uint4 x[kMovesEach];
+    bool live[kMovesEach];
+    int64_t to[kMovesEach];
+#pragma unroll
+    for (int i = 0; i < kMovesEach; ++i) {
+      const int m = i * lanes + lane;
+      live[i] = works && m < count && m < batch;
+      if (live[i]) {
+        const Move y = s_move[half][m];
+        live[i] = y.from >= 0;
+        to[i] = y.to;
+        if (live[i]) x[i] = *reinterpret_cast<const uint4 *>(base + y.from);
+      }
+    }
+    const bool more = end == INT_MAX && m0 + batch < p.moves;
+    if (more) look(m0 + batch, half ^ 1);
+    if (end != INT_MAX && (end & 1) && reports && tid == 0) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
+    __syncthreads();  // everything of this batch is read, the next one's places are known
+#pragma unroll
+    for (int i = 0; i < kMovesEach; ++i)
+      if (live[i]) *reinterpret_cast<uint4 *>(base + to[i]) = x[i];
+    if (!more) return;
+    half ^= 1;
+  }
+}
+
+// ------------------------------------------------------------------ copy
+constexpr int kCopyThreads = 256, kCopyEach = 4;
+
+struct CopyParams {
+  Cache k, v;
+  const int32_t *copies;
+  int64_t num_pages;
+  int32_t page_size;
+  uint32_t *err;
+};
+
+// CTA (entry, head, K or V).
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) {
+  grid_dependency();
+  const int32_t *entry = p.copies + 3 * (int64_t)blockIdx.x;
+  const int32_t from = entry[0], to = entry[1], rows = entry[2];
+  if (from < 0 || to < 0 || rows <= 0) return;
+  if (from >= p.num_pages || to >= p.num_pages || rows > p.page_size) {
+    if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
+    return;
+  }
+  if (from == to) return;
+  const Cache &c = blockIdx.z == 0 ? p.k : p.v;
+  const char *src = c.ptr + from * c.page + blockIdx.y * c.head;
+  char *dst = c.ptr + to * c.page + blockIdx.y * c.head;
+  const int n = rows * c.chunks;  // (at most 1024 rows of 64)
+  for (int i0 = threadIdx.x; i0 < n; i0 += kCopyThreads * kCopyEach) {
+    uint4 x[kCopyEach];
+    int64_t at[kCopyEach];
+#pragma unroll
+    for (int k = 0; k < kCopyEach; ++k) {
+      const int i = i0 + k * kCopyThreads;
+      if (i < n) {
+        const int row = i / c.chunks;
+        at[k] = row * c.token + (i - row * c.chunks) * 16;
+        x[k] = *reinterpret_cast<const uint4 *>(src + at[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kCopyEach; ++k)
+      if (i0 + k * kCopyThreads < n) *reinterpret_cast<uint4 *>(dst + at[k]) = x[k];
+  }
+}
+
+// ------------------------------------------------------------------ remap
+constexpr int kMapThreads = 1024, kMapCtas = 8, kMapWarps = kMapThreads / 32;
+constexpr int kPagesEach = 4;  // pages of a thread in a scan's round
+
+struct RemapParams {
+  const int32_t *block_table;
+  int64_t block_table_stride;
+  int32_t *new_table;
+  int64_t new_table_stride;
+  const int32_t *parents, *keep, *room, *refs;
+  int32_t *refs_out, *copies, *short_pages;
+  // workspace: per page its uses, the rows that keep part of it and the first of them; the
+  // fresh pages in order; per row the fresh pages before it, from its CTA's first row on
+  int32_t *uses, *parts, *first, *fresh, *before;
+  int32_t *totals;  // [2][kMapCtas]: free pages, needed pages of each CTA's share
+  int64_t num_pages;
+  int32_t num_rows, new_rows, max_pages, page_shift;
+  uint32_t *err;
+};
+
+__device__ __forceinline__ void cluster_sync_global() {
+  __threadfence();
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Sum over the CTA's threads before this one, and *all of them.
+__device__ __forceinline__ int32_t scan(int32_t x, int32_t *s_warp, int32_t *all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int32_t y = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t z = __shfl_up_sync(~0u, y, o);
+    if (lane >= o) y += z;
+  }
+  if (lane == 31) s_warp[warp] = y;
+  __syncthreads();
+  int32_t w = s_warp[lane], total = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t z = __shfl_up_sync(~0u, total, o);
+    if (lane >= o) total += z;
+  }
+  *all = __shfl_sync(~0u, total, 31);
+  const int32_t base = __shfl_sync(~0u, total - w, warp);
+  __syncthreads();  // (s_warp is used again)
+  return base + y - x;
+}
+
+// What a new row takes over, in tokens and columns.
+struct Row {
+  int32_t parent;           // -1: none
+  int32_t keep, cols_kept;  // columns that hold kept tokens
+  int32_t cols;             // of the row
+  bool part;                // the last kept column holds other tokens too
+  bool bad;
+};
+
+__device__ __forceinline__ Row row_of(const RemapParams &p, int i) {
+  Row r;
+  const int32_t limit = p.max_pages << p.page_shift;  // (the host keeps it below 2^31)
+  r.parent = p.parents[i];
+  int32_t keep = p.keep[i], room = p.room[i];
+  r.bad = r.parent >= p.num_rows || keep < 0 || keep > limit || room > limit;
+  if (r.parent < 0 || r.parent >= p.num_rows) r.parent = -1;
+  r.keep = r.parent < 0 ? 0 : max(0, min(keep, limit));
+  room = max(r.keep, min(room, limit));
+  const int32_t up = (1 << p.page_shift) - 1;
+  r.cols_kept = (int32_t)(((int64_t)r.keep + up) >> p.page_shift);
+  r.cols = (int32_t)(((int64_t)room + up) >> p.page_shift);
+  r.part = (r.keep & up) != 0;
+  return r;
+}
+
+__device__ __forceinline__ bool is_page(const RemapParams &p, int32_t x) { return x >= 0 && x < p.num_pages; }
+
+// Whether row i's last kept page, of which it keeps a part, has to be copied
+// (after all uses are counted, each shared page once for every row that keeps it).
+__device__ __forceinline__ bool copied(const RemapParams &p, int i, int32_t page) {
+  return __ldcg(p.uses + page) != __ldcg(p.parts + page) || __ldcg(p.first + page) != i;
+}
+
+// One cluster: its 8192 threads hold the counters of a usual pool in one or two
+// rounds, and the phases are barriers of the cluster instead of launches.  All
+// sums are of integers, so that the order of the atomics does not show.
+__global__ void __launch_bounds__(kMapThreads) remap_kernel(const RemapParams p) {
+  __shared__ int32_t s_warp[32];
+  grid_dependency();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+  bool bad = false;
+  // ---- this CTA's pages: counters, and how many are free
+  const int64_t per_cta = (p.num_pages + kMapCtas - 1) / kMapCtas;
+  const int64_t page0 = min(p.num_pages, cta * per_cta), page1 = min(p.num_pages, page0 + per_cta);
+  int32_t free_pages = 0;
+  for (int64_t x = page0 + tid; x < page1; x += kMapThreads) {
+    const int32_t n = p.refs[x];
+    p.uses[x] = n;
+    p.parts[x] = 0;
+    p.first[x] = INT_MAX;
+    free_pages += n == 0;
+  }
+  int32_t all_free;
+  scan(free_pages, s_warp, &all_free);
+  if (tid == 0) p.totals[cta] = all_free;
+  cluster_sync_global();
+
+  // ---- uses: a warp per row of either table
+  const int all_warps = kMapCtas * kMapWarps, gw = cta * kMapWarps + warp;
+  for (int i = gw; i < p.num_rows; i += all_warps) {
+    const int32_t *row = p.block_table + i * p.block_table_stride;
+    for (int j = lane; j < p.max_pages; j += 32) {
+      const int32_t x = row[j];
+      if (is_page(p, x)) atomicSub(p.uses + x, 1);
+    }
+  }
+  for (int i = gw; i < p.new_rows; i += all_warps) {
+    const Row r = row_of(p, i);
+    bad |= r.bad;
+    if (r.parent < 0) continue;
+    const int32_t *row = p.block_table + r.parent * p.block_table_stride;
+    for (int j = lane; j < r.cols_kept; j += 32) {
+      const int32_t x = row[j];
+      if (!is_page(p, x)) {
+        bad = true;
+        continue;
+      }
+      atomicAdd(p.uses + x, 1);
+      if (r.part && j == r.cols_kept - 1) {
+        atomicAdd(p.parts + x, 1);
+        atomicMin(p.first + x, i);
+      }
+    }
+  }
+  cluster_sync_global();
+
+  // ---- this CTA's rows: the fresh pages each needs, and those before it
+  const int32_t rows_each = (int32_t)(((int64_t)p.new_rows + kMapCtas - 1) / kMapCtas);
+  const int32_t row0 = (int32_t)min((int64_t)p.new_rows, (int64_t)cta * rows_each), row1 = min(p.new_rows, row0 + rows_each);
+  int32_t needed = 0;
+  for (int32_t i0 = row0; i0 < row1; i0 += kMapThreads) {
+    const int i = i0 + tid;
+    int32_t need = 0;
+    if (i < row1) {
+      const Row r = row_of(p, i);
+      need = r.cols - r.cols_kept;
+      if (r.part) {
+        const int32_t x = p.block_table[r.parent * p.block_table_stride + r.cols_kept - 1];
+        if (is_page(p, x) && copied(p, i, x)) ++need;
+      }
+    }
+    int32_t all;
+    const int32_t at = scan(need, s_warp, &all);
+    if (i < row1) p.before[i] = needed + at;
+    needed += all;
+  }
+  if (tid == 0) p.totals[kMapCtas + cta] = needed;
+  cluster_sync_global();
+
+  // ---- counts out, and the fresh pages in order
+  int64_t all_needed = 0, total_free = 0;
+  int32_t free_before = 0;
+#pragma unroll
+  for (int k = 0; k < kMapCtas; ++k) {
+    const int32_t f = __ldcg(p.totals + k);
+    if (k < cta) free_before += f;
+    total_free += f;
+    all_needed += __ldcg(p.totals + kMapCtas + k);
+  }
+  const int64_t given = min(all_needed, total_free);
+  if (cta == 0 && tid == 0) *p.short_pages = (int32_t)(all_needed - given);
+  for (int64_t x0 = page0; x0 < page1; x0 += kMapThreads * kPagesEach) {
+    const int64_t mine = x0 + (int64_t)tid * kPagesEach;
+    int32_t n[kPagesEach], here = 0;
+#pragma unroll
+    for (int k = 0; k < kPagesEach; ++k) {
+      n[k] = mine + k < page1 ? p.refs[mine + k] : 1;
+      here += n[k] == 0;
+    }
+    int32_t all;
+    int32_t rank = free_before + scan(here, s_warp, &all);
+#pragma unroll
+    for (int k = 0; k < kPagesEach; ++k) {
+      const int64_t x = mine + k;
+      if (x >= page1) continue;
+      const int32_t parts = __ldcg(p.parts + x);
+      int32_t uses = __ldcg(p.uses + x);
+      bad |= uses < 0;
+      uses -= parts > 0 && uses == parts ? parts - 1 : parts;  // (copied: not kept)
+      if (n[k] == 0) {
+        if (rank < given) {
+          p.fresh[rank] = (int32_t)x;
+          ++uses;
+        }
+        ++rank;
+      }
+      p.refs_out[x] = uses;
+    }
+    free_before += all;
+  }
+  cluster_sync_global();
+
+  // ---- the new table: a warp per row
+  for (int i = gw; i < p.new_rows; i += all_warps) {
+    const Row r = row_of(p, i);
+    const int32_t *old = p.block_table + (int64_t)max(r.parent, 0) * p.block_table_stride;
+    int64_t rank = __ldcg(p.before + i);
+    const int owner = i / rows_each;
+    for (int k = 0; k < owner; ++k) rank += __ldcg(p.totals + kMapCtas + k);
+    int32_t last = -1, to = -1;
+    bool copy = false;
+    if (r.part) {
+      last = old[r.cols_kept - 1];
+      copy = is_page(p, last) && copied(p, i, last);
+    }
+    const int32_t held = r.cols_kept - (copy ? 1 : 0);
+    for (int j = lane; j < p.max_pages; j += 32) {
+      int32_t x = -1;
+      if (j < held) {
+        x = old[j];
+        if (!is_page(p, x)) x = -1;
+      } else if (j < r.cols && (copy || j >= r.cols_kept)) {
+        const int64_t k = rank + (j - held);
+        if (k < given) x = __ldcg(p.fresh + k);
+      }
+      p.new_table[i * p.new_table_stride + j] = x;
+    }
+    if (copy && rank < given) to = __ldcg(p.fresh + rank);
+    if (lane < 3) p.copies[3 * (int64_t)i + lane] = lane == 2 ? (to >= 0 ? r.keep & ((1 << p.page_shift) - 1) : 0) : to < 0 ? -1 : lane == 0 ? last : to;
+  }
+  if (bad) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
+}
+
+}  // namespace
+}  // namespace splash
+
+splash_status splash_paged_compact_launch(const splash_paged_compact_args &a, cudaStream_t stream, uint32_t *err_word) {
+  using namespace splash;
+  const int64_t size = a.cache_type == SPLASH_CACHE_E4M3 ? 1 : 2;
+  CompactParams p = {};
+  p.k = cache(a.k_cache, size, a.dqk);
+  p.v = cache(a.v_cache, size, a.dv);
+  p.k_slices = (p.k.chunks + 7) / 8;
+  p.v_slices = (p.v.chunks + 7) / 8;
+  p.block_table = a.block_table;
+  p.block_table_stride = a.block_table_stride;
+  p.src = a.src;
+  p.src_stride = a.src_stride;
+  p.start = a.start;
+  p.num_pages = a.num_pages;
+  p.moves = a.moves;
+  p.max_pages = a.max_pages;
+  p.page_shift = __builtin_ctz((unsigned)a.page_size);
+  p.err = err_word;
+  const dim3 grid((unsigned)a.B, (unsigned)a.Hkv, (unsigned)(p.k_slices + p.v_slices));
+  SPLASH_CUDA_TRY(launch_dependent(compact_kernel, grid, dim3(kMoveThreads), 0, 1, stream, p));
+  splash_count_launches(1);
+  return SPLASH_OK;
+}
+
+splash_status splash_paged_copy_launch(const splash_paged_copy_args &a, cudaStream_t stream, uint32_t *err_word) {
+  using namespace splash;
+  const int64_t size = a.cache_type == SPLASH_CACHE_E4M3 ? 1 : 2;
+  CopyParams p = {};
+  p.k = cache(a.k_cache, size, a.dqk);
+  p.v = cache(a.v_cache, size, a.dv);
+  p.copies = a.copies;
+  p.num_pages = a.num_pages;
+  p.page_size = a.page_size;
+  p.err = err_word;
+  const dim3 grid((unsigned)a.count, (unsigned)a.Hkv, 2);
+  SPLASH_CUDA_TRY(launch_dependent(copy_kernel, grid, dim3(kCopyThreads), 0, 1, stream, p));
+  splash_count_launches(1);
+  return SPLASH_OK;
+}
+
+size_t splash_paged_remap_workspace_bytes(int64_t num_pages, int32_t new_rows) {
+  return (size_t)(4 * (4 * num_pages + (int64_t)new_rows + 2 * splash::kMapCtas) + 15) & ~(size_t)15;
+}
+
+splash_status splash_paged_remap_launch(const splash_paged_remap_args &a, cudaStream_t stream, uint32_t *err_word) {
+  using namespace splash;
+  RemapParams p = {};
+  p.block_table = a.block_table;
+  p.block_table_stride = a.block_table_stride;
+  p.new_table = a.new_table;
+  p.new_table_stride = a.new_table_stride;
+  p.parents = a.parents;
+  p.keep = a.keep;
+  p.room = a.room;
+  p.refs = a.refs;
+  p.refs_out = a.refs_out;
+  p.copies = a.copies;
+  p.short_pages = a.short_pages;
+  p.uses = static_cast<int32_t *>(a.workspace);
+  p.parts = p.uses + a.num_pages;
+  p.first = p.parts + a.num_pages;
+  p.fresh = p.first + a.num_pages;
+  p.before = p.fresh + a.num_pages;
+  p.totals = p.before + a.new_rows;
+  p.num_pages = a.num_pages;
+  p.num_rows = a.num_rows;
+  p.new_rows = a.new_rows;
+  p.max_pages = a.max_pages;
+  p.page_shift = __builtin_ctz((unsigned)a.page_size);
+  p.err = err_word;
+  SPLASH_CUDA_TRY(launch_dependent(remap_kernel, dim3(kMapCtas), dim3(kMapThreads), 0, kMapCtas, stream, p));
+  splash_count_launches(1);
+  return SPLASH_OK;
+}

@@ -54,6 +54,11 @@ struct Params {
   int32_t rot, rot_offset;
   float sign;  // of the sines: -1 for the gradient
   uint32_t *err;
+  // several axes: the position of axis a is rot_positions[a * rot_a + b * rot_b + l]
+  const int32_t *rot_positions;
+  int64_t rot_a, rot_b;
+  int32_t num_axes;
+  uint32_t axes[16];  // two bits for each pair
 };
 
 // Element offsets of a thread's two chunks in its row.
@@ -119,6 +124,44 @@ __device__ __forceinline__ void load_turn(const Params &p, int64_t position, int
   }
 }
 
+// The same where each pair has its own axis (`code`: two bits for each of the
+// 8).  Pairs whose axis has no rotation at this position get a bit in the
+// result and are left as they are.  Vector reads for each axis among the 8
+// instead of a read per pair: at most 4 x 4 reads of 16 bytes, against 16 of 4.
+__device__ __forceinline__ uint32_t load_turn_axes(const Params &p, const int32_t (&at)[SPLASH_MAX_AXES], uint32_t code,
+                                                   int pair, Turn &t) {
+  uint32_t still = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t.c[i] = 1.f, t.s[i] = 0.f;
+#pragma unroll
+  for (int a = 0; a < SPLASH_MAX_AXES; ++a) {
+    uint32_t has = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) has |= ((code >> (2 * i)) & 3u) == (uint32_t)a ? 1u << i : 0u;
+    if (has == 0) continue;
+    if (at[a] < 0 || at[a] >= p.table_rows) {
+      still |= has;
+      continue;
+    }
+    Turn x;
+    load_turn(p, at[a], pair, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (has >> i & 1u) t.c[i] = x.c[i], t.s[i] = x.s[i];
+  }
+  return still;
+}
+
+// The pairs of `still` in x as they were in y.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void keep(float (&x0)[8], float (&x1)[8], const float (&y0)[8], const float (&y1)[8], uint32_t still) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (INTERLEAVED ? still >> (i / 2) & 1u : still >> i & 1u) x0[i] = y0[i];
+    if (INTERLEAVED ? still >> (i / 2 + 4) & 1u : still >> i & 1u) x1[i] = y1[i];
+  }
+}
+
 // y = the 16 elements in fp32, turned.
 template <bool INTERLEAVED>
 __device__ __forceinline__ void turn(float (&y0)[8], float (&y1)[8], const Turn &t) {
@@ -161,8 +204,9 @@ __device__ __forceinline__ uint2 to_e4m3(const float (&f)[8], float scale) {
 // HEADS of a token's rows (q heads, k heads and with APPEND v heads).  All of
 // a thread's rows are loaded before anything else: the reads of the data do
 // not wait for those of the position and of the rotation, and HEADS rows use
-// one rotation.
-template <bool INTERLEAVED, bool APPEND, bool E4M3, int HEADS>
+// one rotation.  With AXES each pair turns by the position of its own axis, and
+// where a token is stored (positions) is not what it turns by (rot_positions).
+template <bool INTERLEAVED, bool APPEND, bool E4M3, int HEADS, bool AXES>
 __global__ void __launch_bounds__(128) rope_kernel(const Params p) {
   grid_dependency();
   const int u = threadIdx.x;
@@ -185,10 +229,19 @@ __global__ void __launch_bounds__(128) rope_kernel(const Params p) {
       x[i] = load(p.v.ptr + b * p.v.b + (h - p.Hq - p.Hkv) * p.v.h + l * p.v.l, cv);
     }
   }
-  const int64_t pos = p.positions[b * p.positions_stride + l];
+  const int64_t pos = AXES && !APPEND ? 0 : p.positions[b * p.positions_stride + l];
   bool bad = false;
-  bool rotate = p.table != nullptr && pos >= 0;
-  if (rotate && pos >= p.table_rows) rotate = false, bad = true;
+  bool rotate = AXES || (p.table != nullptr && pos >= 0);
+  int32_t at[SPLASH_MAX_AXES];
+  if constexpr (AXES) {
+#pragma unroll
+    for (int a = 0; a < SPLASH_MAX_AXES; ++a) {
+      at[a] = a < p.num_axes ? p.rot_positions[a * p.rot_a + b * p.rot_b + l] : -1;
+      bad |= at[a] >= p.table_rows;
+    }
+  } else if (rotate && pos >= p.table_rows) {
+    rotate = false, bad = true;
+  }
   int64_t page = -1;
   if (APPEND && pos >= 0) {
     const int64_t seq = p.seq_ids != nullptr ? p.seq_ids[b * p.seq_ids_stride + l] : b;
@@ -202,7 +255,22 @@ __global__ void __launch_bounds__(128) rope_kernel(const Params p) {
   if (bad && u == 0 && h0 == 0) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
   rotate = rotate && c.pair >= 0;
   Turn t;
-  if (rotate) load_turn(p, pos, c.pair, t);
+  uint32_t still = 0;
+  if constexpr (AXES) {
+    if (rotate) {
+      const uint32_t code = p.axes[u >> 1] >> (16 * (u & 1)) & 0xffffu, first = code & 3u;
+      if (code == first * 0x5555u) {  // one axis
+        const int32_t turned_by = first == 0 ? at[0] : first == 1 ? at[1] : first == 2 ? at[2] : at[3];
+        rotate = turned_by >= 0 && turned_by < p.table_rows;
+        if (rotate) load_turn(p, turned_by, c.pair, t);
+      } else {
+        still = load_turn_axes(p, at, code, c.pair, t);
+        rotate = still != 0xffu;
+      }
+    }
+  } else {
+    if (rotate) load_turn(p, pos, c.pair, t);
+  }
   const int64_t slot = APPEND ? pos & (((int64_t)1 << p.page_shift) - 1) : 0;
 
 #pragma unroll
@@ -220,7 +288,15 @@ __global__ void __launch_bounds__(128) rope_kernel(const Params p) {
         unpack(o1, y1);
       }
       if (rotate) {
-        turn<INTERLEAVED>(y0, y1, t);
+        if (AXES && still != 0) {
+          float z0[8], z1[8];
+          unpack(o0, z0);
+          unpack(o1, z1);
+          turn<INTERLEAVED>(y0, y1, t);
+          keep<INTERLEAVED>(y0, y1, z0, z1, still);
+        } else {
+          turn<INTERLEAVED>(y0, y1, t);
+        }
         o0 = pack(y0);
         o1 = pack(y1);
       }
@@ -262,19 +338,19 @@ Cache cache(const splash_cache_view &v, int64_t size) {
   return {static_cast<char *>(v.ptr), size * v.stride_page, size * v.stride_head, size * v.stride_token};
 }
 
-template <bool APPEND, bool E4M3, int HEADS>
+template <bool APPEND, bool E4M3, int HEADS, bool AXES>
 splash_status launch_heads(const Params &p, bool interleaved, cudaStream_t stream) {
   // 128 threads: a packed prompt of 32768 tokens 98 us, against 104 with 256 and 133 with 64
   const int ty = std::max(1, 128 / p.units);
   // (a call may have 2^31 - 1 tokens: adding to that would overflow)
   const dim3 block(p.units, ty), grid((p.tokens - 1) / ty + 1, (p.heads + HEADS - 1) / HEADS);
-  SPLASH_CUDA_TRY(launch_dependent(interleaved ? rope_kernel<true, APPEND, E4M3, HEADS> : rope_kernel<false, APPEND, E4M3, HEADS>,
+  SPLASH_CUDA_TRY(launch_dependent(interleaved ? rope_kernel<true, APPEND, E4M3, HEADS, AXES> : rope_kernel<false, APPEND, E4M3, HEADS, AXES>,
                                    grid, block, 0, 1, stream, p));
   splash_count_launches(1);
   return SPLASH_OK;
 }
 
-template <bool APPEND, bool E4M3>
+template <bool APPEND, bool E4M3, bool AXES>
 splash_status launch(const Params &p, bool interleaved, cudaStream_t stream) {
   // Four rows per thread where that still gives every SM 1024 threads (152 x
   // 1024): q and k of 2 x 4096 tokens 27.8 us against 28.3 with one row, 128
@@ -284,16 +360,12 @@ splash_status launch(const Params &p, bool interleaved, cudaStream_t stream) {
   // of 256 requests 3.0 against 5.1.
   if constexpr (!APPEND) {
     if ((int64_t)p.tokens * p.units * ((p.heads + 3) / 4) >= 152 * 1024)
-      return launch_heads<APPEND, E4M3, 4>(p, interleaved, stream);
+      return launch_heads<APPEND, E4M3, 4, AXES>(p, interleaved, stream);
   }
-  return launch_heads<APPEND, E4M3, 1>(p, interleaved, stream);
+  return launch_heads<APPEND, E4M3, 1, AXES>(p, interleaved, stream);
 }
 
-}  // namespace
-}  // namespace splash
-
-splash_status splash_rope_launch(const splash_rope_args &a, cudaStream_t stream, uint32_t *err_word) {
-  using namespace splash;
+Params params(const splash_rope_args &a, uint32_t *err_word) {
   Params p = {};
   p.q = view(a.q);
   p.q_out = view(a.q_out);
@@ -313,11 +385,10 @@ splash_status splash_rope_launch(const splash_rope_args &a, cudaStream_t stream,
   p.rot_offset = a.rot_offset;
   p.sign = a.inverse ? -1.f : 1.f;
   p.err = err_word;
-  return launch<false, false>(p, a.interleaved != 0, stream);
+  return p;
 }
 
-splash_status splash_paged_append_launch(const splash_paged_append_args &a, cudaStream_t stream, uint32_t *err_word) {
-  using namespace splash;
+Params params(const splash_paged_append_args &a, uint32_t *err_word) {
   const bool e4m3 = a.cache_type == SPLASH_CACHE_E4M3;
   Params p = {};
   p.q = view(a.q);
@@ -353,6 +424,45 @@ splash_status splash_paged_append_launch(const splash_paged_append_args &a, cuda
   p.rot_offset = a.table != nullptr ? a.rot_offset : 0;
   p.sign = 1.f;
   p.err = err_word;
+  return p;
+}
+
+void set_axes(Params &p, const uint8_t *axes, int32_t num_axes, const int32_t *positions, int64_t stride_a, int64_t stride_b) {
+  p.rot_positions = positions;
+  p.rot_a = stride_a;
+  p.rot_b = stride_b;
+  p.num_axes = num_axes;
+  for (int i = 0; i < p.rot / 2; ++i) p.axes[i / 16] |= (uint32_t)axes[i] << (2 * (i % 16));
+}
+
+}  // namespace
+}  // namespace splash
+
+splash_status splash_rope_launch(const splash_rope_args &a, cudaStream_t stream, uint32_t *err_word) {
+  using namespace splash;
+  return launch<false, false, false>(params(a, err_word), a.interleaved != 0, stream);
+}
+
+splash_status splash_paged_append_launch(const splash_paged_append_args &a, cudaStream_t stream, uint32_t *err_word) {
+  using namespace splash;
+  const Params p = params(a, err_word);
   const bool inter = a.table != nullptr && a.interleaved != 0;
-  return e4m3 ? launch<true, true>(p, inter, stream) : launch<true, false>(p, inter, stream);
+  return a.cache_type == SPLASH_CACHE_E4M3 ? launch<true, true, false>(p, inter, stream)
+                                           : launch<true, false, false>(p, inter, stream);
+}
+
+splash_status splash_rope_axes_launch(const splash_rope_axes_args &a, cudaStream_t stream, uint32_t *err_word) {
+  using namespace splash;
+  Params p = params(a.rope, err_word);
+  set_axes(p, a.axes, a.num_axes, a.rope.positions, a.positions_stride_a, a.rope.positions_stride_b);
+  return launch<false, false, true>(p, a.rope.interleaved != 0, stream);
+}
+
+splash_status splash_paged_append_axes_launch(const splash_paged_append_axes_args &a, cudaStream_t stream, uint32_t *err_word) {
+  using namespace splash;
+  Params p = params(a.append, err_word);
+  set_axes(p, a.axes, a.num_axes, a.rot_positions, a.rot_positions_stride_a, a.rot_positions_stride_b);
+  const bool inter = a.append.interleaved != 0;
+  return a.append.cache_type == SPLASH_CACHE_E4M3 ? launch<true, true, true>(p, inter, stream)
+                                                  : launch<true, false, true>(p, inter, stream);
 }

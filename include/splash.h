@@ -588,6 +588,229 @@ splash_status splash_paged_decode_workspace_size(int32_t B, int32_t Hq, int32_t 
                                                  int64_t window_left, size_t *bytes);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Several position axes, trees of drafted tokens, upkeep of the paged cache
+ * ---------------------------------------------------------------------------
+ * Images and video have positions in time, height and width; a draft model
+ * proposes a tree of continuations that is checked at once; samples and beams
+ * fork a sequence.  The calls below go with the three above, in their manner
+ * (struct_bytes, kernels queued on cuda_stream, capturable, device indices
+ * checked on the device).  One step with drafts is
+ *   splash_paged_append_axes   keys and values of the drafts, slot n + l, turned by depth
+ *   splash_paged_tree_decode   their attention over the cache and their own branch
+ *   splash_paged_compact       the accepted branch's tokens to the slots n, n + 1, ...
+ * and one with forks splash_paged_remap, then splash_paged_copy for each layer.
+ */
+
+/* Most position axes of a rotation. */
+#define SPLASH_MAX_AXES 4
+
+/*
+ * splash_rope_axes -- splash_rope where pair i turns by the position of axis
+ * axes[i]: c = table[positions[axes[i]][b][l]][i], s likewise.  (The table's
+ * columns are the frequencies of the pairs, whatever their axis: one ladder for
+ * all pairs or one for each axis is a matter of the table.)  The gradient
+ * (inverse = 1) is the transposed rotation.  A negative position is the identity
+ * for the pairs of its axis; one >= table_rows also, and is reported.
+ *
+ *   rope        the arguments of splash_rope; its positions are device int32
+ *               [num_axes][B][L], axis a at positions_stride_a * a
+ *   axes        host, rot_dim / 2 entries below num_axes
+ *   num_axes    1 .. SPLASH_MAX_AXES
+ * Errors as for splash_rope (axes out of range: INVALID_ARG; more of them:
+ * UNSUPPORTED).
+ */
+typedef struct {
+    uint64_t struct_bytes;
+    splash_rope_args rope;
+    int64_t positions_stride_a;
+    const uint8_t *axes;
+    int32_t num_axes;
+    int32_t reserved; /* 0 */
+} splash_rope_axes_args;
+splash_status splash_rope_axes(const splash_rope_axes_args *args, void *cuda_stream);
+
+/*
+ * splash_paged_append_axes -- splash_paged_append where a token's slot and its
+ * rotation are apart: it is stored at append.positions[b][l] and turned by
+ * rot_positions[axis][b][l], pair by pair as in splash_rope_axes.  With one axis
+ * this stores a tree of drafts (slots in a row, rotations by depth); with more,
+ * images and video.  A negative slot is padding, as in splash_paged_append;
+ * q_out / k_out are rotated all the same.  A rotation position >= table_rows is
+ * reported and the token not stored.
+ *
+ *   append      the arguments of splash_paged_append; table required
+ *   rot_positions  device int32 [num_axes][B][L], strides in elements
+ *   axes, num_axes as for splash_rope_axes
+ */
+typedef struct {
+    uint64_t struct_bytes;
+    splash_paged_append_args append;
+    const int32_t *rot_positions;
+    int64_t rot_positions_stride_a, rot_positions_stride_b;
+    const uint8_t *axes;
+    int32_t num_axes;
+    int32_t reserved; /* 0 */
+} splash_paged_append_axes_args;
+splash_status splash_paged_append_axes(const splash_paged_append_axes_args *args, void *cuda_stream);
+
+/* Most tokens of a tree in one splash_paged_tree_decode call. */
+#define SPLASH_MAX_TREE_TOKENS 64
+
+/*
+ * splash_paged_tree_decode -- splash_paged_decode for a tree of T = decode.Lq
+ * new tokens instead of a chain.  Sequence b has n = seq_lens[b] cached tokens,
+ * the tree's in the slots n - T .. n - 1 (token l in slot n - T + l) behind a
+ * context of n - T.  parents[b][l] is -1 for a token that continues the context,
+ * else the token that it continues, an earlier one.  With depth(l) the number
+ * of l's ancestors in the tree, token l sits at position n - T + depth(l) and
+ * sees the context, its ancestors and itself (with window_left >= 0 only those
+ * whose position is at most window_left before its own).  out and lse as in
+ * splash_paged_decode; a chain (parents l - 1) gives that call's result.
+ *
+ * A parent below -1 marks padding: the token sees nothing (out = 0,
+ * lse = -inf), and neither do its descendants; a sequence may thus have fewer
+ * tokens than T.  A parent that is not an earlier token (>= l) counts as padding
+ * and is reported.  Tokens whose slot is negative (n < T) are padding too.
+ * Cache rows that no token sees are not read, or do not reach a result; rows
+ * that some tokens see do not reach the others, whatever they hold.
+ *
+ *   decode      the arguments of splash_paged_decode, with 1 <= Lq <=
+ *               SPLASH_MAX_TREE_TOKENS; the workspace is that of
+ *               splash_paged_tree_decode_workspace_size
+ *   parents     device int32 [B][T], row stride parents_stride_b (0: one tree)
+ * Supported sizes as for splash_paged_decode but for Lq.  The cache is read once
+ * for every 256 of the Hq/Hkv * T rows.  The result does not depend on timing.
+ *
+ * Precision as splash_paged_decode: for a bf16 cache each probability is taken
+ * to 2^-16 of it, for an e4m3 one to 2^-11.
+ */
+typedef struct {
+    uint64_t struct_bytes;
+    splash_paged_decode_args decode;
+    const int32_t *parents;
+    int64_t parents_stride_b;
+} splash_paged_tree_decode_args;
+splash_status splash_paged_tree_decode(const splash_paged_tree_decode_args *args, void *cuda_stream);
+splash_status splash_paged_tree_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t dqk,
+                                                      int32_t dv, int32_t max_pages, int32_t page_size,
+                                                      int32_t cache_type, int64_t window_left, size_t *bytes);
+
+/*
+ * splash_paged_compact -- moves tokens inside their sequences: the token at
+ * position src[b][m] becomes the one at start[b] + m, in K and V of every head,
+ * for m = 0, 1, ... up to the row's end or its first negative entry.  This keeps
+ * the accepted branch of a tree (start = the context's length), or what an
+ * eviction leaves of a sequence.  All other rows stay as they are; the
+ * sequence's new length and the pages behind it are the caller's (see
+ * splash_paged_remap).
+ *
+ * Positions ascend: src[b][m] >= start[b] + m and src[b][m] > src[b][m - 1], so
+ * that no source is overwritten before it is read.  A row's list ends at the
+ * first entry that breaks this, lies outside the block table's row or is on a
+ * page outside [0, num_pages) (as source or destination), which is reported.
+ * Sequences that share a page must not write to it.
+ *
+ *   src         device int32 [B][moves], row stride src_stride
+ *   start       device int32 [B], >= 0 (a negative one: reported, nothing moves)
+ *   caches, block_table, page_size, dqk, dv  as for splash_paged_append
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA as for splash_paged_append.
+ */
+typedef struct {
+    uint64_t struct_bytes;
+    splash_cache_view k_cache, v_cache;
+    const int32_t *block_table;
+    int64_t block_table_stride;
+    const int32_t *src;
+    int64_t src_stride;
+    const int32_t *start;
+    int64_t num_pages, moves;
+    int32_t B, Hkv, dqk, dv, max_pages, page_size, cache_type;
+    int32_t reserved; /* 0 */
+} splash_paged_compact_args;
+splash_status splash_paged_compact(const splash_paged_compact_args *args, void *cuda_stream);
+
+/*
+ * splash_paged_remap -- a new block table from an old one: sequences fork, grow,
+ * shrink, begin and end, pages are shared by reference count, copied on write,
+ * given out and released.  New row i takes over the first keep[i] tokens of row
+ * parents[i] (negative: of none, keep counts as 0) and gets pages for
+ * max(room[i], keep[i]) tokens.  With P = page_size, row i has the columns
+ * j < ceil(max(room, keep) / P), the others are -1:
+ *   (j + 1) P <= keep[i]       the parent's page, shared;
+ *   j P < keep[i] < (j + 1) P  the parent's page if no other row uses it.  Of
+ *                              several rows that keep part of a page which
+ *                              nobody else uses, the first keeps it; the others
+ *                              get a fresh page and an entry in copies;
+ *   j P >= keep[i]             a fresh page.
+ * refs[p] counts the uses of page p: those by rows of the old table (every entry
+ * in [0, num_pages) is one) and any others, which stay.  refs_out = refs - uses
+ * by the old table + uses by the new one.  Fresh pages are those with refs = 0,
+ * in ascending order, given out in the order of (i, j).  So this call forks
+ * (equal parents), reserves (room above the old one), truncates or rolls back
+ * (keep below it), frees (rows of the old table without heirs) and admits
+ * (parents = -1); pages released by it are free from the next call on.
+ *
+ * Where the free pages do not suffice, *short_pages is the number that is
+ * missing, their columns are -1 and their copies are left out: the caller drops
+ * the results and tries fewer rows.  (The old table and refs are still there
+ * unless refs_out was refs.)  The page contents are copied by splash_paged_copy,
+ * once for each layer that goes by this table.
+ *
+ * A parent >= num_rows counts as negative, a keep beyond the parent's row as its
+ * end, a room beyond the new row as that, and a negative keep as 0; a page outside
+ * [0, num_pages) among the kept ones counts as absent (its column is -1).  Each is
+ * reported, and so are counts that become negative.
+ *
+ *   block_table device int32 [num_rows][max_pages], row stride block_table_stride
+ *   new_table   device int32 [new_rows][max_pages], row stride new_table_stride;
+ *               must not overlap block_table
+ *   parents, keep, room  device int32 [new_rows]
+ *   refs, refs_out  device int32 [num_pages] (may be the same array)
+ *   copies      device int32 [new_rows][3]: source page, destination page, rows
+ *               to copy, or -1, -1, 0
+ *   short_pages device int32 [1]
+ *   workspace   device, 16-byte aligned, of splash_paged_remap_workspace_size
+ *               bytes; overwritten, holds nothing between calls
+ * num_rows may be 0 (block_table is not read).  Errors: INVALID_ARG; UNSUPPORTED
+ * (page_size, or tables of 2^31 entries or more); CUDA.
+ */
+typedef struct {
+    uint64_t struct_bytes;
+    const int32_t *block_table;
+    int64_t block_table_stride;
+    int32_t *new_table;
+    int64_t new_table_stride;
+    const int32_t *parents, *keep, *room, *refs;
+    int32_t *refs_out, *copies, *short_pages;
+    void *workspace;
+    uint64_t workspace_bytes;
+    int64_t num_pages;
+    int32_t num_rows, new_rows, max_pages, page_size;
+} splash_paged_remap_args;
+splash_status splash_paged_remap(const splash_paged_remap_args *args, void *cuda_stream);
+splash_status splash_paged_remap_workspace_size(int64_t num_pages, int32_t new_rows, size_t *bytes);
+
+/*
+ * splash_paged_copy -- for every entry (source page, destination page, n) of
+ * copies: rows 0 .. n - 1 of the source page to the destination page, in K and V
+ * of every head.  Entries with a negative page or n <= 0 are skipped; pages or n
+ * past their ends are reported and skipped.  A page that is a destination may not
+ * be in another entry.
+ *
+ *   copies      device int32 [count][3], dense
+ *   caches      as for splash_paged_append
+ */
+typedef struct {
+    uint64_t struct_bytes;
+    splash_cache_view k_cache, v_cache;
+    const int32_t *copies;
+    int64_t num_pages;
+    int32_t count, Hkv, dqk, dv, page_size, cache_type;
+} splash_paged_copy_args;
+splash_status splash_paged_copy(const splash_paged_copy_args *args, void *cuda_stream);
+
+/*
  * splash_classify_blocks_noalloc -- the block classification of a mask
  * (block_mask and its totals), computed without allocating any device memory.
  * The pages have no counterpart: this exists for callers that must not call

@@ -1,0 +1,339 @@
+"""paged_tree_decode on the GPU against the float64 reference.
+
+Bounds, as for paged_decode: with A = sum_j p_j |v_j| and u what the
+probabilities lose on their way to the second product (bf16 caches 2^-16, e4m3
+2^-11 and fp16's smallest step, 2^-25, on each of n keys):
+  |out - exact| <= (u + 2 e) A + 2^-8 |exact| + n 2^-25 max|v|
+  |lse - exact| <= e + 2^-20 + 2^-22 |exact|
+where e bounds a score's error: dqk products summed in fp32, (dqk + 8) 2^-23 of
+the sum of their absolute values, and with a cap 2^-20 of it for tanh."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import workloads
+from oracle import drafting_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def splash():
+    from block_sparse_flash_gb300 import build as b
+    b.build()
+    import block_sparse_flash_gb300 as m
+    return m
+
+
+def host(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def make_trees(B, T, shape, seed):
+    """Parents int32 [B, T]: an earlier token, -1 or padding."""
+    rng = np.random.default_rng(seed)
+    p = np.zeros((B, T), dtype=np.int32)
+    for b in range(B):
+        tokens = int(rng.integers((T + 1) // 2, T + 1)) if shape == "ragged" else T
+        for l in range(T):
+            p[b, l] = l - 1 if shape == "chain" else -1 if shape == "roots" else l // 2 - 1 if shape == "binary" else \
+                int(rng.integers(-1, l)) if l < tokens else int(rng.integers(-9, -1))
+    return torch.from_numpy(p)
+
+
+def make(lens, T, Hq, Hkv, dqk, dv, page, kind="bf16", layout="heads", shape="ragged", seed=0, spare=3, extra_cols=2):
+    """Caches whose unused rows and pages are NaN, a shuffled block table whose
+    unused entries point nowhere, queries and trees."""
+    g = torch.Generator().manual_seed(seed)
+    B = len(lens)
+    need = [-(-n // page) for n in lens]
+    pages = sum(need) + spare
+    order = torch.randperm(pages, generator=g).tolist()
+    bt = torch.full((B, max(need + [1]) + extra_cols), -(1 << 30), dtype=torch.int32)
+    used = torch.zeros(pages, page, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        for c in range(need[b]):
+            p = order.pop()
+            bt[b, c] = p
+            used[p, :min(page, n - c * page)] = True
+    caches, scales = [], [None, None]
+    for i, d in enumerate((dqk, dv)):
+        x = workloads.normal_bf16((pages, Hkv, page, d), seed + 1 + i).float()
+        if kind == "e4m3":
+            s = torch.linspace(0.01, 0.02, Hkv) * (1 + i)
+            scales[i] = s.cuda()
+            x = (x / s[:, None, None]).clamp(-448, 448)
+        x = x.masked_fill(~used[:, None, :, None], float("nan"))
+        x = x.to(torch.float8_e4m3fn if kind == "e4m3" else torch.bfloat16).cuda()
+        if layout == "tokens":
+            x = x.transpose(1, 2).contiguous().transpose(1, 2)
+        caches.append(x)
+    q = workloads.normal_bf16((B, Hq, T, dqk), seed + 3).cuda()
+    return dict(q=q, k_cache=caches[0], v_cache=caches[1], block_table=bt.cuda(),
+                seq_lens=torch.tensor(lens, dtype=torch.int32).cuda(), parents=make_trees(B, T, shape, seed).cuda(),
+                scale=1 / math.sqrt(dqk), k_scale=scales[0], v_scale=scales[1])
+
+
+def bounds(x, cap=0.0, window=-1):
+    out, lse, A, reach = ref.tree_decode(host(x["q"]), host(x["k_cache"]), host(x["v_cache"]), x["block_table"].cpu().numpy(),
+                                         x["seq_lens"].cpu().numpy(), x["parents"].cpu().numpy(), x["scale"], cap, window,
+                                         host(x["k_scale"]), host(x["v_scale"]))
+    e = (x["q"].shape[3] + 8) * 2.0 ** -23 * reach + (cap * 2.0 ** -20 if cap > 0 else 0)
+    small, u = 0, 2.0 ** -16
+    if x["k_scale"] is not None:
+        u = 2.0 ** -11
+        small = int(x["seq_lens"].max()) * 2.0 ** -25 * np.nanmax(np.abs(host(x["v_cache"]))) * host(x["v_scale"]).max()
+    return out, lse, (u + 2 * e[..., None]) * A + 2.0 ** -8 * np.abs(out) + small, \
+        e + 2.0 ** -20 + 2.0 ** -22 * np.abs(np.where(np.isinf(lse), 0, lse))
+
+
+def check(got, want):
+    out, lse, room_o, room_l = want
+    o, l = host(got[0]), host(got[1])
+    empty = np.isneginf(lse)
+    assert np.array_equal(np.isneginf(l), empty) and (o[empty] == 0).all()
+    assert np.isfinite(o).all() and np.isfinite(l[~empty]).all()
+    assert (np.abs(o - out) <= room_o).all(), float((np.abs(o - out) - room_o).max())
+    assert (np.abs(l[~empty] - lse[~empty]) <= room_l[~empty]).all()
+
+
+CASES = [
+    # lens, T, Hq, Hkv, dqk, dv, page, kind, layout, shape, window, cap
+    ([1], 1, 1, 1, 64, 64, 16, "bf16", "heads", "chain", -1, 0.0),
+    ([316], 16, 32, 8, 128, 128, 16, "bf16", "heads", "ragged", -1, 0.0),
+    ([0, 5, 15, 16, 17, 63, 64, 65], 5, 4, 2, 128, 128, 16, "bf16", "tokens", "ragged", -1, 0.0),
+    ([0, 9, 64, 65, 127, 128, 129], 9, 8, 2, 128, 128, 32, "e4m3", "heads", "ragged", -1, 0.0),
+    ([5, 0, 2, 3, 200, 1], 4, 6, 2, 64, 64, 16, "bf16", "heads", "binary", -1, 0.0),
+    ([64, 130, 77, 30], 64, 8, 2, 128, 128, 64, "bf16", "heads", "ragged", -1, 0.0),
+    ([63, 130, 577], 63, 8, 1, 128, 128, 16, "bf16", "heads", "ragged", -1, 0.0),
+    ([63, 130, 577], 33, 3, 1, 64, 64, 16, "e4m3", "tokens", "binary", -1, 0.0),
+    ([900, 31], 32, 16, 8, 128, 128, 128, "e4m3", "heads", "ragged", -1, 30.0),
+    ([513, 1000, 20], 7, 4, 4, 192, 128, 64, "bf16", "tokens", "ragged", -1, 0.0),
+    ([513, 164, 20], 64, 8, 2, 192, 128, 16, "bf16", "heads", "ragged", -1, 0.0),
+    ([513, 164, 20], 64, 8, 2, 192, 128, 16, "e4m3", "heads", "ragged", -1, 0.0),
+    ([513, 64, 20], 17, 4, 4, 192, 128, 16, "e4m3", "heads", "roots", -1, 0.0),
+    ([700, 100, 33, 5, 0], 10, 4, 1, 128, 128, 16, "bf16", "heads", "ragged", 40, 5.0),
+    ([700, 100, 33, 5, 1], 30, 4, 1, 128, 128, 16, "bf16", "heads", "ragged", 0, 0.0),
+    ([700, 128, 33, 2], 40, 8, 2, 64, 64, 16, "e4m3", "heads", "chain", 65, 0.0),
+    ([700, 128, 330], 64, 8, 2, 64, 64, 16, "bf16", "heads", "chain", 20, 0.0),
+    ([700, 61], 60, 4, 2, 64, 64, 1024, "bf16", "heads", "ragged", 10 ** 12, 0.0),
+    ([150, 70], 50, 24, 2, 64, 64, 16, "bf16", "heads", "ragged", -1, 0.0),
+    ([4000], 31, 2, 1, 128, 128, 16, "bf16", "heads", "ragged", -1, 0.0),
+    ([2500], 64, 16, 1, 128, 128, 256, "e4m3", "heads", "ragged", -1, 0.0),
+    ([300, 90], 64, 9, 1, 128, 128, 32, "bf16", "heads", "roots", -1, 2.0),
+]
+
+
+@pytest.mark.parametrize("long_rows", [False, True], ids=["short", "long"])
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_tree_decode_matches_the_reference(splash, case, long_rows):
+    lens, T, Hq, Hkv, dqk, dv, page, kind, layout, shape, window, cap = case
+    x = make(lens, T, Hq, Hkv, dqk, dv, page, kind, layout, shape, seed=100 + CASES.index(case),
+             extra_cols=1 + 40000 // page if long_rows else 0)
+    got = splash.paged_tree_decode(**x, softcap=cap, window_left=window)
+    splash.check_device_error()
+    check(got, bounds(x, cap, window))
+    again = splash.paged_tree_decode(**x, softcap=cap, window_left=window)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("T", [1, 4, 8, 15, 16, 31, 32, 33, 64])
+@pytest.mark.parametrize("Hq, Hkv", [(1, 1), (4, 1), (8, 1), (10, 2)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_every_number_of_rows(splash, kind, Hq, Hkv, T):
+    for dqk, dv in ((64, 64), (128, 128), (192, 128)):
+        x = make([177, 350, T], T, Hq, Hkv, dqk, dv, 32, kind, seed=T + dqk)
+        got = splash.paged_tree_decode(**x)
+        splash.check_device_error()
+        check(got, bounds(x))
+
+
+@pytest.mark.parametrize("B", [1, 130, 300])
+def test_many_sequences_of_mixed_lengths(splash, B):
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 200, (B,), generator=g).tolist()
+    lens[0] = 1500
+    for T, Hq in ((3, 2), (20, 4)):
+        x = make(lens, T, Hq, 1, 64, 64, 16, seed=7)
+        got = splash.paged_tree_decode(**x)
+        splash.check_device_error()
+        check(got, bounds(x))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [2, 40])
+def test_large_scores(splash, kind, T):
+    """Scores of thousands: the running maximum moves by whole hundreds, and
+    queries of very different sizes share a tile."""
+    x = make([400, 90], T, 4, 2, 64, 64, 16, kind, seed=60)
+    x["q"] *= torch.tensor([1e-30, 1.0, 60.0, 3000.0], device="cuda").bfloat16().view(1, 4, 1, 1)
+    x["scale"] = 1.0
+    got = splash.paged_tree_decode(**x)
+    splash.check_device_error()
+    check(got, bounds(x))
+
+
+def test_a_chain_is_the_plain_decode(splash):
+    for kind in ("bf16", "e4m3"):
+        x = make([700, 100, 33], 16, 8, 2, 128, 128, 16, kind, shape="chain", seed=65)
+        want = bounds(x, 0.0, 50)
+        got = splash.paged_tree_decode(**x, window_left=50)
+        x.pop("parents")
+        plain = splash.paged_decode(**x, window_left=50)
+        splash.check_device_error()
+        assert (np.abs(host(got[0]) - host(plain[0])) <= 2 * want[2]).all()
+        assert (np.abs(host(got[1]) - host(plain[1])) <= 2 * want[3]).all()
+
+
+def test_rows_before_the_window_are_not_read(splash):
+    """Pages that have left the window may be gone: their entries point
+    nowhere, their rows hold NaN."""
+    n, page, window, T = 500, 16, 100, 20
+    x = make([n], T, 4, 2, 128, 128, page, shape="chain", seed=70, extra_cols=100)
+    want = bounds(x, 0.0, window)
+    kc, vc, bt = x["k_cache"], x["v_cache"], x["block_table"]
+    lo = n - T - window  # first key of the shallowest token
+    for c in range(lo // page):
+        kc[bt[0, c].item()] = float("nan")
+        vc[bt[0, c].item()] = float("inf")
+        bt[0, c] = 1 << 30
+    part = bt[0, lo // page].item()
+    kc[part, :, :lo % page] = float("nan")
+    vc[part, :, :lo % page] = float("nan")
+    got = splash.paged_tree_decode(**x, window_left=window)
+    splash.check_device_error()
+    check(got, want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq, T, window", [(2, 4, -1), (8, 30, -1), (8, 30, 70), (16, 9, 3), (2, 64, 16)])
+def test_values_that_only_some_tokens_see(splash, kind, Hq, T, window):
+    """A token's key and value reach its descendants alone, NaN and infinities
+    among them; so do keys before the window of some."""
+    n, d = 250, 64
+    x = make([n, 90], T, Hq, 1, d, d, 16, kind, shape="binary", seed=85)
+    want = bounds(x, 0.0, window)
+    kc, vc, bt, parents = x["k_cache"], x["v_cache"], x["block_table"], x["parents"].cpu().numpy()
+    nan = torch.tensor(float("nan"), device="cuda").to(kc.dtype)
+    hit = np.zeros((2, T), dtype=bool)   # the value is not finite
+    lost = np.zeros((2, T), dtype=bool)  # the score is NaN
+    for b, total in enumerate((n, 90)):
+        keys = [set(k) for k, _ in ref.tree_keys(parents[b], total, window)]
+        def spoil(key, what):
+            cache, value = what
+            cache[bt[b, key // 16], :, key % 16] = value
+            for l in range(T):
+                if key in keys[l]:
+                    (lost if cache is kc else hit)[b, l] = True
+        spoil(total - T + T // 2, (vc, nan if kind == "e4m3" else float("-inf")))
+        spoil(total - 1, (kc, nan))
+        if window >= 0 and total - T - window > 0:
+            spoil(total - T - window, (vc, nan))  # the roots' alone
+    got = splash.paged_tree_decode(**x, window_left=window)
+    splash.check_device_error()
+    o, l = host(got[0]), host(got[1])
+    for b in range(2):
+        for t in range(T):
+            if lost[b, t]:
+                assert np.isnan(o[b, :, t]).all() and np.isnan(l[b, :, t]).all()
+                continue
+            assert (np.abs(l - want[1]) <= want[3])[b, :, t].all()
+            if hit[b, t]:
+                assert not np.isfinite(o[b, :, t]).any()
+            else:
+                assert (np.abs(o - want[0]) <= want[2])[b, :, t].all()
+    assert hit.any() and not (hit | lost).all()
+
+
+def test_an_infinite_value_keeps_its_sign(splash):
+    """One that every token sees, and one of a tree's token: infinity in both."""
+    for T, Hq in ((5, 2), (40, 4)):
+        x = make([200], T, Hq, 1, 64, 64, 16, shape="binary", seed=86)
+        want = bounds(x)
+        bt = x["block_table"]
+        x["v_cache"][bt[0, 3], 0, 5, 7] = float("inf")
+        at = 200 - T  # the first root
+        x["v_cache"][bt[0, at // 16], 0, at % 16, 9] = float("-inf")
+        got = splash.paged_tree_decode(**x)
+        splash.check_device_error()
+        o = host(got[0])
+        below = np.array([at in k for k, _ in ref.tree_keys(x["parents"].cpu().numpy()[0], 200)])
+        assert (o[0, :, :, 7] == np.inf).all() and (o[0][:, below, 9] == -np.inf).all() and below.any() and not below.all()
+        others = [c for c in range(64) if c not in (7, 9)]
+        assert (np.abs(o - want[0]) <= want[2])[..., others].all()
+        assert (np.abs(o - want[0]) <= want[2])[0][:, ~below, 9].all()
+
+
+def test_strided_queries_shared_trees_and_given_outputs(splash):
+    lens, Hq, Hkv, d, T = [100, 100, 37], 8, 2, 128, 12
+    x = make(lens, T, Hq, Hkv, d, d, 16, seed=80, extra_cols=2600)
+    bt = x["block_table"]
+    bt[1, :5] = bt[0, :5]  # a shared prefix
+    x["parents"] = x["parents"][2].contiguous()  # one tree for all
+    wide = torch.zeros(3, T, Hq + 5, d, dtype=torch.bfloat16, device="cuda")
+    wide[:, :, 2:2 + Hq] = x["q"].transpose(1, 2)
+    x["q"] = wide[:, :, 2:2 + Hq].transpose(1, 2)
+    kv = torch.stack((x["k_cache"], x["v_cache"]), 1)  # K and V of a page side by side
+    x["k_cache"], x["v_cache"] = kv[:, 0], kv[:, 1]
+    out = torch.full((3, Hq, T, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(3, Hq, T, device="cuda")
+    size = splash.paged_tree_decode_workspace_size(x["q"], x["k_cache"], x["v_cache"], bt)
+    ws = torch.full((size + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    got = splash.paged_tree_decode(**x, out=out, lse=lse, workspace=ws[:size])
+    assert got[0] is out and got[1] is lse
+    splash.check_device_error()
+    check(got, bounds({**x, "parents": x["parents"].expand(3, T)}))
+    assert (ws[size:] == 0xA5).all()
+    if size:
+        with pytest.raises(splash.SplashError):
+            splash.paged_tree_decode(**x, workspace=ws[:size - 16])
+
+
+@pytest.mark.parametrize("T, Hq", [(3, 2), (40, 8)])
+def test_what_is_wrong_is_reported(splash, T, Hq):
+    x = make([140, 120, 133], T, Hq, 1, 64, 64, 16, shape="binary", seed=90, extra_cols=0)
+    good = splash.paged_tree_decode(**x)
+    assert splash.last_device_error() == 0
+
+    def others(got):
+        return all(torch.equal(got[k][i], good[k][i]) for k in (0, 1) for i in (0, 2))
+    for entry in (-1, x["k_cache"].shape[0], 2 ** 31 - 1, -2 ** 31):
+        bad = x["block_table"].clone()
+        bad[1, 0] = entry
+        got = splash.paged_tree_decode(**{**x, "block_table": bad})
+        assert splash.last_device_error() == 7 and others(got) and torch.isfinite(got[0]).all()
+    for length in (-3, 10 ** 6):
+        lens = x["seq_lens"].clone()
+        lens[1] = length
+        got = splash.paged_tree_decode(**{**x, "seq_lens": lens})
+        assert splash.last_device_error() == 7 and others(got)
+        if length < 0:
+            assert not got[0][1].any() and torch.isneginf(got[1][1]).all()
+    for parent in (1, T - 1, T, 2 ** 31 - 1):
+        p = x["parents"].clone()
+        p[1, 1] = parent
+        got = splash.paged_tree_decode(**{**x, "parents": p})
+        assert splash.last_device_error() == 7 and others(got)
+        assert not got[0][1][:, 1].any() and torch.isneginf(got[1][1][:, 1]).all() and torch.equal(got[0][1][:, 0], good[0][1][:, 0])
+
+
+def test_offsets_past_32_bits(splash):
+    """A cache of more than 2^31 elements (and 2^32 bytes): keys in its last pages."""
+    pages, Hkv, page, d = 2100, 8, 1024, 128
+    kc = torch.empty(pages, Hkv, page, d, dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    at = [pages - 1, pages - 2]
+    small = workloads.normal_bf16((2, 2, Hkv, page, d), 95).cuda()
+    for i, p in enumerate(at):
+        kc[p], vc[p] = small[0, i], small[1, i]
+    bt = torch.tensor([at], dtype=torch.int32, device="cuda")
+    n = torch.tensor([1500], dtype=torch.int32, device="cuda")
+    parents = make_trees(1, 30, "ragged", 3).cuda()
+    q = workloads.normal_bf16((1, Hkv, 30, d), 96).cuda()
+    got = splash.paged_tree_decode(q, kc, vc, bt, n, parents, 0.1)
+    near = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")
+    want = splash.paged_tree_decode(q, small[0], small[1], near, n, parents, 0.1)
+    splash.check_device_error()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
