@@ -4,6 +4,8 @@
 // For a row (query head h, token l): s_j = scale q.k_j over the keys it sees --
 // the context and its ancestors --, out = sum exp(s_j - m) v_j / sum exp(s_j - m),
 // lse = m + ln sum exp(s_j - m), in one pass over the keys.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -11,7 +13,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
-#include <type_traits>
+#include <mutex>
 
 #include "dependent_launch.cuh"
 #include "internal.h"
@@ -40,8 +42,11 @@ constexpr float kTiny = 0x1p-126f;
 struct Params {
   const char *q;
   int64_t q_b, q_h, q_l;  // byte strides
-  const char *k, *v;
-  int64_t k_page, k_head, k_token, v_page, v_head, v_token;  // byte strides
+  const char *v;
+  int64_t v_page, v_head, v_token;  // byte strides
+  // coordinates of a head and a page in the tensor maps: times 0 where the tensor repeats
+  // them; the first page coordinate outside, which reads as zeros
+  int32_t k_head_on, v_head_on, k_page_on, v_page_on, k_page_end, v_page_end;
   const float *k_scale, *v_scale;
   const int32_t *block_table;
   int64_t block_table_stride;
@@ -59,28 +64,35 @@ struct Params {
   uint32_t *err;
 };
 
-// A tile of NT x 128 rows of a KV head and steps of KW keys.
-template <int DQK_, int DV_, bool E4M3_, int NT_>
+// Steps of KW keys for two groups of four softmax warps.  PAIR: 129 rows of a KV head
+// and more, two tiles of 128 rows that share the keys.  Otherwise one tile of rows,
+// and the groups take turns: even and odd steps, each with its own maximum, sum and
+// output, joined at a piece's end.
+template <int DQK_, int DV_, bool E4M3_, bool PAIR_>
 struct Config {
-  static constexpr int DQK = DQK_, DV = DV_, NT = NT_, KW = 64;
-  static constexpr bool E4M3 = E4M3_;
+  static constexpr int DQK = DQK_, DV = DV_, KW = 64;
+  static constexpr bool E4M3 = E4M3_, PAIR = PAIR_;
+  static constexpr int NT = PAIR ? 2 : 1, TILE = 128 * NT;                   // tiles of rows, rows
   static constexpr int RK = DQK * (E4M3 ? 1 : 2), RV = DV * (E4M3 ? 1 : 2);  // bytes of a cache row
   // Operand tiles in shared memory: 64-element (128-byte) columns of rows, 128-byte swizzle.
   static constexpr int COLUMN = KW * 128, K_BYTES = KW * DQK * 2, STAGE = K_BYTES + KW * DV * 2;
   static constexpr int Q_COLUMN = 128 * 128, Q_BYTES = 128 * DQK * 2;
   static constexpr int RAW = E4M3 ? KW * (RK + RV) : 0;  // an e4m3 step as it is in the cache
   static constexpr int BUDGET = 222 * 1024 - NT * Q_BYTES;
-  static constexpr int STAGES = E4M3 ? (BUDGET >= 3 * STAGE + 2 * RAW ? 3 : 2) : std::min(8, BUDGET / STAGE);
+  // (a step's scores are computed LOOK steps before its products with the values)
+  static constexpr int LOOK = PAIR ? 1 : 2;
+  static constexpr int STAGES = E4M3 ? (BUDGET >= 4 * STAGE + 3 * RAW ? 4 : BUDGET >= 3 * STAGE + 2 * RAW ? 3 : 2)
+                                     : std::min(8, BUDGET / STAGE);
   static constexpr int RAWS = E4M3 ? std::min(6, (BUDGET - STAGES * STAGE) / std::max(RAW, 1)) : 0;
-  static constexpr int RING = E4M3 ? RAWS : 1;
   static constexpr int TILES = NT * Q_BYTES + STAGES * STAGE + RAWS * RAW;
-  static_assert(E4M3 ? STAGES >= 2 && RAWS >= 2 : STAGES >= 3, "the loader's lookahead");
-  // Barriers: full[STAGES] empty[STAGES], per tile s_full[2] p_full[2] o_done q_full, then drain
-  static constexpr int BARS = 2 * STAGES + 6 * NT + 1;
+  static_assert(STAGES > LOOK && (!E4M3 || RAWS >= 2), "a step's stage is free before it is waited for");
+  // Barriers: full[STAGES] empty[STAGES], per group s_full[2] p_full[2] o_done q_full, drain, raw_full[RAWS] raw_empty[RAWS]
+  static constexpr int BARS = 2 * STAGES + 13 + 2 * RAWS;
   static constexpr int SMEM = 1024 + TILES + BARS * 8;
-  static constexpr int WARPS = 4 * NT + 5, THREADS = 32 * WARPS;  // softmax, loaders, MMA
-  // Tensor memory: per tile two buffers of scores (64 columns each, P in their place) and O.
-  static constexpr int TILE_COLS = 2 * KW + DV, COLS = NT * TILE_COLS <= 256 ? 256 : 512;
+  // Warps: softmax (8), for e4m3 four that widen, then loads and products.
+  static constexpr int LOAD = E4M3 ? 12 : 8, MMA = LOAD + 1, WARPS = MMA + 1, THREADS = 32 * WARPS;
+  // Tensor memory: per group two buffers of scores (64 columns each, P in their place) and O.
+  static constexpr int GROUP_COLS = 2 * KW + DV, COLS = 512;
   static constexpr uint32_t FORMAT = E4M3 ? 0u : (1u << 7) | (1u << 10);  // fp16 or bf16 operands
   static constexpr uint32_t IDESC_QK = (idesc_bf16_f32(128, KW, false) & ~((1u << 7) | (1u << 10))) | FORMAT;
   static constexpr uint32_t IDESC_PV = (idesc_bf16_f32(128, DV, true) & ~((1u << 7) | (1u << 10))) | FORMAT;
@@ -188,18 +200,18 @@ __device__ __forceinline__ uint64_t visible(int32_t key0, int32_t ctx, int32_t l
   return seen != 0 ? m : 0;
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const char *src, bool read) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint4 load_shared4(uint32_t addr) {
   uint4 x;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr) : "memory");
   return x;
+}
+// 4-D tiled load of the box at (x, y, z, w), completing its bytes on the mbarrier.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z, int32_t w,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
@@ -214,6 +226,8 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// f x; an infinite value stays one however small its factor (0 x infinity would be NaN).
+__device__ __forceinline__ float scaled(float f, float x) { return fabsf(x) == INFINITY ? x : f * x; }
 // A number cut off to bf16.
 __device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
@@ -247,6 +261,21 @@ __device__ __forceinline__ float tanh_of(float x) {
   return fabsf(x) <= kTanhSeriesLimit ? fmaf(x * u, fmaf(u, kTanhC2, kTanhC1), x) : copysignf(__fdividef(1.f - e, 1.f + e), x);
 }
 
+// A chunk of 16 e4m3 values into a row of an operand tile.
+template <class C>
+__device__ __forceinline__ void widen_chunk(uint32_t src, uint32_t dst, int row, int c) {
+  const uint4 y = load_shared4(src);
+  uint32_t w[8];
+  widen(y.x, w[0], w[1]);
+  widen(y.y, w[2], w[3]);
+  widen(y.z, w[4], w[5]);
+  widen(y.w, w[6], w[7]);
+  dst += (c >> 2) * C::COLUMN + row * 128;
+  const int cc = 2 * (c & 3);
+  st_shared_v4(dst + ((cc ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+  st_shared_v4(dst + (((cc + 1) ^ (row & 7)) << 4), w[4], w[5], w[6], w[7]);
+}
+
 template <class C>
 struct Bars {
   uint32_t base;
@@ -256,7 +285,9 @@ struct Bars {
   __device__ __forceinline__ uint32_t p_full(int t, int x) const { return base + 8u * (2 * C::STAGES + 6 * t + 2 + x); }
   __device__ __forceinline__ uint32_t o_done(int t) const { return base + 8u * (2 * C::STAGES + 6 * t + 4); }
   __device__ __forceinline__ uint32_t q_full(int t) const { return base + 8u * (2 * C::STAGES + 6 * t + 5); }
-  __device__ __forceinline__ uint32_t drain() const { return base + 8u * (2 * C::STAGES + 6 * C::NT); }
+  __device__ __forceinline__ uint32_t drain() const { return base + 8u * (2 * C::STAGES + 12); }
+  __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8u * (2 * C::STAGES + 13 + s); }
+  __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8u * (2 * C::STAGES + 13 + C::RAWS + s); }
 };
 
 __device__ __forceinline__ void give_up(const Params &p, volatile int *abort, uint32_t bit) {
@@ -264,225 +295,160 @@ __device__ __forceinline__ void give_up(const Params &p, volatile int *abort, ui
   *abort = 1;
 }
 
-// ------------------------------------------------------------------ loaders
-// Four warps bring the steps of the CTA's part in order, running ahead of the
-// products and across the borders of pieces: bf16 rows by 16-byte asynchronous
-// copies straight into the swizzled operand tiles, e4m3 rows by way of a ring of
-// raw steps, from which the thread that asked for a chunk widens it to fp16.
-// Rows that no token sees become zeros and are not read.  In a step that only some
-// tokens see in whole, values that are not finite become zeros too, since the
-// product adds 0 x value for the others; `lost` then tells the epilogue to add
-// them where they are seen.
-// A thread's copies of a step's rows of CH 16-byte chunks.
-template <class C, int CH>
-__device__ __forceinline__ void ask(uint32_t stage, uint32_t raw, const char *const (&from)[C::KW / 16],
-                                    const bool (&there)[C::KW / 16], int64_t token, const char *base, int32_t key0, const Span &s,
-                                    int tid) {
-  if constexpr (C::E4M3) {
-#pragma unroll
-    for (int e = 0; e < C::KW * CH / 128; ++e) {
-      const int at = tid + 128 * e, row = at / CH, c = at % CH, block = row >> 4;
-      const char *src = block == 0 ? from[0] : block == 1 ? from[1] : block == 2 ? from[2] : from[3];
-      const bool in = block == 0 ? there[0] : block == 1 ? there[1] : block == 2 ? there[2] : there[3];
-      const int32_t key = key0 + row;
-      const bool read = in && key >= s.lo && key < s.n;
-      copy16(raw + at * 16, read ? src + (row & 15) * token + c * 16 : base, read);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < C::KW / 16; ++j) {
-      const int row = 16 * j + (tid >> 3), c = tid & 7;
-      const int32_t key = key0 + row;
-      const bool read = there[j] && key >= s.lo && key < s.n;
-      const char *src = read ? from[j] + (tid >> 3) * token + c * 16 : base;
-#pragma unroll
-      for (int x = 0; x < CH / 8; ++x)
-        copy16(stage + x * C::COLUMN + row * 128 + ((c ^ (row & 7)) << 4), read ? src + x * 128 : base, read);
-    }
-  }
-}
-
-// A chunk of 16 e4m3 values into a row of an operand tile.
+// ------------------------------------------------------------------ loads
+// One warp brings the steps of the CTA's part in order, across the borders of
+// pieces: boxes of up to 64 rows (16-row pages: four) of the pages, one lane each,
+// bf16 straight into the swizzled operand tiles (a box per 64 columns), e4m3 as it
+// is into a ring of raw steps.  A box with no visible key, or of a page that does not
+// exist, lies outside the tensor and arrives as zeros; a box's other rows that no
+// token sees are masked by the softmax.
 template <class C>
-__device__ __forceinline__ void widen_chunk(uint32_t src, uint32_t dst, int row, int c, bool check, bool &found) {
-  const uint4 y = load_shared4(src);
-  uint32_t w[8];
-  widen(y.x, w[0], w[1]);
-  widen(y.y, w[2], w[3]);
-  widen(y.z, w[4], w[5]);
-  widen(y.w, w[6], w[7]);
-  if (check) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = finite(w[i], 0x7c00u, found);
-  }
-  dst += (c >> 2) * C::COLUMN + row * 128;
-  const int cc = 2 * (c & 3);
-  st_shared_v4(dst + ((cc ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
-  st_shared_v4(dst + (((cc + 1) ^ (row & 7)) << 4), w[4], w[5], w[6], w[7]);
-}
-
-template <class C>
-__device__ __forceinline__ void run_loader(const Params &p, Walk<C::KW> walk, const Bars<C> bar, uint32_t stages, uint32_t raws,
-                                           int tid, volatile int *abort, volatile int *lost) {
-  constexpr int KW = C::KW, BLOCKS = KW / 16;
-  constexpr int AHEAD = C::E4M3 ? C::RAWS - 1 : C::STAGES - 2;  // steps asked for before one is handed over
-  constexpr int CK = C::RK / 16, CV = C::RV / 16, EK = KW * CK / 128, EV = KW * CV / 128;  // chunks of a row, of a thread
-  uint32_t asked = 0, given = 0, partial = 0;  // partial: a bit for each step asked for, the newest lowest
-  Piece x;
-  int32_t entry[BLOCKS];
+__device__ __forceinline__ void run_loads(const Params &p, Walk<C::KW> walk, const Bars<C> bar, const CUtensorMap *map_k,
+                                          const CUtensorMap *map_v, uint32_t stages, uint32_t raws, volatile int *abort) {
+  constexpr int KW = C::KW, CK = C::E4M3 ? 1 : C::DQK / 64, CV = C::E4M3 ? 1 : C::DV / 64;  // boxes of a block's rows
+  constexpr int RING = C::E4M3 ? C::RAWS : C::STAGES;
+  const int lane = threadIdx.x & 31;
+  const int rows = min(KW, 1 << p.page_shift), blocks = KW / rows;
+  const int block = lane / (CK + CV), c = lane % (CK + CV);
+  const bool mine = block < blocks, is_v = c >= CK;
+  const int column = is_v ? c - CK : c;
+  const uint32_t to = C::E4M3 ? (is_v ? KW * C::RK + block * rows * C::RV : block * rows * C::RK)
+                              : (is_v ? C::K_BYTES : 0) + column * C::COLUMN + block * rows * 128;
+  const CUtensorMap *map = is_v ? map_v : map_k;
+  uint32_t n = 0;
   bool ok = true;
-
-  auto hand_over = [&]() {
-    const int st = given % C::STAGES;
-    const bool clean = (partial >> (asked - given - 1) & 1u) != 0;
-    const uint32_t stage = stages + st * C::STAGE;
-    bool found = false;
-    if constexpr (C::E4M3) {
-      if (given >= C::STAGES && !mbar_wait(bar.empty(st), (given / C::STAGES - 1) & 1u, abort, kTimeoutNs)) return false;
-      const uint32_t raw = raws + (given % C::RING) * C::RAW;
-#pragma unroll
-      for (int i = 0; i < EK; ++i) {
-        const int at = tid + 128 * i;
-        widen_chunk<C>(raw + at * 16, stage, at / CK, at % CK, false, found);
-      }
-#pragma unroll
-      for (int i = 0; i < EV; ++i) {
-        const int at = tid + 128 * i;
-        widen_chunk<C>(raw + KW * C::RK + at * 16, stage + C::K_BYTES, at / CV, at % CV, clean, found);
-      }
-    } else if (clean) {
-#pragma unroll 1
-      for (int i = 0; i < BLOCKS * (CV / 8); ++i) {
-        const int row = 16 * (i / (CV / 8)) + (tid >> 3);
-        const uint32_t at = stage + C::K_BYTES + (i % (CV / 8)) * C::COLUMN + row * 128 + (((tid & 7) ^ (row & 7)) << 4);
-        const uint4 y = load_shared4(at);
-        bool here = false;
-        const uint32_t w[4] = {finite(y.x, 0x7f80u, here), finite(y.y, 0x7f80u, here), finite(y.z, 0x7f80u, here),
-                               finite(y.w, 0x7f80u, here)};
-        if (here) st_shared_v4(at, w[0], w[1], w[2], w[3]);
-        found |= here;
+  Piece x;
+  while (ok && walk.next(x)) {
+    const int head = (x.seg / p.row_groups) * (is_v ? p.v_head_on : p.k_head_on);
+    const int32_t *pages = p.block_table + x.b * p.block_table_stride;
+    int32_t key = (x.s.step0 + x.step) * KW + block * rows;
+    auto look = [&](int32_t at) { return mine && at < x.s.n && at + rows > x.s.lo ? pages[at >> p.page_shift] : INT32_MIN; };
+    int32_t next = look(key);
+    for (int i = 0; i < x.steps; ++i, ++n, key += KW) {
+      const int32_t entry = next;
+      if (i + 1 < x.steps) next = look(key + KW);
+      const int st = n % RING;
+      const uint32_t full = C::E4M3 ? bar.raw_full(st) : bar.full(st), empty = C::E4M3 ? bar.raw_empty(st) : bar.empty(st);
+      if (n >= RING && !(ok = __all_sync(~0u, mbar_wait(empty, (n / RING - 1) & 1u, abort, kTimeoutNs)))) break;
+      if (lane == 0) mbar_arrive_expect_tx(full, C::E4M3 ? C::RAW : C::STAGE);
+      __syncwarp();
+      if (mine) {
+        const bool there = entry >= 0 && entry < p.num_pages;
+        if (!there && key < x.s.n && key + rows > x.s.lo) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
+        const int32_t page = !there ? (is_v ? p.v_page_end : p.k_page_end) : entry * (is_v ? p.v_page_on : p.k_page_on);
+        load_box((C::E4M3 ? raws + st * C::RAW : stages + st * C::STAGE) + to, map, 64 * column, key & ((1 << p.page_shift) - 1),
+                 head, page, full);
       }
     }
-    if (found) *lost = 1;
-    __threadfence_block();
+  }
+  if (!ok && lane == 0) give_up(p, abort, SPLASH_DEV_TIMEOUT_PRODUCER);
+  // the last load into every slot has landed before the memory is given back
+  bool landed = true;
+  for (uint32_t k = n > RING ? n - RING : 0; k < n; ++k)
+    landed &= mbar_wait_drain(C::E4M3 ? bar.raw_full(k % RING) : bar.full(k % RING), (k / RING) & 1u, kTimeoutNs);
+  if (!landed && lane == 0) atomicOr(p.err, SPLASH_DEV_TIMEOUT_DRAIN);
+}
+
+// e4m3: four warps widen the raw steps to fp16 operand tiles.
+template <class C>
+__device__ __forceinline__ void run_widen(const Params &p, uint32_t steps, const Bars<C> bar, uint32_t stages, uint32_t raws, int tid,
+                                          volatile int *abort) {
+  constexpr int KW = C::KW, CK = C::RK / 16, CV = C::RV / 16, RING = C::E4M3 ? C::RAWS : 1;  // 16-byte chunks of a row
+  for (uint32_t n = 0; n < steps; ++n) {
+    const uint32_t st = n % C::STAGES, slot = n % RING;
+    if (!mbar_wait(bar.raw_full(slot), (n / RING) & 1u, abort, kTimeoutNs) ||
+        (n >= C::STAGES && !mbar_wait(bar.empty(st), (n / C::STAGES - 1) & 1u, abort, kTimeoutNs))) {
+      give_up(p, abort, SPLASH_DEV_TIMEOUT_PRODUCER);
+      return;
+    }
+    const uint32_t stage = stages + st * C::STAGE, raw = raws + slot * C::RAW;
+#pragma unroll
+    for (int i = 0; i < KW * CK / 128; ++i) {
+      const int at = tid + 128 * i;
+      widen_chunk<C>(raw + at * 16, stage, at / CK, at % CK);
+    }
+#pragma unroll
+    for (int i = 0; i < KW * CV / 128; ++i) {
+      const int at = tid + 128 * i;
+      widen_chunk<C>(raw + KW * C::RK + at * 16, stage + C::K_BYTES, at / CV, at % CV);
+    }
     fence_proxy_async_shared();
     mbar_arrive(bar.full(st));
-    ++given;
-    return true;
-  };
-
-  while (ok && walk.next(x)) {
-    const int head = x.seg / p.row_groups;
-    const char *k = p.k + head * p.k_head, *v = p.v + head * p.v_head;
-    const int32_t *pages = p.block_table + x.b * p.block_table_stride;
-    auto look = [&](int32_t key0) {
-#pragma unroll
-      for (int i = 0; i < BLOCKS; ++i) {
-        const int32_t key = key0 + 16 * i;
-        entry[i] = key < x.s.n && key + 16 > x.s.lo ? pages[key >> p.page_shift] : 0;
-      }
-    };
-    int32_t key0 = (x.s.step0 + x.step) * KW;
-    look(key0);
-    for (int i = 0; i < x.steps && ok; ++i, key0 += KW) {
-      const int st = asked % C::STAGES;
-      if (!C::E4M3 && asked >= C::STAGES && !mbar_wait(bar.empty(st), (asked / C::STAGES - 1) & 1u, abort, kTimeoutNs)) {
-        ok = false;
-        break;
-      }
-      const char *from_k[BLOCKS], *from_v[BLOCKS];
-      bool there[BLOCKS];
-#pragma unroll
-      for (int j = 0; j < BLOCKS; ++j) {
-        const int32_t key = key0 + 16 * j;
-        there[j] = entry[j] >= 0 && entry[j] < p.num_pages;
-        if (!there[j] && tid == 0) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
-        const int64_t page = there[j] ? entry[j] : 0, slot = key & ((1 << p.page_shift) - 1);
-        from_k[j] = k + page * p.k_page + slot * p.k_token;
-        from_v[j] = v + page * p.v_page + slot * p.v_token;
-      }
-      if (i + 1 < x.steps) look(key0 + KW);
-      const uint32_t stage = stages + st * C::STAGE, raw = raws + (C::E4M3 ? asked % C::RING : 0u) * C::RAW;
-      ask<C, CK>(stage, raw, from_k, there, p.k_token, k, key0, x.s, tid);
-      ask<C, CV>(stage + C::K_BYTES, raw + KW * C::RK, from_v, there, p.v_token, v, key0, x.s, tid);
-      copy_commit();
-      partial = partial << 1 | (whole<KW>(p, x.s, key0) ? 0u : 1u);
-      ++asked;
-      if (asked - given > AHEAD) {
-        copy_wait<AHEAD>();
-        ok = hand_over();
-      }
-    }
+    mbar_arrive(bar.raw_empty(slot));
   }
-  copy_wait<0>();
-  while (ok && given < asked) ok = hand_over();
-  if (!ok) give_up(p, abort, SPLASH_DEV_TIMEOUT_PRODUCER);
 }
 
 // ------------------------------------------------------------------ products
-// One warp: S = Q K^T of a step for each tile, one step ahead of the softmax, and
-// O += P V.  For a bf16 cache P is two terms (see the softmax), each a product.
+// One warp: S = Q K^T of a step, LOOK steps ahead of its O += P V.  For a bf16 cache
+// P is two terms (see the softmax), each a product.
 template <class C>
 __device__ __forceinline__ void run_mma(const Params &p, Walk<C::KW> walk, const Bars<C> bar, uint32_t tmem, uint32_t q_addr,
                                         uint32_t stages, volatile int *abort) {
   constexpr uint32_t HI = sdesc_hi_sw128(1024);
   constexpr int KW = C::KW;
   const uint32_t leader = elect_one_sync();
-  uint32_t cnt[2] = {0, 0}, pieces[2] = {0, 0}, step = 0;  // of each tile, of the CTA
+  uint32_t cnt[2] = {0, 0}, pieces[2] = {0, 0}, step = 0;  // of each group, of the CTA
   bool ok = true;
   Piece x;
+  // S of step i of the piece for group t, its j-th
+  auto scores = [&](int t, uint32_t j, uint32_t kd) {
+    const uint32_t buf = j & 1u, qd = sdesc_lo(q_addr + (C::PAIR ? t * C::Q_BYTES : 0), 16), d = tmem + t * C::GROUP_COLS + buf * KW;
+#pragma unroll
+    for (int kk = 0; kk < C::DQK / 16; ++kk)
+      mma_ss_lhp(leader, d, qd + (uint32_t)(((kk / 4) * C::Q_COLUMN + (kk % 4) * 32) >> 4), HI,
+                 kd + (uint32_t)(((kk / 4) * C::COLUMN + (kk % 4) * 32) >> 4), HI, C::IDESC_QK, kk != 0);
+    tc_commit_p(leader, bar.s_full(t, buf));
+  };
+  auto values = [&](int t, uint32_t j, bool first, uint32_t vd) {
+    const uint32_t buf = j & 1u;
+    if (!mbar_wait(bar.p_full(t, buf), (j >> 1) & 1u, abort, kTimeoutNs)) return false;
+    tc_fence_after();
+    const uint32_t pa = tmem + t * C::GROUP_COLS + buf * KW, o = tmem + t * C::GROUP_COLS + 2 * KW;
+#pragma unroll
+    for (int kk = 0; kk < KW / 16; ++kk)
+      mma_ts_lhp(leader, o, pa + 8u * kk, vd + (uint32_t)((kk * 2048) >> 4), HI, C::IDESC_PV, !first || kk > 0);
+    if constexpr (!C::E4M3) {
+#pragma unroll
+      for (int kk = 0; kk < KW / 16; ++kk)
+        mma_ts_lhp(leader, o, pa + KW / 2 + 8u * kk, vd + (uint32_t)((kk * 2048) >> 4), HI, C::IDESC_PV, 1);
+    }
+    tc_commit_p(leader, bar.o_done(t));
+    return true;
+  };
   while (ok && walk.next(x)) {
-    const int rows = min(C::NT * 128, p.nrows - (x.seg % p.row_groups) * C::NT * 128), tiles = (rows + 127) / 128;
+    const int groups = C::PAIR && p.nrows - (x.seg % p.row_groups) * C::TILE <= 128 ? 1 : 2;  // (a last tile may be missing)
 #pragma unroll
     for (int t = 0; t < C::NT; ++t)
-      if (t < tiles) ok = ok && mbar_wait(bar.q_full(t), pieces[t]++ & 1u, abort, kTimeoutNs);
+      if (t < groups) ok = ok && mbar_wait(bar.q_full(t), pieces[t]++ & 1u, abort, kTimeoutNs);
     if (!ok) break;
     tc_fence_after();
-    for (int i = 0; i <= x.steps && ok; ++i) {
+    for (int i = 0; i < x.steps + C::LOOK && ok; ++i) {
       if (i < x.steps) {
         const uint32_t u = step + i, st = u % C::STAGES;
         if (!(ok = mbar_wait(bar.full(st), (u / C::STAGES) & 1u, abort, kTimeoutNs))) break;
         tc_fence_after();
         const uint32_t kd = sdesc_lo(stages + st * C::STAGE, 16);
-#pragma unroll
-        for (int t = 0; t < C::NT; ++t) {
-          if (t >= tiles) break;
-          const uint32_t buf = (cnt[t] + i) & 1u, qd = sdesc_lo(q_addr + t * C::Q_BYTES, 16);
-          const uint32_t d = tmem + t * C::TILE_COLS + buf * KW;
-#pragma unroll
-          for (int kk = 0; kk < C::DQK / 16; ++kk)
-            mma_ss_lhp(leader, d, qd + (uint32_t)(((kk / 4) * C::Q_COLUMN + (kk % 4) * 32) >> 4), HI,
-                       kd + (uint32_t)(((kk / 4) * C::COLUMN + (kk % 4) * 32) >> 4), HI, C::IDESC_QK, kk != 0);
-          tc_commit_p(leader, bar.s_full(t, buf));
+        if constexpr (C::PAIR) {
+          scores(0, cnt[0] + i, kd);
+          if (groups > 1) scores(1, cnt[1] + i, kd);
+        } else {
+          scores(i & 1, (i & 1 ? cnt[1] : cnt[0]) + (i >> 1), kd);
         }
       }
-      if (i > 0) {
-        const uint32_t u = step + i - 1, st = u % C::STAGES;
-        const uint32_t vd = sdesc_lo(stages + st * C::STAGE + C::K_BYTES, C::COLUMN);
-#pragma unroll
-        for (int t = 0; t < C::NT; ++t) {
-          if (t >= tiles) break;
-          const uint32_t c = cnt[t] + i - 1, buf = c & 1u;
-          if (!(ok = mbar_wait(bar.p_full(t, buf), (c >> 1) & 1u, abort, kTimeoutNs))) break;
-          tc_fence_after();
-          const uint32_t pa = tmem + t * C::TILE_COLS + buf * KW, o = tmem + t * C::TILE_COLS + 2 * KW;
-#pragma unroll
-          for (int kk = 0; kk < KW / 16; ++kk)
-            mma_ts_lhp(leader, o, pa + 8u * kk, vd + (uint32_t)((kk * 2048) >> 4), HI, C::IDESC_PV, i > 1 || kk > 0);
-          if constexpr (!C::E4M3) {
-#pragma unroll
-            for (int kk = 0; kk < KW / 16; ++kk)
-              mma_ts_lhp(leader, o, pa + KW / 2 + 8u * kk, vd + (uint32_t)((kk * 2048) >> 4), HI, C::IDESC_PV, 1);
-          }
-          tc_commit_p(leader, bar.o_done(t));
+      const int k = i - C::LOOK;
+      if (k >= 0) {
+        const uint32_t st = (step + k) % C::STAGES, vd = sdesc_lo(stages + st * C::STAGE + C::K_BYTES, C::COLUMN);
+        if constexpr (C::PAIR) {
+          ok = values(0, cnt[0] + k, k == 0, vd) && (groups < 2 || values(1, cnt[1] + k, k == 0, vd));
+        } else {
+          ok = values(k & 1, (k & 1 ? cnt[1] : cnt[0]) + (k >> 1), k < 2, vd);
         }
         if (ok) tc_commit_p(leader, bar.empty(st));
       }
     }
     step += x.steps;
-#pragma unroll
-    for (int t = 0; t < C::NT; ++t)
-      if (t < tiles) cnt[t] += x.steps;
+    cnt[0] += C::PAIR ? x.steps : (x.steps + 1) / 2;
+    if (groups > 1) cnt[1] += C::PAIR ? x.steps : x.steps / 2;
   }
   if (!ok && leader) give_up(p, abort, SPLASH_DEV_TIMEOUT_MMA);
   tc_commit_p(leader, bar.drain());
@@ -493,9 +459,10 @@ __device__ __forceinline__ void run_mma(const Params &p, Walk<C::KW> walk, const
 // A row's queries, the row of its tile; zeros for rows that do not exist.  For an
 // e4m3 cache they become fp16, scaled by the power of two that brings the row's
 // largest element into [1, 2): exact but for elements 2^14 times smaller, whose
-// error, 2^-25 of the largest, is below that of an fp32 sum.  Returns the factor.
+// error, 2^-25 of the largest, is below that of an fp32 sum.  Returns the factor.  Two
+// groups that share a tile write a half of the row each (share).
 template <class C>
-__device__ __forceinline__ float load_query(const char *q, bool real, uint32_t dst, int row, bool negate) {
+__device__ __forceinline__ float load_query(const char *q, bool real, uint32_t dst, int row, bool negate, int share) {
   float down = negate ? -1.f : 1.f, factor = 1.f;
   if (C::E4M3 && real) {
     uint32_t top = 0;
@@ -509,7 +476,7 @@ __device__ __forceinline__ float load_query(const char *q, bool real, uint32_t d
     factor = __uint_as_float(top << 23);
   }
 #pragma unroll 4
-  for (int c = 0; c < C::DQK / 8; ++c) {
+  for (int c = C::PAIR ? 0 : share * (C::DQK / 16); c < (C::PAIR ? C::DQK / 8 : (share + 1) * (C::DQK / 16)); ++c) {
     uint4 y = make_uint4(0, 0, 0, 0);
     if (real) y = reinterpret_cast<const uint4 *>(q)[c];
     if (C::E4M3) y = make_uint4(to_half(y.x, down), to_half(y.y, down), to_half(y.z, down), to_half(y.w, down));
@@ -540,35 +507,56 @@ __device__ __noinline__ void add_lost(const Params &p, const Piece &x, int head,
   }
 }
 
-// Four warps per tile, a thread per row.
+// The values of a step that are not finite become zeros: the product adds 0 x value
+// for the rows that do not see a key.  128 threads; returns whether there were any.
+template <class C>
+__device__ __forceinline__ bool clean_values(uint32_t tile, int tid) {
+  constexpr uint32_t TOP = C::E4M3 ? 0x7c00u : 0x7f80u;
+  bool found = false;
+#pragma unroll 1
+  for (int i = tid; i < C::KW * C::DV / 8; i += 128) {
+    const uint4 y = load_shared4(tile + i * 16);
+    bool here = false;
+    const uint32_t w[4] = {finite(y.x, TOP, here), finite(y.y, TOP, here), finite(y.z, TOP, here), finite(y.w, TOP, here)};
+    if (here) st_shared_v4(tile + i * 16, w[0], w[1], w[2], w[3]);
+    found |= here;
+  }
+  if (found) fence_proxy_async_shared();
+  return found;
+}
+
+// Two groups of four warps, a thread per row of a tile: group t has tile t (PAIR) or
+// every other step.
 template <class C>
 __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, const Bars<C> bar, uint32_t tmem, uint32_t q_addr,
-                                            int32_t *s_parents, int t, int part, volatile int *abort, volatile int *lost) {
+                                            uint32_t stages, int32_t *s_parents, float2 (*s_ml)[128], int t, int part,
+                                            volatile int *abort, volatile int *lost) {
   constexpr int KW = C::KW;
-  constexpr bool E4M3 = C::E4M3;
+  constexpr bool E4M3 = C::E4M3, PAIR = C::PAIR;
   const int tid = threadIdx.x & 127, warp = tid >> 5;
-  const uint32_t base = tmem + t * C::TILE_COLS + ((uint32_t)(32 * warp) << 16), o_col = base + 2 * KW;
-  uint32_t cnt = 0;
+  const uint32_t lanes = (uint32_t)(32 * warp) << 16, base = tmem + t * C::GROUP_COLS + lanes, o_col = base + 2 * KW;
+  const int bar_id = PAIR ? 1 + t : 1, bar_threads = PAIR ? 128 : 256;
+  uint32_t cnt = 0, other = 0, step = 0;  // steps of this group, of the other one, of the CTA
   bool ok = true;
   Piece x;
-  while (ok && walk.next(x)) {
-    const int head = x.seg / p.row_groups, row0 = (x.seg % p.row_groups) * C::NT * 128;
-    const int rows = min(128, p.nrows - row0 - t * 128);  // of this tile (none: <= 0)
+  for (; ok && walk.next(x); step += x.steps) {
+    const int head = x.seg / p.row_groups, row0 = (x.seg % p.row_groups) * C::TILE + (PAIR ? t * 128 : 0);
+    const int rows = min(128, p.nrows - row0);  // of this tile (none: <= 0)
     const int slot = part;
     part |= 1;  // what follows the first piece and is not complete is the last one
     if (rows <= 0) continue;
     const bool real = tid < rows, busy = 32 * warp < rows;
-    const int r = row0 + t * 128 + tid, g = real ? r / p.T : 0, l = real ? r - g * p.T : 0;
-    bar_sync(1 + t, 128);  // (the tree before is no longer read)
-    if (tid < p.T) s_parents[tid] = p.parents[x.b * p.parents_stride + tid];
+    const int r = row0 + tid, g = real ? r / p.T : 0, l = real ? r - g * p.T : 0;
+    bar_sync(bar_id, bar_threads);  // (the tree before is no longer read, nor the other group's sums)
+    if (tid < p.T && (PAIR || t == 0)) s_parents[tid] = p.parents[x.b * p.parents_stride + tid];
     const float ks = E4M3 ? p.k_scale[head] : 1.f;
-    const char *q = p.q + x.b * p.q_b + ((int64_t)head * p.G + g) * p.q_h + l * p.q_l;
     float factor = (p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e) * fabsf(ks);
-    factor *= load_query<C>(q, real, q_addr + t * C::Q_BYTES, tid, ks < 0.f);
+    factor *= load_query<C>(p.q + x.b * p.q_b + ((int64_t)head * p.G + g) * p.q_h + l * p.q_l, real,
+                            q_addr + (PAIR ? t * C::Q_BYTES : 0), tid, ks < 0.f, PAIR ? 0 : t);
     if (factor < kTiny) factor = kTiny;  // (NaN stays)
     fence_proxy_async_shared();
-    mbar_arrive(bar.q_full(t));
-    bar_sync(1 + t, 128);
+    mbar_arrive(bar.q_full(PAIR ? t : 0));
+    bar_sync(bar_id, bar_threads);
     Branch me = {0, 0};
     if (real) {
       bool bad = false;
@@ -576,15 +564,22 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
       if (bad) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
     }
     const int32_t lo = p.window < 0 ? 0 : max(0, x.s.ctx + me.depth - p.window);
+    const float times = p.cap > 0.f ? 1.f : factor;
     float m = -INFINITY, sum = 0.f;
 
-    for (int i = 0; i < x.steps; ++i, ++cnt) {
+    for (int i = PAIR ? 0 : t; i < x.steps; i += PAIR ? 1 : 2, ++cnt) {
       const uint32_t buf = cnt & 1u;
       if (!(ok = __all_sync(~0u, mbar_wait(bar.s_full(t, buf), (cnt >> 1) & 1u, abort, kTimeoutNs)))) break;
+      const int32_t key0 = (x.s.step0 + x.step + i) * KW;
+      const bool all = whole<KW>(p, x.s, key0);
+      if (!all && (!PAIR || t == 0)) {
+        // (the step's products wait for these threads, for the first tile's before the second's)
+        const uint32_t st = (step + i) % C::STAGES;
+        if (!(ok = __all_sync(~0u, mbar_wait(bar.full(st), ((step + i) / C::STAGES) & 1u, abort, kTimeoutNs)))) break;
+        if (clean_values<C>(stages + st * C::STAGE + C::K_BYTES, tid)) *lost = 1;
+      }
       if (busy) {
         tc_fence_after();
-        const int32_t key0 = (x.s.step0 + x.step + i) * KW;
-        const bool all = whole<KW>(p, x.s, key0);
         uint32_t a[32], b[32];
         tmem_ld32(base + buf * KW, a);
         tmem_ld32(base + buf * KW + 32, b);
@@ -607,18 +602,24 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
             if (!((uint32_t)(see >> 32) >> j & 1u)) s[32 + j] = -INFINITY;
           }
         }
-        const float times = p.cap > 0.f ? 1.f : factor;
-        float top = s[0];
+        float top;
+        {
+          float y[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int j = 1; j + 1 < KW; j += 2) top = fmax3(top, s[j], s[j + 1]);
-        top = fmaxf(top, s[KW - 1]) * times;
+          for (int j = 4; j + 7 < KW; j += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = fmax3(y[k], s[j + k], s[j + 4 + k]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] = fmaxf(y[k], s[KW - 4 + k]);
+          top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * times;
+        }
         if (E4M3) top -= kBelowTop;
         if (__any_sync(~0u, top > m + kSlack)) {
           const float high = fmaxf(top, m), alpha = m == -INFINITY ? 0.f : ex2_approx(m - high);
           m = high;
           sum *= alpha;
-          if (i > 0) {
-            // (only the product of the step before can still be running: this one's waits for us)
+          if (i >= (PAIR ? 1 : 2)) {
+            // (only the product of the group's step before can still be running: this one's waits for us)
             if (!(ok = __all_sync(~0u, mbar_wait(bar.o_done(t), (cnt - 1) & 1u, abort, kTimeoutNs)))) break;
             tc_fence_after();
 #pragma unroll
@@ -634,15 +635,15 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        f32x2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
+        f32x2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
         for (int j = 0; j < KW; j += 2) {
           const f32x2 y = ffma2({s[j], s[j + 1]}, {times, times}, {-ref, -ref});
           s[j] = ex2_approx(y.x);
           s[j + 1] = ex2_approx(y.y);
-          acc[j / 2 & 1] = fadd2(acc[j / 2 & 1], {s[j], s[j + 1]});
+          acc[j / 2 & 3] = fadd2(acc[j / 2 & 3], {s[j], s[j + 1]});
         }
-        acc[0] = fadd2(acc[0], acc[1]);
+        acc[0] = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
         sum += acc[0].x + acc[0].y;
         if constexpr (E4M3) {
 #pragma unroll
@@ -670,23 +671,56 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
       mbar_arrive(bar.p_full(t, buf));
     }
     if (!ok) break;
+    if (!PAIR) other += t == 0 ? x.steps / 2 : (x.steps + 1) / 2;
 
     // ---- finished rows, or this CTA's part of them
-    if (!(ok = __all_sync(~0u, mbar_wait(bar.o_done(t), (cnt - 1) & 1u, abort, kTimeoutNs)))) break;
+    const bool two = !PAIR && x.steps > 1;  // the other group has steps too
+    const bool own = PAIR || t == 0 || two;
+    if (own) ok = __all_sync(~0u, mbar_wait(bar.o_done(t), (cnt - 1) & 1u, abort, kTimeoutNs));
+    if (PAIR) {
+      if (!ok) break;
+    } else {
+      if (t == 1 || two) ok = __all_sync(~0u, mbar_wait(bar.o_done(t ^ 1), (other - 1) & 1u, abort, kTimeoutNs)) && ok;
+      if (!ok) break;
+      s_ml[t][tid] = make_float2(m, sum);
+      bar_sync(bar_id, bar_threads);
+    }
     tc_fence_after();
     if (busy) {
+      // the groups' outputs, O_0 f_0 + O_1 f_1; group t takes every other 32 columns
+      float f0 = 1.f, f1 = 0.f;
+      if (two) {
+        const float2 z = s_ml[t ^ 1][tid];
+        const float high = fmaxf(m, z.x), ref = high == -INFINITY ? 0.f : high;
+        const float mine = ex2_approx(m - ref), theirs = ex2_approx(z.x - ref);
+        sum = sum * mine + z.y * theirs;
+        m = high;
+        f0 = t == 0 ? mine : theirs;
+        f1 = t == 0 ? theirs : mine;
+      } else if (!own) {
+        m = s_ml[0][tid].x;
+        sum = s_ml[0][tid].y;
+      }
       const bool empty = sum == 0.f || me.seen == 0;
       const float inv = (E4M3 ? p.v_scale[head] : 1.f) / sum;
-      const int64_t row = x.complete ? ((int64_t)x.b * p.Hkv + head) * p.nrows + r : (int64_t)slot * p.part_rows + t * 128 + tid;
+      const int64_t row = x.complete ? ((int64_t)x.b * p.Hkv + head) * p.nrows + r : (int64_t)slot * p.part_rows + (PAIR ? t * 128 : 0) + tid;
+      const uint32_t o_0 = tmem + (PAIR ? t * C::GROUP_COLS : 0) + lanes + 2 * KW;
 #pragma unroll 1
-      for (int c = 0; c < C::DV / 32; ++c) {
+      for (int c = PAIR ? 0 : t; c < C::DV / 32; c += PAIR ? 1 : 2) {
         uint32_t y[32];
         float o[32];
-        tmem_ld32(o_col + 32 * c, y);
+        tmem_ld32(o_0 + 32 * c, y);
         tmem_wait_ld();
         reg_fence32(y);
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(y[j]);
+        if (two) {
+          tmem_ld32(o_0 + C::GROUP_COLS + 32 * c, y);
+          tmem_wait_ld();
+          reg_fence32(y);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = scaled(f0, o[j]) + scaled(f1, __uint_as_float(y[j]));
+        }
         if (*lost && real) {
           float z[32];  // (in memory: the call takes its address)
 #pragma unroll
@@ -710,7 +744,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
         }
         __syncwarp();
       }
-      if (real) {
+      if (real && (PAIR || t == 0)) {
         if (x.complete)
           p.lse[row] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
         else
@@ -723,35 +757,45 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const Params p) {
+__global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid_constant__ CUtensorMap map_k,
+                                                                  const __grid_constant__ CUtensorMap map_v, const Params p) {
   constexpr int KW = C::KW;
   extern __shared__ char smem_raw[];
   __shared__ int32_t s_scan[C::WARPS], s_seq, s_before, s_parents[C::NT][SPLASH_MAX_TREE_TOKENS];
+  __shared__ float2 s_ml[2][128];  // (maximum, sum) of the groups' rows
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_lost;
   const uint32_t tiles = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const Bars<C> bar{tiles + C::TILES};
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (warp == C::WARPS - 1) {
+  if (warp == C::MMA) {
     tmem_alloc(smem_u32(&s_tmem), C::COLS);
     tmem_relinquish();
   }
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(bar.full(s), 128);
+      mbar_init(bar.full(s), C::E4M3 ? 128 : 1);
       mbar_init(bar.empty(s), 1);
     }
-    for (int t = 0; t < C::NT; ++t) {
+    for (int s = 0; s < C::RAWS; ++s) {
+      mbar_init(bar.raw_full(s), 1);
+      mbar_init(bar.raw_empty(s), 128);
+    }
+    for (int t = 0; t < 2; ++t) {
       for (int x = 0; x < 2; ++x) {
         mbar_init(bar.s_full(t, x), 1);
         mbar_init(bar.p_full(t, x), 128);
       }
       mbar_init(bar.o_done(t), 1);
-      mbar_init(bar.q_full(t), 128);
+      mbar_init(bar.q_full(t), C::PAIR ? 128 : 256);
     }
     mbar_init(bar.drain(), 1);
     mbar_fence_init();
     s_abort = s_lost = 0;
+  }
+  if (tid == 32 * C::LOAD) {
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
   }
   // (the allocation comes before the next kernel may start: one that waits for this one cannot
   // hold what this one still needs)
@@ -803,20 +847,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const Params
     walk.seg = (uint32_t)in_seq / (uint32_t)walk.s.nst;
     walk.step = in_seq - walk.seg * walk.s.nst;
     const uint32_t q_addr = tiles, stages = tiles + C::NT * C::Q_BYTES, raws = stages + C::STAGES * C::STAGE;
-    // (registers: 13 warps are launched with 128 a thread; 2 x 128 x 152 + 128 x 80 + 32 x 128 of them)
-    if (warp < 4 * C::NT) {
-      if constexpr (C::NT == 2) regs_increase<152>();
-      run_softmax<C>(p, walk, bar, s_tmem, q_addr, s_parents[warp >> 2], warp >> 2, 2 * blockIdx.x, &s_abort, &s_lost);
-    } else if (warp < C::WARPS - 1) {
-      if constexpr (C::NT == 2) regs_decrease<80>();
-      run_loader<C>(p, walk, bar, stages, raws, tid - 128 * C::NT, &s_abort, &s_lost);
-    } else {
+    // (registers for e4m3: 14 warps are launched with 128 a thread; 8 take 152 and 4 leave 48 each)
+    if (warp < 8) {
+      if constexpr (C::E4M3) regs_increase<152>();
+      run_softmax<C>(p, walk, bar, s_tmem, q_addr, stages, s_parents[C::PAIR ? warp >> 2 : 0], s_ml, warp >> 2, 2 * blockIdx.x, &s_abort,
+                     &s_lost);
+    } else if (warp == C::MMA) {
       run_mma<C>(p, walk, bar, s_tmem, q_addr, stages, &s_abort);
+    } else if (warp == C::LOAD) {
+      run_loads<C>(p, walk, bar, &map_k, &map_v, stages, raws, &s_abort);
+    } else if constexpr (C::E4M3) {
+      regs_decrease<80>();
+      run_widen<C>(p, end - begin, bar, stages, raws, tid - 256, &s_abort);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == C::WARPS - 1) {
+  if (warp == C::MMA) {
     tc_fence_after();
     tmem_dealloc(s_tmem, C::COLS);
   }
@@ -847,8 +894,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const Params
   float top = -INFINITY, sum = 0.f, acc[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-  // (an infinite value stays one however small its part's factor: 0 x infinity would be NaN)
-  auto scaled = [](float f, float x) { return fabsf(x) == INFINITY ? x : f * x; };
   for (int c = c0 + warp; c <= c1; c += kJoinWarps * AHEAD) {
     float2 ml[AHEAD];
     float x[AHEAD][PER];
@@ -915,10 +960,46 @@ int64_t most_steps(int32_t T, int32_t max_pages, int32_t page_size, int64_t wind
   return window < 0 ? most : std::min(most, (window + T) / 64 + 3);
 }
 
+// A cache as a 4-D tensor [pages][heads][tokens][d]; boxes of `rows` rows by 64 bf16 columns
+// (swizzled) or by a whole e4m3 row.  Dimensions of one entry, and those that repeat it
+// (stride 0), have one entry in the map.
+splash_status make_map(CUtensorMap *map, const splash_cache_view &v, int64_t pages, int32_t heads, int32_t page_size, int32_t d,
+                       bool e4m3, int32_t *head_on, int32_t *page_on, int32_t *page_end) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  if (encode == nullptr) return SPLASH_ERR_CUDA;
+  const int64_t size = e4m3 ? 1 : 2, limit = (int64_t)1 << 40;
+  *head_on = heads > 1 && v.stride_head > 0;
+  *page_on = pages > 1 && v.stride_page > 0;
+  *page_end = *page_on ? (int32_t)pages : 1;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page_size, (cuuint64_t)(*head_on ? heads : 1), (cuuint64_t)*page_end};
+  const cuuint64_t strides[3] = {(cuuint64_t)(size * v.stride_token), (cuuint64_t)(size * (*head_on ? v.stride_head : d)),
+                                 (cuuint64_t)(size * (*page_on ? v.stride_page : d))};
+  for (cuuint64_t s : strides)
+    if (s == 0 || s >= (cuuint64_t)limit) return SPLASH_ERR_UNSUPPORTED;
+  const cuuint32_t box[4] = {(cuuint32_t)(e4m3 ? d : 64), (cuuint32_t)std::min(page_size, 64), 1, 1}, ones[4] = {1, 1, 1, 1};
+  const CUresult r = encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.ptr, dims, strides, box,
+                            ones, CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SPLASH_OK : SPLASH_ERR_CUDA;
+}
+
 template <class C>
 splash_status launch(const splash_paged_decode_args &a, Params p, cudaStream_t stream) {
-  p.row_groups = (p.nrows + C::NT * 128 - 1) / (C::NT * 128);
-  p.part_rows = std::min(p.nrows, C::NT * 128);
+  CUtensorMap map_k, map_v;
+  splash_status st = make_map(&map_k, a.k_cache, a.num_pages, a.Hkv, a.page_size, a.dqk, C::E4M3, &p.k_head_on, &p.k_page_on, &p.k_page_end);
+  if (st != SPLASH_OK) return st;
+  st = make_map(&map_v, a.v_cache, a.num_pages, a.Hkv, a.page_size, a.dv, C::E4M3, &p.v_head_on, &p.v_page_on, &p.v_page_end);
+  if (st != SPLASH_OK) return st;
+  p.row_groups = (p.nrows + C::TILE - 1) / C::TILE;
+  p.part_rows = std::min(p.nrows, C::TILE);
   char *ws = static_cast<char *>(a.workspace);
   p.before = reinterpret_cast<int32_t *>(ws);
   ws += align16(4 * ((int64_t)p.B + 1));
@@ -936,18 +1017,18 @@ splash_status launch(const splash_paged_decode_args &a, Params p, cudaStream_t s
   const int64_t most = most_steps(a.Lq, a.max_pages, a.page_size, a.window_left), segments = (int64_t)p.B * p.Hkv * p.row_groups;
   p.min_steps = 1;
   p.ctas = (int)std::min<int64_t>({most * segments, (int64_t)sms, (int64_t)kMaxCtas});
-  SPLASH_CUDA_TRY(launch_dependent(tree_decode_kernel<C>, dim3(p.ctas), dim3(C::THREADS), C::SMEM, 1, stream, p));
+  SPLASH_CUDA_TRY(launch_dependent(tree_decode_kernel<C>, dim3(p.ctas), dim3(C::THREADS), C::SMEM, 1, stream, map_k, map_v, p));
   splash_count_launches(1);
   if (most <= 1) return SPLASH_OK;  // (no segment has more than one step: nothing to join)
   const dim3 rows((unsigned)((int64_t)p.B * p.Hkv * p.nrows));
-  SPLASH_CUDA_TRY(launch_dependent(tree_join_kernel<C::DV, C::NT * 128>, rows, dim3(32 * kJoinWarps), 0, 1, stream, p));
+  SPLASH_CUDA_TRY(launch_dependent(tree_join_kernel<C::DV, C::TILE>, rows, dim3(32 * kJoinWarps), 0, 1, stream, p));
   splash_count_launches(1);
   return SPLASH_OK;
 }
 
 template <int DQK, int DV, bool E4M3>
 splash_status pick(const splash_paged_decode_args &a, const Params &p, cudaStream_t stream) {
-  return p.nrows <= 128 ? launch<Config<DQK, DV, E4M3, 1>>(a, p, stream) : launch<Config<DQK, DV, E4M3, 2>>(a, p, stream);
+  return p.nrows <= 128 ? launch<Config<DQK, DV, E4M3, false>>(a, p, stream) : launch<Config<DQK, DV, E4M3, true>>(a, p, stream);
 }
 
 }  // namespace
@@ -968,10 +1049,6 @@ splash_status splash_paged_tree_decode_launch(const splash_paged_tree_decode_arg
   p.q_b = 2 * a.q.stride_b;
   p.q_h = 2 * a.q.stride_h;
   p.q_l = 2 * a.q.stride_l;
-  p.k = static_cast<const char *>(a.k_cache.ptr);
-  p.k_page = size * a.k_cache.stride_page;
-  p.k_head = size * a.k_cache.stride_head;
-  p.k_token = size * a.k_cache.stride_token;
   p.v = static_cast<const char *>(a.v_cache.ptr);
   p.v_page = size * a.v_cache.stride_page;
   p.v_head = size * a.v_cache.stride_head;
