@@ -25,6 +25,9 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 constexpr int kMaxCtas = 160;              // of the grid; the workspace holds two parts for each
+// A piece's start and end cost a CTA about as much as this many steps: a segment
+// counts for so many more when the list is cut into equal parts.
+constexpr int kPieceSteps = 2;
 constexpr uint64_t kTimeoutNs = 1000000000ull;  // of a wait
 
 // A running maximum is only moved when a score passes it by more than this (in
@@ -55,7 +58,7 @@ struct Params {
   __nv_bfloat16 *out;
   float *lse;
   float *part_o, *part_ml;  // [2 * CTAs][part_rows][DV], [2 * CTAs][part_rows][2] (maximum, sum)
-  int32_t *before;          // [B + 1] list entries (of one head and row group) before each sequence
+  int32_t *before;          // [B + 1] list entries (of one head and row group) before each sequence's
   int64_t num_pages;
   int32_t B, Hkv, T, G, nrows, row_groups, part_rows;  // nrows = G * T rows per KV head
   int32_t max_pages, page_shift, window;               // window < 0: none
@@ -86,8 +89,8 @@ struct Config {
   static constexpr int RAWS = E4M3 ? std::min(6, (BUDGET - STAGES * STAGE) / std::max(RAW, 1)) : 0;
   static constexpr int TILES = NT * Q_BYTES + STAGES * STAGE + RAWS * RAW;
   static_assert(STAGES > LOOK && (!E4M3 || RAWS >= 2), "a step's stage is free before it is waited for");
-  // Barriers: full[STAGES] empty[STAGES], per group s_full[2] p_full[2] o_done q_full, drain, raw_full[RAWS] raw_empty[RAWS]
-  static constexpr int BARS = 2 * STAGES + 13 + 2 * RAWS;
+  // Barriers: full[STAGES] empty[STAGES], per group s_full[2] p_full[2] o_done q_full o_last, drain, raw_full[RAWS] raw_empty[RAWS]
+  static constexpr int BARS = 2 * STAGES + 15 + 2 * RAWS;
   static constexpr int SMEM = 1024 + TILES + BARS * 8;
   // Warps: softmax (8), for e4m3 four that widen, then loads and products.
   static constexpr int LOAD = E4M3 ? 12 : 8, MMA = LOAD + 1, WARPS = MMA + 1, THREADS = 32 * WARPS;
@@ -124,7 +127,8 @@ __device__ __forceinline__ bool whole(const Params &p, const Span &s, int32_t ke
 }
 
 // Equal contiguous parts of T entries, of at least p.min_steps each: CTA w takes
-// [begin(w), begin(w + 1)).
+// [begin(w), begin(w + 1)).  A segment has kPieceSteps entries for its start, then one
+// for each step.
 struct Parts {
   int32_t total, count, each, more;  // the first `more` take one entry more
   __device__ __forceinline__ Parts(const Params &p, int32_t T)
@@ -141,30 +145,34 @@ struct Parts {
 struct Piece {
   int32_t b, seg, step, steps;
   Span s;
-  bool complete;  // all of the segment's steps
+  // Where a part of the segment goes in the workspace, -1 for a segment in whole.  A CTA has
+  // at most one that begins a segment and one that goes on with another.
+  __device__ __forceinline__ int slot(int cta) const { return steps == s.nst ? -1 : 2 * cta + (step == 0 ? 1 : 0); }
 };
 template <int KW>
 struct Walk {
   const Params &p;
   int32_t u, end, per_seq;
-  int32_t b, seg, step;
+  int32_t b, seg, entry;  // the entry of segment seg that u is
   Span s;
   __device__ __forceinline__ bool next(Piece &x) {
-    if (u >= end) return false;
-    x.b = b;
-    x.seg = seg;
-    x.step = step;
-    x.steps = min(s.nst - step, end - u);
-    x.s = s;
-    x.complete = x.steps == s.nst;
-    u += x.steps;
-    step = 0;
-    if (++seg == per_seq) {
-      seg = 0;
-      ++b;
-      if (u < end) s = span_of<KW>(p, b);
+    while (u < end) {
+      const int32_t to = min(s.nst + kPieceSteps, entry + (end - u));
+      x.b = b;
+      x.seg = seg;
+      x.step = max(entry - kPieceSteps, 0);
+      x.steps = max(to - kPieceSteps, 0) - x.step;
+      x.s = s;
+      u += to - entry;
+      entry = 0;
+      if (++seg == per_seq) {
+        seg = 0;
+        ++b;
+        if (u < end) s = span_of<KW>(p, b);
+      }
+      if (x.steps > 0) return true;
     }
-    return true;
+    return false;
   }
 };
 
@@ -205,12 +213,14 @@ __device__ __forceinline__ uint4 load_shared4(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr) : "memory");
   return x;
 }
-// 4-D tiled load of the box at (x, y, z, w), completing its bytes on the mbarrier.
-__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z, int32_t w,
+// 4-D tiled load of the box at (x, y, z, w), completing its bytes on the mbarrier; issued by the
+// lane of a converged warp whose `leader` is not 0.
+__device__ __forceinline__ void load_box(uint32_t leader, uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z, int32_t w,
                                          uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %7, 0;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "r"(leader)
       : "memory");
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
@@ -230,12 +240,6 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 __device__ __forceinline__ float scaled(float f, float x) { return fabsf(x) == INFINITY ? x : f * x; }
 // A number cut off to bf16.
 __device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // The larger exponent field of a word's two bf16 values, and the word as fp16
 // values times `down`.
 __device__ __forceinline__ uint32_t exponent(uint32_t x) { return max((x >> 7) & 255u, (x >> 23) & 255u); }
@@ -281,13 +285,14 @@ struct Bars {
   uint32_t base;
   __device__ __forceinline__ uint32_t full(int s) const { return base + 8u * s; }
   __device__ __forceinline__ uint32_t empty(int s) const { return base + 8u * (C::STAGES + s); }
-  __device__ __forceinline__ uint32_t s_full(int t, int x) const { return base + 8u * (2 * C::STAGES + 6 * t + x); }
-  __device__ __forceinline__ uint32_t p_full(int t, int x) const { return base + 8u * (2 * C::STAGES + 6 * t + 2 + x); }
-  __device__ __forceinline__ uint32_t o_done(int t) const { return base + 8u * (2 * C::STAGES + 6 * t + 4); }
-  __device__ __forceinline__ uint32_t q_full(int t) const { return base + 8u * (2 * C::STAGES + 6 * t + 5); }
-  __device__ __forceinline__ uint32_t drain() const { return base + 8u * (2 * C::STAGES + 12); }
-  __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8u * (2 * C::STAGES + 13 + s); }
-  __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8u * (2 * C::STAGES + 13 + C::RAWS + s); }
+  __device__ __forceinline__ uint32_t s_full(int t, int x) const { return base + 8u * (2 * C::STAGES + 7 * t + x); }
+  __device__ __forceinline__ uint32_t p_full(int t, int x) const { return base + 8u * (2 * C::STAGES + 7 * t + 2 + x); }
+  __device__ __forceinline__ uint32_t o_done(int t) const { return base + 8u * (2 * C::STAGES + 7 * t + 4); }
+  __device__ __forceinline__ uint32_t q_full(int t) const { return base + 8u * (2 * C::STAGES + 7 * t + 5); }
+  __device__ __forceinline__ uint32_t o_last(int t) const { return base + 8u * (2 * C::STAGES + 7 * t + 6); }
+  __device__ __forceinline__ uint32_t drain() const { return base + 8u * (2 * C::STAGES + 14); }
+  __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8u * (2 * C::STAGES + 15 + s); }
+  __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8u * (2 * C::STAGES + 15 + C::RAWS + s); }
 };
 
 __device__ __forceinline__ void give_up(const Params &p, volatile int *abort, uint32_t bit) {
@@ -297,48 +302,62 @@ __device__ __forceinline__ void give_up(const Params &p, volatile int *abort, ui
 
 // ------------------------------------------------------------------ loads
 // One warp brings the steps of the CTA's part in order, across the borders of
-// pieces: boxes of up to 64 rows (16-row pages: four) of the pages, one lane each,
-// bf16 straight into the swizzled operand tiles (a box per 64 columns), e4m3 as it
-// is into a ring of raw steps.  A box with no visible key, or of a page that does not
-// exist, lies outside the tensor and arrives as zeros; a box's other rows that no
-// token sees are masked by the softmax.
+// pieces: boxes of up to 64 rows (16-row pages: four) of the pages, bf16 straight into
+// the swizzled operand tiles (a box per 64 columns), e4m3 as it is into a ring of raw
+// steps.  Lanes 0 .. 3 look up a page each, two steps ahead; the warp issues the boxes
+// together (from diverged lanes each took 100 cycles).  A box with no visible key, or
+// of a page that does not exist, lies outside the tensor and arrives as zeros; a box's
+// other rows that no token sees are masked by the softmax.
 template <class C>
 __device__ __forceinline__ void run_loads(const Params &p, Walk<C::KW> walk, const Bars<C> bar, const CUtensorMap *map_k,
                                           const CUtensorMap *map_v, uint32_t stages, uint32_t raws, volatile int *abort) {
   constexpr int KW = C::KW, CK = C::E4M3 ? 1 : C::DQK / 64, CV = C::E4M3 ? 1 : C::DV / 64;  // boxes of a block's rows
   constexpr int RING = C::E4M3 ? C::RAWS : C::STAGES;
   const int lane = threadIdx.x & 31;
-  const int rows = min(KW, 1 << p.page_shift), blocks = KW / rows;
-  const int block = lane / (CK + CV), c = lane % (CK + CV);
-  const bool mine = block < blocks, is_v = c >= CK;
-  const int column = is_v ? c - CK : c;
-  const uint32_t to = C::E4M3 ? (is_v ? KW * C::RK + block * rows * C::RV : block * rows * C::RK)
-                              : (is_v ? C::K_BYTES : 0) + column * C::COLUMN + block * rows * 128;
-  const CUtensorMap *map = is_v ? map_v : map_k;
-  uint32_t n = 0;
+  const uint32_t leader = elect_one_sync();
+  const int shift = min(6, p.page_shift), rows = 1 << shift, blocks = KW >> shift, in_page = (1 << p.page_shift) - 1;
+  uint32_t n = 0, st = 0, turn = 1;  // steps asked for; the next one's slot, and the parity of its last use
   bool ok = true;
   Piece x;
   while (ok && walk.next(x)) {
-    const int head = (x.seg / p.row_groups) * (is_v ? p.v_head_on : p.k_head_on);
+    const int head = x.seg / p.row_groups, head_k = head * p.k_head_on, head_v = head * p.v_head_on;
     const int32_t *pages = p.block_table + x.b * p.block_table_stride;
-    int32_t key = (x.s.step0 + x.step) * KW + block * rows;
-    auto look = [&](int32_t at) { return mine && at < x.s.n && at + rows > x.s.lo ? pages[at >> p.page_shift] : INT32_MIN; };
-    int32_t next = look(key);
-    for (int i = 0; i < x.steps; ++i, ++n, key += KW) {
+    int32_t key0 = (x.s.step0 + x.step) * KW;
+    // the page of this lane's block: -1 where no key of it is seen, -2 where it does not exist
+    auto look = [&](int32_t at) {
+      at += lane * rows;
+      if (lane >= blocks || at >= x.s.n || at + rows <= x.s.lo) return -1;
+      const int32_t page = pages[at >> p.page_shift];
+      return page >= 0 && page < p.num_pages ? page : -2;
+    };
+    int32_t next = look(key0), after = x.steps > 1 ? look(key0 + KW) : -1;
+    for (int i = 0; i < x.steps; ++i, ++n, key0 += KW) {
       const int32_t entry = next;
-      if (i + 1 < x.steps) next = look(key + KW);
-      const int st = n % RING;
+      next = after;
+      if (i + 2 < x.steps) after = look(key0 + 2 * KW);
+      if (entry == -2) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
       const uint32_t full = C::E4M3 ? bar.raw_full(st) : bar.full(st), empty = C::E4M3 ? bar.raw_empty(st) : bar.empty(st);
-      if (n >= RING && !(ok = __all_sync(~0u, mbar_wait(empty, (n / RING - 1) & 1u, abort, kTimeoutNs)))) break;
-      if (lane == 0) mbar_arrive_expect_tx(full, C::E4M3 ? C::RAW : C::STAGE);
+      if (n >= RING && !(ok = __all_sync(~0u, mbar_wait(empty, turn, abort, kTimeoutNs)))) break;
+      if (leader) mbar_arrive_expect_tx(full, C::E4M3 ? C::RAW : C::STAGE);
       __syncwarp();
-      if (mine) {
-        const bool there = entry >= 0 && entry < p.num_pages;
-        if (!there && key < x.s.n && key + rows > x.s.lo) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
-        const int32_t page = !there ? (is_v ? p.v_page_end : p.k_page_end) : entry * (is_v ? p.v_page_on : p.k_page_on);
-        load_box((C::E4M3 ? raws + st * C::RAW : stages + st * C::STAGE) + to, map, 64 * column, key & ((1 << p.page_shift) - 1),
-                 head, page, full);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j >= blocks) break;
+        const int32_t page = __shfl_sync(~0u, entry, j), slot = (key0 + j * rows) & in_page;
+        const int32_t page_k = page < 0 ? p.k_page_end : page * p.k_page_on, page_v = page < 0 ? p.v_page_end : page * p.v_page_on;
+        if constexpr (C::E4M3) {
+          const uint32_t to = raws + st * C::RAW;
+          load_box(leader, to + j * rows * C::RK, map_k, 0, slot, head_k, page_k, full);
+          load_box(leader, to + KW * C::RK + j * rows * C::RV, map_v, 0, slot, head_v, page_v, full);
+        } else {
+          const uint32_t to = stages + st * C::STAGE + j * rows * 128;
+#pragma unroll
+          for (int c = 0; c < CK; ++c) load_box(leader, to + c * C::COLUMN, map_k, 64 * c, slot, head_k, page_k, full);
+#pragma unroll
+          for (int c = 0; c < CV; ++c) load_box(leader, to + C::K_BYTES + c * C::COLUMN, map_v, 64 * c, slot, head_v, page_v, full);
+        }
       }
+      if (++st == RING) st = 0, turn ^= 1u;
     }
   }
   if (!ok && lane == 0) give_up(p, abort, SPLASH_DEV_TIMEOUT_PRODUCER);
@@ -351,9 +370,12 @@ __device__ __forceinline__ void run_loads(const Params &p, Walk<C::KW> walk, con
 
 // e4m3: four warps widen the raw steps to fp16 operand tiles.
 template <class C>
-__device__ __forceinline__ void run_widen(const Params &p, uint32_t steps, const Bars<C> bar, uint32_t stages, uint32_t raws, int tid,
+__device__ __forceinline__ void run_widen(const Params &p, Walk<C::KW> walk, const Bars<C> bar, uint32_t stages, uint32_t raws, int tid,
                                           volatile int *abort) {
   constexpr int KW = C::KW, CK = C::RK / 16, CV = C::RV / 16, RING = C::E4M3 ? C::RAWS : 1;  // 16-byte chunks of a row
+  Piece x;
+  uint32_t steps = 0;
+  while (walk.next(x)) steps += x.steps;
   for (uint32_t n = 0; n < steps; ++n) {
     const uint32_t st = n % C::STAGES, slot = n % RING;
     if (!mbar_wait(bar.raw_full(slot), (n / RING) & 1u, abort, kTimeoutNs) ||
@@ -399,7 +421,7 @@ __device__ __forceinline__ void run_mma(const Params &p, Walk<C::KW> walk, const
                  kd + (uint32_t)(((kk / 4) * C::COLUMN + (kk % 4) * 32) >> 4), HI, C::IDESC_QK, kk != 0);
     tc_commit_p(leader, bar.s_full(t, buf));
   };
-  auto values = [&](int t, uint32_t j, bool first, uint32_t vd) {
+  auto values = [&](int t, uint32_t j, bool first, bool last, uint32_t vd) {
     const uint32_t buf = j & 1u;
     if (!mbar_wait(bar.p_full(t, buf), (j >> 1) & 1u, abort, kTimeoutNs)) return false;
     tc_fence_after();
@@ -413,6 +435,7 @@ __device__ __forceinline__ void run_mma(const Params &p, Walk<C::KW> walk, const
         mma_ts_lhp(leader, o, pa + KW / 2 + 8u * kk, vd + (uint32_t)((kk * 2048) >> 4), HI, C::IDESC_PV, 1);
     }
     tc_commit_p(leader, bar.o_done(t));
+    if (last) tc_commit_p(leader, bar.o_last(C::PAIR ? t : 0));
     return true;
   };
   while (ok && walk.next(x)) {
@@ -439,9 +462,9 @@ __device__ __forceinline__ void run_mma(const Params &p, Walk<C::KW> walk, const
       if (k >= 0) {
         const uint32_t st = (step + k) % C::STAGES, vd = sdesc_lo(stages + st * C::STAGE + C::K_BYTES, C::COLUMN);
         if constexpr (C::PAIR) {
-          ok = values(0, cnt[0] + k, k == 0, vd) && (groups < 2 || values(1, cnt[1] + k, k == 0, vd));
+          ok = values(0, cnt[0] + k, k == 0, k + 1 == x.steps, vd) && (groups < 2 || values(1, cnt[1] + k, k == 0, k + 1 == x.steps, vd));
         } else {
-          ok = values(k & 1, (k & 1 ? cnt[1] : cnt[0]) + (k >> 1), k < 2, vd);
+          ok = values(k & 1, (k & 1 ? cnt[1] : cnt[0]) + (k >> 1), k < 2, k + 1 == x.steps, vd);
         }
         if (ok) tc_commit_p(leader, bar.empty(st));
       }
@@ -456,34 +479,66 @@ __device__ __forceinline__ void run_mma(const Params &p, Walk<C::KW> walk, const
 }
 
 // ------------------------------------------------------------------ softmax
-// A row's queries, the row of its tile; zeros for rows that do not exist.  For an
-// e4m3 cache they become fp16, scaled by the power of two that brings the row's
-// largest element into [1, 2): exact but for elements 2^14 times smaller, whose
-// error, 2^-25 of the largest, is below that of an fp32 sum.  Returns the factor.  Two
-// groups that share a tile write a half of the row each (share).
+// The queries of a tile on their way from memory: eight lanes per row, 16 bytes of each
+// of its 128-byte columns, and one thread's parents.
 template <class C>
-__device__ __forceinline__ float load_query(const char *q, bool real, uint32_t dst, int row, bool negate, int share) {
-  float down = negate ? -1.f : 1.f, factor = 1.f;
-  if (C::E4M3 && real) {
-    uint32_t top = 0;
-#pragma unroll 4
-    for (int c = 0; c < C::DQK / 8; ++c) {
-      const uint4 y = reinterpret_cast<const uint4 *>(q)[c];
-      top = max(max(top, max(exponent(y.x), exponent(y.y))), max(exponent(y.z), exponent(y.w)));
+struct Queries {
+  static constexpr int WARPS = C::PAIR ? 4 : 8, ROWS = 128 / (4 * WARPS), COLS = C::DQK / 64;  // rows of a lane
+  uint4 q[ROWS][COLS];
+  int32_t parent;
+  float k_scale;
+
+  __device__ __forceinline__ static int row(int k) {
+    return 4 * ((int)(threadIdx.x >> 5) % WARPS) + ((threadIdx.x & 31) >> 3) + 4 * WARPS * k;
+  }
+
+  __device__ __forceinline__ void ask(const Params &p, const Piece &x, int row0, int rows) {
+    const int head = x.seg / p.row_groups, thread = threadIdx.x % (32 * WARPS);
+    const char *base = p.q + x.b * p.q_b + (int64_t)head * p.G * p.q_h + (threadIdx.x & 7) * 16;
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const int i = row(k), g = (row0 + i) / p.T, l = row0 + i - g * p.T;
+      const char *src = base + g * p.q_h + l * p.q_l;
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) q[k][c] = i < rows ? *reinterpret_cast<const uint4 *>(src + c * 128) : make_uint4(0, 0, 0, 0);
     }
-    top = min(max(top, 1u), 253u);
-    down *= __uint_as_float((254u - top) << 23);
-    factor = __uint_as_float(top << 23);
+    parent = thread < p.T ? p.parents[x.b * p.parents_stride + thread] : -2;
+    k_scale = C::E4M3 ? p.k_scale[head] : 1.f;
   }
-#pragma unroll 4
-  for (int c = C::PAIR ? 0 : share * (C::DQK / 16); c < (C::PAIR ? C::DQK / 8 : (share + 1) * (C::DQK / 16)); ++c) {
-    uint4 y = make_uint4(0, 0, 0, 0);
-    if (real) y = reinterpret_cast<const uint4 *>(q)[c];
-    if (C::E4M3) y = make_uint4(to_half(y.x, down), to_half(y.y, down), to_half(y.z, down), to_half(y.w, down));
-    st_shared_v4(dst + (c >> 3) * C::Q_COLUMN + row * 128 + (((c & 7) ^ (row & 7)) << 4), y.x, y.y, y.z, y.w);
+
+  // Into the operand tile.  For an e4m3 cache the queries become fp16, a row scaled by the
+  // power of two that brings its largest element into [1, 2): exact but for elements 2^14
+  // times smaller, whose error, 2^-25 of the largest, is below that of an fp32 sum.  The
+  // factors go to s_factor.
+  __device__ __forceinline__ void put(const Params &p, uint32_t tile, int32_t *s_parents, float *s_factor) const {
+    const int thread = threadIdx.x % (32 * WARPS), lane8 = threadIdx.x & 7;
+    if (thread < p.T) s_parents[thread] = parent;
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const int i = row(k);
+      float down = k_scale < 0.f ? -1.f : 1.f;
+      if (C::E4M3) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) {
+          const uint4 y = q[k][c];
+          top = max(top, max(max(exponent(y.x), exponent(y.y)), max(exponent(y.z), exponent(y.w))));
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+        top = min(max(top, 1u), 253u);
+        down *= __uint_as_float((254u - top) << 23);
+        if (lane8 == 0) s_factor[i] = __uint_as_float(top << 23);
+      }
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) {
+        uint4 y = q[k][c];
+        if (C::E4M3) y = make_uint4(to_half(y.x, down), to_half(y.y, down), to_half(y.z, down), to_half(y.w, down));
+        st_shared_v4(tile + c * C::Q_COLUMN + i * 128 + ((lane8 ^ (i & 7)) << 4), y.x, y.y, y.z, y.w);
+      }
+    }
   }
-  return factor;
-}
+};
 
 // Adds to 32 columns of a row the values that are not finite of the keys it sees in
 // a piece's steps that are not whole (the product had zeros in their place).
@@ -513,7 +568,7 @@ template <class C>
 __device__ __forceinline__ bool clean_values(uint32_t tile, int tid) {
   constexpr uint32_t TOP = C::E4M3 ? 0x7c00u : 0x7f80u;
   bool found = false;
-#pragma unroll 1
+#pragma unroll 4
   for (int i = tid; i < C::KW * C::DV / 8; i += 128) {
     const uint4 y = load_shared4(tile + i * 16);
     bool here = false;
@@ -525,45 +580,133 @@ __device__ __forceinline__ bool clean_values(uint32_t tile, int tid) {
   return found;
 }
 
+// What a row has when its piece's steps are done.
+struct Done {
+  Piece x;
+  uint64_t seen;
+  int32_t lo;
+  float m, sum;    // of both groups
+  float f0, f1;    // the outputs' factors: f0 O_0 + f1 O_1
+  bool two;        // O_1 is there
+};
+
+// Writes a finished piece: rows of the result, or this CTA's part of them.
+template <class C>
+__device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint32_t o_0, int t, int row0, int rows, int tid,
+                                           const volatile int *lost) {
+  constexpr bool PAIR = C::PAIR;
+  const int head = d.x.seg / p.row_groups, slot = d.x.slot(blockIdx.x);
+  const bool real = tid < rows, empty = d.sum == 0.f || d.seen == 0;
+  const float inv = (C::E4M3 ? p.v_scale[head] : 1.f) / d.sum;
+  const int64_t row = slot < 0 ? ((int64_t)d.x.b * p.Hkv + head) * p.nrows + row0 + tid : (int64_t)slot * p.part_rows + (PAIR ? t * 128 : 0) + tid;
+#pragma unroll 1
+  for (int c = PAIR ? 0 : t; c < C::DV / 32; c += PAIR ? 1 : 2) {  // (groups that share a tile take every other 32 columns)
+    uint32_t y[32], z[32];
+    float o[32];
+    tmem_ld32(o_0 + 32 * c, y);
+    if (d.two) tmem_ld32(o_0 + C::GROUP_COLS + 32 * c, z);
+    tmem_wait_ld();
+    reg_fence32(y);
+    reg_fence32(z);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(y[j]);
+    if (d.two) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = scaled(d.f0, o[j]) + scaled(d.f1, __uint_as_float(z[j]));
+    }
+    if (*lost && real) {
+      float w[32];  // (in memory: the call takes its address)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) w[j] = o[j];
+      add_lost<C>(p, d.x, head, d.lo, d.seen, 32 * c, w);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = w[j];
+    }
+    if (real && slot < 0) {
+      uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * C::DV + 32 * c);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = empty ? 0.f : o[j] * inv;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        dst[j] = make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
+                            pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7]));
+    } else if (real) {
+      float4 *dst = reinterpret_cast<float4 *>(p.part_o + row * C::DV + 32 * c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dst[j] = empty ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+    }
+    __syncwarp();
+  }
+  if (real && (PAIR || t == 0)) {
+    if (slot < 0)
+      p.lse[row] = empty ? -INFINITY : (d.m + log2f(d.sum)) * kLn2;
+    else
+      *reinterpret_cast<float2 *>(p.part_ml + 2 * row) = empty ? make_float2(-INFINITY, 0.f) : make_float2(d.m, d.sum);
+  }
+}
+
 // Two groups of four warps, a thread per row of a tile: group t has tile t (PAIR) or
-// every other step.
+// every other step.  From piece to piece: the next queries are read while the last
+// products run, go to shared memory as soon as those are done, and the finished rows
+// are written while the next piece's first scores are computed.
 template <class C>
 __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, const Bars<C> bar, uint32_t tmem, uint32_t q_addr,
-                                            uint32_t stages, int32_t *s_parents, float2 (*s_ml)[128], int t, int part,
+                                            uint32_t stages, int32_t *s_parents, float *s_factor, float2 (*s_ml)[128], int t,
                                             volatile int *abort, volatile int *lost) {
   constexpr int KW = C::KW;
   constexpr bool E4M3 = C::E4M3, PAIR = C::PAIR;
   const int tid = threadIdx.x & 127, warp = tid >> 5;
   const uint32_t lanes = (uint32_t)(32 * warp) << 16, base = tmem + t * C::GROUP_COLS + lanes, o_col = base + 2 * KW;
+  const uint32_t o_0 = tmem + (PAIR ? t * C::GROUP_COLS : 0) + lanes + 2 * KW, q_tile = q_addr + (PAIR ? t * C::Q_BYTES : 0);
   const int bar_id = PAIR ? 1 + t : 1, bar_threads = PAIR ? 128 : 256;
-  uint32_t cnt = 0, other = 0, step = 0;  // steps of this group, of the other one, of the CTA
-  bool ok = true;
+  uint32_t cnt = 0, pieces = 0, step = 0, skipped = 0;  // of this group; steps of the CTA before x
+  int row0 = 0, rows = 0, done_row0 = 0, done_rows = 0, tree = -1;
+  bool ok = true, some = false;  // some: a piece is finished and not written
   Piece x;
-  for (; ok && walk.next(x); step += x.steps) {
-    const int head = x.seg / p.row_groups, row0 = (x.seg % p.row_groups) * C::TILE + (PAIR ? t * 128 : 0);
-    const int rows = min(128, p.nrows - row0);  // of this tile (none: <= 0)
-    const int slot = part;
-    part |= 1;  // what follows the first piece and is not complete is the last one
-    if (rows <= 0) continue;
+  Done d;
+  Queries<C> queries;
+  Branch me = {0, 0};
+  // the next piece that has rows for this group (the second tile of a last row group may be missing)
+  auto advance = [&]() {
+    while (walk.next(x)) {
+      row0 = (x.seg % p.row_groups) * C::TILE + (PAIR ? t * 128 : 0);
+      rows = min(128, p.nrows - row0);
+      if (rows > 0) return true;
+      skipped += x.steps;
+    }
+    return false;
+  };
+  bool more = advance();
+  if (more) queries.ask(p, x, row0, rows);
+  while (more || some) {
+    if (more) {
+      queries.put(p, q_tile, s_parents, s_factor);
+      fence_proxy_async_shared();
+      mbar_arrive(bar.q_full(PAIR ? t : 0));
+    }
+    if (some) {
+      tc_fence_after();
+      if (32 * warp < done_rows) write_rows<C>(p, d, o_0, t, done_row0, done_rows, tid, lost);
+      tc_fence_before();
+      some = false;
+    }
+    if (!more) break;
+    bar_sync(bar_id, bar_threads);  // (tree and factors are there; nobody still reads an output that the next products replace)
     const bool real = tid < rows, busy = 32 * warp < rows;
-    const int r = row0 + tid, g = real ? r / p.T : 0, l = real ? r - g * p.T : 0;
-    bar_sync(bar_id, bar_threads);  // (the tree before is no longer read, nor the other group's sums)
-    if (tid < p.T && (PAIR || t == 0)) s_parents[tid] = p.parents[x.b * p.parents_stride + tid];
-    const float ks = E4M3 ? p.k_scale[head] : 1.f;
-    float factor = (p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e) * fabsf(ks);
-    factor *= load_query<C>(p.q + x.b * p.q_b + ((int64_t)head * p.G + g) * p.q_h + l * p.q_l, real,
-                            q_addr + (PAIR ? t * C::Q_BYTES : 0), tid, ks < 0.f, PAIR ? 0 : t);
-    if (factor < kTiny) factor = kTiny;  // (NaN stays)
-    fence_proxy_async_shared();
-    mbar_arrive(bar.q_full(PAIR ? t : 0));
-    bar_sync(bar_id, bar_threads);
-    Branch me = {0, 0};
-    if (real) {
+    step += skipped;
+    skipped = 0;
+    if (tree != x.b || p.row_groups > 1) {
+      const int r = row0 + tid;
       bool bad = false;
-      me = branch_of(s_parents, l, max(0, -x.s.ctx), p.window, &bad);
+      me = {0, 0};
+      if (real) me = branch_of(s_parents, r % p.T, max(0, -x.s.ctx), p.window, &bad);
       if (bad) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
+      tree = x.b;
     }
     const int32_t lo = p.window < 0 ? 0 : max(0, x.s.ctx + me.depth - p.window);
+    float factor = (p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e) * fabsf(queries.k_scale);
+    if (E4M3) factor *= s_factor[tid];
+    if (factor < kTiny) factor = kTiny;  // (NaN stays)
     const float times = p.cap > 0.f ? 1.f : factor;
     float m = -INFINITY, sum = 0.f;
 
@@ -619,7 +762,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
           m = high;
           sum *= alpha;
           if (i >= (PAIR ? 1 : 2)) {
-            // (only the product of the group's step before can still be running: this one's waits for us)
+            // (these scores came after the products of all steps but the one before)
             if (!(ok = __all_sync(~0u, mbar_wait(bar.o_done(t), (cnt - 1) & 1u, abort, kTimeoutNs)))) break;
             tc_fence_after();
 #pragma unroll
@@ -651,16 +794,15 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
           tmem_st32(base + buf * KW, a);
         } else {
           // P in two bf16 terms, cut off and rest: 2^-16 of each p, where bf16 alone
-          // loses 2^-8, as much as the rounding of the result.  The rest is kept above 0 in
-          // whole steps: an infinite value times either term then has its sign, and the
-          // sum is that infinity (0 x infinity is NaN); the floor, the smallest normal
-          // number, adds 2^-126 of a value.  In the other steps values are finite.
-          const uint32_t floor = all ? 0x00800080u : 0u;
+          // loses 2^-8, as much as the rounding of the result.  The rest is taken of
+          // (1 + 2^-23) p, which keeps it above 0: an infinite value times either term
+          // then has its sign, and the sum is that infinity (0 x infinity is NaN).
+          constexpr float above = 1.f + 0x1p-23f;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             a[j] = __byte_perm(__float_as_uint(s[2 * j]), __float_as_uint(s[2 * j + 1]), 0x7632);
-            const f32x2 rest = fadd2({s[2 * j], s[2 * j + 1]}, {-cut(s[2 * j]), -cut(s[2 * j + 1])});
-            b[j] = max_bf16x2(pack_bf16x2(rest.x, rest.y), floor);
+            const f32x2 rest = ffma2({s[2 * j], s[2 * j + 1]}, {above, above}, {-cut(s[2 * j]), -cut(s[2 * j + 1])});
+            b[j] = pack_bf16x2(rest.x, rest.y);
           }
           tmem_st32(base + buf * KW, a);
           tmem_st32(base + buf * KW + 32, b);
@@ -671,86 +813,38 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
       mbar_arrive(bar.p_full(t, buf));
     }
     if (!ok) break;
-    if (!PAIR) other += t == 0 ? x.steps / 2 : (x.steps + 1) / 2;
 
-    // ---- finished rows, or this CTA's part of them
-    const bool two = !PAIR && x.steps > 1;  // the other group has steps too
-    const bool own = PAIR || t == 0 || two;
-    if (own) ok = __all_sync(~0u, mbar_wait(bar.o_done(t), (cnt - 1) & 1u, abort, kTimeoutNs));
-    if (PAIR) {
-      if (!ok) break;
-    } else {
-      if (t == 1 || two) ok = __all_sync(~0u, mbar_wait(bar.o_done(t ^ 1), (other - 1) & 1u, abort, kTimeoutNs)) && ok;
-      if (!ok) break;
+    d.x = x;
+    d.seen = me.seen;
+    d.lo = lo;
+    d.m = m;
+    d.sum = sum;
+    d.f0 = 1.f;
+    d.f1 = 0.f;
+    d.two = !PAIR && x.steps > 1;  // the other group has steps too
+    done_row0 = row0;
+    done_rows = rows;
+    some = true;
+    step += x.steps;
+    more = advance();
+    if (more) queries.ask(p, x, row0, rows);
+    // (o_done may be two products behind here, which its parity would not tell from none)
+    if (!(ok = __all_sync(~0u, mbar_wait(bar.o_last(PAIR ? t : 0), pieces++ & 1u, abort, kTimeoutNs)))) break;
+    if (!PAIR) {
       s_ml[t][tid] = make_float2(m, sum);
       bar_sync(bar_id, bar_threads);
-    }
-    tc_fence_after();
-    if (busy) {
-      // the groups' outputs, O_0 f_0 + O_1 f_1; group t takes every other 32 columns
-      float f0 = 1.f, f1 = 0.f;
-      if (two) {
-        const float2 z = s_ml[t ^ 1][tid];
+      const float2 z = s_ml[t ^ 1][tid];
+      if (d.two) {
         const float high = fmaxf(m, z.x), ref = high == -INFINITY ? 0.f : high;
         const float mine = ex2_approx(m - ref), theirs = ex2_approx(z.x - ref);
-        sum = sum * mine + z.y * theirs;
-        m = high;
-        f0 = t == 0 ? mine : theirs;
-        f1 = t == 0 ? theirs : mine;
-      } else if (!own) {
-        m = s_ml[0][tid].x;
-        sum = s_ml[0][tid].y;
+        d.sum = sum * mine + z.y * theirs;
+        d.m = high;
+        d.f0 = t == 0 ? mine : theirs;
+        d.f1 = t == 0 ? theirs : mine;
+      } else if (t == 1) {
+        d.m = z.x;
+        d.sum = z.y;
       }
-      const bool empty = sum == 0.f || me.seen == 0;
-      const float inv = (E4M3 ? p.v_scale[head] : 1.f) / sum;
-      const int64_t row = x.complete ? ((int64_t)x.b * p.Hkv + head) * p.nrows + r : (int64_t)slot * p.part_rows + (PAIR ? t * 128 : 0) + tid;
-      const uint32_t o_0 = tmem + (PAIR ? t * C::GROUP_COLS : 0) + lanes + 2 * KW;
-#pragma unroll 1
-      for (int c = PAIR ? 0 : t; c < C::DV / 32; c += PAIR ? 1 : 2) {
-        uint32_t y[32];
-        float o[32];
-        tmem_ld32(o_0 + 32 * c, y);
-        tmem_wait_ld();
-        reg_fence32(y);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(y[j]);
-        if (two) {
-          tmem_ld32(o_0 + C::GROUP_COLS + 32 * c, y);
-          tmem_wait_ld();
-          reg_fence32(y);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = scaled(f0, o[j]) + scaled(f1, __uint_as_float(y[j]));
-        }
-        if (*lost && real) {
-          float z[32];  // (in memory: the call takes its address)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) z[j] = o[j];
-          add_lost<C>(p, x, head, lo, me.seen, 32 * c, z);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = z[j];
-        }
-        if (real && x.complete) {
-          uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * C::DV + 32 * c);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = empty ? 0.f : o[j] * inv;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            dst[j] = make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
-                                pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7]));
-        } else if (real) {
-          float4 *dst = reinterpret_cast<float4 *>(p.part_o + row * C::DV + 32 * c);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) dst[j] = empty ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-        }
-        __syncwarp();
-      }
-      if (real && (PAIR || t == 0)) {
-        if (x.complete)
-          p.lse[row] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
-        else
-          *reinterpret_cast<float2 *>(p.part_ml + 2 * row) = empty ? make_float2(-INFINITY, 0.f) : make_float2(m, sum);
-      }
-      tc_fence_before();
     }
   }
   if (!ok && (threadIdx.x & 31) == 0) give_up(p, abort, SPLASH_DEV_TIMEOUT_SOFTMAX);
@@ -763,6 +857,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid
   extern __shared__ char smem_raw[];
   __shared__ int32_t s_scan[C::WARPS], s_seq, s_before, s_parents[C::NT][SPLASH_MAX_TREE_TOKENS];
   __shared__ float2 s_ml[2][128];  // (maximum, sum) of the groups' rows
+  __shared__ float s_factor[C::NT][128];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_lost;
   const uint32_t tiles = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -787,6 +882,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid
         mbar_init(bar.p_full(t, x), 128);
       }
       mbar_init(bar.o_done(t), 1);
+      mbar_init(bar.o_last(t), 1);
       mbar_init(bar.q_full(t), C::PAIR ? 128 : 256);
     }
     mbar_init(bar.drain(), 1);
@@ -806,7 +902,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid
   const int per = (p.B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   int32_t own = 0;
-  for (int b = b0; b < b1; ++b) own += span_of<KW>(p, b).nst;
+  for (int b = b0; b < b1; ++b) own += span_of<KW>(p, b).nst + kPieceSteps;
   int32_t before = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -830,13 +926,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid
     int32_t at = before;
     for (int b = b0; b < b1; ++b) {
       const Span s = span_of<KW>(p, b);
-      if (begin >= at * per_seq && begin < (at + s.nst) * per_seq) s_seq = b, s_before = at;
+      const int32_t entries = s.nst + kPieceSteps;
+      if (begin >= at * per_seq && begin < (at + entries) * per_seq) s_seq = b, s_before = at;
       if (blockIdx.x == 0) {
         p.before[b] = at;
-        if (b == p.B - 1) p.before[p.B] = at + s.nst;
+        if (b == p.B - 1) p.before[p.B] = at + entries;
         if (s.n != p.seq_lens[b]) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
       }
-      at += s.nst;
+      at += entries;
     }
   }
   __syncthreads();
@@ -844,21 +941,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid
     Walk<KW> walk{p, begin, end, per_seq, s_seq, 0, 0, {}};
     walk.s = span_of<KW>(p, walk.b);
     const int32_t in_seq = begin - s_before * per_seq;
-    walk.seg = (uint32_t)in_seq / (uint32_t)walk.s.nst;
-    walk.step = in_seq - walk.seg * walk.s.nst;
+    walk.seg = (uint32_t)in_seq / (uint32_t)(walk.s.nst + kPieceSteps);
+    walk.entry = in_seq - walk.seg * (walk.s.nst + kPieceSteps);
     const uint32_t q_addr = tiles, stages = tiles + C::NT * C::Q_BYTES, raws = stages + C::STAGES * C::STAGE;
     // (registers for e4m3: 14 warps are launched with 128 a thread; 8 take 152 and 4 leave 48 each)
     if (warp < 8) {
       if constexpr (C::E4M3) regs_increase<152>();
-      run_softmax<C>(p, walk, bar, s_tmem, q_addr, stages, s_parents[C::PAIR ? warp >> 2 : 0], s_ml, warp >> 2, 2 * blockIdx.x, &s_abort,
-                     &s_lost);
+      const int t = warp >> 2, tile = C::PAIR ? t : 0;
+      run_softmax<C>(p, walk, bar, s_tmem, q_addr, stages, s_parents[tile], s_factor[tile], s_ml, t, &s_abort, &s_lost);
     } else if (warp == C::MMA) {
       run_mma<C>(p, walk, bar, s_tmem, q_addr, stages, &s_abort);
     } else if (warp == C::LOAD) {
       run_loads<C>(p, walk, bar, &map_k, &map_v, stages, raws, &s_abort);
     } else if constexpr (C::E4M3) {
       regs_decrease<80>();
-      run_widen<C>(p, end - begin, bar, stages, raws, tid - 256, &s_abort);
+      run_widen<C>(p, walk, bar, stages, raws, tid - 256, &s_abort);
     }
   }
   tc_fence_before();
@@ -869,87 +966,70 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid
   }
 }
 
-// Joins the parts of a row that several CTAs computed: with (m_c, l_c, o_c) of
-// part c and m = max m_c: out = sum exp(m_c - m) o_c / sum exp(m_c - m) l_c, in the
-// order of the keys.  One CTA per row, its warps taking every fourth part.
-constexpr int kJoinWarps = 4;
+// Joins the parts of a segment that several CTAs computed: with (m_c, l_c, o_c) of part c
+// of a row and m = max m_c: out = sum exp(m_c - m) o_c / sum exp(m_c - m) l_c, in the
+// order of the keys.  A CTA takes kJoinRows rows of a segment, a warp one at a time.
+constexpr int kJoinWarps = 8, kJoinRows = 32;
 template <int DV, int TILE>
-__global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const Params p) {
-  __shared__ float s_o[kJoinWarps][DV], s_sum[kJoinWarps], s_top[kJoinWarps];
+__global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const Params p, int slices) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int PER = DV / 32;
-  const int64_t row = blockIdx.x;  // (b, KV head, row)
-  const int head_row = (int)(row % p.nrows), head = (int)(row / p.nrows % p.Hkv), b = (int)(row / p.nrows / p.Hkv);
+  constexpr int PER = DV / 32, AHEAD = 8;  // columns of a lane; parts read at once
   const int per_seq = p.Hkv * p.row_groups;
+  const int64_t segment = blockIdx.x / slices;
+  const int b = (int)(segment / per_seq), seg = (int)(segment % per_seq), head = seg / p.row_groups;
   grid_dependency();
   const Parts parts(p, p.before[p.B] * per_seq);
   const int32_t entries = p.before[b + 1] - p.before[b];
-  const int32_t u0 = p.before[b] * per_seq + entries * (head * p.row_groups + head_row / TILE);
-  const int c0 = parts.owner(u0), c1 = parts.owner(u0 + entries - 1);
+  const int32_t u0 = p.before[b] * per_seq + entries * seg + kPieceSteps, u1 = u0 + entries - kPieceSteps - 1;
+  const int c0 = parts.owner(u0), c1 = parts.owner(u1);
   if (c0 == c1) return;  // written by that CTA
-  const int r = head_row % TILE;
-  // It is the first piece of CTA c0 if nothing of the one before is that CTA's.
-  const int64_t first = (int64_t)2 * c0 + (parts.begin(c0) >= u0 ? 0 : 1);
-  constexpr int AHEAD = 4;  // parts read at once
-  float top = -INFINITY, sum = 0.f, acc[PER];
+  const int tile0 = (seg % p.row_groups) * TILE, rows = min(TILE, p.nrows - tile0);
+  const float v_scale = p.v_scale != nullptr ? p.v_scale[head] : 1.f;
+  for (int r = blockIdx.x % slices * kJoinRows + warp; r < min(rows, (int)(blockIdx.x % slices + 1) * kJoinRows); r += kJoinWarps) {
+    float top = -INFINITY, sum = 0.f, acc[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-  for (int c = c0 + warp; c <= c1; c += kJoinWarps * AHEAD) {
-    float2 ml[AHEAD];
-    float x[AHEAD][PER];
-    float above = top;
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+    for (int c = c0; c <= c1; c += AHEAD) {
+      float2 ml[AHEAD];
+      float x[AHEAD][PER];
+      float above = top;
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
-      const int ca = c + a * kJoinWarps;
-      ml[a] = make_float2(-INFINITY, 0.f);
-      if (ca <= c1) {
-        const int64_t at = (ca == c0 ? first : (int64_t)2 * ca) * p.part_rows + r;
-        ml[a] = *reinterpret_cast<const float2 *>(p.part_ml + at * 2);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) x[a][i] = p.part_o[at * DV + i * 32 + lane];
+      for (int a = 0; a < AHEAD; ++a) {
+        ml[a] = make_float2(-INFINITY, 0.f);
+        if (c + a <= c1) {
+          const int64_t at = (int64_t)(2 * (c + a) + (c + a == c0 ? 1 : 0)) * p.part_rows + r;
+          ml[a] = *reinterpret_cast<const float2 *>(p.part_ml + at * 2);
+          if constexpr (PER == 4)
+            *reinterpret_cast<float4 *>(x[a]) = reinterpret_cast<const float4 *>(p.part_o + at * DV)[lane];
+          else
+            *reinterpret_cast<float2 *>(x[a]) = reinterpret_cast<const float2 *>(p.part_o + at * DV)[lane];
+        }
       }
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) above = fmaxf(above, ml[a].x);
+      const float ref = above == -INFINITY ? 0.f : above, f0 = ex2_approx(top - ref);
+      sum *= f0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] = scaled(f0, acc[i]);
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) {
+        if (c + a > c1) break;
+        const float f = ex2_approx(ml[a].x - ref);
+        sum += f * ml[a].y;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] += scaled(f, x[a][i]);
+      }
+      top = above;
     }
-#pragma unroll
-    for (int a = 0; a < AHEAD; ++a) above = fmaxf(above, ml[a].x);
-    const float ref = above == -INFINITY ? 0.f : above, f0 = ex2_approx(top - ref);
-    sum *= f0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = scaled(f0, acc[i]);
-#pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
-      if (c + a * kJoinWarps > c1) break;
-      const float f = ex2_approx(ml[a].x - ref);
-      sum += f * ml[a].y;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] += scaled(f, x[a][i]);
-    }
-    top = above;
+    const float inv = sum == 0.f ? 0.f : v_scale / sum;
+    const int64_t row = ((int64_t)b * p.Hkv + head) * p.nrows + tile0 + r;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + row * DV) + lane * (PER / 2);
+    if constexpr (PER == 4)
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    else
+      *dst = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
   }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) s_o[warp][i * 32 + lane] = acc[i];
-  if (lane == 0) s_sum[warp] = sum, s_top[warp] = top;
-  __syncthreads();
-  float f[kJoinWarps];
-  top = -INFINITY;
-  sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w]);
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    f[w] = ex2_approx(s_top[w] - (top == -INFINITY ? 0.f : top));
-    sum += f[w] * s_sum[w];
-  }
-  const float inv = sum == 0.f ? 0.f : (p.v_scale != nullptr ? p.v_scale[head] : 1.f) / sum;
-  if ((int)threadIdx.x < DV / 2) {
-    float x = 0.f, y = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      x += scaled(f[w], s_o[w][2 * threadIdx.x]);
-      y += scaled(f[w], s_o[w][2 * threadIdx.x + 1]);
-    }
-    reinterpret_cast<uint32_t *>(p.out + row * DV)[threadIdx.x] = pack_bf16x2(x * inv, y * inv);
-  }
-  if (threadIdx.x == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 int64_t align16(int64_t x) { return (x + 15) & ~(int64_t)15; }
@@ -1020,8 +1100,9 @@ splash_status launch(const splash_paged_decode_args &a, Params p, cudaStream_t s
   SPLASH_CUDA_TRY(launch_dependent(tree_decode_kernel<C>, dim3(p.ctas), dim3(C::THREADS), C::SMEM, 1, stream, map_k, map_v, p));
   splash_count_launches(1);
   if (most <= 1) return SPLASH_OK;  // (no segment has more than one step: nothing to join)
-  const dim3 rows((unsigned)((int64_t)p.B * p.Hkv * p.nrows));
-  SPLASH_CUDA_TRY(launch_dependent(tree_join_kernel<C::DV, C::TILE>, rows, dim3(32 * kJoinWarps), 0, 1, stream, p));
+  const int slices = (p.part_rows + kJoinRows - 1) / kJoinRows;
+  SPLASH_CUDA_TRY(launch_dependent(tree_join_kernel<C::DV, C::TILE>, dim3((unsigned)(segments * slices)), dim3(32 * kJoinWarps), 0, 1,
+                                   stream, p, slices));
   splash_count_launches(1);
   return SPLASH_OK;
 }

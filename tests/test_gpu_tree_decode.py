@@ -304,11 +304,15 @@ def test_what_is_wrong_is_reported(splash, T, Hq):
         bad[1, 0] = entry
         got = splash.paged_tree_decode(**{**x, "block_table": bad})
         assert splash.last_device_error() == 7 and others(got) and torch.isfinite(got[0]).all()
+    want = bounds(x)
     for length in (-3, 10 ** 6):
         lens = x["seq_lens"].clone()
         lens[1] = length
         got = splash.paged_tree_decode(**{**x, "seq_lens": lens})
-        assert splash.last_device_error() == 7 and others(got)
+        assert splash.last_device_error() == 7
+        # (other lengths cut the list of steps elsewhere: the others' sums are rounded in another order)
+        for i in (0, 2):
+            assert (np.abs(host(got[0]) - want[0]) <= want[2])[i].all() and (np.abs(host(got[1]) - want[1]) <= want[3])[i].all()
         if length < 0:
             assert not got[0][1].any() and torch.isneginf(got[1][1]).all()
     for parent in (1, T - 1, T, 2 ** 31 - 1):
