@@ -58,6 +58,7 @@ struct Params {
   __nv_bfloat16 *out;
   float *lse;
   float *part_o, *part_ml;  // [2 * CTAs][part_rows][DV], [2 * CTAs][part_rows][2] (maximum, sum)
+  int32_t *lost;            // [CTAs] whether it put zeros in the place of values
   int32_t *before;          // [B + 1] list entries (of one head and row group) before each sequence's
   int64_t num_pages;
   int32_t B, Hkv, T, G, nrows, row_groups, part_rows;  // nrows = G * T rows per KV head
@@ -540,30 +541,9 @@ struct Queries {
   }
 };
 
-// Adds to 32 columns of a row the values that are not finite of the keys it sees in
-// a piece's steps that are not whole (the product had zeros in their place).
-template <class C>
-__device__ __noinline__ void add_lost(const Params &p, const Piece &x, int head, int32_t lo, uint64_t seen, int col, float (&o)[32]) {
-  for (int i = 0; i < x.steps; ++i) {
-    const int32_t key0 = (x.s.step0 + x.step + i) * C::KW;
-    if (whole<C::KW>(p, x.s, key0)) continue;
-    for (uint64_t m = visible(key0, x.s.ctx, lo, seen); m != 0; m &= m - 1) {
-      const int32_t key = key0 + __ffsll(m) - 1;
-      const int32_t page = p.block_table[x.b * p.block_table_stride + (key >> p.page_shift)];
-      if (page < 0 || page >= p.num_pages) continue;
-      const char *v = p.v + page * p.v_page + head * p.v_head + (key & ((1 << p.page_shift) - 1)) * p.v_token;
-#pragma unroll 1
-      for (int c = 0; c < 32; ++c) {
-        const float y = C::E4M3 ? (float)reinterpret_cast<const __nv_fp8_e4m3 *>(v)[col + c]
-                                : __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(v)[col + c]);
-        if (!(fabsf(y) < INFINITY)) o[c] += y;
-      }
-    }
-  }
-}
-
 // The values of a step that are not finite become zeros: the product adds 0 x value
-// for the rows that do not see a key.  128 threads; returns whether there were any.
+// for the rows that do not see a key.  128 threads; returns whether there were any
+// (then the join adds them where they are seen).
 template <class C>
 __device__ __forceinline__ bool clean_values(uint32_t tile, int tid) {
   constexpr uint32_t TOP = C::E4M3 ? 0x7c00u : 0x7f80u;
@@ -583,8 +563,7 @@ __device__ __forceinline__ bool clean_values(uint32_t tile, int tid) {
 // What a row has when its piece's steps are done.
 struct Done {
   Piece x;
-  uint64_t seen;
-  int32_t lo;
+  bool empty;      // padding
   float m, sum;    // of both groups
   float f0, f1;    // the outputs' factors: f0 O_0 + f1 O_1
   bool two;        // O_1 is there
@@ -592,11 +571,10 @@ struct Done {
 
 // Writes a finished piece: rows of the result, or this CTA's part of them.
 template <class C>
-__device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint32_t o_0, int t, int row0, int rows, int tid,
-                                           const volatile int *lost) {
+__device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint32_t o_0, int t, int row0, int rows, int tid) {
   constexpr bool PAIR = C::PAIR;
   const int head = d.x.seg / p.row_groups, slot = d.x.slot(blockIdx.x);
-  const bool real = tid < rows, empty = d.sum == 0.f || d.seen == 0;
+  const bool real = tid < rows, empty = d.sum == 0.f || d.empty;
   const float inv = (C::E4M3 ? p.v_scale[head] : 1.f) / d.sum;
   const int64_t row = slot < 0 ? ((int64_t)d.x.b * p.Hkv + head) * p.nrows + row0 + tid : (int64_t)slot * p.part_rows + (PAIR ? t * 128 : 0) + tid;
 #pragma unroll 1
@@ -613,14 +591,6 @@ __device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint3
     if (d.two) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) o[j] = scaled(d.f0, o[j]) + scaled(d.f1, __uint_as_float(z[j]));
-    }
-    if (*lost && real) {
-      float w[32];  // (in memory: the call takes its address)
-#pragma unroll
-      for (int j = 0; j < 32; ++j) w[j] = o[j];
-      add_lost<C>(p, d.x, head, d.lo, d.seen, 32 * c, w);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = w[j];
     }
     if (real && slot < 0) {
       uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * C::DV + 32 * c);
@@ -686,7 +656,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
     }
     if (some) {
       tc_fence_after();
-      if (32 * warp < done_rows) write_rows<C>(p, d, o_0, t, done_row0, done_rows, tid, lost);
+      if (32 * warp < done_rows) write_rows<C>(p, d, o_0, t, done_row0, done_rows, tid);
       tc_fence_before();
       some = false;
     }
@@ -815,8 +785,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
     if (!ok) break;
 
     d.x = x;
-    d.seen = me.seen;
-    d.lo = lo;
+    d.empty = me.seen == 0;
     d.m = m;
     d.sum = sum;
     d.f0 = 1.f;
@@ -960,18 +929,49 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0) p.lost[blockIdx.x] = s_lost;
   if (warp == C::MMA) {
     tc_fence_after();
     tmem_dealloc(s_tmem, C::COLS);
   }
 }
 
+// Adds to a row's columns the values that are not finite of the keys that it sees in the
+// segment's steps that are not whole (the products had zeros in their place): a value
+// that is infinite or NaN is the result's, whatever else is in it.  A warp; returns
+// whether there were any.
+template <int DV, bool E4M3>
+__device__ __noinline__ bool add_lost(const Params &p, const Span &s, int b, int head, int row, float (&acc)[DV / 32]) {
+  constexpr int KW = 64, PER = DV / 32;
+  bool bad = false, found = false;
+  const Branch me = branch_of(p.parents + b * p.parents_stride, row % p.T, max(0, -s.ctx), p.window, &bad);
+  const int32_t lo = p.window < 0 ? 0 : max(0, s.ctx + me.depth - p.window);
+  for (int i = 0; i < s.nst; ++i) {
+    const int32_t key0 = (s.step0 + i) * KW;
+    if (whole<KW>(p, s, key0)) continue;
+    for (uint64_t m = visible(key0, s.ctx, lo, me.seen); m != 0; m &= m - 1) {
+      const int32_t key = key0 + __ffsll((long long)m) - 1;
+      const int32_t page = p.block_table[b * p.block_table_stride + (key >> p.page_shift)];
+      if (page < 0 || page >= p.num_pages) continue;
+      const char *v = p.v + page * p.v_page + head * p.v_head + (key & ((1 << p.page_shift) - 1)) * p.v_token;
+#pragma unroll
+      for (int c = 0; c < PER; ++c) {
+        const int col = (threadIdx.x & 31) * PER + c;
+        const float y = E4M3 ? (float)reinterpret_cast<const __nv_fp8_e4m3 *>(v)[col]
+                             : __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(v)[col]);
+        if (!(fabsf(y) < INFINITY)) acc[c] += y, found = true;
+      }
+    }
+  }
+  return __any_sync(~0u, found);
+}
+
 // Joins the parts of a segment that several CTAs computed: with (m_c, l_c, o_c) of part c
 // of a row and m = max m_c: out = sum exp(m_c - m) o_c / sum exp(m_c - m) l_c, in the
-// order of the keys.  A CTA takes kJoinRows rows of a segment, a warp one at a time.
-constexpr int kJoinWarps = 8, kJoinRows = 32;
-template <int DV, int TILE>
-__global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const Params p, int slices) {
+// order of the keys.  A CTA takes `each` rows of a segment, a warp one at a time.
+constexpr int kJoinWarps = 8;
+template <int DV, int TILE, bool E4M3>
+__global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const Params p, int slices, int each) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int PER = DV / 32, AHEAD = 8;  // columns of a lane; parts read at once
   const int per_seq = p.Hkv * p.row_groups;
@@ -982,14 +982,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const Params
   const int32_t entries = p.before[b + 1] - p.before[b];
   const int32_t u0 = p.before[b] * per_seq + entries * seg + kPieceSteps, u1 = u0 + entries - kPieceSteps - 1;
   const int c0 = parts.owner(u0), c1 = parts.owner(u1);
-  if (c0 == c1) return;  // written by that CTA
+  bool lost = false;
+  for (int c = c0 + lane; c <= c1; c += 32) lost |= p.lost[c] != 0;
+  lost = __any_sync(~0u, lost);
+  if (c0 == c1 && !lost) return;  // written by that CTA
   const int tile0 = (seg % p.row_groups) * TILE, rows = min(TILE, p.nrows - tile0);
-  const float v_scale = p.v_scale != nullptr ? p.v_scale[head] : 1.f;
-  for (int r = blockIdx.x % slices * kJoinRows + warp; r < min(rows, (int)(blockIdx.x % slices + 1) * kJoinRows); r += kJoinWarps) {
+  const float v_scale = E4M3 ? p.v_scale[head] : 1.f;
+  const int r0 = blockIdx.x % slices * each, r1 = min(rows, r0 + each);
+  for (int r = r0 + warp; r < r1; r += kJoinWarps) {
+    const int64_t row = ((int64_t)b * p.Hkv + head) * p.nrows + tile0 + r;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + row * DV) + lane * (PER / 2);
     float top = -INFINITY, sum = 0.f, acc[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-    for (int c = c0; c <= c1; c += AHEAD) {
+    for (int c = c0; c <= c1 && c0 < c1; c += AHEAD) {
       float2 ml[AHEAD];
       float x[AHEAD][PER];
       float above = top;
@@ -1022,13 +1028,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const Params
       top = above;
     }
     const float inv = sum == 0.f ? 0.f : v_scale / sum;
-    const int64_t row = ((int64_t)b * p.Hkv + head) * p.nrows + tile0 + r;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + row * DV) + lane * (PER / 2);
+    if (c0 < c1 && lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = c0 < c1 ? acc[i] * inv : __bfloat162float(p.out[row * DV + lane * PER + i]);
+    bool changed = false;
+    if (lost) {
+      float w[PER];  // (in memory: the call takes its address)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) w[i] = acc[i];
+      changed = add_lost<DV, E4M3>(p, span_of<64>(p, b), b, head, tile0 + r, w);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] = w[i];
+    }
+    if (c0 == c1 && !changed) continue;
     if constexpr (PER == 4)
-      *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
     else
-      *dst = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+      *dst = pack_bf16x2(acc[0], acc[1]);
   }
 }
 
@@ -1083,6 +1099,8 @@ splash_status launch(const splash_paged_decode_args &a, Params p, cudaStream_t s
   char *ws = static_cast<char *>(a.workspace);
   p.before = reinterpret_cast<int32_t *>(ws);
   ws += align16(4 * ((int64_t)p.B + 1));
+  p.lost = reinterpret_cast<int32_t *>(ws);
+  ws += 4 * kMaxCtas;
   p.part_ml = reinterpret_cast<float *>(ws);
   ws += (int64_t)2 * kMaxCtas * p.part_rows * 2 * 4;
   p.part_o = reinterpret_cast<float *>(ws);
@@ -1099,10 +1117,10 @@ splash_status launch(const splash_paged_decode_args &a, Params p, cudaStream_t s
   p.ctas = (int)std::min<int64_t>({most * segments, (int64_t)sms, (int64_t)kMaxCtas});
   SPLASH_CUDA_TRY(launch_dependent(tree_decode_kernel<C>, dim3(p.ctas), dim3(C::THREADS), C::SMEM, 1, stream, map_k, map_v, p));
   splash_count_launches(1);
-  if (most <= 1) return SPLASH_OK;  // (no segment has more than one step: nothing to join)
-  const int slices = (p.part_rows + kJoinRows - 1) / kJoinRows;
-  SPLASH_CUDA_TRY(launch_dependent(tree_join_kernel<C::DV, C::TILE>, dim3((unsigned)(segments * slices)), dim3(32 * kJoinWarps), 0, 1,
-                                   stream, p, slices));
+  // a row per warp, or four where that still fills the GPU
+  const int each = segments * p.part_rows >= 32 * 1024 ? 4 * kJoinWarps : kJoinWarps, slices = (p.part_rows + each - 1) / each;
+  SPLASH_CUDA_TRY(launch_dependent(tree_join_kernel<C::DV, C::TILE, C::E4M3>, dim3((unsigned)(segments * slices)), dim3(32 * kJoinWarps), 0, 1,
+                                   stream, p, slices, each));
   splash_count_launches(1);
   return SPLASH_OK;
 }
@@ -1118,7 +1136,7 @@ splash_status pick(const splash_paged_decode_args &a, const Params &p, cudaStrea
 size_t splash_paged_tree_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t, int32_t dv, int32_t, int32_t,
                                                 int32_t, int64_t) {
   const int64_t rows = std::min<int64_t>((int64_t)(Hq / Hkv) * T, 256);
-  return (size_t)(splash::align16(4 * ((int64_t)B + 1)) + (int64_t)2 * splash::kMaxCtas * rows * 4 * (dv + 2));
+  return (size_t)(splash::align16(4 * ((int64_t)B + 1)) + 4 * splash::kMaxCtas + (int64_t)2 * splash::kMaxCtas * rows * 4 * (dv + 2));
 }
 
 splash_status splash_paged_tree_decode_launch(const splash_paged_tree_decode_args &args, cudaStream_t stream, uint32_t *err_word) {
