@@ -503,8 +503,8 @@ struct Queries {
 #pragma unroll
       for (int c = 0; c < COLS; ++c) q[k][c] = i < rows ? *reinterpret_cast<const uint4 *>(src + c * 128) : make_uint4(0, 0, 0, 0);
     }
-    parent = thread < p.T ? p.parents[x.b * p.parents_stride + thread] : -2;
-    k_scale = C::E4M3 ? p.k_scale[head] : 1.f;
+    parent = rows > 0 && thread < p.T ? p.parents[x.b * p.parents_stride + thread] : -2;
+    k_scale = C::E4M3 && rows > 0 ? p.k_scale[head] : 1.f;
   }
 
   // Into the operand tile.  For an e4m3 cache the queries become fp16, a row scaled by the
@@ -579,18 +579,19 @@ __device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint3
   const int64_t row = slot < 0 ? ((int64_t)d.x.b * p.Hkv + head) * p.nrows + row0 + tid : (int64_t)slot * p.part_rows + (PAIR ? t * 128 : 0) + tid;
 #pragma unroll 1
   for (int c = PAIR ? 0 : t; c < C::DV / 32; c += PAIR ? 1 : 2) {  // (groups that share a tile take every other 32 columns)
-    uint32_t y[32], z[32];
+    uint32_t y[32];
     float o[32];
     tmem_ld32(o_0 + 32 * c, y);
-    if (d.two) tmem_ld32(o_0 + C::GROUP_COLS + 32 * c, z);
     tmem_wait_ld();
     reg_fence32(y);
-    reg_fence32(z);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(y[j]);
+    for (int j = 0; j < 32; ++j) o[j] = d.two ? scaled(d.f0, __uint_as_float(y[j])) : __uint_as_float(y[j]);
     if (d.two) {
+      tmem_ld32(o_0 + C::GROUP_COLS + 32 * c, y);
+      tmem_wait_ld();
+      reg_fence32(y);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = scaled(d.f0, o[j]) + scaled(d.f1, __uint_as_float(z[j]));
+      for (int j = 0; j < 32; ++j) o[j] += scaled(d.f1, __uint_as_float(y[j]));
     }
     if (real && slot < 0) {
       uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * C::DV + 32 * c);
@@ -632,7 +633,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
   uint32_t cnt = 0, pieces = 0, step = 0, skipped = 0;  // of this group; steps of the CTA before x
   int row0 = 0, rows = 0, done_row0 = 0, done_rows = 0, tree = -1;
   bool ok = true, some = false;  // some: a piece is finished and not written
-  Piece x;
+  Piece x = {};
   Done d;
   Queries<C> queries;
   Branch me = {0, 0};
@@ -647,7 +648,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
     return false;
   };
   bool more = advance();
-  if (more) queries.ask(p, x, row0, rows);
+  queries.ask(p, x, row0, more ? rows : 0);
   while (more || some) {
     if (more) {
       queries.put(p, q_tile, s_parents, s_factor);
@@ -796,7 +797,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
     some = true;
     step += x.steps;
     more = advance();
-    if (more) queries.ask(p, x, row0, rows);
+    queries.ask(p, x, row0, more ? rows : 0);  // (always: nothing of the last ones stays in registers)
     // (o_done may be two products behind here, which its parity would not tell from none)
     if (!(ok = __all_sync(~0u, mbar_wait(bar.o_last(PAIR ? t : 0), pieces++ & 1u, abort, kTimeoutNs)))) break;
     if (!PAIR) {
