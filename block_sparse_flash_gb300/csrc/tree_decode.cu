@@ -27,7 +27,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxCtas = 160;              // of the grid; the workspace holds two parts for each
 // A piece's start and end cost a CTA about as much as this many steps: a segment
 // counts for so many more when the list is cut into equal parts.
-constexpr int kPieceSteps = 2;
+constexpr int kPieceSteps = 9;
 constexpr uint64_t kTimeoutNs = 1000000000ull;  // of a wait
 
 // A running maximum is only moved when a score passes it by more than this (in
