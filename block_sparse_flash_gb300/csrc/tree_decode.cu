@@ -63,6 +63,7 @@ struct Params {
   int64_t num_pages;
   int32_t B, Hkv, T, G, nrows, row_groups, part_rows;  // nrows = G * T rows per KV head
   int32_t max_pages, page_shift, window;               // window < 0: none
+  uint32_t over_T;                                     // rounded up 2^32 / T: n / T for n T < 2^32
   int32_t ctas, min_steps;                             // of the grid; least steps of a CTA's part
   float scale, cap;                                    // cap <= 0: none
   uint32_t *err;
@@ -109,10 +110,9 @@ struct Span {
 };
 
 template <int KW>
-__device__ __forceinline__ Span span_of(const Params &p, int b) {
+__device__ __forceinline__ Span span_of(const Params &p, int32_t n) {  // n: the sequence's length as given
   Span s;
   const int64_t most = (int64_t)p.max_pages << p.page_shift;
-  const int32_t n = p.seq_lens[b];
   s.n = n < 0 ? 0 : n > most ? (int32_t)most : n;
   s.ctx = s.n - p.T;
   s.lo = p.window < 0 ? 0 : max(0, s.ctx - p.window);
@@ -155,9 +155,10 @@ struct Walk {
   const Params &p;
   int32_t u, end, per_seq;
   int32_t b, seg, entry;  // the entry of segment seg that u is
-  Span s;
+  int32_t length;         // of sequence b, as given (read when b is entered, needed at its first piece)
   __device__ __forceinline__ bool next(Piece &x) {
     while (u < end) {
+      const Span s = span_of<KW>(p, length);
       const int32_t to = min(s.nst + kPieceSteps, entry + (end - u));
       x.b = b;
       x.seg = seg;
@@ -169,7 +170,7 @@ struct Walk {
       if (++seg == per_seq) {
         seg = 0;
         ++b;
-        if (u < end) s = span_of<KW>(p, b);
+        if (u < end) length = p.seq_lens[b];
       }
       if (x.steps > 0) return true;
     }
@@ -237,8 +238,9 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// f x; an infinite value stays one however small its factor (0 x infinity would be NaN).
-__device__ __forceinline__ float scaled(float f, float x) { return fabsf(x) == INFINITY ? x : f * x; }
+// 2^x as the factor of a sum of parts: never 0, so that an infinite part stays one (0 x
+// infinity would be NaN); 2^-149 of a finite one is nothing.
+__device__ __forceinline__ float factor_of(float x) { return fmaxf(ex2_approx(x), 0x1p-149f); }
 // A number cut off to bf16.
 __device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 // The larger exponent field of a word's two bf16 values, and the word as fp16
@@ -249,9 +251,9 @@ __device__ __forceinline__ uint32_t to_half(uint32_t x, float down) {
 }
 
 // A word's 16-bit values that are not finite (exponent bits `top` all set) become 0.
-__device__ __forceinline__ uint32_t finite(uint32_t x, uint32_t top, bool &lost) {
-  if ((x & top) == top) x &= 0xffff0000u, lost = true;
-  if ((x >> 16 & top) == top) x &= 0xffffu, lost = true;
+__device__ __forceinline__ uint32_t finite(uint32_t x, uint32_t top) {
+  if ((x & top) == top) x &= 0xffff0000u;
+  if ((x >> 16 & top) == top) x &= 0xffffu;
   return x;
 }
 
@@ -498,7 +500,7 @@ struct Queries {
     const char *base = p.q + x.b * p.q_b + (int64_t)head * p.G * p.q_h + (threadIdx.x & 7) * 16;
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
-      const int i = row(k), g = (row0 + i) / p.T, l = row0 + i - g * p.T;
+      const int i = row(k), g = p.T == 1 ? row0 + i : (int)__umulhi(row0 + i, p.over_T), l = row0 + i - g * p.T;
       const char *src = base + g * p.q_h + l * p.q_l;
 #pragma unroll
       for (int c = 0; c < COLS; ++c) q[k][c] = i < rows ? *reinterpret_cast<const uint4 *>(src + c * 128) : make_uint4(0, 0, 0, 0);
@@ -546,55 +548,62 @@ struct Queries {
 // (then the join adds them where they are seen).
 template <class C>
 __device__ __forceinline__ bool clean_values(uint32_t tile, int tid) {
-  constexpr uint32_t TOP = C::E4M3 ? 0x7c00u : 0x7f80u;
-  bool found = false;
-#pragma unroll 4
-  for (int i = tid; i < C::KW * C::DV / 8; i += 128) {
-    const uint4 y = load_shared4(tile + i * 16);
-    bool here = false;
-    const uint32_t w[4] = {finite(y.x, TOP, here), finite(y.y, TOP, here), finite(y.z, TOP, here), finite(y.w, TOP, here)};
-    if (here) st_shared_v4(tile + i * 16, w[0], w[1], w[2], w[3]);
-    found |= here;
+  constexpr uint32_t TOP = C::E4M3 ? 0x7c007c00u : 0x7f807f80u, STEP = C::E4M3 ? 0x04000400u : 0x00800080u;
+  constexpr int EACH = C::KW * C::DV / 8 / 128;
+  uint32_t high = 0;  // the top bit of a half: some exponent had all its bits set
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const uint4 y = load_shared4(tile + (tid + 128 * i) * 16);
+    high |= ((y.x & TOP) + STEP) | ((y.y & TOP) + STEP) | ((y.z & TOP) + STEP) | ((y.w & TOP) + STEP);
   }
-  if (found) fence_proxy_async_shared();
-  return found;
+  if ((high & 0x80008000u) == 0) return false;
+#pragma unroll 1
+  for (int i = 0; i < EACH; ++i) {
+    const uint32_t at = tile + (tid + 128 * i) * 16;
+    const uint4 y = load_shared4(at);
+    st_shared_v4(at, finite(y.x, TOP & 0xffffu), finite(y.y, TOP & 0xffffu), finite(y.z, TOP & 0xffffu), finite(y.w, TOP & 0xffffu));
+  }
+  fence_proxy_async_shared();
+  return true;
 }
 
 // What a row has when its piece's steps are done.
 struct Done {
-  Piece x;
-  bool empty;      // padding
+  int64_t row;     // of the result, or of the parts
+  float scale;     // of the values
   float m, sum;    // of both groups
   float f0, f1;    // the outputs' factors: f0 O_0 + f1 O_1
+  bool complete;   // the result's
+  bool empty;      // padding
   bool two;        // O_1 is there
 };
 
 // Writes a finished piece: rows of the result, or this CTA's part of them.
 template <class C>
-__device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint32_t o_0, int t, int row0, int rows, int tid) {
+__device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint32_t o_0, int t, bool real) {
   constexpr bool PAIR = C::PAIR;
-  const int head = d.x.seg / p.row_groups, slot = d.x.slot(blockIdx.x);
-  const bool real = tid < rows, empty = d.sum == 0.f || d.empty;
-  const float inv = (C::E4M3 ? p.v_scale[head] : 1.f) / d.sum;
-  const int64_t row = slot < 0 ? ((int64_t)d.x.b * p.Hkv + head) * p.nrows + row0 + tid : (int64_t)slot * p.part_rows + (PAIR ? t * 128 : 0) + tid;
+  const bool empty = d.sum == 0.f || d.empty;
+  const float inv = __fdividef(d.scale, d.sum);
+  // (groups that share a tile take a half of the columns each)
+  constexpr int COLS = PAIR ? C::DV : C::DV / 2;
 #pragma unroll 1
-  for (int c = PAIR ? 0 : t; c < C::DV / 32; c += PAIR ? 1 : 2) {  // (groups that share a tile take every other 32 columns)
+  for (int c = PAIR ? 0 : t * COLS; c < (PAIR ? COLS : (t + 1) * COLS); c += 32) {
     uint32_t y[32];
     float o[32];
-    tmem_ld32(o_0 + 32 * c, y);
+    tmem_ld32(o_0 + c, y);
     tmem_wait_ld();
     reg_fence32(y);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) o[j] = d.two ? scaled(d.f0, __uint_as_float(y[j])) : __uint_as_float(y[j]);
+    for (int j = 0; j < 32; ++j) o[j] = d.two ? d.f0 * __uint_as_float(y[j]) : __uint_as_float(y[j]);
     if (d.two) {
-      tmem_ld32(o_0 + C::GROUP_COLS + 32 * c, y);
+      tmem_ld32(o_0 + C::GROUP_COLS + c, y);
       tmem_wait_ld();
       reg_fence32(y);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] += scaled(d.f1, __uint_as_float(y[j]));
+      for (int j = 0; j < 32; ++j) o[j] += d.f1 * __uint_as_float(y[j]);
     }
-    if (real && slot < 0) {
-      uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * C::DV + 32 * c);
+    if (real && d.complete) {
+      uint4 *dst = reinterpret_cast<uint4 *>(p.out + d.row * C::DV + c);
 #pragma unroll
       for (int j = 0; j < 32; ++j) o[j] = empty ? 0.f : o[j] * inv;
 #pragma unroll
@@ -602,17 +611,17 @@ __device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint3
         dst[j] = make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
                             pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7]));
     } else if (real) {
-      float4 *dst = reinterpret_cast<float4 *>(p.part_o + row * C::DV + 32 * c);
+      float4 *dst = reinterpret_cast<float4 *>(p.part_o + d.row * C::DV + c);
 #pragma unroll
       for (int j = 0; j < 8; ++j) dst[j] = empty ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
     }
     __syncwarp();
   }
   if (real && (PAIR || t == 0)) {
-    if (slot < 0)
-      p.lse[row] = empty ? -INFINITY : (d.m + log2f(d.sum)) * kLn2;
+    if (d.complete)
+      p.lse[d.row] = empty ? -INFINITY : (d.m + log2f(d.sum)) * kLn2;
     else
-      *reinterpret_cast<float2 *>(p.part_ml + 2 * row) = empty ? make_float2(-INFINITY, 0.f) : make_float2(d.m, d.sum);
+      *reinterpret_cast<float2 *>(p.part_ml + 2 * d.row) = empty ? make_float2(-INFINITY, 0.f) : make_float2(d.m, d.sum);
   }
 }
 
@@ -631,7 +640,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
   const uint32_t o_0 = tmem + (PAIR ? t * C::GROUP_COLS : 0) + lanes + 2 * KW, q_tile = q_addr + (PAIR ? t * C::Q_BYTES : 0);
   const int bar_id = PAIR ? 1 + t : 1, bar_threads = PAIR ? 128 : 256;
   uint32_t cnt = 0, pieces = 0, step = 0, skipped = 0;  // of this group; steps of the CTA before x
-  int row0 = 0, rows = 0, done_row0 = 0, done_rows = 0, tree = -1;
+  int row0 = 0, rows = 0, done_rows = 0, tree = -1;
   bool ok = true, some = false;  // some: a piece is finished and not written
   Piece x = {};
   Done d;
@@ -657,7 +666,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
     }
     if (some) {
       tc_fence_after();
-      if (32 * warp < done_rows) write_rows<C>(p, d, o_0, t, done_row0, done_rows, tid);
+      if (32 * warp < done_rows) write_rows<C>(p, d, o_0, t, tid < done_rows);
       tc_fence_before();
       some = false;
     }
@@ -670,7 +679,8 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
       const int r = row0 + tid;
       bool bad = false;
       me = {0, 0};
-      if (real) me = branch_of(s_parents, r % p.T, max(0, -x.s.ctx), p.window, &bad);
+      const int l = p.T == 1 ? 0 : r - (int)__umulhi(r, p.over_T) * p.T;
+      if (real) me = branch_of(s_parents, l, max(0, -x.s.ctx), p.window, &bad);
       if (bad) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
       tree = x.b;
     }
@@ -704,9 +714,23 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
 #pragma unroll
         for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(a[j]), s[32 + j] = __uint_as_float(b[j]);
         if (p.cap > 0.f) {
+          // tanh by the series alone where it holds for the whole warp's step
           const float cap = p.cap * kLog2e;
+          float most = 0.f;
 #pragma unroll
-          for (int j = 0; j < KW; ++j) s[j] = cap * tanh_of(s[j] * factor);
+          for (int j = 0; j < KW; ++j) most = fmaxf(most, fabsf(s[j]));
+          if (__any_sync(~0u, most * factor > kTanhSeriesLimit)) {  // (NaN stays NaN either way)
+#pragma unroll
+            for (int j = 0; j < KW; ++j) s[j] = cap * tanh_of(s[j] * factor);
+          } else {
+#pragma unroll
+            for (int j = 0; j < KW; j += 2) {
+              const f32x2 x = fmul2({s[j], s[j + 1]}, {factor, factor}), u = fmul2(x, x);
+              const f32x2 y = fmul2(ffma2(fmul2(x, u), ffma2(u, {kTanhC2, kTanhC2}, {kTanhC1, kTanhC1}), x), {cap, cap});
+              s[j] = y.x;
+              s[j + 1] = y.y;
+            }
+          }
         }
         if (!all) {
           const uint64_t see = visible(key0, x.s.ctx, lo, me.seen);
@@ -749,35 +773,35 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
+        // P in 16 bits, half of the keys at a time (the registers of their scores are free then).
+        // fp16 for an e4m3 cache; for bf16 two terms, cut off and rest: 2^-16 of each p, where
+        // bf16 alone loses 2^-8, as much as the rounding of the result.  The rest is taken of
+        // (1 + 2^-23) p, which keeps it above 0: an infinite value times either term then
+        // has its sign, and the sum is that infinity (0 x infinity is NaN).
+        constexpr float above = 1.f + 0x1p-23f;
         f32x2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-        for (int j = 0; j < KW; j += 2) {
-          const f32x2 y = ffma2({s[j], s[j + 1]}, {times, times}, {-ref, -ref});
-          s[j] = ex2_approx(y.x);
-          s[j + 1] = ex2_approx(y.y);
-          acc[j / 2 & 3] = fadd2(acc[j / 2 & 3], {s[j], s[j + 1]});
+        for (int h = 0; h < 2; ++h) {
+          uint32_t u[16], v[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int k = 32 * h + 2 * j;
+            const f32x2 y = ffma2({s[k], s[k + 1]}, {times, times}, {-ref, -ref});
+            const f32x2 e = {ex2_approx(y.x), ex2_approx(y.y)};
+            acc[j & 3] = fadd2(acc[j & 3], e);
+            if (E4M3) {
+              u[j] = pack_half2(e.x, e.y);
+            } else {
+              u[j] = __byte_perm(__float_as_uint(e.x), __float_as_uint(e.y), 0x7632);
+              const f32x2 rest = ffma2(e, {above, above}, {-cut(e.x), -cut(e.y)});
+              v[j] = pack_bf16x2(rest.x, rest.y);
+            }
+          }
+          tmem_st16(base + buf * KW + 16 * h, u);
+          if (!E4M3) tmem_st16(base + buf * KW + 32 + 16 * h, v);
         }
         acc[0] = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
         sum += acc[0].x + acc[0].y;
-        if constexpr (E4M3) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) a[j] = pack_half2(s[2 * j], s[2 * j + 1]);
-          tmem_st32(base + buf * KW, a);
-        } else {
-          // P in two bf16 terms, cut off and rest: 2^-16 of each p, where bf16 alone
-          // loses 2^-8, as much as the rounding of the result.  The rest is taken of
-          // (1 + 2^-23) p, which keeps it above 0: an infinite value times either term
-          // then has its sign, and the sum is that infinity (0 x infinity is NaN).
-          constexpr float above = 1.f + 0x1p-23f;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            a[j] = __byte_perm(__float_as_uint(s[2 * j]), __float_as_uint(s[2 * j + 1]), 0x7632);
-            const f32x2 rest = ffma2({s[2 * j], s[2 * j + 1]}, {above, above}, {-cut(s[2 * j]), -cut(s[2 * j + 1])});
-            b[j] = pack_bf16x2(rest.x, rest.y);
-          }
-          tmem_st32(base + buf * KW, a);
-          tmem_st32(base + buf * KW + 32, b);
-        }
         tmem_wait_st();
         tc_fence_before();
       }
@@ -785,14 +809,16 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
     }
     if (!ok) break;
 
-    d.x = x;
+    const int head = x.seg / p.row_groups, slot = x.slot(blockIdx.x);
+    d.complete = slot < 0;
+    d.row = slot < 0 ? ((int64_t)x.b * p.Hkv + head) * p.nrows + row0 + tid : (int64_t)slot * p.part_rows + (PAIR ? t * 128 : 0) + tid;
+    d.scale = E4M3 ? p.v_scale[head] : 1.f;
     d.empty = me.seen == 0;
     d.m = m;
     d.sum = sum;
     d.f0 = 1.f;
     d.f1 = 0.f;
     d.two = !PAIR && x.steps > 1;  // the other group has steps too
-    done_row0 = row0;
     done_rows = rows;
     some = true;
     step += x.steps;
@@ -806,7 +832,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
       const float2 z = s_ml[t ^ 1][tid];
       if (d.two) {
         const float high = fmaxf(m, z.x), ref = high == -INFINITY ? 0.f : high;
-        const float mine = ex2_approx(m - ref), theirs = ex2_approx(z.x - ref);
+        const float mine = factor_of(m - ref), theirs = factor_of(z.x - ref);
         d.sum = sum * mine + z.y * theirs;
         d.m = high;
         d.f0 = t == 0 ? mine : theirs;
@@ -872,7 +898,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid
   const int per = (p.B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   int32_t own = 0;
-  for (int b = b0; b < b1; ++b) own += span_of<KW>(p, b).nst + kPieceSteps;
+  for (int b = b0; b < b1; ++b) own += span_of<KW>(p, p.seq_lens[b]).nst + kPieceSteps;
   int32_t before = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -895,7 +921,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid
   if (blockIdx.x == 0 || (begin >= before * per_seq && begin < (before + own) * per_seq)) {
     int32_t at = before;
     for (int b = b0; b < b1; ++b) {
-      const Span s = span_of<KW>(p, b);
+      const Span s = span_of<KW>(p, p.seq_lens[b]);
       const int32_t entries = s.nst + kPieceSteps;
       if (begin >= at * per_seq && begin < (at + entries) * per_seq) s_seq = b, s_before = at;
       if (blockIdx.x == 0) {
@@ -908,11 +934,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid
   }
   __syncthreads();
   if (begin < end) {
-    Walk<KW> walk{p, begin, end, per_seq, s_seq, 0, 0, {}};
-    walk.s = span_of<KW>(p, walk.b);
+    Walk<KW> walk{p, begin, end, per_seq, s_seq, 0, 0, 0};
+    walk.length = p.seq_lens[walk.b];
+    const int32_t nst = span_of<KW>(p, walk.length).nst;
     const int32_t in_seq = begin - s_before * per_seq;
-    walk.seg = (uint32_t)in_seq / (uint32_t)(walk.s.nst + kPieceSteps);
-    walk.entry = in_seq - walk.seg * (walk.s.nst + kPieceSteps);
+    walk.seg = (uint32_t)in_seq / (uint32_t)(nst + kPieceSteps);
+    walk.entry = in_seq - walk.seg * (nst + kPieceSteps);
     const uint32_t q_addr = tiles, stages = tiles + C::NT * C::Q_BYTES, raws = stages + C::STAGES * C::STAGE;
     // (registers for e4m3: 14 warps are launched with 128 a thread; 8 take 152 and 4 leave 48 each)
     if (warp < 8) {
@@ -1014,17 +1041,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const Params
       }
 #pragma unroll
       for (int a = 0; a < AHEAD; ++a) above = fmaxf(above, ml[a].x);
-      const float ref = above == -INFINITY ? 0.f : above, f0 = ex2_approx(top - ref);
+      const float ref = above == -INFINITY ? 0.f : above, f0 = factor_of(top - ref);
       sum *= f0;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] = scaled(f0, acc[i]);
+      for (int i = 0; i < PER; ++i) acc[i] *= f0;
 #pragma unroll
       for (int a = 0; a < AHEAD; ++a) {
         if (c + a > c1) break;
-        const float f = ex2_approx(ml[a].x - ref);
+        const float f = factor_of(ml[a].x - ref);
         sum += f * ml[a].y;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] += scaled(f, x[a][i]);
+        for (int i = 0; i < PER; ++i) acc[i] += f * x[a][i];
       }
       top = above;
     }
@@ -1037,7 +1064,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const Params
       float w[PER];  // (in memory: the call takes its address)
 #pragma unroll
       for (int i = 0; i < PER; ++i) w[i] = acc[i];
-      changed = add_lost<DV, E4M3>(p, span_of<64>(p, b), b, head, tile0 + r, w);
+      changed = add_lost<DV, E4M3>(p, span_of<64>(p, p.seq_lens[b]), b, head, tile0 + r, w);
 #pragma unroll
       for (int i = 0; i < PER; ++i) acc[i] = w[i];
     }
@@ -1168,6 +1195,7 @@ splash_status splash_paged_tree_decode_launch(const splash_paged_tree_decode_arg
   p.T = a.Lq;
   p.G = a.Hq / a.Hkv;
   p.nrows = p.G * a.Lq;
+  p.over_T = (uint32_t)((((uint64_t)1 << 32) + a.Lq - 1) / a.Lq);
   p.max_pages = a.max_pages;
   p.page_shift = __builtin_ctz((unsigned)a.page_size);
   // (differences of positions stay below 2^31 - 64)
