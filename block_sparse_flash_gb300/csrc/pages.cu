@@ -31,7 +31,7 @@ constexpr int kMovesEach = 4;                       // chunks that a thread has 
 
 struct CompactParams {
   Cache k, v;
-  int32_t k_slices, v_slices;  // groups of up to 8 chunk columns (128 bytes)
+  int32_t k_slices, v_slices;  // groups of up to 8 chunk columns
   const int32_t *block_table, *src, *start;
   int64_t block_table_stride, src_stride, num_pages;
   int64_t moves;
@@ -94,11 +94,8 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactPara
     bool stop, bad;
     const Move x = place(m0 + tid, &stop, &bad);
     s_move[half][tid] = x;
-    if (stop) {
-      // (an entry behind the list's end is not reported: the first one that ends it is)
-      const int before = atomicMin(&s_end[half], 2 * tid + (bad ? 1 : 0));
-      (void)before;
-    }
+    // (an entry behind the list's end is not reported: the first one that ends it is)
+    if (stop) atomicMin(&s_end[half], 2 * tid + (bad ? 1 : 0));
   };
 
   if (tid < 2) s_end[tid] = INT_MAX;
@@ -182,7 +179,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) 
 
 // ------------------------------------------------------------------ remap
 constexpr int kMapThreads = 1024, kMapCtas = 8, kMapWarps = kMapThreads / 32;
-constexpr int kPagesEach = 4;  // pages of a thread in a scan's round
+constexpr int kPagesEach = 4;    // pages of a thread in a scan's round
+constexpr int kSharedRows = 4096;  // new rows whose needs every CTA adds up by itself
 
 struct RemapParams {
   const int32_t *block_table;
@@ -192,7 +190,7 @@ struct RemapParams {
   const int32_t *parents, *keep, *room, *refs;
   int32_t *refs_out, *copies, *short_pages;
   // workspace: per page its uses, the rows that keep part of it and the first of them; the
-  // fresh pages in order; per row the fresh pages before it, from its CTA's first row on
+  // free pages in order; per row the fresh pages before it
   int32_t *uses, *parts, *first, *fresh, *before;
   int32_t *totals;  // [2][kMapCtas]: free pages, needed pages of each CTA's share
   int64_t num_pages;
@@ -200,8 +198,9 @@ struct RemapParams {
   uint32_t *err;
 };
 
-__device__ __forceinline__ void cluster_sync_global() {
-  __threadfence();
+// Every thread of every CTA of the cluster arrives and waits; what they wrote before is
+// visible after it (global memory too: the barrier releases and acquires).
+__device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -259,14 +258,28 @@ __device__ __forceinline__ bool is_page(const RemapParams &p, int32_t x) { retur
 // Whether row i's last kept page, of which it keeps a part, has to be copied
 // (after all uses are counted, each shared page once for every row that keeps it).
 __device__ __forceinline__ bool copied(const RemapParams &p, int i, int32_t page) {
-  return __ldcg(p.uses + page) != __ldcg(p.parts + page) || __ldcg(p.first + page) != i;
+  const int32_t uses = __ldcg(p.uses + page), parts = __ldcg(p.parts + page), first = __ldcg(p.first + page);
+  return uses != parts || first != i;
+}
+
+// Fresh pages that row i needs.
+__device__ __forceinline__ int32_t need_of(const RemapParams &p, int i) {
+  const Row r = row_of(p, i);
+  int32_t need = r.cols - r.cols_kept;
+  if (r.part) {
+    const int32_t x = p.block_table[r.parent * p.block_table_stride + r.cols_kept - 1];
+    if (is_page(p, x) && copied(p, i, x)) ++need;
+  }
+  return need;
 }
 
 // One cluster: its 8192 threads hold the counters of a usual pool in one or two
-// rounds, and the phases are barriers of the cluster instead of launches.  All
-// sums are of integers, so that the order of the atomics does not show.
+// rounds, and the phases are barriers of the cluster instead of launches.  What
+// bounds it is the chain of dependent reads: counts; entries, and the counts that they
+// change; last pages and their counts; fresh pages.  All sums are of integers, so that the order of
+// the atomics does not show.
 __global__ void __launch_bounds__(kMapThreads) remap_kernel(const RemapParams p) {
-  __shared__ int32_t s_warp[32];
+  __shared__ int32_t s_warp[32], s_before[kSharedRows];
   grid_dependency();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
   bool bad = false;
@@ -284,81 +297,118 @@ __global__ void __launch_bounds__(kMapThreads) remap_kernel(const RemapParams p)
   int32_t all_free;
   scan(free_pages, s_warp, &all_free);
   if (tid == 0) p.totals[cta] = all_free;
-  cluster_sync_global();
+  cluster_barrier();
 
-  // ---- uses: a warp per row of either table
-  const int all_warps = kMapCtas * kMapWarps, gw = cta * kMapWarps + warp;
-  for (int i = gw; i < p.num_rows; i += all_warps) {
-    const int32_t *row = p.block_table + i * p.block_table_stride;
-    for (int j = lane; j < p.max_pages; j += 32) {
-      const int32_t x = row[j];
-      if (is_page(p, x)) atomicSub(p.uses + x, 1);
-    }
+  // ---- uses: a warp per 32 columns of a row of either table
+  const uint32_t chunks = (uint32_t)(p.max_pages + 31) / 32, all_warps = kMapCtas * kMapWarps, gw = cta * kMapWarps + warp;
+  const uint32_t old_units = p.num_rows * chunks, new_units = p.new_rows * chunks;  // (below 2^31)
+  for (uint32_t unit = gw; unit < old_units; unit += all_warps) {
+    const int32_t i = unit / chunks, j = (unit - i * chunks) * 32 + lane;
+    const int32_t x = j < p.max_pages ? p.block_table[i * p.block_table_stride + j] : -1;
+    if (is_page(p, x)) atomicSub(p.uses + x, 1);
   }
-  for (int i = gw; i < p.new_rows; i += all_warps) {
+  for (uint32_t unit = gw; unit < new_units; unit += all_warps) {
+    const int32_t i = unit / chunks, j = (unit - i * chunks) * 32 + lane;
     const Row r = row_of(p, i);
     bad |= r.bad;
-    if (r.parent < 0) continue;
-    const int32_t *row = p.block_table + r.parent * p.block_table_stride;
-    for (int j = lane; j < r.cols_kept; j += 32) {
-      const int32_t x = row[j];
-      if (!is_page(p, x)) {
-        bad = true;
-        continue;
-      }
-      atomicAdd(p.uses + x, 1);
-      if (r.part && j == r.cols_kept - 1) {
-        atomicAdd(p.parts + x, 1);
-        atomicMin(p.first + x, i);
-      }
+    if (j >= r.cols_kept) continue;
+    const int32_t x = p.block_table[r.parent * p.block_table_stride + j];
+    if (!is_page(p, x)) {
+      bad = true;
+      continue;
+    }
+    atomicAdd(p.uses + x, 1);
+    if (r.part && j == r.cols_kept - 1) {
+      atomicAdd(p.parts + x, 1);
+      atomicMin(p.first + x, i);
     }
   }
-  cluster_sync_global();
-
-  // ---- this CTA's rows: the fresh pages each needs, and those before it
-  const int32_t rows_each = (int32_t)(((int64_t)p.new_rows + kMapCtas - 1) / kMapCtas);
-  const int32_t row0 = (int32_t)min((int64_t)p.new_rows, (int64_t)cta * rows_each), row1 = min(p.new_rows, row0 + rows_each);
-  int32_t needed = 0;
-  for (int32_t i0 = row0; i0 < row1; i0 += kMapThreads) {
-    const int i = i0 + tid;
-    int32_t need = 0;
-    if (i < row1) {
-      const Row r = row_of(p, i);
-      need = r.cols - r.cols_kept;
-      if (r.part) {
-        const int32_t x = p.block_table[r.parent * p.block_table_stride + r.cols_kept - 1];
-        if (is_page(p, x) && copied(p, i, x)) ++need;
-      }
-    }
-    int32_t all;
-    const int32_t at = scan(need, s_warp, &all);
-    if (i < row1) p.before[i] = needed + at;
-    needed += all;
-  }
-  if (tid == 0) p.totals[kMapCtas + cta] = needed;
-  cluster_sync_global();
-
-  // ---- counts out, and the fresh pages in order
-  int64_t all_needed = 0, total_free = 0;
+  // (and, meanwhile, the free pages in order)
+  int64_t total_free = 0;
   int32_t free_before = 0;
 #pragma unroll
   for (int k = 0; k < kMapCtas; ++k) {
     const int32_t f = __ldcg(p.totals + k);
     if (k < cta) free_before += f;
     total_free += f;
-    all_needed += __ldcg(p.totals + kMapCtas + k);
   }
-  const int64_t given = min(all_needed, total_free);
-  if (cta == 0 && tid == 0) *p.short_pages = (int32_t)(all_needed - given);
+  const int32_t rank0 = free_before;
   for (int64_t x0 = page0; x0 < page1; x0 += kMapThreads * kPagesEach) {
     const int64_t mine = x0 + (int64_t)tid * kPagesEach;
-    int32_t n[kPagesEach], here = 0;
+    int32_t n[kPagesEach], here = 0, all;
 #pragma unroll
     for (int k = 0; k < kPagesEach; ++k) {
       n[k] = mine + k < page1 ? p.refs[mine + k] : 1;
       here += n[k] == 0;
     }
+    int32_t rank = free_before + scan(here, s_warp, &all);
+#pragma unroll
+    for (int k = 0; k < kPagesEach; ++k)
+      if (n[k] == 0) p.fresh[rank++] = (int32_t)(mine + k);
+    free_before += all;
+  }
+  cluster_barrier();
+
+  // ---- the fresh pages that each row needs, and those before it: every CTA for all rows, or where
+  // there are many, its share of them, joined by another barrier
+  int64_t all_needed = 0;
+  const bool shared = p.new_rows <= kSharedRows;
+  const int32_t rows_each = shared ? p.new_rows : (int32_t)(((int64_t)p.new_rows + kMapCtas - 1) / kMapCtas);
+  const int32_t row0 = shared ? 0 : (int32_t)min((int64_t)p.new_rows, (int64_t)cta * rows_each), row1 = min(p.new_rows, row0 + rows_each);
+  int32_t needed = 0;
+  for (int32_t i0 = row0; i0 < row1; i0 += kMapThreads) {
+    const int i = i0 + tid;
     int32_t all;
+    const int32_t at = needed + scan(i < row1 ? need_of(p, i) : 0, s_warp, &all);
+    if (i < row1) (shared ? s_before : p.before)[i] = at;
+    needed += all;
+  }
+  if (shared) {
+    all_needed = needed;
+    __syncthreads();
+  } else {
+    if (tid == 0) p.totals[kMapCtas + cta] = needed;
+    cluster_barrier();
+    for (int k = 0; k < kMapCtas; ++k) all_needed += __ldcg(p.totals + kMapCtas + k);
+  }
+  const int64_t given = min(all_needed, total_free);
+  if (cta == 0 && tid == 0) *p.short_pages = (int32_t)(all_needed - given);
+
+  // ---- the new table: a warp per 32 columns of a row
+  for (uint32_t unit = gw; unit < new_units; unit += all_warps) {
+    const int32_t i = unit / chunks, c = unit - i * chunks, j = c * 32 + lane;
+    const Row r = row_of(p, i);
+    const int32_t *old = p.block_table + (int64_t)max(r.parent, 0) * p.block_table_stride;
+    const int32_t kept = j < r.cols_kept ? old[j] : -1, last = r.part ? old[r.cols_kept - 1] : -1;
+    int64_t rank = shared ? s_before[i] : __ldcg(p.before + i);
+    if (!shared)
+      for (int k = 0; k < i / rows_each; ++k) rank += __ldcg(p.totals + kMapCtas + k);
+    const bool copy = r.part && is_page(p, last) && copied(p, i, last);
+    const int32_t held = r.cols_kept - (copy ? 1 : 0);
+    int32_t x = -1;
+    if (j < held) {
+      x = is_page(p, kept) ? kept : -1;
+    } else if (j < r.cols && (copy || j >= r.cols_kept)) {
+      const int64_t k = rank + (j - held);
+      if (k < given) x = __ldcg(p.fresh + k);
+    }
+    if (j < p.max_pages) p.new_table[i * p.new_table_stride + j] = x;
+    if (c == 0 && lane < 3) {
+      const int32_t to = copy && rank < given ? __ldcg(p.fresh + rank) : -1;
+      const int32_t y = lane == 0 ? last : lane == 1 ? to : r.keep & ((1 << p.page_shift) - 1);
+      p.copies[3 * (int64_t)i + lane] = to >= 0 ? y : lane == 2 ? 0 : -1;
+    }
+  }
+  // ---- counts out (in place: nobody reads refs any more but this thread)
+  free_before = rank0;
+  for (int64_t x0 = page0; x0 < page1; x0 += kMapThreads * kPagesEach) {
+    const int64_t mine = x0 + (int64_t)tid * kPagesEach;
+    int32_t n[kPagesEach], here = 0, all;
+#pragma unroll
+    for (int k = 0; k < kPagesEach; ++k) {
+      n[k] = mine + k < page1 ? p.refs[mine + k] : 1;
+      here += n[k] == 0;
+    }
     int32_t rank = free_before + scan(here, s_warp, &all);
 #pragma unroll
     for (int k = 0; k < kPagesEach; ++k) {
@@ -368,46 +418,10 @@ __global__ void __launch_bounds__(kMapThreads) remap_kernel(const RemapParams p)
       int32_t uses = __ldcg(p.uses + x);
       bad |= uses < 0;
       uses -= parts > 0 && uses == parts ? parts - 1 : parts;  // (copied: not kept)
-      if (n[k] == 0) {
-        if (rank < given) {
-          p.fresh[rank] = (int32_t)x;
-          ++uses;
-        }
-        ++rank;
-      }
+      if (n[k] == 0 && rank++ < given) ++uses;
       p.refs_out[x] = uses;
     }
     free_before += all;
-  }
-  cluster_sync_global();
-
-  // ---- the new table: a warp per row
-  for (int i = gw; i < p.new_rows; i += all_warps) {
-    const Row r = row_of(p, i);
-    const int32_t *old = p.block_table + (int64_t)max(r.parent, 0) * p.block_table_stride;
-    int64_t rank = __ldcg(p.before + i);
-    const int owner = i / rows_each;
-    for (int k = 0; k < owner; ++k) rank += __ldcg(p.totals + kMapCtas + k);
-    int32_t last = -1, to = -1;
-    bool copy = false;
-    if (r.part) {
-      last = old[r.cols_kept - 1];
-      copy = is_page(p, last) && copied(p, i, last);
-    }
-    const int32_t held = r.cols_kept - (copy ? 1 : 0);
-    for (int j = lane; j < p.max_pages; j += 32) {
-      int32_t x = -1;
-      if (j < held) {
-        x = old[j];
-        if (!is_page(p, x)) x = -1;
-      } else if (j < r.cols && (copy || j >= r.cols_kept)) {
-        const int64_t k = rank + (j - held);
-        if (k < given) x = __ldcg(p.fresh + k);
-      }
-      p.new_table[i * p.new_table_stride + j] = x;
-    }
-    if (copy && rank < given) to = __ldcg(p.fresh + rank);
-    if (lane < 3) p.copies[3 * (int64_t)i + lane] = lane == 2 ? (to >= 0 ? r.keep & ((1 << p.page_shift) - 1) : 0) : to < 0 ? -1 : lane == 0 ? last : to;
   }
   if (bad) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
 }
@@ -421,8 +435,11 @@ splash_status splash_paged_compact_launch(const splash_paged_compact_args &a, cu
   CompactParams p = {};
   p.k = cache(a.k_cache, size, a.dqk);
   p.v = cache(a.v_cache, size, a.dv);
-  p.k_slices = (p.k.chunks + 7) / 8;
-  p.v_slices = (p.v.chunks + 7) / 8;
+  // slices of 128 bytes of a row, or of 64 where those leave an SM with fewer than four CTAs
+  int width = 8;
+  if ((int64_t)a.B * a.Hkv * ((p.k.chunks + 7) / 8 + (p.v.chunks + 7) / 8) < 4 * 152) width = 4;
+  p.k_slices = (p.k.chunks + width - 1) / width;
+  p.v_slices = (p.v.chunks + width - 1) / width;
   p.block_table = a.block_table;
   p.block_table_stride = a.block_table_stride;
   p.src = a.src;

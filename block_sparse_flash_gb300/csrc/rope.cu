@@ -358,7 +358,8 @@ splash_status launch(const Params &p, bool interleaved, cudaStream_t stream) {
   // row); 257 tokens of 4 heads 2.2 against 1.7 us.  Appending always takes
   // one: a prompt of 32768 tokens 99.2 us against 98.0 with four, the next token
   // of 256 requests 3.0 against 5.1.
-  if constexpr (!APPEND) {
+  // With several axes it takes four there too.
+  if constexpr (!APPEND || AXES) {
     if ((int64_t)p.tokens * p.units * ((p.heads + 3) / 4) >= 152 * 1024)
       return launch_heads<APPEND, E4M3, 4, AXES>(p, interleaved, stream);
   }
