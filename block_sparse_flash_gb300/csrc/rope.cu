@@ -126,28 +126,23 @@ __device__ __forceinline__ void load_turn(const Params &p, int64_t position, int
 
 // The same where each pair has its own axis (`code`: two bits for each of the
 // 8).  Pairs whose axis has no rotation at this position get a bit in the
-// result and are left as they are.  Vector reads for each axis among the 8
-// instead of a read per pair: at most 4 x 4 reads of 16 bytes, against 16 of 4.
+// result and are left as they are.  16 reads of 4 bytes: with the vectors of every
+// axis among the 8 and a choice from them (12 reads of 16 bytes for three axes) groups of
+// several axes take 40.8 us instead of 42.8 (the gradient of 1111 tokens, 128 + 128 heads of
+// 192), but the registers that it needs cost the others more (groups of one axis: 16384
+// tokens of 32 + 8 heads 51.0 -> 52.3, appending 8192 of them 36.4 -> 38.1).
 __device__ __forceinline__ uint32_t load_turn_axes(const Params &p, const int32_t (&at)[SPLASH_MAX_AXES], uint32_t code,
                                                    int pair, Turn &t) {
   uint32_t still = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t.c[i] = 1.f, t.s[i] = 0.f;
-#pragma unroll
-  for (int a = 0; a < SPLASH_MAX_AXES; ++a) {
-    uint32_t has = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) has |= ((code >> (2 * i)) & 3u) == (uint32_t)a ? 1u << i : 0u;
-    if (has == 0) continue;
-    if (at[a] < 0 || at[a] >= p.table_rows) {
-      still |= has;
-      continue;
-    }
-    Turn x;
-    load_turn(p, at[a], pair, x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (has >> i & 1u) t.c[i] = x.c[i], t.s[i] = x.s[i];
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t a = code >> (2 * i) & 3u;
+    const int32_t x = a == 0 ? at[0] : a == 1 ? at[1] : a == 2 ? at[2] : at[3];
+    const bool on = x >= 0 && x < p.table_rows;
+    const float *row = p.table + (int64_t)(on ? x : 0) * p.rot + pair + i;
+    t.c[i] = row[0];
+    t.s[i] = p.sign * row[p.rot / 2];
+    still |= on ? 0u : 1u << i;
   }
   return still;
 }
@@ -358,7 +353,8 @@ splash_status launch(const Params &p, bool interleaved, cudaStream_t stream) {
   // row); 257 tokens of 4 heads 2.2 against 1.7 us.  Appending always takes
   // one: a prompt of 32768 tokens 99.2 us against 98.0 with four, the next token
   // of 256 requests 3.0 against 5.1.
-  // With several axes it takes four there too.
+  // With several axes appending takes four there too: 8192 tokens of 32 + 8 + 8 heads
+  // 52.5 us with one (three more positions to wait for before the rotation), 38.1 with four.
   if constexpr (!APPEND || AXES) {
     if ((int64_t)p.tokens * p.units * ((p.heads + 3) / 4) >= 152 * 1024)
       return launch_heads<APPEND, E4M3, 4, AXES>(p, interleaved, stream);

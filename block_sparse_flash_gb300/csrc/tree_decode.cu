@@ -66,6 +66,7 @@ struct Params {
   uint32_t over_T;                                     // rounded up 2^32 / T: n / T for n T < 2^32
   int32_t ctas, min_steps;                             // of the grid; least steps of a CTA's part
   float scale, cap;                                    // cap <= 0: none
+  bool out_wide;                                       // out is 32-byte aligned
   uint32_t *err;
 };
 
@@ -578,7 +579,8 @@ struct Done {
   bool two;        // O_1 is there
 };
 
-// Writes a finished piece: rows of the result, or this CTA's part of them.
+// Writes a finished piece: rows of the result, or this CTA's part of them.  A lane has a
+// row, so that a store touches 32 lines however little it writes to each: 32 bytes a lane.
 template <class C>
 __device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint32_t o_0, int t, bool real) {
   constexpr bool PAIR = C::PAIR;
@@ -603,17 +605,24 @@ __device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint3
       for (int j = 0; j < 32; ++j) o[j] += d.f1 * __uint_as_float(y[j]);
     }
     if (real && d.complete) {
-      uint4 *dst = reinterpret_cast<uint4 *>(p.out + d.row * C::DV + c);
+      uint32_t w[16];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = empty ? 0.f : o[j] * inv;
+      for (int j = 0; j < 16; ++j) w[j] = empty ? 0u : pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
+      __nv_bfloat16 *dst = p.out + d.row * C::DV + c;
+      if (p.out_wide) {
+        st_global_v8(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+        st_global_v8(dst + 16, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        dst[j] = make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
-                            pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7]));
+        for (int j = 0; j < 4; ++j) reinterpret_cast<uint4 *>(dst)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      }
     } else if (real) {
-      float4 *dst = reinterpret_cast<float4 *>(p.part_o + d.row * C::DV + c);
+      float *dst = p.part_o + d.row * C::DV + c;
+      uint32_t w[32];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dst[j] = empty ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+      for (int j = 0; j < 32; ++j) w[j] = empty ? 0u : __float_as_uint(o[j]);
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) st_global_v8(dst + j, w[j], w[j + 1], w[j + 2], w[j + 3], w[j + 4], w[j + 5], w[j + 6], w[j + 7]);
     }
     __syncwarp();
   }
@@ -1131,7 +1140,7 @@ splash_status launch(const splash_paged_decode_args &a, Params p, cudaStream_t s
   ws += 4 * kMaxCtas;
   p.part_ml = reinterpret_cast<float *>(ws);
   ws += (int64_t)2 * kMaxCtas * p.part_rows * 2 * 4;
-  p.part_o = reinterpret_cast<float *>(ws);
+  p.part_o = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + 31) & ~(uintptr_t)31);
   int dev = 0, sms = 0;
   SPLASH_CUDA_TRY(cudaGetDevice(&dev));
   SPLASH_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
@@ -1164,7 +1173,7 @@ splash_status pick(const splash_paged_decode_args &a, const Params &p, cudaStrea
 size_t splash_paged_tree_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t, int32_t dv, int32_t, int32_t,
                                                 int32_t, int64_t) {
   const int64_t rows = std::min<int64_t>((int64_t)(Hq / Hkv) * T, 256);
-  return (size_t)(splash::align16(4 * ((int64_t)B + 1)) + 4 * splash::kMaxCtas + (int64_t)2 * splash::kMaxCtas * rows * 4 * (dv + 2));
+  return (size_t)(16 + splash::align16(4 * ((int64_t)B + 1)) + 4 * splash::kMaxCtas + (int64_t)2 * splash::kMaxCtas * rows * 4 * (dv + 2));
 }
 
 splash_status splash_paged_tree_decode_launch(const splash_paged_tree_decode_args &args, cudaStream_t stream, uint32_t *err_word) {
@@ -1189,6 +1198,7 @@ splash_status splash_paged_tree_decode_launch(const splash_paged_tree_decode_arg
   p.parents_stride = args.parents_stride_b;
   p.out = static_cast<__nv_bfloat16 *>(a.out);
   p.lse = a.lse;
+  p.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   p.num_pages = a.num_pages;
   p.B = a.B;
   p.Hkv = a.Hkv;
