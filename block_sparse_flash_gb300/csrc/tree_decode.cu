@@ -271,8 +271,7 @@ __device__ __forceinline__ float tanh_of(float x) {
 
 // A chunk of 16 e4m3 values into a row of an operand tile.
 template <class C>
-__device__ __forceinline__ void widen_chunk(uint32_t src, uint32_t dst, int row, int c) {
-  const uint4 y = load_shared4(src);
+__device__ __forceinline__ void widen_chunk(const uint4 &y, uint32_t dst, int row, int c) {
   uint32_t w[8];
   widen(y.x, w[0], w[1]);
   widen(y.y, w[2], w[3]);
@@ -308,8 +307,8 @@ __device__ __forceinline__ void give_up(const Params &p, volatile int *abort, ui
 // One warp brings the steps of the CTA's part in order, across the borders of
 // pieces: boxes of up to 64 rows (16-row pages: four) of the pages, bf16 straight into
 // the swizzled operand tiles (a box per 64 columns), e4m3 as it is into a ring of raw
-// steps.  Lanes 0 .. 3 look up a page each, two steps ahead; the warp issues the boxes
-// together (from diverged lanes each took 100 cycles).  A box with no visible key, or
+// steps.  The lanes look up 32 blocks at a time and as many ahead (a step at a time, the
+// look up cost each step 700 cycles); the warp issues the boxes together.  A box with no visible key, or
 // of a page that does not exist, lies outside the tensor and arrives as zeros; a box's
 // other rows that no token sees are masked by the softmax.
 template <class C>
@@ -327,19 +326,20 @@ __device__ __forceinline__ void run_loads(const Params &p, Walk<C::KW> walk, con
     const int head = x.seg / p.row_groups, head_k = head * p.k_head_on, head_v = head * p.v_head_on;
     const int32_t *pages = p.block_table + x.b * p.block_table_stride;
     int32_t key0 = (x.s.step0 + x.step) * KW;
-    // the page of this lane's block: -1 where no key of it is seen, -2 where it does not exist
+    // the pages of the next 32 blocks, one a lane: -1 where no key is seen, -2 where it does not exist
     auto look = [&](int32_t at) {
       at += lane * rows;
-      if (lane >= blocks || at >= x.s.n || at + rows <= x.s.lo) return -1;
+      if (at >= x.s.n || at + rows <= x.s.lo) return -1;
       const int32_t page = pages[at >> p.page_shift];
       return page >= 0 && page < p.num_pages ? page : -2;
     };
-    int32_t next = look(key0), after = x.steps > 1 ? look(key0 + KW) : -1;
-    for (int i = 0; i < x.steps; ++i, ++n, key0 += KW) {
-      const int32_t entry = next;
-      next = after;
-      if (i + 2 < x.steps) after = look(key0 + 2 * KW);
-      if (entry == -2) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
+    int32_t entries = look(key0), ahead = look(key0 + 32 * rows);
+    for (int i = 0, block = 0; i < x.steps; ++i, ++n, key0 += KW, block += blocks) {
+      if (block == 32) {
+        block = 0;
+        entries = ahead;
+        ahead = look(key0 + 32 * rows);
+      }
       const uint32_t full = C::E4M3 ? bar.raw_full(st) : bar.full(st), empty = C::E4M3 ? bar.raw_empty(st) : bar.empty(st);
       if (n >= RING && !(ok = __all_sync(~0u, mbar_wait(empty, turn, abort, kTimeoutNs)))) break;
       if (leader) mbar_arrive_expect_tx(full, C::E4M3 ? C::RAW : C::STAGE);
@@ -347,7 +347,8 @@ __device__ __forceinline__ void run_loads(const Params &p, Walk<C::KW> walk, con
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j >= blocks) break;
-        const int32_t page = __shfl_sync(~0u, entry, j), slot = (key0 + j * rows) & in_page;
+        const int32_t page = __shfl_sync(~0u, entries, block + j), slot = (key0 + j * rows) & in_page;
+        if (page == -2 && leader) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
         const int32_t page_k = page < 0 ? p.k_page_end : page * p.k_page_on, page_v = page < 0 ? p.v_page_end : page * p.v_page_on;
         if constexpr (C::E4M3) {
           const uint32_t to = raws + st * C::RAW;
@@ -382,25 +383,25 @@ __device__ __forceinline__ void run_widen(const Params &p, Walk<C::KW> walk, con
   while (walk.next(x)) steps += x.steps;
   for (uint32_t n = 0; n < steps; ++n) {
     const uint32_t st = n % C::STAGES, slot = n % RING;
-    if (!mbar_wait(bar.raw_full(slot), (n / RING) & 1u, abort, kTimeoutNs) ||
-        (n >= C::STAGES && !mbar_wait(bar.empty(st), (n / C::STAGES - 1) & 1u, abort, kTimeoutNs))) {
+    bool ok = mbar_wait(bar.raw_full(slot), (n / RING) & 1u, abort, kTimeoutNs);
+    ok = ok && (n < C::STAGES || mbar_wait(bar.empty(st), (n / C::STAGES - 1) & 1u, abort, kTimeoutNs));
+    if (!ok) {
       give_up(p, abort, SPLASH_DEV_TIMEOUT_PRODUCER);
       return;
     }
     const uint32_t stage = stages + st * C::STAGE, raw = raws + slot * C::RAW;
+    // (all reads before the first write: a thread's chunks of a step wait for shared memory once)
+    constexpr int EK = KW * CK / 128, EV = KW * CV / 128;
+    uint4 y[EK + EV];
 #pragma unroll
-    for (int i = 0; i < KW * CK / 128; ++i) {
-      const int at = tid + 128 * i;
-      widen_chunk<C>(raw + at * 16, stage, at / CK, at % CK);
-    }
+    for (int i = 0; i < EK + EV; ++i) y[i] = load_shared4(raw + (tid + 128 * i) * 16);
+    mbar_arrive(bar.raw_empty(slot));
 #pragma unroll
-    for (int i = 0; i < KW * CV / 128; ++i) {
-      const int at = tid + 128 * i;
-      widen_chunk<C>(raw + KW * C::RK + at * 16, stage + C::K_BYTES, at / CV, at % CV);
-    }
+    for (int i = 0; i < EK; ++i) widen_chunk<C>(y[i], stage, (tid + 128 * i) / CK, (tid + 128 * i) % CK);
+#pragma unroll
+    for (int i = 0; i < EV; ++i) widen_chunk<C>(y[EK + i], stage + C::K_BYTES, (tid + 128 * i) / CV, (tid + 128 * i) % CV);
     fence_proxy_async_shared();
     mbar_arrive(bar.full(st));
-    mbar_arrive(bar.raw_empty(slot));
   }
 }
 
