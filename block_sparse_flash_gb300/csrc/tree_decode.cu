@@ -92,8 +92,8 @@ struct Config {
   static constexpr int RAWS = E4M3 ? std::min(6, (BUDGET - STAGES * STAGE) / std::max(RAW, 1)) : 0;
   static constexpr int TILES = NT * Q_BYTES + STAGES * STAGE + RAWS * RAW;
   static_assert(STAGES > LOOK && (!E4M3 || RAWS >= 2), "a step's stage is free before it is waited for");
-  // Barriers: full[STAGES] empty[STAGES], per group s_full[2] p_full[2] o_done q_full o_last, drain, raw_full[RAWS] raw_empty[RAWS]
-  static constexpr int BARS = 2 * STAGES + 15 + 2 * RAWS;
+  // Barriers: full[STAGES] empty[STAGES], per group s_full[2] p_full[2] q_full o_last, drain, raw_full[RAWS] raw_empty[RAWS]
+  static constexpr int BARS = 2 * STAGES + 13 + 2 * RAWS;
   static constexpr int SMEM = 1024 + TILES + BARS * 8;
   // Warps: softmax (8), for e4m3 four that widen, then loads and products.
   static constexpr int LOAD = E4M3 ? 12 : 8, MMA = LOAD + 1, WARPS = MMA + 1, THREADS = 32 * WARPS;
@@ -288,14 +288,13 @@ struct Bars {
   uint32_t base;
   __device__ __forceinline__ uint32_t full(int s) const { return base + 8u * s; }
   __device__ __forceinline__ uint32_t empty(int s) const { return base + 8u * (C::STAGES + s); }
-  __device__ __forceinline__ uint32_t s_full(int t, int x) const { return base + 8u * (2 * C::STAGES + 7 * t + x); }
-  __device__ __forceinline__ uint32_t p_full(int t, int x) const { return base + 8u * (2 * C::STAGES + 7 * t + 2 + x); }
-  __device__ __forceinline__ uint32_t o_done(int t) const { return base + 8u * (2 * C::STAGES + 7 * t + 4); }
-  __device__ __forceinline__ uint32_t q_full(int t) const { return base + 8u * (2 * C::STAGES + 7 * t + 5); }
-  __device__ __forceinline__ uint32_t o_last(int t) const { return base + 8u * (2 * C::STAGES + 7 * t + 6); }
-  __device__ __forceinline__ uint32_t drain() const { return base + 8u * (2 * C::STAGES + 14); }
-  __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8u * (2 * C::STAGES + 15 + s); }
-  __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8u * (2 * C::STAGES + 15 + C::RAWS + s); }
+  __device__ __forceinline__ uint32_t s_full(int t, int x) const { return base + 8u * (2 * C::STAGES + 6 * t + x); }
+  __device__ __forceinline__ uint32_t p_full(int t, int x) const { return base + 8u * (2 * C::STAGES + 6 * t + 2 + x); }
+  __device__ __forceinline__ uint32_t q_full(int t) const { return base + 8u * (2 * C::STAGES + 6 * t + 4); }
+  __device__ __forceinline__ uint32_t o_last(int t) const { return base + 8u * (2 * C::STAGES + 6 * t + 5); }
+  __device__ __forceinline__ uint32_t drain() const { return base + 8u * (2 * C::STAGES + 12); }
+  __device__ __forceinline__ uint32_t raw_full(int s) const { return base + 8u * (2 * C::STAGES + 13 + s); }
+  __device__ __forceinline__ uint32_t raw_empty(int s) const { return base + 8u * (2 * C::STAGES + 13 + C::RAWS + s); }
 };
 
 __device__ __forceinline__ void give_up(const Params &p, volatile int *abort, uint32_t bit) {
@@ -439,7 +438,6 @@ __device__ __forceinline__ void run_mma(const Params &p, Walk<C::KW> walk, const
       for (int kk = 0; kk < KW / 16; ++kk)
         mma_ts_lhp(leader, o, pa + KW / 2 + 8u * kk, vd + (uint32_t)((kk * 2048) >> 4), HI, C::IDESC_PV, 1);
     }
-    tc_commit_p(leader, bar.o_done(t));
     if (last) tc_commit_p(leader, bar.o_last(C::PAIR ? t : 0));
     return true;
   };
@@ -767,8 +765,10 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
           m = high;
           sum *= alpha;
           if (i >= (PAIR ? 1 : 2)) {
-            // (these scores came after the products of all steps but the one before)
-            if (!(ok = __all_sync(~0u, mbar_wait(bar.o_done(t), (cnt - 1) & 1u, abort, kTimeoutNs)))) break;
+            // (these scores came after the products of all the group's steps but the one before: its stage is free when
+            // that one is done)
+            const uint32_t u = step + i - (PAIR ? 1 : 2);
+            if (!(ok = __all_sync(~0u, mbar_wait(bar.empty(u % C::STAGES), (u / C::STAGES) & 1u, abort, kTimeoutNs)))) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < C::DV / 32; ++c) {
@@ -834,7 +834,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
     step += x.steps;
     more = advance();
     queries.ask(p, x, row0, more ? rows : 0);  // (always: nothing of the last ones stays in registers)
-    // (o_done may be two products behind here, which its parity would not tell from none)
+    // (a barrier of its own: one with a phase per step may be two behind here, which its parity would not tell)
     if (!(ok = __all_sync(~0u, mbar_wait(bar.o_last(PAIR ? t : 0), pieces++ & 1u, abort, kTimeoutNs)))) break;
     if (!PAIR) {
       s_ml[t][tid] = make_float2(m, sum);
@@ -887,7 +887,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid
         mbar_init(bar.s_full(t, x), 1);
         mbar_init(bar.p_full(t, x), 128);
       }
-      mbar_init(bar.o_done(t), 1);
       mbar_init(bar.o_last(t), 1);
       mbar_init(bar.q_full(t), C::PAIR ? 128 : 256);
     }
