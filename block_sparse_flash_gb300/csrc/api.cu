@@ -665,6 +665,7 @@ splash_status splash_paged_tree_decode_workspace_size(int32_t B, int32_t Hq, int
   if (bytes == nullptr) return SPLASH_ERR_INVALID_ARG;
   const splash_status st = check_decode_sizes(B, Hq, Hkv, T, SPLASH_MAX_TREE_TOKENS, dqk, dv, max_pages, page_size, cache_type, window_left);
   if (st != SPLASH_OK) return st;
+  if (splash_paged_tree_decode_entries(B, Hq, Hkv, T, max_pages, page_size, window_left) > INT32_MAX) return SPLASH_ERR_UNSUPPORTED;
   *bytes = splash_paged_tree_decode_workspace_bytes(B, Hq, Hkv, T, dqk, dv, max_pages, page_size, cache_type, window_left);
   return SPLASH_OK;
 }

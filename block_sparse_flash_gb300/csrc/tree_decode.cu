@@ -4,6 +4,34 @@
 // For a row (query head h, token l): s_j = scale q.k_j over the keys it sees --
 // the context and its ancestors --, out = sum exp(s_j - m) v_j / sum exp(s_j - m),
 // lse = m + ln sum exp(s_j - m), in one pass over the keys.
+//
+// A KV head has Hq/Hkv * T rows, up to hundreds, that share its keys: 2 rows FLOP per
+// byte of a bf16 cache, 4 of an e4m3 one.  Reading the cache bounds the call up to some
+// 256 rows, the products beyond, so that the rows are the 128 lanes of tensor memory
+// and the cache is read once for 256 of them.
+//
+//  * Work.  As in paged_decode: the steps of 64 keys of all (sequence, KV head, row
+//    group) segments form one list and every CTA, one per SM, takes an equal contiguous
+//    part; a segment's start counts as nine more steps.  Segments in whole are finished
+//    there, parts go to the workspace and a second kernel joins them in the order of the
+//    keys: the result does not depend on timing.
+//  * Warps.  One loads boxes of the pages (TMA), one issues the products
+//    (tcgen05.mma, S = Q K^T from shared memory, O += P V with P from tensor memory), two
+//    groups of four do the softmax, a thread per row; for e4m3 four widen the keys and
+//    values to fp16 on the way.  More than 128 rows: a group per tile of 128, both on the
+//    same keys.  Fewer: the groups take even and odd steps, so that two softmaxes are
+//    under way in either case.
+//  * Masks.  A row's keys are a range of the context and 64 bits for the tree, from its
+//    ancestors.  Only the steps at a window's start and at the tree are masked.
+//
+// Measured (device time, 32 query and 8 KV heads of 128 unless said; us, and what bounds
+// it): 32 requests of 32 .. 4096 tokens and 32 drafts, bf16, 84 (floor 44: a step of 64
+// keys arrives every 1700 cycles, 1390 at the copy rate, and a segment's start and end cost
+// 19000 of which the other SMs hide nothing); 16 requests of up to 32768 tokens and 64 drafts,
+// e4m3, 250 (floor 149, the products: shared memory, which the products' operands, the
+// widening and the loads fill to 80 %); 128 / 128 heads of 192 through a window of 1023,
+// 7 drafts, 130 (floor 75); 1 request of 300 tokens and 16 drafts 12.4 (two launches, eight
+// dependent reads, the join).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -26,7 +54,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 constexpr int kMaxCtas = 160;              // of the grid; the workspace holds two parts for each
 // A piece's start and end cost a CTA about as much as this many steps: a segment
-// counts for so many more when the list is cut into equal parts.
+// counts for so many more when the list is cut into equal parts.  (32 requests of 32 ..
+// 4096 tokens, 32 drafts: 113.6 us with 2, 94.2 with 6, 88.9 with 9, 87.7 with 12; 64 requests,
+// one draft: 148, 122, 121.6, 123.3.)
 constexpr int kPieceSteps = 9;
 constexpr uint64_t kTimeoutNs = 1000000000ull;  // of a wait
 
@@ -64,7 +94,7 @@ struct Params {
   int32_t B, Hkv, T, G, nrows, row_groups, part_rows;  // nrows = G * T rows per KV head
   int32_t max_pages, page_shift, window;               // window < 0: none
   uint32_t over_T;                                     // rounded up 2^32 / T: n / T for n T < 2^32
-  int32_t ctas, min_steps;                             // of the grid; least steps of a CTA's part
+  int32_t ctas;                                        // of the grid
   float scale, cap;                                    // cap <= 0: none
   bool out_wide;                                       // out is 32-byte aligned
   uint32_t *err;
@@ -128,13 +158,12 @@ __device__ __forceinline__ bool whole(const Params &p, const Span &s, int32_t ke
   return key0 + KW <= s.ctx && (p.window < 0 || key0 >= s.ctx + p.T - 1 - p.window);
 }
 
-// Equal contiguous parts of T entries, of at least p.min_steps each: CTA w takes
-// [begin(w), begin(w + 1)).  A segment has kPieceSteps entries for its start, then one
+// Equal contiguous parts of T entries: CTA w takes [begin(w), begin(w + 1)).  A segment has kPieceSteps entries for its start, then one
 // for each step.
 struct Parts {
   int32_t total, count, each, more;  // the first `more` take one entry more
   __device__ __forceinline__ Parts(const Params &p, int32_t T)
-      : total(T), count(max(1, min(p.ctas, T / p.min_steps))), each((uint32_t)T / (uint32_t)count), more(T - each * count) {}
+      : total(T), count(max(1, min(p.ctas, T))), each((uint32_t)T / (uint32_t)count), more(T - each * count) {}
   __device__ __forceinline__ int32_t begin(int32_t w) const { return w >= count ? total : each * w + min(w, more); }
   __device__ __forceinline__ int32_t owner(int32_t u) const {
     const int32_t cut = (each + 1) * more;
@@ -1150,7 +1179,6 @@ splash_status launch(const splash_paged_decode_args &a, Params p, cudaStream_t s
     ready[dev & 63].store(true, std::memory_order_release);
   }
   const int64_t most = most_steps(a.Lq, a.max_pages, a.page_size, a.window_left), segments = (int64_t)p.B * p.Hkv * p.row_groups;
-  p.min_steps = 1;
   p.ctas = (int)std::min<int64_t>({most * segments, (int64_t)sms, (int64_t)kMaxCtas});
   SPLASH_CUDA_TRY(launch_dependent(tree_decode_kernel<C>, dim3(p.ctas), dim3(C::THREADS), C::SMEM, 1, stream, map_k, map_v, p));
   splash_count_launches(1);
@@ -1169,6 +1197,12 @@ splash_status pick(const splash_paged_decode_args &a, const Params &p, cudaStrea
 
 }  // namespace
 }  // namespace splash
+
+int64_t splash_paged_tree_decode_entries(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t max_pages, int32_t page_size,
+                                         int64_t window) {
+  const int64_t rows = (int64_t)(Hq / Hkv) * T, tile = rows <= 128 ? 128 : 256;
+  return (splash::most_steps(T, max_pages, page_size, window) + splash::kPieceSteps) * B * Hkv * ((rows + tile - 1) / tile);
+}
 
 size_t splash_paged_tree_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t, int32_t dv, int32_t, int32_t,
                                                 int32_t, int64_t) {

@@ -617,8 +617,8 @@ splash_status splash_paged_decode_workspace_size(int32_t B, int32_t Hq, int32_t 
  *               [num_axes][B][L], axis a at positions_stride_a * a
  *   axes        host, rot_dim / 2 entries below num_axes
  *   num_axes    1 .. SPLASH_MAX_AXES
- * Errors as for splash_rope (axes out of range: INVALID_ARG; more of them:
- * UNSUPPORTED).
+ * Errors as for splash_rope (an axis >= num_axes among axes: INVALID_ARG; more than
+ * SPLASH_MAX_AXES: UNSUPPORTED).
  */
 typedef struct {
     uint64_t struct_bytes;
@@ -679,8 +679,13 @@ splash_status splash_paged_append_axes(const splash_paged_append_axes_args *args
  *               SPLASH_MAX_TREE_TOKENS; the workspace is that of
  *               splash_paged_tree_decode_workspace_size
  *   parents     device int32 [B][T], row stride parents_stride_b (0: one tree)
- * Supported sizes as for splash_paged_decode but for Lq.  The cache is read once
- * for every 256 of the Hq/Hkv * T rows.  The result does not depend on timing.
+ * Supported sizes as for splash_paged_decode but for Lq, and for the number of
+ * steps: those of 64 keys (at most max_pages * page_size / 64 + 1, or (window_left +
+ * T) / 64 + 3) and nine more, over all sequences, KV heads and groups of 256 rows (of
+ * 128, up to 128 rows), are to be fewer than 2^31.  The caches' strides are below 2^40
+ * bytes, and a page's tokens do not share a row (stride_token > 0).  The cache is read
+ * once for every 256 of the Hq/Hkv * T rows.  The result does not depend on timing:
+ * the same inputs give the same bits on the same GPU.
  *
  * Precision as splash_paged_decode: for a bf16 cache each probability is taken
  * to 2^-16 of it, for an e4m3 one to 2^-11.

@@ -161,6 +161,13 @@ def test_tree_refusals(splash):
     assert status(splash, "splash_paged_tree_decode", a) == CUDA
     a = tree_args(17)  # more than a chain may have
     assert status(splash, "splash_paged_tree_decode", a) == CUDA
+    # 2^31 steps and starts of segments: 65535 sequences x 4096 heads x (1 + 9)
+    a = tree_args(1)
+    a.decode.B, a.decode.Hq, a.decode.Hkv, a.decode.max_pages = 65535, 4096, 4096, 1
+    assert status(splash, "splash_paged_tree_decode", a) == UNSUPPORTED
+    a.decode.Hq = a.decode.Hkv = 3000
+    a.decode.q, a.decode.k_cache, a.decode.v_cache = dense(3000, 1, 128), dense(3000, 16, 128), dense(3000, 16, 128)
+    assert status(splash, "splash_paged_tree_decode", a) == CUDA
 
 
 @no_device
