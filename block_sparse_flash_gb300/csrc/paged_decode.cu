@@ -48,6 +48,7 @@
 #include <atomic>
 #include <cmath>
 
+#include "cluster.cuh"
 #include "dependent_launch.cuh"
 #include "internal.h"
 #include "sm103_ptx.cuh"
@@ -367,41 +368,6 @@ __device__ __forceinline__ void add_part(float4 &acc, float &sum, float high, fl
   acc.y += f * x.y;
   acc.z += f * x.z;
   acc.w += f * x.w;
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t n;
-  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
-  return n;
-}
-// Every thread of every CTA of the cluster arrives and waits.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-// The same shared memory address in another CTA of the cluster.
-__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
-  float4 x;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-               : "r"(addr)
-               : "memory");
-  return x;
-}
-__device__ __forceinline__ float2 load_cluster2(uint32_t addr) {
-  float2 x;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(addr) : "memory");
-  return x;
 }
 
 // The pairs of keys of a step that a query sees (2 tq, 2 tq + 1 and the same + 8

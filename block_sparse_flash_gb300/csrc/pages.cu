@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <climits>
 
+#include "cluster.cuh"
 #include "dependent_launch.cuh"
 #include "internal.h"
 
@@ -198,13 +199,6 @@ struct RemapParams {
   uint32_t *err;
 };
 
-// Every thread of every CTA of the cluster arrives and waits; what they wrote before is
-// visible after it (global memory too: the barrier releases and acquires).
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-
 // Sum over the CTA's threads before this one, and *all of them.
 __device__ __forceinline__ int32_t scan(int32_t x, int32_t *s_warp, int32_t *all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -297,7 +291,7 @@ __global__ void __launch_bounds__(kMapThreads) remap_kernel(const RemapParams p)
   int32_t all_free;
   scan(free_pages, s_warp, &all_free);
   if (tid == 0) p.totals[cta] = all_free;
-  cluster_barrier();
+  cluster_sync();
 
   // ---- uses: a warp per 32 columns of a row of either table
   const uint32_t chunks = (uint32_t)(p.max_pages + 31) / 32, all_warps = kMapCtas * kMapWarps, gw = cta * kMapWarps + warp;
@@ -347,7 +341,7 @@ __global__ void __launch_bounds__(kMapThreads) remap_kernel(const RemapParams p)
       if (n[k] == 0) p.fresh[rank++] = (int32_t)(mine + k);
     free_before += all;
   }
-  cluster_barrier();
+  cluster_sync();
 
   // ---- the fresh pages that each row needs, and those before it: every CTA for all rows, or where
   // there are many, its share of them, joined by another barrier
@@ -368,7 +362,7 @@ __global__ void __launch_bounds__(kMapThreads) remap_kernel(const RemapParams p)
     __syncthreads();
   } else {
     if (tid == 0) p.totals[kMapCtas + cta] = needed;
-    cluster_barrier();
+    cluster_sync();
     for (int k = 0; k < kMapCtas; ++k) all_needed += __ldcg(p.totals + kMapCtas + k);
   }
   const int64_t given = min(all_needed, total_free);

@@ -1,5 +1,6 @@
 // tree_decode.cu -- attention of a tree of drafted tokens over a paged cache
-// (splash_paged_tree_decode in splash.h).
+// (splash_paged_tree_decode in splash.h).  Compiled once for each cache type
+// (SPLASH_TREE_E4M3 = 0, 1), so that the instantiations build in parallel.
 //
 // For a row (query head h, token l): s_j = scale q.k_j over the keys it sees --
 // the context and its ancestors --, out = sum exp(s_j - m) v_j / sum exp(s_j - m),
@@ -14,7 +15,9 @@
 //    group) segments form one list and every CTA, one per SM, takes an equal contiguous
 //    part; a segment's start counts as nine more steps.  Segments in whole are finished
 //    there, parts go to the workspace and a second kernel joins them in the order of the
-//    keys: the result does not depend on timing.
+//    keys: the result does not depend on timing.  Where there are few segments and none can
+//    be very long, each takes a cluster of CTAs, whose parts are joined through distributed
+//    shared memory: no scan, no workspace, no second kernel.
 //  * Warps.  One loads boxes of the pages (TMA), one issues the products
 //    (tcgen05.mma, S = Q K^T from shared memory, O += P V with P from tensor memory), two
 //    groups of four do the softmax, a thread per row; for e4m3 four widen the keys and
@@ -30,8 +33,8 @@
 // 19000 of which the other SMs hide nothing); 16 requests of up to 32768 tokens and 64 drafts,
 // e4m3, 250 (floor 149, the products: shared memory, which the products' operands, the
 // widening and the loads fill to 80 %); 128 / 128 heads of 192 through a window of 1023,
-// 7 drafts, 130 (floor 75); 1 request of 300 tokens and 16 drafts 12.4 (two launches, eight
-// dependent reads, the join).
+// 7 drafts, 130 (floor 75); 1 request of 300 tokens and 16 drafts 10.0 (the launch, eight
+// dependent reads, the first fetch of the code).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -43,6 +46,7 @@
 #include <cmath>
 #include <mutex>
 
+#include "cluster.cuh"
 #include "dependent_launch.cuh"
 #include "internal.h"
 #include "sm103_ptx.cuh"
@@ -258,7 +262,7 @@ __device__ __forceinline__ void load_box(uint32_t leader, uint32_t dst, const CU
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 // Four e4m3 values to two pairs of fp16 (exact).
-__device__ __forceinline__ void widen(uint32_t x, uint32_t &lo, uint32_t &hi) {
+[[maybe_unused]] __device__ __forceinline__ void widen(uint32_t x, uint32_t &lo, uint32_t &hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(x));
@@ -609,8 +613,10 @@ struct Done {
 
 // Writes a finished piece: rows of the result, or this CTA's part of them.  A lane has a
 // row, so that a store touches 32 lines however little it writes to each: 32 bytes a lane.
-template <class C>
-__device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint32_t o_0, int t, bool real) {
+// In a cluster parts go to shared memory, at `rows`, each followed by 16 bytes that keep
+// neighbours on different banks.
+template <class C, bool TOGETHER>
+__device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint32_t o_0, int t, bool real, uint32_t rows, float2 *s_part) {
   constexpr bool PAIR = C::PAIR;
   const bool empty = d.sum == 0.f || d.empty;
   const float inv = __fdividef(d.scale, d.sum);
@@ -632,7 +638,14 @@ __device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint3
 #pragma unroll
       for (int j = 0; j < 32; ++j) o[j] += d.f1 * __uint_as_float(y[j]);
     }
-    if (real && d.complete) {
+    if (TOGETHER) {
+      const uint32_t dst = rows + ((uint32_t)d.row * (C::DV + 4) + c) * 4;
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        if (real)
+          st_shared_v4(dst + 4 * j, empty ? 0u : __float_as_uint(o[j]), empty ? 0u : __float_as_uint(o[j + 1]),
+                       empty ? 0u : __float_as_uint(o[j + 2]), empty ? 0u : __float_as_uint(o[j + 3]));
+    } else if (real && d.complete) {
       uint32_t w[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) w[j] = empty ? 0u : pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
@@ -655,7 +668,9 @@ __device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint3
     __syncwarp();
   }
   if (real && (PAIR || t == 0)) {
-    if (d.complete)
+    if (TOGETHER)
+      s_part[d.row] = empty ? make_float2(-INFINITY, 0.f) : make_float2(d.m, d.sum);
+    else if (d.complete)
       p.lse[d.row] = empty ? -INFINITY : (d.m + log2f(d.sum)) * kLn2;
     else
       *reinterpret_cast<float2 *>(p.part_ml + 2 * d.row) = empty ? make_float2(-INFINITY, 0.f) : make_float2(d.m, d.sum);
@@ -666,9 +681,9 @@ __device__ __forceinline__ void write_rows(const Params &p, const Done &d, uint3
 // every other step.  From piece to piece: the next queries are read while the last
 // products run, go to shared memory as soon as those are done, and the finished rows
 // are written while the next piece's first scores are computed.
-template <class C>
+template <class C, bool TOGETHER>
 __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, const Bars<C> bar, uint32_t tmem, uint32_t q_addr,
-                                            uint32_t stages, int32_t *s_parents, float *s_factor, float2 (*s_ml)[128], int t,
+                                            uint32_t stages, int32_t *s_parents, float *s_factor, float2 (*s_ml)[128], float2 *s_part, int t,
                                             volatile int *abort, volatile int *lost) {
   constexpr int KW = C::KW;
   constexpr bool E4M3 = C::E4M3, PAIR = C::PAIR;
@@ -703,7 +718,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
     }
     if (some) {
       tc_fence_after();
-      if (32 * warp < done_rows) write_rows<C>(p, d, o_0, t, tid < done_rows);
+      if (32 * warp < done_rows) write_rows<C, TOGETHER>(p, d, o_0, t, tid < done_rows, q_addr, s_part);
       tc_fence_before();
       some = false;
     }
@@ -848,7 +863,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
     }
     if (!ok) break;
 
-    const int head = x.seg / p.row_groups, slot = x.slot(blockIdx.x);
+    const int head = x.seg / p.row_groups, slot = TOGETHER ? 0 : x.slot(blockIdx.x);
     d.complete = slot < 0;
     d.row = slot < 0 ? ((int64_t)x.b * p.Hkv + head) * p.nrows + row0 + tid : (int64_t)slot * p.part_rows + (PAIR ? t * 128 : 0) + tid;
     d.scale = E4M3 ? p.v_scale[head] : 1.f;
@@ -865,6 +880,9 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
     queries.ask(p, x, row0, more ? rows : 0);  // (always: nothing of the last ones stays in registers)
     // (a barrier of its own: one with a phase per step may be two behind here, which its parity would not tell)
     if (!(ok = __all_sync(~0u, mbar_wait(bar.o_last(PAIR ? t : 0), pieces++ & 1u, abort, kTimeoutNs)))) break;
+    if (TOGETHER && PAIR && p.nrows - (row0 - t * 128) > 128) {  // (the rows go where the other tile's operands are)
+      if (!(ok = __all_sync(~0u, mbar_wait(bar.o_last(t ^ 1), 0u, abort, kTimeoutNs)))) break;
+    }
     if (!PAIR) {
       s_ml[t][tid] = make_float2(m, sum);
       bar_sync(bar_id, bar_threads);
@@ -885,13 +903,50 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
   if (!ok && (threadIdx.x & 31) == 0) give_up(p, abort, SPLASH_DEV_TIMEOUT_SOFTMAX);
 }
 
-template <class C>
+// Adds to a row's columns the values that are not finite of the keys that it sees in the
+// segment's steps that are not whole (the products had zeros in their place): a value
+// that is infinite or NaN is the result's, whatever else is in it.  A warp; returns
+// whether there were any.
+template <int DV, bool E4M3>
+__device__ __noinline__ bool add_lost(const Params &p, const Span &s, int b, int head, int row, float (&acc)[DV / 32]) {
+  constexpr int KW = 64, PER = DV / 32;
+  bool bad = false, found = false;
+  const Branch me = branch_of(p.parents + b * p.parents_stride, row % p.T, max(0, -s.ctx), p.window, &bad);
+  const int32_t lo = p.window < 0 ? 0 : max(0, s.ctx + me.depth - p.window);
+  for (int i = 0; i < s.nst; ++i) {
+    const int32_t key0 = (s.step0 + i) * KW;
+    if (whole<KW>(p, s, key0)) continue;
+    for (uint64_t m = visible(key0, s.ctx, lo, me.seen); m != 0; m &= m - 1) {
+      const int32_t key = key0 + __ffsll((long long)m) - 1;
+      const int32_t page = p.block_table[b * p.block_table_stride + (key >> p.page_shift)];
+      if (page < 0 || page >= p.num_pages) continue;
+      const char *v = p.v + page * p.v_page + head * p.v_head + (key & ((1 << p.page_shift) - 1)) * p.v_token;
+#pragma unroll
+      for (int c = 0; c < PER; ++c) {
+        const int col = (threadIdx.x & 31) * PER + c;
+        const float y = E4M3 ? (float)reinterpret_cast<const __nv_fp8_e4m3 *>(v)[col]
+                             : __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(v)[col]);
+        if (!(fabsf(y) < INFINITY)) acc[c] += y, found = true;
+      }
+    }
+  }
+  return __any_sync(~0u, found);
+}
+
+// Where CTA `rank` of a cluster (of a power of two) begins in n steps.
+__device__ __forceinline__ int32_t share(int32_t n, uint32_t rank, uint32_t ctas) {
+  return (int32_t)((int64_t)n * rank >> (31 - __clz((int)ctas)));
+}
+
+// TOGETHER: a cluster of CTAs per segment, which share its steps; otherwise equal parts of the list.
+template <class C, bool TOGETHER>
 __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                                                                   const __grid_constant__ CUtensorMap map_v, const Params p) {
   constexpr int KW = C::KW;
   extern __shared__ char smem_raw[];
   __shared__ int32_t s_scan[C::WARPS], s_seq, s_before, s_parents[C::NT][SPLASH_MAX_TREE_TOKENS];
   __shared__ float2 s_ml[2][128];  // (maximum, sum) of the groups' rows
+  __shared__ float2 s_part[TOGETHER ? C::TILE : 1];  // of this CTA's part of them
   __shared__ float s_factor[C::NT][128];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_lost;
@@ -931,59 +986,78 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid
   // hold what this one still needs)
   grid_dependency();
 
-  // ---- this CTA's part of the list: a scan over the sequences
   const int per_seq = p.Hkv * p.row_groups;
-  const int per = (p.B + C::THREADS - 1) / C::THREADS;
-  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  int32_t own = 0;
-  for (int b = b0; b < b1; ++b) own += span_of<KW>(p, p.seq_lens[b]).nst + kPieceSteps;
-  int32_t before = own;
+  Walk<KW> walk{p, 0, 0, per_seq, 0, 0, 0, 0};
+  if constexpr (TOGETHER) {
+    const uint32_t ctas = cluster_size(), rank = cluster_rank(), segment = blockIdx.x / ctas;
+    walk.b = segment / per_seq;
+    walk.seg = segment % per_seq;
+    walk.length = p.seq_lens[walk.b];
+    const Span s = span_of<KW>(p, walk.length);
+    walk.u = walk.entry = kPieceSteps + share(s.nst, rank, ctas);
+    walk.end = kPieceSteps + share(s.nst, rank + 1, ctas);
+    if (walk.seg == 0 && rank == 0 && tid == 0 && s.n != walk.length) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  } else {
+    // ---- this CTA's part of the list: a scan over the sequences
+    const int per = (p.B + C::THREADS - 1) / C::THREADS;
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    int32_t own = 0;
+    for (int b = b0; b < b1; ++b) own += span_of<KW>(p, p.seq_lens[b]).nst + kPieceSteps;
+    int32_t before = own;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int32_t y = __shfl_up_sync(~0u, before, o);
-    if (lane >= o) before += y;
-  }
-  if (lane == 31) s_scan[warp] = before;
-  before -= own;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  int32_t total = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(~0u, before, o);
+      if (lane >= o) before += y;
+    }
+    if (lane == 31) s_scan[warp] = before;
+    before -= own;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int32_t total = 0;
 #pragma unroll
-  for (int w = 0; w < C::WARPS; ++w) {
-    if (w < warp) before += s_scan[w];
-    total += s_scan[w];
-  }
-  const Parts parts(p, total * per_seq);
-  const int32_t begin = parts.begin(blockIdx.x), end = parts.begin(blockIdx.x + 1);
-  if (blockIdx.x == 0 || (begin >= before * per_seq && begin < (before + own) * per_seq)) {
-    int32_t at = before;
-    for (int b = b0; b < b1; ++b) {
-      const Span s = span_of<KW>(p, p.seq_lens[b]);
-      const int32_t entries = s.nst + kPieceSteps;
-      if (begin >= at * per_seq && begin < (at + entries) * per_seq) s_seq = b, s_before = at;
-      if (blockIdx.x == 0) {
-        p.before[b] = at;
-        if (b == p.B - 1) p.before[p.B] = at + entries;
-        if (s.n != p.seq_lens[b]) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
+    for (int w = 0; w < C::WARPS; ++w) {
+      if (w < warp) before += s_scan[w];
+      total += s_scan[w];
+    }
+    const Parts parts(p, total * per_seq);
+    const int32_t begin = parts.begin(blockIdx.x);
+    walk.end = parts.begin(blockIdx.x + 1);
+    if (blockIdx.x == 0 || (begin >= before * per_seq && begin < (before + own) * per_seq)) {
+      int32_t at = before;
+      for (int b = b0; b < b1; ++b) {
+        const Span s = span_of<KW>(p, p.seq_lens[b]);
+        const int32_t entries = s.nst + kPieceSteps;
+        if (begin >= at * per_seq && begin < (at + entries) * per_seq) s_seq = b, s_before = at;
+        if (blockIdx.x == 0) {
+          p.before[b] = at;
+          if (b == p.B - 1) p.before[p.B] = at + entries;
+          if (s.n != p.seq_lens[b]) atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
+        }
+        at += entries;
       }
-      at += entries;
+    }
+    __syncthreads();
+    walk.u = begin;
+    if (begin < walk.end) {
+      walk.b = s_seq;
+      walk.length = p.seq_lens[walk.b];
+      const int32_t entries = span_of<KW>(p, walk.length).nst + kPieceSteps, in_seq = begin - s_before * per_seq;
+      walk.seg = (uint32_t)in_seq / (uint32_t)entries;
+      walk.entry = in_seq - walk.seg * entries;
     }
   }
-  __syncthreads();
-  if (begin < end) {
-    Walk<KW> walk{p, begin, end, per_seq, s_seq, 0, 0, 0};
-    walk.length = p.seq_lens[walk.b];
-    const int32_t nst = span_of<KW>(p, walk.length).nst;
-    const int32_t in_seq = begin - s_before * per_seq;
-    walk.seg = (uint32_t)in_seq / (uint32_t)(nst + kPieceSteps);
-    walk.entry = in_seq - walk.seg * (nst + kPieceSteps);
+  const int32_t mine_b = walk.b, mine_seg = walk.seg;
+  if (walk.u < walk.end) {
     const uint32_t q_addr = tiles, stages = tiles + C::NT * C::Q_BYTES, raws = stages + C::STAGES * C::STAGE;
     // (registers for e4m3: 14 warps are launched with 128 a thread; 8 take 152 and 4 leave 48 each)
     if (warp < 8) {
       if constexpr (C::E4M3) regs_increase<152>();
       const int t = warp >> 2, tile = C::PAIR ? t : 0;
-      run_softmax<C>(p, walk, bar, s_tmem, q_addr, stages, s_parents[tile], s_factor[tile], s_ml, t, &s_abort, &s_lost);
+      run_softmax<C, TOGETHER>(p, walk, bar, s_tmem, q_addr, stages, s_parents[tile], s_factor[tile], s_ml, s_part, t, &s_abort, &s_lost);
     } else if (warp == C::MMA) {
       run_mma<C>(p, walk, bar, s_tmem, q_addr, stages, &s_abort);
     } else if (warp == C::LOAD) {
@@ -995,41 +1069,60 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid
   }
   tc_fence_before();
   __syncthreads();
-  if (tid == 0) p.lost[blockIdx.x] = s_lost;
+  if (!TOGETHER && tid == 0) p.lost[blockIdx.x] = s_lost;
   if (warp == C::MMA) {
     tc_fence_after();
     tmem_dealloc(s_tmem, C::COLS);
   }
-}
-
-// Adds to a row's columns the values that are not finite of the keys that it sees in the
-// segment's steps that are not whole (the products had zeros in their place): a value
-// that is infinite or NaN is the result's, whatever else is in it.  A warp; returns
-// whether there were any.
-template <int DV, bool E4M3>
-__device__ __noinline__ bool add_lost(const Params &p, const Span &s, int b, int head, int row, float (&acc)[DV / 32]) {
-  constexpr int KW = 64, PER = DV / 32;
-  bool bad = false, found = false;
-  const Branch me = branch_of(p.parents + b * p.parents_stride, row % p.T, max(0, -s.ctx), p.window, &bad);
-  const int32_t lo = p.window < 0 ? 0 : max(0, s.ctx + me.depth - p.window);
-  for (int i = 0; i < s.nst; ++i) {
-    const int32_t key0 = (s.step0 + i) * KW;
-    if (whole<KW>(p, s, key0)) continue;
-    for (uint64_t m = visible(key0, s.ctx, lo, me.seen); m != 0; m &= m - 1) {
-      const int32_t key = key0 + __ffsll((long long)m) - 1;
-      const int32_t page = p.block_table[b * p.block_table_stride + (key >> p.page_shift)];
-      if (page < 0 || page >= p.num_pages) continue;
-      const char *v = p.v + page * p.v_page + head * p.v_head + (key & ((1 << p.page_shift) - 1)) * p.v_token;
+  if constexpr (TOGETHER) {
+    // ---- the segment's rows: every CTA finishes some of them, a warp a row
+    constexpr int PER = C::DV / 32;
+    const uint32_t ctas = cluster_size(), rank = cluster_rank();
+    cluster_sync();
+    const Span s = span_of<KW>(p, p.seq_lens[mine_b]);
+    const int head = mine_seg / p.row_groups, tile0 = (mine_seg % p.row_groups) * C::TILE, rows = min(C::TILE, p.nrows - tile0);
+    const float v_scale = C::E4M3 ? p.v_scale[head] : 1.f;
+    auto has = [&](uint32_t k) { return share(s.nst, k, ctas) < share(s.nst, k + 1, ctas); };
+    const bool lost = __any_sync(~0u, lane < ctas && load_cluster(in_cta(smem_u32(&s_lost), lane)) != 0);
+    const int r1 = (int)(rows * (rank + 1) / ctas);
+    for (int r = (int)(rows * rank / ctas) + warp; r < r1; r += C::WARPS) {
+      const uint32_t ml = smem_u32(&s_part[r]), from = tiles + (r * (C::DV + 4) + lane * PER) * 4;
+      const float2 mine = lane < ctas && has(lane) ? load_cluster2(in_cta(ml, lane)) : make_float2(-INFINITY, 0.f);
+      float top = mine.x;
 #pragma unroll
-      for (int c = 0; c < PER; ++c) {
-        const int col = (threadIdx.x & 31) * PER + c;
-        const float y = E4M3 ? (float)reinterpret_cast<const __nv_fp8_e4m3 *>(v)[col]
-                             : __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(v)[col]);
-        if (!(fabsf(y) < INFINITY)) acc[c] += y, found = true;
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+      const float f = factor_of(mine.x - (top == -INFINITY ? 0.f : top));
+      float sum = f * mine.y, acc[PER];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+#pragma unroll 4
+      for (uint32_t k = 0; k < ctas; ++k) {
+        const float g = __shfl_sync(~0u, f, k);
+        if (!has(k)) continue;
+        if constexpr (PER == 4) {
+          const float4 x = load_cluster4(in_cta(from, k));
+          acc[0] += g * x.x, acc[1] += g * x.y, acc[2] += g * x.z, acc[3] += g * x.w;
+        } else {
+          const float2 x = load_cluster2(in_cta(from, k));
+          acc[0] += g * x.x, acc[1] += g * x.y;
+        }
       }
+      const float inv = sum == 0.f ? 0.f : v_scale / sum;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] *= inv;
+      if (lost) add_lost<C::DV, C::E4M3>(p, s, mine_b, head, tile0 + r, acc);
+      const int64_t row = ((int64_t)mine_b * p.Hkv + head) * p.nrows + tile0 + r;
+      uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + row * C::DV) + lane * (PER / 2);
+      if constexpr (PER == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+      else
+        *dst = pack_bf16x2(acc[0], acc[1]);
+      if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
+    cluster_sync();  // (no CTA ends while another reads its shared memory)
   }
-  return __any_sync(~0u, found);
 }
 
 // Joins the parts of a segment that several CTAs computed: with (m_c, l_c, o_c) of part c
@@ -1153,6 +1246,51 @@ splash_status make_map(CUtensorMap *map, const splash_cache_view &v, int64_t pag
   return r == CUDA_SUCCESS ? SPLASH_OK : SPLASH_ERR_CUDA;
 }
 
+// Sets the kernels up on first use and picks the CTAs per segment (0: the list): the
+// largest cluster of which one for every segment runs at the same time, where its share of
+// the longest possible sequence is at most what the list would take for sequences four fifths
+// as long, and three steps for the second kernel.  (32 / 8 heads of 128, list -> clusters:
+// 1 request of 300 keys and 16 drafts 12.4 -> 10.0 us, 64 drafts 16.2 -> 15.3; 8 requests of
+// up to 2048 keys 23.5 -> 22.7; but 1 request of 16384 keys 28.1 -> 33.3, as clusters of 16
+// have room for 7 segments and those of 8 leave half of the SMs idle.)
+template <class C>
+splash_status cluster_for(int dev, int sms, int64_t segments, int64_t most, int *cluster) {
+  static std::atomic<uint64_t> room[64];  // per device: 12 bits each for clusters of 1, 2, 4, 8, 16 CTAs; 0: not asked yet
+  uint64_t fits = room[dev & 63].load(std::memory_order_acquire);
+  if (fits == 0) {
+    SPLASH_CUDA_TRY(cudaFuncSetAttribute(tree_decode_kernel<C, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+    SPLASH_CUDA_TRY(cudaFuncSetAttribute(tree_decode_kernel<C, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+    SPLASH_CUDA_TRY(cudaFuncSetAttribute(tree_decode_kernel<C, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    fits = (uint64_t)1 << 60;
+    for (int i = 0; i < 5; ++i) {
+      cudaLaunchConfig_t config = {};
+      config.gridDim = dim3(1u << i);
+      config.blockDim = dim3(C::THREADS);
+      config.dynamicSmemBytes = C::SMEM;
+      cudaLaunchAttribute attr = {};
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = 1u << i;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      config.attrs = &attr;
+      config.numAttrs = 1;
+      int clusters = 0;
+      if (cudaOccupancyMaxActiveClusters(&clusters, tree_decode_kernel<C, true>, &config) != cudaSuccess) {
+        (void)cudaGetLastError();  // (a size that the device does not place)
+        clusters = 0;
+      }
+      fits |= (uint64_t)std::min(clusters, 4095) << (12 * i);
+    }
+    room[dev & 63].store(fits, std::memory_order_release);
+  }
+  *cluster = 0;
+  for (int i = 4; i >= 0; --i) {
+    if ((int64_t)(fits >> (12 * i) & 4095u) < segments || ((int64_t)1 << i) >= 2 * most) continue;
+    if ((((most + ((int64_t)1 << i) - 1) >> i) - 3) * 5 * sms <= (most + kPieceSteps) * segments * 4) *cluster = 1 << i;
+    break;
+  }
+  return SPLASH_OK;
+}
+
 template <class C>
 splash_status launch(const splash_paged_decode_args &a, Params p, cudaStream_t stream) {
   CUtensorMap map_k, map_v;
@@ -1170,17 +1308,19 @@ splash_status launch(const splash_paged_decode_args &a, Params p, cudaStream_t s
   p.part_ml = reinterpret_cast<float *>(ws);
   ws += (int64_t)2 * kMaxCtas * p.part_rows * 2 * 4;
   p.part_o = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + 31) & ~(uintptr_t)31);
-  int dev = 0, sms = 0;
+  const int64_t most = most_steps(a.Lq, a.max_pages, a.page_size, a.window_left), segments = (int64_t)p.B * p.Hkv * p.row_groups;
+  int dev = 0, sms = 0, cluster = 0;
   SPLASH_CUDA_TRY(cudaGetDevice(&dev));
   SPLASH_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  static std::atomic<bool> ready[64];  // per device: the kernel may use its shared memory
-  if (!ready[dev & 63].load(std::memory_order_acquire)) {
-    SPLASH_CUDA_TRY(cudaFuncSetAttribute(tree_decode_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
-    ready[dev & 63].store(true, std::memory_order_release);
+  if ((st = cluster_for<C>(dev, sms, segments, most, &cluster)) != SPLASH_OK) return st;
+  if (cluster > 0) {
+    SPLASH_CUDA_TRY(launch_dependent(tree_decode_kernel<C, true>, dim3((unsigned)(segments * cluster)), dim3(C::THREADS), C::SMEM, cluster,
+                                     stream, map_k, map_v, p));
+    splash_count_launches(1);
+    return SPLASH_OK;
   }
-  const int64_t most = most_steps(a.Lq, a.max_pages, a.page_size, a.window_left), segments = (int64_t)p.B * p.Hkv * p.row_groups;
   p.ctas = (int)std::min<int64_t>({most * segments, (int64_t)sms, (int64_t)kMaxCtas});
-  SPLASH_CUDA_TRY(launch_dependent(tree_decode_kernel<C>, dim3(p.ctas), dim3(C::THREADS), C::SMEM, 1, stream, map_k, map_v, p));
+  SPLASH_CUDA_TRY(launch_dependent(tree_decode_kernel<C, false>, dim3(p.ctas), dim3(C::THREADS), C::SMEM, 1, stream, map_k, map_v, p));
   splash_count_launches(1);
   // a row per warp, or four where that still fills the GPU
   const int each = segments * p.part_rows >= 32 * 1024 ? 4 * kJoinWarps : kJoinWarps, slices = (p.part_rows + each - 1) / each;
@@ -1190,14 +1330,16 @@ splash_status launch(const splash_paged_decode_args &a, Params p, cudaStream_t s
   return SPLASH_OK;
 }
 
-template <int DQK, int DV, bool E4M3>
+template <int DQK, int DV>
 splash_status pick(const splash_paged_decode_args &a, const Params &p, cudaStream_t stream) {
+  constexpr bool E4M3 = SPLASH_TREE_E4M3 != 0;
   return p.nrows <= 128 ? launch<Config<DQK, DV, E4M3, false>>(a, p, stream) : launch<Config<DQK, DV, E4M3, true>>(a, p, stream);
 }
 
 }  // namespace
 }  // namespace splash
 
+#if !SPLASH_TREE_E4M3
 int64_t splash_paged_tree_decode_entries(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t max_pages, int32_t page_size,
                                          int64_t window) {
   const int64_t rows = (int64_t)(Hq / Hkv) * T, tile = rows <= 128 ? 128 : 256;
@@ -1211,6 +1353,16 @@ size_t splash_paged_tree_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t H
 }
 
 splash_status splash_paged_tree_decode_launch(const splash_paged_tree_decode_args &args, cudaStream_t stream, uint32_t *err_word) {
+  return args.decode.cache_type == SPLASH_CACHE_E4M3 ? splash_paged_tree_decode_launch_e4m3(args, stream, err_word)
+                                                     : splash_paged_tree_decode_launch_bf16(args, stream, err_word);
+}
+#endif
+
+#if SPLASH_TREE_E4M3
+splash_status splash_paged_tree_decode_launch_e4m3(const splash_paged_tree_decode_args &args, cudaStream_t stream, uint32_t *err_word) {
+#else
+splash_status splash_paged_tree_decode_launch_bf16(const splash_paged_tree_decode_args &args, cudaStream_t stream, uint32_t *err_word) {
+#endif
   using namespace splash;
   const splash_paged_decode_args &a = args.decode;
   const int64_t size = a.cache_type == SPLASH_CACHE_E4M3 ? 1 : 2;
@@ -1249,7 +1401,7 @@ splash_status splash_paged_tree_decode_launch(const splash_paged_tree_decode_arg
   // score below 2^88 as it is)
   p.cap = a.softcap < 0x1p100f ? a.softcap : 0.f;
   p.err = err_word;
-  const auto f = size == 1 ? (a.dqk == 64 ? pick<64, 64, true> : a.dqk == 128 ? pick<128, 128, true> : pick<192, 128, true>)
-                           : (a.dqk == 64 ? pick<64, 64, false> : a.dqk == 128 ? pick<128, 128, false> : pick<192, 128, false>);
-  return f(a, p, stream);
+  if (a.dqk == 64) return pick<64, 64>(a, p, stream);
+  if (a.dqk == 128) return pick<128, 128>(a, p, stream);
+  return pick<192, 128>(a, p, stream);
 }
