@@ -43,6 +43,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 
@@ -126,6 +127,7 @@ struct Config {
   static constexpr int RAWS = E4M3 ? std::min(6, (BUDGET - STAGES * STAGE) / std::max(RAW, 1)) : 0;
   static constexpr int TILES = NT * Q_BYTES + STAGES * STAGE + RAWS * RAW;
   static_assert(STAGES > LOOK && (!E4M3 || RAWS >= 2), "a step's stage is free before it is waited for");
+  static_assert(TILE * (DV + 4) * 4 <= TILES, "a cluster's parts fit where the operands were");
   // Barriers: full[STAGES] empty[STAGES], per group s_full[2] p_full[2] q_full o_last, drain, raw_full[RAWS] raw_empty[RAWS]
   static constexpr int BARS = 2 * STAGES + 13 + 2 * RAWS;
   static constexpr int SMEM = 1024 + TILES + BARS * 8;
@@ -740,6 +742,7 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
     float factor = (p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e) * fabsf(queries.k_scale);
     if (E4M3) factor *= s_factor[tid];
     if (factor < kTiny) factor = kTiny;  // (NaN stays)
+    if (factor > FLT_MAX) factor = FLT_MAX;  // (0 times it stays 0)
     const float times = p.cap > 0.f ? 1.f : factor;
     float m = -INFINITY, sum = 0.f;
 

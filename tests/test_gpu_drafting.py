@@ -300,3 +300,43 @@ def test_calls_on_other_streams_and_two_at_once(splash, T, Hq):
         for y, z in zip(x, (qr, *want, *remapped)):
             assert torch.equal(y, z)
     assert splash.last_device_error() == 0
+
+
+@pytest.mark.parametrize("per", [12, 2600], ids=["short rows of pages", "long rows of pages"])
+def test_two_captured_draft_steps(splash, per):
+    """Two graphs with one workspace, replayed one after the other, and two with their own,
+    replayed at the same time on two streams."""
+    states = [tree_state(per, T, Hq=Hq, seed=500 + T) for T, Hq in ((10, 8), (33, 8))]
+    sizes = [splash.paged_tree_decode_workspace_size(s[0][0], *s[1:4]) for s in states]
+    shared = torch.empty(max(sizes), dtype=torch.uint8, device="cuda")
+    want = [splash.paged_tree_decode(s[0][0], *s[1:4], s[4] + s[0][0].shape[2], s[5], 0.1) for s in states]
+    torch.cuda.synchronize()
+
+    def capture(s, ws, out, lse):
+        lens = s[4] + s[0][0].shape[2]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            splash.paged_tree_decode(s[0][0], *s[1:4], lens, s[5], 0.1, out=out, lse=lse, workspace=ws)
+        return graph, lens
+    results = [[torch.empty_like(y) for y in w] for w in want]
+    graphs = [capture(s, shared, *r) for s, r in zip(states, results)]
+    own = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+    results_own = [[torch.empty_like(y) for y in w] for w in want]
+    apart = [capture(s, ws, *r) for s, ws, r in zip(states, own, results_own)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(30):
+        for r in results + results_own:
+            for y in r:
+                y.fill_(float("nan"))
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for (g, _), stream in zip(apart, streams):
+            with torch.cuda.stream(stream):
+                for _ in range(3):
+                    g.replay()
+        torch.cuda.synchronize()
+        for w, r, o in zip(want, results, results_own):
+            assert all(torch.equal(a, b) for a, b in zip(w, r)) and all(torch.equal(a, b) for a, b in zip(w, o))
+    assert splash.last_device_error() == 0

@@ -341,3 +341,64 @@ def test_offsets_past_32_bits(splash):
     want = splash.paged_tree_decode(q, small[0], small[1], near, n, parents, 0.1)
     splash.check_device_error()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("T, Hq", [(7, 2), (50, 8)])
+@pytest.mark.parametrize("extra", [0, 2600], ids=["short", "long"])
+def test_outputs_at_any_16_bytes(splash, extra, T, Hq):
+    """A result that begins 16 bytes past a multiple of 32, its neighbours untouched."""
+    x = make([140, 420, 133], T, Hq, 1, 64, 64, 16, seed=120, extra_cols=extra)
+    want = splash.paged_tree_decode(**x)
+    n = 3 * Hq * T * 64
+    room = torch.full((n + 24,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = room[8:8 + n].view(3, Hq, T, 64)
+    assert out.data_ptr() % 32 == 16
+    got = splash.paged_tree_decode(**x, out=out)
+    splash.check_device_error()
+    assert torch.equal(out, want[0]) and torch.equal(got[1], want[1])
+    assert (room[:8] == 7).all() and (room[8 + n:] == 7).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T, Hq", [(7, 8), (50, 8)])
+def test_heads_and_pages_that_are_one_in_memory(splash, kind, T, Hq):
+    """Caches whose heads, or pages, repeat (stride 0); a pool of a single page."""
+    heads, d, page = 2, 64, 64
+    g = torch.Generator().manual_seed(5)
+    for pages, one_head, one_page in ((9, True, False), (9, False, True), (9, True, True), (1, False, False), (1, True, False)):
+        base = [torch.randn(1 if one_page else pages, 1 if one_head else heads, page, d, generator=g).bfloat16().cuda() for _ in range(2)]
+        x = dict(q=workloads.normal_bf16((2, Hq, T, d), 7).cuda(), scale=0.125, k_scale=None, v_scale=None,
+                 block_table=torch.tensor([[i % pages for i in range(4)], [(3 * i + 1) % pages for i in range(4)]], dtype=torch.int32).cuda(),
+                 seq_lens=torch.tensor([250, 61], dtype=torch.int32).cuda(), parents=make_trees(2, T, "ragged", 3).cuda())
+        if kind == "e4m3":
+            base = [b.to(torch.float8_e4m3fn) for b in base]
+            x["k_scale"], x["v_scale"] = torch.tensor([0.7, -1.3]).cuda(), torch.tensor([1.0, 0.5]).cuda()
+        x["k_cache"], x["v_cache"] = (b.expand(pages, heads, page, d) for b in base)
+        got = splash.paged_tree_decode(**x)
+        splash.check_device_error()
+        check(got, bounds(x))
+
+
+def test_two_thousand_rows_of_a_head(splash):
+    """All of 32 query heads on one KV head, 64 tokens each: eight groups of 256 rows."""
+    for lens, extra in (([200, 64, 700], 0), ([1900], 2600)):
+        x = make(lens, 64, 32, 1, 128, 128, 16, seed=130, extra_cols=extra)
+        got = splash.paged_tree_decode(**x)
+        splash.check_device_error()
+        check(got, bounds(x))
+
+
+def test_scales_at_the_ends_of_the_range(splash):
+    """The scores' factor would leave fp32's range; keys of zero still score 0, and
+    those next to its lower end next to 0."""
+    for kind in ("bf16", "e4m3"):
+        x = make([90, 30], 9, 4, 2, 64, 64, 16, kind, seed=140)
+        want = {}
+        x["k_cache"] = torch.zeros_like(x["k_cache"])
+        for scale, cap in ((3.4e38, 0.0), (3e38, 1e-3), (1e-38, 0.0)):
+            x["scale"] = 1.0  # (the keys are 0: any scale gives the same scores)
+            want = bounds(x, cap)
+            x["scale"] = scale
+            got = splash.paged_tree_decode(**x, softcap=cap)
+            splash.check_device_error()
+            check(got, want)
