@@ -571,6 +571,18 @@ splash_status check_decode(const splash_paged_decode_args &a, size_t need) {
   return check_view(a.q, a.B, a.Hq, a.Lq, a.dqk, false);
 }
 
+// Whether two tables of int32 rows share an entry (conservative where their strides differ).
+bool tables_overlap(const int32_t *x, int64_t rows_x, int64_t stride_x, const int32_t *y, int64_t rows_y, int64_t stride_y, int64_t cols) {
+  if (rows_x == 0 || rows_y == 0) return false;
+  if (rows_x == 1) stride_x = rows_y == 1 ? 0 : stride_y;
+  if (rows_y == 1) stride_y = stride_x;
+  const uintptr_t end_x = addr(x) + 4 * ((rows_x - 1) * stride_x + cols), end_y = addr(y) + 4 * ((rows_y - 1) * stride_y + cols);
+  if (end_x <= addr(y) || end_y <= addr(x)) return false;
+  if (stride_x != stride_y || stride_x < cols) return true;
+  const int64_t off = (addr(y) > addr(x) ? addr(y) - addr(x) : addr(x) - addr(y)) / 4 % stride_x;  // columns of one buffer's rows
+  return off < cols || off > stride_x - cols;
+}
+
 splash_status check_decode_values(const splash_paged_decode_args &a) {
   if (a.seq_lens == nullptr || a.out == nullptr || a.lse == nullptr || a.reserved != 0) return SPLASH_ERR_INVALID_ARG;
   if (((addr(a.out) | addr(a.workspace)) & 15u) != 0 || ((addr(a.seq_lens) | addr(a.lse)) & 3u) != 0)
@@ -683,6 +695,12 @@ splash_status splash_paged_tree_decode(const splash_paged_tree_decode_args *args
                                                a.window_left, &need);
   if (st != SPLASH_OK) return st;
   if ((st = check_decode(a, need)) != SPLASH_OK) return st;
+  // what a tensor map holds
+  const int64_t size = a.cache_type == SPLASH_CACHE_E4M3 ? 1 : 2;
+  for (const splash_cache_view *v : {&a.k_cache, &a.v_cache})
+    for (const Dim x : {Dim{a.num_pages, v->stride_page}, Dim{a.Hkv, v->stride_head}, Dim{2, v->stride_token}})
+      if (x.size > 1 && size * x.stride >= (int64_t)1 << 40) return SPLASH_ERR_UNSUPPORTED;
+  if (a.k_cache.stride_token == 0 || a.v_cache.stride_token == 0) return SPLASH_ERR_UNSUPPORTED;
   uint32_t *err = nullptr;
   if ((st = current_error_word(&err)) != SPLASH_OK) return st;
   return splash_paged_tree_decode_launch(*args, static_cast<cudaStream_t>(cuda_stream), err);
@@ -692,6 +710,7 @@ splash_status splash_paged_compact(const splash_paged_compact_args *args, void *
   if (args == nullptr || args->struct_bytes != sizeof *args) return SPLASH_ERR_INVALID_ARG;
   const splash_paged_compact_args &a = *args;
   if (a.B <= 0 || a.Hkv <= 0 || a.dqk <= 0 || a.dv <= 0 || a.moves <= 0 || a.reserved != 0) return SPLASH_ERR_INVALID_ARG;
+  if (a.k_cache.ptr == a.v_cache.ptr) return SPLASH_ERR_INVALID_ARG;  // (rows would move twice)
   if (a.src == nullptr || a.start == nullptr || ((addr(a.src) | addr(a.start)) & 3u) != 0 || (a.B > 1 && a.src_stride < 0))
     return SPLASH_ERR_INVALID_ARG;
   if (!valid_head_dim(a.dqk) || !valid_head_dim(a.dv) || a.Hkv > 65535 || a.moves > INT32_MAX) return SPLASH_ERR_UNSUPPORTED;
@@ -729,9 +748,14 @@ splash_status splash_paged_remap(const splash_paged_remap_args *args, void *cuda
   splash_status st = check_page_sizes(a.page_size, a.max_pages);
   if (st != SPLASH_OK) return st;
   if ((int64_t)a.num_rows * a.max_pages > INT32_MAX || (int64_t)a.new_rows * a.max_pages > INT32_MAX) return SPLASH_ERR_UNSUPPORTED;
+  if ((a.num_rows > 1 && a.block_table_stride > ((int64_t)1 << 29)) || (a.new_rows > 1 && a.new_table_stride > ((int64_t)1 << 29)))
+    return SPLASH_ERR_UNSUPPORTED;
   size_t need = 0;
   if ((st = splash_paged_remap_workspace_size(a.num_pages, a.new_rows, &need)) != SPLASH_OK) return st;
   if (a.workspace_bytes < need) return SPLASH_ERR_INVALID_ARG;
+  if (tables_overlap(a.block_table, a.num_rows, a.block_table_stride, a.new_table, a.new_rows, a.new_table_stride, a.max_pages) ||
+      (a.refs != a.refs_out && tables_overlap(a.refs, 1, 0, a.refs_out, 1, 0, a.num_pages)))
+    return SPLASH_ERR_INVALID_ARG;
   uint32_t *err = nullptr;
   if ((st = current_error_word(&err)) != SPLASH_OK) return st;
   return splash_paged_remap_launch(a, static_cast<cudaStream_t>(cuda_stream), err);

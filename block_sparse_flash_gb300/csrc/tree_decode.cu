@@ -1233,15 +1233,13 @@ splash_status make_map(CUtensorMap *map, const splash_cache_view &v, int64_t pag
       encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
   });
   if (encode == nullptr) return SPLASH_ERR_CUDA;
-  const int64_t size = e4m3 ? 1 : 2, limit = (int64_t)1 << 40;
+  const int64_t size = e4m3 ? 1 : 2;
   *head_on = heads > 1 && v.stride_head > 0;
   *page_on = pages > 1 && v.stride_page > 0;
   *page_end = *page_on ? (int32_t)pages : 1;
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page_size, (cuuint64_t)(*head_on ? heads : 1), (cuuint64_t)*page_end};
   const cuuint64_t strides[3] = {(cuuint64_t)(size * v.stride_token), (cuuint64_t)(size * (*head_on ? v.stride_head : d)),
                                  (cuuint64_t)(size * (*page_on ? v.stride_page : d))};
-  for (cuuint64_t s : strides)
-    if (s == 0 || s >= (cuuint64_t)limit) return SPLASH_ERR_UNSUPPORTED;
   const cuuint32_t box[4] = {(cuuint32_t)(e4m3 ? d : 64), (cuuint32_t)std::min(page_size, 64), 1, 1}, ones[4] = {1, 1, 1, 1};
   const CUresult r = encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.ptr, dims, strides, box,
                             ones, CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,

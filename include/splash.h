@@ -714,7 +714,8 @@ splash_status splash_paged_tree_decode_workspace_size(int32_t B, int32_t Hq, int
  * that no source is overwritten before it is read.  A row's list ends at the
  * first entry that breaks this, lies outside the block table's row or is on a
  * page outside [0, num_pages) (as source or destination), which is reported.
- * Sequences that share a page must not write to it.
+ * Sequences that share a page must not write to it, and K and V caches do not
+ * overlap (one and the same for both: INVALID_ARG).
  *
  *   src         device int32 [B][moves], row stride src_stride
  *   start       device int32 [B], >= 0 (a negative one: reported, nothing moves)
@@ -777,8 +778,9 @@ splash_status splash_paged_compact(const splash_paged_compact_args *args, void *
  *   short_pages device int32 [1]
  *   workspace   device, 16-byte aligned, of splash_paged_remap_workspace_size
  *               bytes; overwritten, holds nothing between calls
- * num_rows may be 0 (block_table is not read).  Errors: INVALID_ARG; UNSUPPORTED
- * (page_size, or tables of 2^31 entries or more); CUDA.
+ * num_rows may be 0 (block_table is not read).  Errors: INVALID_ARG (also where
+ * new_table overlaps block_table, or refs_out a part of refs); UNSUPPORTED
+ * (page_size, tables of 2^31 entries or more, rows more than 2^29 apart); CUDA.
  */
 typedef struct {
     uint64_t struct_bytes;

@@ -61,6 +61,11 @@ def sized(a):
     return a
 
 
+def apart(view):
+    view.ptr += 1 << 20
+    return view
+
+
 def rope_axes_args():
     return sized(RopeAxesArgs(rope=rope_args(), positions_stride_a=16, axes=AXES_PTR, num_axes=3))
 
@@ -77,13 +82,13 @@ def tree_args(T=5):
 
 
 def compact_args():
-    return sized(CompactArgs(k_cache=dense(2, 16, 128), v_cache=dense(2, 16, 128), block_table=OK_PTR, block_table_stride=4,
+    return sized(CompactArgs(k_cache=dense(2, 16, 128), v_cache=apart(dense(2, 16, 128)), block_table=OK_PTR, block_table_stride=4,
                              src=OK_PTR, src_stride=8, start=OK_PTR, num_pages=9, moves=8, B=2, Hkv=2, dqk=128, dv=128,
                              max_pages=4, page_size=16))
 
 
 def remap_args():
-    return sized(RemapArgs(block_table=OK_PTR, block_table_stride=4, new_table=OK_PTR, new_table_stride=4, parents=OK_PTR,
+    return sized(RemapArgs(block_table=OK_PTR, block_table_stride=4, new_table=OK_PTR + (1 << 20), new_table_stride=4, parents=OK_PTR,
                            keep=OK_PTR, room=OK_PTR, refs=OK_PTR, refs_out=OK_PTR, copies=OK_PTR, short_pages=OK_PTR,
                            workspace=OK_PTR, workspace_bytes=1 << 20, num_pages=100, num_rows=2, new_rows=3, max_pages=4,
                            page_size=16))
@@ -171,6 +176,14 @@ def test_tree_refusals(splash):
 
 
 @no_device
+def test_tree_strides(splash):
+    check(splash, "splash_paged_tree_decode", [
+        ("decode.k_cache.c", 0, UNSUPPORTED), ("decode.v_cache.c", 0, UNSUPPORTED), ("decode.k_cache.a", 1 << 39, UNSUPPORTED),
+        ("decode.v_cache.b", 1 << 39, UNSUPPORTED), ("decode.v_cache.a", (1 << 39) - 8, CUDA), ("decode.k_cache.b", 0, CUDA),
+        ("decode.k_cache.a", 0, CUDA)])
+
+
+@no_device
 def test_upkeep_refusals(splash):
     check(splash, "splash_paged_compact", BAD_PAIR + [
         ("B", 0, INVALID), ("moves", 0, INVALID), ("moves", 1 << 31, UNSUPPORTED), ("src", None, INVALID),
@@ -191,6 +204,26 @@ def test_upkeep_refusals(splash):
     a = remap_args()  # no old table at all
     a.num_rows, a.block_table = 0, None
     assert status(splash, "splash_paged_remap", a) == CUDA
+
+
+@no_device
+def test_upkeep_refuses_what_overlaps(splash):
+    a = compact_args()
+    a.v_cache = a.k_cache
+    assert status(splash, "splash_paged_compact", a) == INVALID
+    rows, cols, MIB = 3, 4, 1 << 20
+    # (the new table's place and stride in entries, behind the old one's, which is 2 rows of 4 every 4)
+    for offset, stride, old_stride, new_rows, want in (
+            (0, 4, 4, rows, INVALID), (7, 4, 4, rows, INVALID), (8, 4, 4, rows, CUDA), (-11, 4, 4, rows, INVALID), (-12, 4, 4, rows, CUDA),
+            (4, 8, 8, rows, CUDA), (3, 8, 8, rows, INVALID), (5, 8, 8, rows, INVALID), (-4, 8, 8, rows, CUDA), (-3, 8, 8, rows, INVALID),
+            (4, 9, 8, rows, INVALID), (4, 4, 8, 1, CUDA), (2, 4, 0, 1, INVALID), (4, 4, 0, 1, CUDA)):
+        a = remap_args()
+        a.new_table, a.new_table_stride, a.block_table_stride, a.new_rows = OK_PTR + 4 * offset, stride, old_stride, new_rows
+        assert status(splash, "splash_paged_remap", a) == want, (offset, stride, old_stride, new_rows)
+    check(splash, "splash_paged_remap", [("refs_out", OK_PTR + 4, INVALID), ("refs_out", OK_PTR - 4 * 99, INVALID),
+                                         ("refs_out", OK_PTR + 400, CUDA), ("refs_out", OK_PTR + MIB, CUDA),
+                                         ("new_table_stride", (1 << 29) + 1, UNSUPPORTED),
+                                         ("block_table_stride", (1 << 29) + 1, UNSUPPORTED)])
 
 
 def test_workspace_sizes(splash):
