@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libsplash.so")
 # (source, object, defines): attention_fwd.cu is compiled once per pattern
-# mode, paged_decode.cu and tree_decode.cu once per cache type, so that their kernel
+# mode, paged_decode.cu (for chains and for trees) and tree_decode.cu once per cache type, so that their kernel
 # instantiations build in parallel
 SOURCES = [("api.cu", "api", []), ("mask_info.cu", "mask_info", []),
            ("attention_fwd.cu", "attention_fwd", ["-DSPLASH_FWD_PM=0"]),
@@ -27,8 +27,10 @@ SOURCES = [("api.cu", "api", []), ("mask_info.cu", "mask_info", []),
            ("rope.cu", "rope", []), ("pages.cu", "pages", []),
            ("tree_decode.cu", "tree_decode_bf16", ["-DSPLASH_TREE_E4M3=0"]),
            ("tree_decode.cu", "tree_decode_e4m3", ["-DSPLASH_TREE_E4M3=1"]),
-           ("paged_decode.cu", "paged_decode_bf16", ["-DSPLASH_DECODE_E4M3=0"]),
-           ("paged_decode.cu", "paged_decode_e4m3", ["-DSPLASH_DECODE_E4M3=1"])]
+           ("paged_decode.cu", "paged_decode_bf16", ["-DSPLASH_DECODE_E4M3=0", "-DSPLASH_DECODE_TREE=0"]),
+           ("paged_decode.cu", "paged_decode_e4m3", ["-DSPLASH_DECODE_E4M3=1", "-DSPLASH_DECODE_TREE=0"]),
+           ("paged_decode.cu", "tree_rows_bf16", ["-DSPLASH_DECODE_E4M3=0", "-DSPLASH_DECODE_TREE=1"]),
+           ("paged_decode.cu", "tree_rows_e4m3", ["-DSPLASH_DECODE_E4M3=1", "-DSPLASH_DECODE_TREE=1"])]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # the compiled part of the Python binding, for this Python and this torch
 BINDING_SOURCE = "binding.cpp"

@@ -174,6 +174,9 @@ splash_status splash_paged_append_axes_launch(const splash_paged_append_axes_arg
 splash_status splash_paged_tree_decode_launch(const splash_paged_tree_decode_args &a, cudaStream_t stream, uint32_t *err_word);
 splash_status splash_paged_tree_decode_launch_bf16(const splash_paged_tree_decode_args &a, cudaStream_t stream, uint32_t *err_word);
 splash_status splash_paged_tree_decode_launch_e4m3(const splash_paged_tree_decode_args &a, cudaStream_t stream, uint32_t *err_word);
+// (paged_decode.cu: up to 16 rows per KV head)
+splash_status splash_paged_tree_rows_launch_bf16(const splash_paged_tree_decode_args &a, cudaStream_t stream, uint32_t *err_word);
+splash_status splash_paged_tree_rows_launch_e4m3(const splash_paged_tree_decode_args &a, cudaStream_t stream, uint32_t *err_word);
 // entries of the kernel's list, at most
 int64_t splash_paged_tree_decode_entries(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t max_pages, int32_t page_size,
                                          int64_t window);

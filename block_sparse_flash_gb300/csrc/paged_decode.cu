@@ -1,6 +1,8 @@
 // paged_decode.cu -- attention of new tokens over a paged key/value cache
 // (splash_paged_decode in splash.h).  Compiled once for each cache type
-// (SPLASH_DECODE_E4M3 = 0, 1), so that the instantiations build in parallel.
+// (SPLASH_DECODE_E4M3 = 0, 1), so that the instantiations build in parallel, and
+// once more for trees of new tokens (SPLASH_DECODE_TREE = 1: splash_paged_tree_decode
+// with up to 16 rows per KV head; tree_decode.cu has the larger ones).
 //
 // For a query row: s_j = scale q.k_j, m = max s_j, l = sum exp(s_j - m),
 // out = sum exp(s_j - m) v_j / l, lse = m + ln l, in one pass over the keys.
@@ -46,6 +48,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 
 #include "cluster.cuh"
@@ -57,6 +60,7 @@ namespace splash {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr bool kTree = SPLASH_DECODE_TREE != 0;
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kMaxWarps = 1216;  // of the grid; the workspace holds two parts for each
 
@@ -92,6 +96,8 @@ struct Params {
   int32_t max_pages, page_shift, window;         // window < 0: none
   float scale, cap;                              // cap <= 0: none
   uint32_t *err;
+  const int32_t *parents;  // of a tree's tokens
+  int64_t parents_stride;
 };
 
 // Keys of a step, from the bytes of a key and its value: 8 KB or so per step.
@@ -446,6 +452,54 @@ __device__ __forceinline__ void add_values(float (&o)[C::MT][C::DV / 8][4], cons
   }
 }
 
+// A token of a tree of up to 16: bits 0 .. 15 which tokens it sees (itself among
+// them; none for padding), from bit 16 on how many ancestors it has.  Lane l looks
+// at token l; the warp walks up together, a shuffle a level.
+[[maybe_unused]] __device__ __forceinline__ int32_t branch_of(const Params &p, int b, int32_t ctx, int lane) {
+  int32_t up = lane < p.Lq && lane >= -ctx ? p.parents[b * p.parents_stride + lane] : -2;  // (a slot before the first: padding)
+  if (up >= lane) {  // not an earlier token
+    atomicOr(p.err, SPLASH_DEV_BAD_TABLE);
+    up = -2;
+  }
+  int32_t seen = 0, depth = 0, at = lane;
+  while (__any_sync(~0u, at >= 0)) {
+    const int32_t next = __shfl_sync(~0u, up, max(at, 0));
+    if (at < 0) continue;
+    if (p.window < 0 || depth <= p.window) seen |= 1 << at;
+    if (next < -1) seen = 0;
+    depth += next >= 0;
+    at = max(next, -1);
+  }
+  return lane < p.Lq && seen != 0 ? (seen & 0xffff) | depth << 16 : 0;
+}
+
+// The keys of [key0, key0 + 32) that a token of a tree sees, as bits.
+__device__ __forceinline__ uint32_t visible(const Params &p, int32_t key0, int32_t ctx, int32_t branch) {
+  const uint32_t seen = branch & 0xffff;
+  const int32_t lo = p.window < 0 ? 0 : ctx + (branch >> 16 & 0xff) - p.window;
+  const int32_t first = max(0, lo - key0), d = ctx - key0, count = min(32, d) - first;
+  uint32_t m = count <= 0 ? 0 : (count >= 32 ? ~0u : (1u << count) - 1) << first;
+  if (d < 32 && d > -32) m |= d >= 0 ? seen << d : seen >> -d;
+  return seen != 0 ? m : 0;
+}
+
+// Whether all of a step's values are finite and below 2^64: then 0 in the place of a
+// key's probability (or 2^-126, the floor of its rest) is as good as 0 in that of its value.
+template <class C>
+__device__ __forceinline__ bool tame(uint32_t vs, int lane) {
+  uint32_t high = 0;
+#pragma unroll
+  for (int i = 0; i < C::KW * C::RV / 512; ++i) {
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(vs + (i * 32 + lane) * 16) : "memory");
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)  // a carry into the top bit of a value's place: bf16 exponents from 191 on, e4m3's NaN
+      high |= C::E4M3 ? ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u : ((w[k] & 0x7f807f80u) + 0x20802080u) & 0x80008000u;
+  }
+  return !__any_sync(~0u, high != 0);
+}
+
 // TOGETHER: a cluster of CTAs per segment; otherwise equal parts of the list per warp.
 template <class C, bool TOGETHER>
 __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params p) {
@@ -559,7 +613,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
     const float base_factor = (p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e) * (E4M3 ? p.k_scale[head] : 1.f);
     uint32_t qa[MT == 1 ? DQK / 16 : 1][4];
     float factor[MT][E], m[MT][E], l[MT][E], o[MT][DV / 8][4];
-    int32_t pos[MT][E];  // the row's position (rows past the last one see what the last query sees)
+    // The row's position (rows past the last one see what the last query sees); for a tree its
+    // token's branch, and the token from bit 24 on (rows past the last one: none).
+    int32_t pos[MT][E], branch = 0;
+    if constexpr (kTree) branch = branch_of(p, b, sp.n - Lq, lane);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -567,7 +624,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
         const int r = mt * 16 + quad + 8 * e;
         const int g = (row0 + r) / Lq, lq = (row0 + r) - g * Lq;
         factor[mt][e] = base_factor;
-        pos[mt][e] = sp.n - Lq + (r < rows ? lq : Lq - 1);
+        if constexpr (kTree) {
+          pos[mt][e] = __shfl_sync(~0u, branch, lq & 31) | lq << 24;
+          if (r >= rows) pos[mt][e] = 31 << 24;
+          if (factor[mt][e] > FLT_MAX) factor[mt][e] = FLT_MAX;  // (0 times it stays 0)
+        } else {
+          pos[mt][e] = sp.n - Lq + (r < rows ? lq : Lq - 1);
+        }
         m[mt][e] = -INFINITY;
         l[mt][e] = 0.f;
         if (MT == 1) {
@@ -603,6 +666,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
               qa[kk][2 + e] = to_half(qa[kk][2 + e], top);
             }
             factor[mt][e] *= __uint_as_float(top << 23);
+            if (kTree && fabsf(factor[mt][e]) > FLT_MAX) factor[mt][e] = copysignf(FLT_MAX, factor[mt][e]);
           }
         }
       }
@@ -710,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
       }
 
       // scores in powers of two; masked where some row does not see some key
-      const bool whole = key0 + C::KW <= sp.n - Lq + 1 && (p.window < 0 || key0 >= sp.n - 1 - p.window);
+      const bool whole = key0 + C::KW <= sp.n - Lq + (kTree ? 0 : 1) && (p.window < 0 || key0 >= sp.n - 1 - p.window);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -745,7 +809,19 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
               for (int i = 0; i < 2 * E; ++i) s[mt][j][i] = cap * tanh_series(s[mt][j][i]);
         }
       }
-      if (!whole) {
+      if (kTree && !whole) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const uint32_t see = visible(p, key0, sp.n - Lq, pos[mt][e]) >> (2 * tq);
+#pragma unroll
+            for (int j = 0; j < 2 * NB; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (!(see >> (8 * j + i) & 1u)) s[mt][j][2 * e + i] = -INFINITY;
+          }
+      } else if (!whole) {
         const uint32_t reach = p.window < 0 ? 0x7fffffffu : (uint32_t)p.window;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -839,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
             }
           }
       }
-      if (!C::MULTI || whole) {
+      if (!C::MULTI || whole || (kTree && tame<C>(vs, lane))) {
         add_values<C, false>(o, w, vs, lane, Seen<C>());
       } else if constexpr (C::MULTI) {
         // Some of the step's values are one query's and not another's: a
@@ -849,18 +925,22 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
         for (int lq = 0; lq < Lq; ++lq) {
           const int32_t last = sp.n - Lq + lq;
           const uint32_t reach = p.window < 0 ? 0x7fffffffu : (uint32_t)p.window;
+          const uint32_t see = kTree ? visible(p, key0, sp.n - Lq, __shfl_sync(~0u, branch, lq)) >> (2 * tq) : 0;
           Seen<C> seen;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint32_t behind = (uint32_t)(last - (key0 + 16 * nb + 8 * i + 2 * tq));
-              seen.keys[nb][i] = (behind <= reach ? 0xffffu : 0u) | (behind - 1u <= reach ? 0xffff0000u : 0u);
+              const uint32_t behind = (uint32_t)(last - (key0 + 16 * nb + 8 * i + 2 * tq)), two = see >> (16 * nb + 8 * i);
+              if (kTree)
+                seen.keys[nb][i] = (two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u);
+              else
+                seen.keys[nb][i] = (behind <= reach ? 0xffffu : 0u) | (behind - 1u <= reach ? 0xffff0000u : 0u);
             }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int e = 0; e < E; ++e) seen.row[mt][e] = pos[mt][e] == last;
+            for (int e = 0; e < E; ++e) seen.row[mt][e] = kTree ? pos[mt][e] >> 24 == lq : pos[mt][e] == last;
           add_values<C, true>(o, w, vs, lane, seen);
         }
       }
@@ -875,6 +955,18 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           if (fabsf(o[0][j][i]) < INFINITY) o[0][j][i] += o[0][j][i + 2];
+    }
+    if constexpr (kTree) {  // padding sees nothing
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if ((pos[mt][e] & 0xffff) != 0) continue;
+          m[mt][e] = -INFINITY;
+          l[mt][e] = 0.f;
+#pragma unroll
+          for (int j = 0; j < DV / 8; ++j) o[mt][j][2 * e] = o[mt][j][2 * e + 1] = 0.f;
+        }
     }
     if constexpr (TOGETHER) {
       copy_wait<0>();
@@ -1180,7 +1272,10 @@ splash_status launch(const Plan &x, void *workspace, Params p, cudaStream_t stre
 template <int DQK, int DV, int ROWS>
 splash_status pick_queries(const Plan &x, void *workspace, const Params &p, cudaStream_t stream) {
   constexpr bool E4M3 = SPLASH_DECODE_E4M3 != 0;
-  return p.Lq == 1 ? launch<Config<DQK, DV, E4M3, ROWS, false>>(x, workspace, p, stream)
+  if constexpr (kTree)
+    return launch<Config<DQK, DV, E4M3, ROWS, true>>(x, workspace, p, stream);
+  else
+    return p.Lq == 1 ? launch<Config<DQK, DV, E4M3, ROWS, false>>(x, workspace, p, stream)
                    : launch<Config<DQK, DV, E4M3, ROWS, true>>(x, workspace, p, stream);
 }
 
@@ -1188,14 +1283,14 @@ template <int DQK, int DV>
 splash_status pick(const splash_paged_decode_args &a, const Params &p, cudaStream_t stream) {
   const Plan x = plan(a.B, a.Hq, a.Hkv, a.Lq, a.dqk, a.dv, a.max_pages, a.page_size, a.cache_type, a.window_left);
   if (x.rows == 8) return pick_queries<DQK, DV, 8>(x, a.workspace, p, stream);
-  if (x.rows == 16) return pick_queries<DQK, DV, 16>(x, a.workspace, p, stream);
-  return pick_queries<DQK, DV, 32>(x, a.workspace, p, stream);
+  if (kTree || x.rows == 16) return pick_queries<DQK, DV, 16>(x, a.workspace, p, stream);
+  return pick_queries<DQK, DV, kTree ? 16 : 32>(x, a.workspace, p, stream);
 }
 
 }  // namespace
 }  // namespace splash
 
-#if !SPLASH_DECODE_E4M3
+#if !SPLASH_DECODE_E4M3 && !SPLASH_DECODE_TREE
 size_t splash_paged_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t dqk, int32_t dv,
                                            int32_t max_pages, int32_t page_size, int32_t type, int64_t window) {
   return splash::plan(B, Hq, Hkv, Lq, dqk, dv, max_pages, page_size, type, window).workspace;
@@ -1207,7 +1302,14 @@ splash_status splash_paged_decode_launch(const splash_paged_decode_args &a, cuda
 }
 #endif
 
+#if SPLASH_DECODE_TREE
 #if SPLASH_DECODE_E4M3
+splash_status splash_paged_tree_rows_launch_e4m3(const splash_paged_tree_decode_args &tree, cudaStream_t stream, uint32_t *err_word) {
+#else
+splash_status splash_paged_tree_rows_launch_bf16(const splash_paged_tree_decode_args &tree, cudaStream_t stream, uint32_t *err_word) {
+#endif
+  const splash_paged_decode_args &a = tree.decode;
+#elif SPLASH_DECODE_E4M3
 splash_status splash_paged_decode_launch_e4m3(const splash_paged_decode_args &a, cudaStream_t stream, uint32_t *err_word) {
 #else
 splash_status splash_paged_decode_launch_bf16(const splash_paged_decode_args &a, cudaStream_t stream, uint32_t *err_word) {
@@ -1249,6 +1351,10 @@ splash_status splash_paged_decode_launch_bf16(const splash_paged_decode_args &a,
   // score below 2^88 as it is)
   p.cap = a.softcap < 0x1p100f ? a.softcap : 0.f;
   p.err = err_word;
+#if SPLASH_DECODE_TREE
+  p.parents = tree.parents;
+  p.parents_stride = tree.parents_stride_b;
+#endif
   if (a.dqk == 64) return pick<64, 64>(a, p, stream);
   if (a.dqk == 128) return pick<128, 128>(a, p, stream);
   return pick<192, 128>(a, p, stream);

@@ -1347,15 +1347,29 @@ int64_t splash_paged_tree_decode_entries(int32_t B, int32_t Hq, int32_t Hkv, int
   return (splash::most_steps(T, max_pages, page_size, window) + splash::kPieceSteps) * B * Hkv * ((rows + tile - 1) / tile);
 }
 
-size_t splash_paged_tree_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t, int32_t dv, int32_t, int32_t,
-                                                int32_t, int64_t) {
+// Up to this many rows of a KV head paged_decode's kernel takes the tree: its tiles of 8
+// and 16 rows keep four times the SMs' warps busy with loads, where here one warp in four
+// has rows, and a step of 64 keys takes as long as with 128 rows.  (Device time, here -> there: 64
+// requests of up to 4096 tokens, 32 / 8 heads of 128, 1 draft 117 -> 92 us, 4 drafts 123 ->
+// 110; in e4m3, up to 8192 tokens, 186 -> 104 and 160 -> 122; 7 drafts, 128 / 128 heads of 192, window
+// of 1023, cap 129 -> 94, 16 drafts without them 137 -> 112, in e4m3 254 -> 116; 1 request of
+// 300 tokens, 4 drafts 9.4 -> 6.1.  With 32 rows: 8 drafts of 32 requests 72 here, and half
+// of the 223 us that 4 tokens of 64 requests with 64 / 8 heads take there.)
+constexpr int kFewRows = 16;
+
+size_t splash_paged_tree_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t dqk, int32_t dv,
+                                                int32_t max_pages, int32_t page_size, int32_t type, int64_t window) {
   const int64_t rows = std::min<int64_t>((int64_t)(Hq / Hkv) * T, 256);
+  if (rows <= kFewRows) return splash_paged_decode_workspace_bytes(B, Hq, Hkv, T, dqk, dv, max_pages, page_size, type, window);
   return (size_t)(16 + splash::align16(4 * ((int64_t)B + 1)) + 4 * splash::kMaxCtas + (int64_t)2 * splash::kMaxCtas * rows * 4 * (dv + 2));
 }
 
 splash_status splash_paged_tree_decode_launch(const splash_paged_tree_decode_args &args, cudaStream_t stream, uint32_t *err_word) {
-  return args.decode.cache_type == SPLASH_CACHE_E4M3 ? splash_paged_tree_decode_launch_e4m3(args, stream, err_word)
-                                                     : splash_paged_tree_decode_launch_bf16(args, stream, err_word);
+  const bool e4m3 = args.decode.cache_type == SPLASH_CACHE_E4M3;
+  if ((int64_t)(args.decode.Hq / args.decode.Hkv) * args.decode.Lq <= kFewRows)
+    return e4m3 ? splash_paged_tree_rows_launch_e4m3(args, stream, err_word) : splash_paged_tree_rows_launch_bf16(args, stream, err_word);
+  return e4m3 ? splash_paged_tree_decode_launch_e4m3(args, stream, err_word)
+              : splash_paged_tree_decode_launch_bf16(args, stream, err_word);
 }
 #endif
 

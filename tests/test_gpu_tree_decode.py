@@ -402,3 +402,65 @@ def test_scales_at_the_ends_of_the_range(splash):
             got = splash.paged_tree_decode(**x, softcap=cap)
             splash.check_device_error()
             check(got, want)
+
+
+FEW = [
+    # lens, T, Hq, Hkv, dqk, dv, page, kind, layout, shape, window, cap
+    ([0, 3, 15, 16, 17, 40, 300], 16, 2, 2, 128, 128, 16, "bf16", "heads", "ragged", -1, 0.0),
+    ([0, 3, 15, 16, 17, 40, 300], 16, 1, 1, 64, 64, 16, "e4m3", "tokens", "binary", -1, 0.0),
+    ([700, 100, 33, 5, 0], 10, 2, 2, 128, 128, 16, "bf16", "heads", "chain", 4, 0.0),
+    ([700, 100, 33, 5, 0], 16, 2, 2, 64, 64, 32, "bf16", "tokens", "chain", 0, 5.0),
+    ([700, 100, 33, 5, 0], 4, 12, 3, 192, 128, 64, "bf16", "heads", "ragged", 33, 0.0),
+    ([700, 100, 33, 5, 0], 16, 4, 4, 192, 128, 64, "e4m3", "heads", "chain", 20, 3.0),
+    ([700, 1000, 333], 2, 16, 2, 128, 128, 128, "e4m3", "heads", "roots", 500, 0.0),
+    ([700, 1000, 333], 3, 10, 2, 128, 128, 16, "bf16", "heads", "ragged", 10 ** 12, 50.0),
+    ([1900], 8, 1, 1, 128, 128, 16, "e4m3", "heads", "ragged", -1, 0.0),
+    ([1900, 1], 1, 8, 1, 192, 128, 16, "bf16", "heads", "roots", -1, 0.0),
+]
+
+
+@pytest.mark.parametrize("long_rows", [False, True], ids=["short", "long"])
+@pytest.mark.parametrize("case", FEW, ids=str)
+def test_few_rows(splash, case, long_rows):
+    lens, T, Hq, Hkv, dqk, dv, page, kind, layout, shape, window, cap = case
+    x = make(lens, T, Hq, Hkv, dqk, dv, page, kind, layout, shape, seed=300 + FEW.index(case),
+             extra_cols=1 + 40000 // page if long_rows else 0)
+    got = splash.paged_tree_decode(**x, softcap=cap, window_left=window)
+    splash.check_device_error()
+    check(got, bounds(x, cap, window))
+    again = splash.paged_tree_decode(**x, softcap=cap, window_left=window)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("value", [2.0 ** 100, 2.0 ** 127, float("inf"), float("nan")])
+@pytest.mark.parametrize("T, Hq, window", [(8, 1, -1), (4, 4, -1), (16, 1, 2), (8, 2, 5), (40, 1, -1)])
+def test_large_values_stay_with_those_who_see_them(splash, value, T, Hq, window):
+    """A token's value, and with a window a key's at its start, far above all others."""
+    x = make([230], T, Hq, 1, 64, 64, 16, shape="binary" if window < 0 else "chain", seed=150)
+    want = bounds(x, 0.0, window)
+    bt, parents = x["block_table"], x["parents"].cpu().numpy()[0]
+    at = [230 - T + T // 2] + ([230 - T - window] if window >= 0 else [])
+    for key in at:
+        x["v_cache"][bt[0, key // 16], :, key % 16] = value
+    got = splash.paged_tree_decode(**x, window_left=window)
+    splash.check_device_error()
+    keys = [set(k) for k, _ in ref.tree_keys(parents, 230, window)]
+    blind = np.array([not any(k in seen for k in at) for seen in keys])
+    assert blind.any() and not blind.all()
+    o, l = host(got[0]), host(got[1])
+    assert (np.abs(o - want[0]) <= want[2])[:, :, blind].all() and (np.abs(l - want[1]) <= want[3]).all()
+    # (a value of 2^100 and more has a probability of 2^-60 at the least here: far above the others)
+    assert not (np.abs(np.nan_to_num(o[:, :, ~blind], nan=np.inf)) < 2.0 ** 30).any()
+
+
+def test_scales_at_the_ends_of_the_range_few_rows(splash):
+    for kind in ("bf16", "e4m3"):
+        x = make([90, 30], 5, 4, 2, 64, 64, 16, kind, seed=141)
+        x["k_cache"] = torch.zeros_like(x["k_cache"])
+        for scale, cap in ((3.4e38, 0.0), (3e38, 1e-3), (1e-38, 0.0)):
+            x["scale"] = 1.0  # (the keys are 0: any scale gives the same scores)
+            want = bounds(x, cap)
+            x["scale"] = scale
+            got = splash.paged_tree_decode(**x, softcap=cap)
+            splash.check_device_error()
+            check(got, want)
