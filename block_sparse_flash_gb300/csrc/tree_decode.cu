@@ -32,9 +32,11 @@
 // keys arrives every 1700 cycles, 1390 at the copy rate, and a segment's start and end cost
 // 19000 of which the other SMs hide nothing); 16 requests of up to 32768 tokens and 64 drafts,
 // e4m3, 250 (floor 149, the products: shared memory, which the products' operands, the
-// widening and the loads fill to 80 %); 128 / 128 heads of 192 through a window of 1023,
-// 7 drafts, 130 (floor 75); 1 request of 300 tokens and 16 drafts 10.0 (the launch, eight
-// dependent reads, the first fetch of the code).
+// widening and the loads fill to 80 %); 1 request of 300 tokens and 16 drafts 10.0 (the launch,
+// eight dependent reads, the first fetch of the code).  Of these the join of the parts is 12, 19
+// and 0.  19 requests of 8192 tokens, 32 drafts, a segment a CTA: 121 (floor 95).
+//
+// Up to 16 rows of a KV head go to paged_decode's kernel (kFewRows below).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -1130,7 +1132,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid
 
 // Joins the parts of a segment that several CTAs computed: with (m_c, l_c, o_c) of part c
 // of a row and m = max m_c: out = sum exp(m_c - m) o_c / sum exp(m_c - m) l_c, in the
-// order of the keys.  A CTA takes `each` rows of a segment, a warp one at a time.
+// order of the keys.  A CTA takes `each` rows of a segment, a warp one at a time.  (CTAs for each
+// place where a segment goes on in another CTA, instead of for each segment: 32 requests of 32
+// drafts 83.2 -> 82.3 us, but 1 request of 16384 tokens, in parts of all CTAs, 33.7 -> 45.)
 constexpr int kJoinWarps = 8;
 template <int DV, int TILE, bool E4M3>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const Params p, int slices, int each) {
