@@ -920,7 +920,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
       } else if constexpr (C::MULTI) {
         // Some of the step's values are one query's and not another's: a
         // product for each query, with zeros in the place of the values that
-        // it does not see, whatever they are (0 x infinity is not 0).
+        // it does not see, whatever they are (0 x infinity is not 0).  (A tree of 16
+        // drafts would take 16 of them at every sequence's end: only where they differ.)
 #pragma unroll 1
         for (int lq = 0; lq < Lq; ++lq) {
           const int32_t last = sp.n - Lq + lq;

@@ -121,12 +121,12 @@ struct Config {
   static constexpr int COLUMN = KW * 128, K_BYTES = KW * DQK * 2, STAGE = K_BYTES + KW * DV * 2;
   static constexpr int Q_COLUMN = 128 * 128, Q_BYTES = 128 * DQK * 2;
   static constexpr int RAW = E4M3 ? KW * (RK + RV) : 0;  // an e4m3 step as it is in the cache
-  static constexpr int BUDGET = 222 * 1024 - NT * Q_BYTES;
+  static constexpr int ROOM = 222 * 1024 - NT * Q_BYTES;
   // (a step's scores are computed LOOK steps before its products with the values)
   static constexpr int LOOK = PAIR ? 1 : 2;
-  static constexpr int STAGES = E4M3 ? (BUDGET >= 4 * STAGE + 3 * RAW ? 4 : BUDGET >= 3 * STAGE + 2 * RAW ? 3 : 2)
-                                     : std::min(8, BUDGET / STAGE);
-  static constexpr int RAWS = E4M3 ? std::min(6, (BUDGET - STAGES * STAGE) / std::max(RAW, 1)) : 0;
+  static constexpr int STAGES = E4M3 ? (ROOM >= 4 * STAGE + 3 * RAW ? 4 : ROOM >= 3 * STAGE + 2 * RAW ? 3 : 2)
+                                     : std::min(8, ROOM / STAGE);
+  static constexpr int RAWS = E4M3 ? std::min(6, (ROOM - STAGES * STAGE) / std::max(RAW, 1)) : 0;
   static constexpr int TILES = NT * Q_BYTES + STAGES * STAGE + RAWS * RAW;
   static_assert(STAGES > LOOK && (!E4M3 || RAWS >= 2), "a step's stage is free before it is waited for");
   static_assert(TILE * (DV + 4) * 4 <= TILES, "a cluster's parts fit where the operands were");
