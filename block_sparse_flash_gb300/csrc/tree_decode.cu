@@ -1216,10 +1216,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const Params
 
 int64_t align16(int64_t x) { return (x + 15) & ~(int64_t)15; }
 
-// Steps that a sequence can have, from its row of pages and the window.
+// Steps that a sequence can have, from its row of pages and the window.  (A window of all
+// its keys is none: with T added the largest ones would overflow.)
 int64_t most_steps(int32_t T, int32_t max_pages, int32_t page_size, int64_t window) {
-  const int64_t most = ((int64_t)max_pages * page_size + 63) / 64;
-  return window < 0 ? most : std::min(most, (window + T) / 64 + 3);
+  const int64_t keys = (int64_t)max_pages * page_size, most = (keys + 63) / 64;
+  return window < 0 || window >= keys ? most : std::min(most, (window + T) / 64 + 3);
 }
 
 // A cache as a 4-D tensor [pages][heads][tokens][d]; boxes of `rows` rows by 64 bf16 columns

@@ -245,6 +245,22 @@ def test_workspace_sizes(splash):
         assert splash.lib().splash_paged_remap_workspace_size(pages, rows, ctypes.byref(n)) == want
 
 
+def test_a_window_past_every_key_is_none(splash):
+    """Sizes and their limits do not overflow next to the end of int64."""
+    n = ctypes.c_size_t(0)
+
+    def tree(window, B=4, Hq=32, Hkv=8, T=20, max_pages=8192):
+        n.value = 0
+        status = splash.lib().splash_paged_tree_decode_workspace_size(B, Hq, Hkv, T, 128, 128, max_pages, 16, 0, window, ctypes.byref(n))
+        return status, n.value
+    for window in (2 ** 63 - 1, 2 ** 63 - 64, 2 ** 63 - 65, 2 ** 62, 8192 * 16, 8192 * 16 - 1):
+        for T in (1, 4, 5, 20, 64):
+            assert tree(window, T=T) == tree(-1, T=T) and tree(window, T=T)[0] == 0
+        # 2^31 steps and starts of segments: 65535 sequences x 4095 heads x (1 + 9)
+        for heads in (4095, 4096):
+            assert tree(window, B=65535, Hq=heads, Hkv=heads, T=1, max_pages=1)[0] == UNSUPPORTED
+
+
 def test_axis_maps(splash):
     assert splash.rope_axis_map((2, 1, 3)) == bytes([0, 0, 1, 2, 2, 2])
     assert splash.rope_axis_map((2, 1, 3), cycled=True) == bytes([0, 1, 2, 0, 2, 2])

@@ -464,3 +464,18 @@ def test_scales_at_the_ends_of_the_range_few_rows(splash):
             got = splash.paged_tree_decode(**x, softcap=cap)
             splash.check_device_error()
             check(got, want)
+
+
+@pytest.mark.parametrize("T, G", [(64, 1), (40, 4), (4, 1)])
+@pytest.mark.parametrize("window", [2 ** 63 - 1, 2 ** 63 - 64])
+def test_a_window_past_every_key_is_none(splash, window, T, G):
+    """64 segments in one list: with the largest numbers it is cut as without a window."""
+    x = make([200, 64, 130, 70, 0, 65, 500, 300], T, 8 * G, 8, 64, 64, 16, seed=160, extra_cols=2600)
+    size = splash.paged_tree_decode_workspace_size(x["q"], x["k_cache"], x["v_cache"], x["block_table"])
+    assert size > 0 and size == splash.paged_tree_decode_workspace_size(x["q"], x["k_cache"], x["v_cache"], x["block_table"], window)
+    want = splash.paged_tree_decode(**x)
+    ws = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    got = splash.paged_tree_decode(**x, window_left=window, workspace=ws[:size])
+    splash.check_device_error()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and (ws[size:] == 0xA5).all()
+    check(got, bounds(x))
