@@ -250,10 +250,10 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
-__device__ __forceinline__ float rest_of(float x) {
-  return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xffff0000u), __uint_as_float(0x00800000u));
+__device__ __forceinline__ float rest_of(float x, float floor) {
+  return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xffff0000u), floor);
 }
-__device__ __forceinline__ uint32_t rest_bf16x2(float lo, float hi) { return pack_bf16x2(rest_of(lo), rest_of(hi)); }
+__device__ __forceinline__ uint32_t rest_bf16x2(float lo, float hi, float floor) { return pack_bf16x2(rest_of(lo, floor), rest_of(hi, floor)); }
 
 // The larger exponent field of a word's two bf16 values, and the word as fp16
 // values over 2^(top - 127).
@@ -483,10 +483,10 @@ __device__ __forceinline__ uint32_t visible(const Params &p, int32_t key0, int32
   return seen != 0 ? m : 0;
 }
 
-// Whether all of a step's values are finite and below 2^64: then 0 in the place of a
-// key's probability (or 2^-126, the floor of its rest) is as good as 0 in that of its value.
+// Whether all of a step's values are finite: then 0 in the place of a key's probability, and
+// of its rest, is as good as 0 in that of its value.
 template <class C>
-__device__ __forceinline__ bool tame(uint32_t vs, int lane) {
+__device__ __forceinline__ bool all_finite(uint32_t vs, int lane) {
   uint32_t high = 0;
 #pragma unroll
   for (int i = 0; i < C::KW * C::RV / 512; ++i) {
@@ -494,8 +494,8 @@ __device__ __forceinline__ bool tame(uint32_t vs, int lane) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(vs + (i * 32 + lane) * 16) : "memory");
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k)  // a carry into the top bit of a value's place: bf16 exponents from 191 on, e4m3's NaN
-      high |= C::E4M3 ? ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u : ((w[k] & 0x7f807f80u) + 0x20802080u) & 0x80008000u;
+    for (int k = 0; k < 4; ++k)  // a carry into the top bit of a value's place: bf16's exponent 255, e4m3's NaN
+      high |= C::E4M3 ? ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u : ((w[k] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
   }
   return !__any_sync(~0u, high != 0);
 }
@@ -879,7 +879,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
       //    is cut off to bf16 and the rest kept above 0: an infinite value times
       //    either has its sign, and the sum is that infinity (0 x infinity and
       //    infinity - infinity are NaN).  The rest's floor, the smallest normal
-      //    number, adds 2^-126 of a value.
+      //    number, adds 2^-126 of a value that its row sees; where a tree's rows do not
+      //    see all of a step and all of its values are finite there is no floor, so that
+      //    a hidden key's rest is 0 as its probability is.
+      const bool product = !C::MULTI || whole || (kTree && all_finite<C>(vs, lane));  // one for all rows, nothing masked in V
+      [[maybe_unused]] const float floor = kTree && product && !whole ? 0.f : __uint_as_float(0x00800000u);
       Weights<C> w;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -902,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
             const float *y = &s[mt][2 * nb + (i >> 1)][E == 1 ? 0 : 2 * (i & 1)];
             if constexpr (C::REST) {
               w.p[mt][nb][i] = cut_bf16x2(y[0], y[1]);
-              w.rest[mt][nb][i] = rest_bf16x2(y[0], y[1]);
+              w.rest[mt][nb][i] = rest_bf16x2(y[0], y[1], floor);
             } else if (E == 2 || (i & 1) == 0) {
               w.p[mt][nb][i] = pack2<E4M3>(y[0], y[1]);
             } else if (E4M3) {
@@ -915,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const Params 
             }
           }
       }
-      if (!C::MULTI || whole || (kTree && tame<C>(vs, lane))) {
+      if (product) {
         add_values<C, false>(o, w, vs, lane, Seen<C>());
       } else if constexpr (C::MULTI) {
         // Some of the step's values are one query's and not another's: a

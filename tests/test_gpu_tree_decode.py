@@ -479,3 +479,28 @@ def test_a_window_past_every_key_is_none(splash, window, T, G):
     splash.check_device_error()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and (ws[size:] == 0xA5).all()
     check(got, bounds(x))
+
+
+@pytest.mark.parametrize("kind, value", [("bf16", 1.0), ("bf16", 2.0 ** 60), ("bf16", 2.0 ** 63), ("bf16", 2.0 ** 64), ("e4m3", 448.0)])
+@pytest.mark.parametrize("T, Hq, window", [(9, 1, -1), (4, 4, -1), (16, 1, -1), (16, 1, 2), (8, 2, 5), (3, 5, 0), (8, 1, -1), (40, 1, -1), (40, 4, 7)])
+def test_nothing_of_a_hidden_value_is_left(splash, T, Hq, window, kind, value):
+    """All that a token sees is 0: so is its result, to the last bit, whatever a
+    sibling, padding or a key before its window holds."""
+    x = make([230, 77], T, Hq, 1, 64, 64, 16, kind, shape="binary" if window < 0 else "chain", seed=151)
+    x["parents"][1, T - 1] = -5
+    v = x["v_cache"].float()
+    v = v.masked_fill(~torch.isnan(v), 0.0)
+    bt, parents = x["block_table"], x["parents"].cpu().numpy()
+    at = [[230 - T + T // 2] + ([230 - T - window] if window >= 0 else []), [76]]  # (the second one's padding)
+    for b in range(2):
+        for key in at[b]:
+            v[bt[b, key // 16], :, key % 16] = value
+    x["v_cache"] = v.to(x["v_cache"].dtype)
+    got = splash.paged_tree_decode(**x, window_left=window)
+    splash.check_device_error()
+    o = host(got[0])
+    for b, n in enumerate((230, 77)):
+        keys = [set(k) for k, _ in ref.tree_keys(parents[b], n, window)]
+        blind = np.array([not any(k in seen for k in at[b]) for seen in keys])
+        assert blind.all() if b else blind.any() and not blind.all()
+        assert (o[b][:, blind] == 0).all() and (o[b][:, ~blind] > 0).all()
