@@ -76,8 +76,10 @@ constexpr float kSlack = 8.f;
 // the slack.  What is dropped at the bottom, half of fp16's 2^-24, is 2^-32 of the
 // largest key.
 constexpr float kBelowTop = 7.f;
-// The smallest factor of the scores: a masked one (-inf) stays -inf times it.
-constexpr float kTiny = 0x1p-126f;
+// The smallest factor of the scores: a masked one (-inf) stays -inf times it.  (fp32's
+// smallest number: with its smallest normal one a scale below that would be rounded up to it,
+// which is wrong by any power of two where the queries are as large as the scale is small.)
+constexpr float kTiny = 0x1p-149f;
 
 struct Params {
   const char *q;

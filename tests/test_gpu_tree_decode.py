@@ -504,3 +504,26 @@ def test_nothing_of_a_hidden_value_is_left(splash, T, Hq, window, kind, value):
         blind = np.array([not any(k in seen for k in at[b]) for seen in keys])
         assert blind.all() if b else blind.any() and not blind.all()
         assert (o[b][:, blind] == 0).all() and (o[b][:, ~blind] > 0).all()
+
+
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("T, Hq", [(4, 4), (16, 1), (9, 4), (40, 8)])
+def test_small_scales(splash, T, Hq, cap):
+    """Factors of the scores below fp32's normal numbers.  They are rounded to multiples of
+    2^-149, which with sums of products below 2^128 moves a score by 2^-22 at the most, so that
+    the usual bounds hold; masked keys stay masked where a factor would be 0."""
+    x = make([190, 70], T, Hq, 1, 64, 64, 16, seed=170)
+    large = {**x, "q": x["q"] * 2.0 ** 118, "scale": 2.0 ** -127}  # scores of 0.02
+    got = splash.paged_tree_decode(**large, softcap=cap)
+    splash.check_device_error()
+    check(got, bounds(large, cap))
+    x["scale"] = 2.0 ** -149
+    got = splash.paged_tree_decode(**x, softcap=cap)
+    splash.check_device_error()
+    check(got, bounds(x, cap))
+    y = make([190, 70], T, Hq, 1, 64, 64, 16, "e4m3", seed=171)
+    for k_scale in (2.0 ** -140, 2.0 ** -149):
+        y["k_scale"] = torch.full_like(y["k_scale"], k_scale)
+        got = splash.paged_tree_decode(**y, softcap=cap)
+        splash.check_device_error()
+        check(got, bounds(y, cap))
