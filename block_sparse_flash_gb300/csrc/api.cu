@@ -552,11 +552,13 @@ splash_status check_decode_sizes(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq,
   if (Hq % Hkv != 0) return SPLASH_ERR_SHAPE;
   if (Lq > most || B > 65535 || Hq > 65535 || (int64_t)B * Hq * Lq > INT32_MAX) return SPLASH_ERR_UNSUPPORTED;
   if (!((dqk == 64 && dv == 64) || (dqk == 128 && dv == 128) || (dqk == 192 && dv == 128))) return SPLASH_ERR_UNSUPPORTED;
-  const splash_status st = check_page_sizes(page_size, max_pages);
-  if (st != SPLASH_OK) return st;
-  // the kernel's list: 16-key steps of every sequence, head and 16 rows, in 32 bits
+  return check_page_sizes(page_size, max_pages);
+}
+
+// paged_decode.cu's list: 16-key steps of every sequence, head and 16 rows, in 32 bits.
+splash_status check_decode_list(int32_t B, int32_t Hq, int32_t Hkv, int32_t Lq, int32_t max_pages, int32_t page_size, int64_t window_left) {
   int64_t steps = (int64_t)max_pages * page_size / 16 + 1;
-  if (window_left >= 0) steps = std::min(steps, window_left / 16 + 4 + (Lq > SPLASH_MAX_NEW_TOKENS ? Lq / 16 : 0));
+  if (window_left >= 0) steps = std::min(steps, window_left / 16 + 4);
   const int64_t segments = (int64_t)B * Hkv * (((int64_t)(Hq / Hkv) * Lq + 15) / 16);
   return steps > INT32_MAX / segments ? SPLASH_ERR_UNSUPPORTED : SPLASH_OK;
 }
@@ -650,8 +652,9 @@ splash_status splash_paged_decode_workspace_size(int32_t B, int32_t Hq, int32_t 
                                                  int32_t max_pages, int32_t page_size, int32_t cache_type,
                                                  int64_t window_left, size_t *bytes) {
   if (bytes == nullptr) return SPLASH_ERR_INVALID_ARG;
-  const splash_status st = check_decode_sizes(B, Hq, Hkv, Lq, SPLASH_MAX_NEW_TOKENS, dqk, dv, max_pages, page_size, cache_type, window_left);
+  splash_status st = check_decode_sizes(B, Hq, Hkv, Lq, SPLASH_MAX_NEW_TOKENS, dqk, dv, max_pages, page_size, cache_type, window_left);
   if (st != SPLASH_OK) return st;
+  if ((st = check_decode_list(B, Hq, Hkv, Lq, max_pages, page_size, window_left)) != SPLASH_OK) return st;
   *bytes = splash_paged_decode_workspace_bytes(B, Hq, Hkv, Lq, dqk, dv, max_pages, page_size, cache_type, window_left);
   return SPLASH_OK;
 }
@@ -675,8 +678,11 @@ splash_status splash_paged_tree_decode_workspace_size(int32_t B, int32_t Hq, int
                                                       int32_t max_pages, int32_t page_size, int32_t cache_type,
                                                       int64_t window_left, size_t *bytes) {
   if (bytes == nullptr) return SPLASH_ERR_INVALID_ARG;
-  const splash_status st = check_decode_sizes(B, Hq, Hkv, T, SPLASH_MAX_TREE_TOKENS, dqk, dv, max_pages, page_size, cache_type, window_left);
+  splash_status st = check_decode_sizes(B, Hq, Hkv, T, SPLASH_MAX_TREE_TOKENS, dqk, dv, max_pages, page_size, cache_type, window_left);
   if (st != SPLASH_OK) return st;
+  if (splash_paged_tree_decode_few_rows(Hq, Hkv, T) &&
+      (st = check_decode_list(B, Hq, Hkv, T, max_pages, page_size, window_left)) != SPLASH_OK)
+    return st;
   if (splash_paged_tree_decode_entries(B, Hq, Hkv, T, max_pages, page_size, window_left) > INT32_MAX) return SPLASH_ERR_UNSUPPORTED;
   *bytes = splash_paged_tree_decode_workspace_bytes(B, Hq, Hkv, T, dqk, dv, max_pages, page_size, cache_type, window_left);
   return SPLASH_OK;

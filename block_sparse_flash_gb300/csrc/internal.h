@@ -177,7 +177,9 @@ splash_status splash_paged_tree_decode_launch_e4m3(const splash_paged_tree_decod
 // (paged_decode.cu: up to 16 rows per KV head)
 splash_status splash_paged_tree_rows_launch_bf16(const splash_paged_tree_decode_args &a, cudaStream_t stream, uint32_t *err_word);
 splash_status splash_paged_tree_rows_launch_e4m3(const splash_paged_tree_decode_args &a, cudaStream_t stream, uint32_t *err_word);
-// entries of the kernel's list, at most
+// whether paged_decode's kernel takes the tree
+bool splash_paged_tree_decode_few_rows(int32_t Hq, int32_t Hkv, int32_t T);
+// entries of the list of 64-key steps, at most
 int64_t splash_paged_tree_decode_entries(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t max_pages, int32_t page_size,
                                          int64_t window);
 size_t splash_paged_tree_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t dqk, int32_t dv,

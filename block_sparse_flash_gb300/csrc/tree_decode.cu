@@ -1364,16 +1364,19 @@ int64_t splash_paged_tree_decode_entries(int32_t B, int32_t Hq, int32_t Hkv, int
 // of the 223 us that 4 tokens of 64 requests with 64 / 8 heads take there.)
 constexpr int kFewRows = 16;
 
+bool splash_paged_tree_decode_few_rows(int32_t Hq, int32_t Hkv, int32_t T) { return (int64_t)(Hq / Hkv) * T <= kFewRows; }
+
 size_t splash_paged_tree_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t dqk, int32_t dv,
                                                 int32_t max_pages, int32_t page_size, int32_t type, int64_t window) {
+  if (splash_paged_tree_decode_few_rows(Hq, Hkv, T))
+    return splash_paged_decode_workspace_bytes(B, Hq, Hkv, T, dqk, dv, max_pages, page_size, type, window);
   const int64_t rows = std::min<int64_t>((int64_t)(Hq / Hkv) * T, 256);
-  if (rows <= kFewRows) return splash_paged_decode_workspace_bytes(B, Hq, Hkv, T, dqk, dv, max_pages, page_size, type, window);
   return (size_t)(16 + splash::align16(4 * ((int64_t)B + 1)) + 4 * splash::kMaxCtas + (int64_t)2 * splash::kMaxCtas * rows * 4 * (dv + 2));
 }
 
 splash_status splash_paged_tree_decode_launch(const splash_paged_tree_decode_args &args, cudaStream_t stream, uint32_t *err_word) {
   const bool e4m3 = args.decode.cache_type == SPLASH_CACHE_E4M3;
-  if ((int64_t)(args.decode.Hq / args.decode.Hkv) * args.decode.Lq <= kFewRows)
+  if (splash_paged_tree_decode_few_rows(args.decode.Hq, args.decode.Hkv, args.decode.Lq))
     return e4m3 ? splash_paged_tree_rows_launch_e4m3(args, stream, err_word) : splash_paged_tree_rows_launch_bf16(args, stream, err_word);
   return e4m3 ? splash_paged_tree_decode_launch_e4m3(args, stream, err_word)
               : splash_paged_tree_decode_launch_bf16(args, stream, err_word);

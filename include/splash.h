@@ -682,8 +682,8 @@ splash_status splash_paged_append_axes(const splash_paged_append_axes_args *args
  * Supported sizes as for splash_paged_decode but for Lq, and for the number of
  * steps: those of 64 keys (at most max_pages * page_size / 64 + 1, or (window_left +
  * T) / 64 + 3) and nine more, over all sequences, KV heads and groups of 256 rows (of
- * 128, up to 128 rows), are to be fewer than 2^31.  The caches' strides are below 2^40
- * bytes, and a page's tokens do not share a row (stride_token > 0).  The cache is read
+ * 128, up to 128 rows), are to be fewer than 2^31; with at most 16 of the Hq/Hkv * T
+ * rows those of splash_paged_decode are too.  The caches' strides are below 2^40 bytes, and a page's tokens do not share a row (stride_token > 0).  The cache is read
  * once for every 256 of the Hq/Hkv * T rows.  The result does not depend on timing:
  * the same inputs give the same bits on the same GPU.
  *

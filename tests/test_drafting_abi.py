@@ -261,6 +261,29 @@ def test_a_window_past_every_key_is_none(splash):
             assert tree(window, B=65535, Hq=heads, Hkv=heads, T=1, max_pages=1)[0] == UNSUPPORTED
 
 
+def test_the_longest_lists(splash):
+    """Each kernel's own limit: more than 16 rows of a KV head have 64-key steps and 256 rows a
+    group, up to 16 rows also the 16-key steps of paged_decode."""
+    n = ctypes.c_size_t(0)
+
+    def size(name, T, max_pages, page, Hq=64, window=-1):
+        return getattr(splash.lib(), f"splash_paged_{name}_workspace_size")(256, Hq, 8, T, 128, 128, max_pages, page, 0, window,
+                                                                            ctypes.byref(n))
+    # 8 rows x 64: (16 pages + 9) x 256 sequences x 8 heads x 2 groups
+    assert size("tree_decode", 64, 65536, 16) == 0
+    assert size("tree_decode", 64, 32767, 1024) == 0 and size("tree_decode", 64, 32768, 1024) == UNSUPPORTED
+    # ... or (window + 64) / 64 + 3 steps
+    assert size("tree_decode", 64, 65536, 1024, window=64 * 524274) == 0
+    for window in (64 * 524275, 2 ** 63 - 1, -1):
+        assert size("tree_decode", 64, 65536, 1024, window=window) == UNSUPPORTED
+    # 17 rows: one group; 16 rows: (pages + 1) x 256 sequences x 8 heads
+    assert size("tree_decode", 17, 1048575, 16, Hq=8) == 0
+    for name in ("tree_decode", "decode"):
+        assert size(name, 16, 1048574, 16, Hq=8) == 0 and size(name, 16, 1048575, 16, Hq=8) == UNSUPPORTED
+        assert size(name, 16, 1048575, 16, Hq=8, window=16 * 1048571) == 0
+        assert size(name, 16, 1048575, 16, Hq=8, window=16 * 1048572) == UNSUPPORTED
+
+
 def test_axis_maps(splash):
     assert splash.rope_axis_map((2, 1, 3)) == bytes([0, 0, 1, 2, 2, 2])
     assert splash.rope_axis_map((2, 1, 3), cycled=True) == bytes([0, 1, 2, 0, 2, 2])

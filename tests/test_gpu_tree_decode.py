@@ -527,3 +527,12 @@ def test_small_scales(splash, T, Hq, cap):
         got = splash.paged_tree_decode(**y, softcap=cap)
         splash.check_device_error()
         check(got, bounds(y, cap))
+
+
+@pytest.mark.parametrize("window", [-1, 100])
+def test_many_rows_over_long_block_tables(splash, window):
+    """Room for 20 million tokens of each sequence, 512 rows of a KV head."""
+    x = make([200, 64, 1, 0, 700, 129, 65, 1100], 64, 64, 8, 64, 64, 1024, seed=180, extra_cols=20000)
+    got = splash.paged_tree_decode(**x, window_left=window)
+    splash.check_device_error()
+    check(got, bounds(x, 0.0, window))
