@@ -4,10 +4,11 @@
 //
 // None of them computes; they read and write each byte once, so HBM bounds the
 // large ones and the chain of dependent reads the small ones.  Measured (device time, 8 KV
-// heads of 128, bf16): 8192 of 16384 tokens of 8 sequences moved 95 us, 5.6 TB/s; the 5
-// accepted drafts of one 1.9 us; 16 requests of 4 beams, up to 2000 tokens, forked and their
-// pages copied 12.0 us; 64 prompts into 8 samples each, pages of 128 tokens, 30 us, of which
-// the remap 14.
+// heads of 128, bf16): 8192 of 16384 tokens of 8 sequences moved 95 us, 5.6 TB/s, of 1
+// sequence 54 us, 1.3 TB/s; the 5 accepted drafts of one 1.9 us; 16 requests of 4 beams, up to
+// 2000 tokens, forked and their pages copied 12.0 us; 64 prompts into 8 samples each, pages of
+// 128 tokens, 30 us, of which the remap 14; 64 requests of 4 beams, up to 16384 tokens in a pool of
+// 134000 pages, 73 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -55,7 +56,9 @@ struct Move {
 // batches read (src > src[m]) is not overwritten by it, so that one barrier per
 // batch is enough.  The places of the next batch (three dependent reads) are
 // looked up while this one's data is on the way.  Slices of 8 chunks, 128 bytes of a row, or of 4
-// where there are few: the half of 8 sequences' tokens 129 us with 8 chunks, 95 with 4.
+// where there are few: the half of 8 sequences' tokens 129 us with 8 chunks, 95 with 4.  The
+// batches of a list follow one another: 32 of 256 moves take one sequence 54 us on 64 CTAs, with
+// one KV head 36 us on 8, where HBM would take 10 and 1.
 __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactParams p) {
   __shared__ Move s_move[2][kMoveRows];
   __shared__ int s_end[2];
@@ -150,8 +153,9 @@ struct CopyParams {
   uint32_t *err;
 };
 
-// CTA (entry, head, K or V): the rows of a page, 16 bytes a thread and four of them in flight
-// (512 entries of pages of up to 128 rows, 8 heads: 16 us, at the rate of L2 and HBM).
+// CTA (entry, head, K or V): the rows of a page, 16 bytes a thread and four of them in flight.
+// (512 entries of pages of up to 128 rows, 8 heads: 16 us.  140 MB pass L2, at 36 % of its rate, 15 MB
+// HBM: what it waits for is each CTA's own chain, the entry and one or two rounds of reads.)
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) {
   grid_dependency();
   const int32_t *entry = p.copies + 3 * (int64_t)blockIdx.x;

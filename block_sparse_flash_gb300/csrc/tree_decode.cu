@@ -6,10 +6,11 @@
 // the context and its ancestors --, out = sum exp(s_j - m) v_j / sum exp(s_j - m),
 // lse = m + ln sum exp(s_j - m), in one pass over the keys.
 //
-// A KV head has Hq/Hkv * T rows, up to hundreds, that share its keys: 2 rows FLOP per
-// byte of a bf16 cache, 4 of an e4m3 one.  Reading the cache bounds the call up to some
-// 256 rows, the products beyond, so that the rows are the 128 lanes of tensor memory
-// and the cache is read once for 256 of them.
+// A KV head has Hq/Hkv * T rows, up to hundreds, that share its keys: `rows` FLOP per
+// byte of a bf16 cache, 2 rows of an e4m3 one.  By these reading the cache bounds the call up
+// to some 290 rows in bf16 (190 with the second term of P, see the softmax) and 145 in e4m3, the
+// products beyond, so that the rows are the 128 lanes of tensor memory and the cache is
+// read once for 256 of them.
 //
 //  * Work.  As in paged_decode: the steps of 64 keys of all (sequence, KV head, row
 //    group) segments form one list and every CTA, one per SM, takes an equal contiguous
@@ -61,9 +62,11 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 constexpr int kMaxCtas = 160;              // of the grid; the workspace holds two parts for each
 // A piece's start and end cost a CTA about as much as this many steps: a segment
-// counts for so many more when the list is cut into equal parts.  (32 requests of 32 ..
-// 4096 tokens, 32 drafts: 113.6 us with 2, 94.2 with 6, 88.9 with 9, 87.7 with 12; 64 requests,
-// one draft: 148, 122, 121.6, 123.3.)
+// counts for so many more when the list is cut into equal parts.  (With 2, 6, 9, 12 and 16,
+// us: 32 requests of up to 4096 tokens, 8 drafts 79.5, 72.1, 73.1, 74.1, 76.0, 32 drafts 100.2,
+// 86.0, 83.9, 84.4, 85.6, 64 drafts 128.2, 113.5, 114.8, 117.1, 119.1; in e4m3, up to 8192 tokens, 32
+// drafts 147.5, 122.9, 120.5, 121.4, 123.0, 16 requests of up to 32768 and 64 drafts 282.9, 259.3,
+// 250.1, 247.7, 249.0; segments of one length 121.4 with any.)
 constexpr int kPieceSteps = 9;
 constexpr uint64_t kTimeoutNs = 1000000000ull;  // of a wait
 
@@ -837,8 +840,9 @@ __device__ __forceinline__ void run_softmax(const Params &p, Walk<C::KW> walk, c
         // P in 16 bits, half of the keys at a time (the registers of their scores are free then).
         // fp16 for an e4m3 cache; for bf16 two terms, cut off and rest: 2^-16 of each p, where
         // bf16 alone loses 2^-8, as much as the rounding of the result.  The rest is taken of
-        // (1 + 2^-23) p, which keeps it above 0: an infinite value times either term then
-        // has its sign, and the sum is that infinity (0 x infinity is NaN).
+        // (1 + 2^-23) p, which keeps it above 0 where p is: an infinite value times either term
+        // then has its sign, and the sum is that infinity (0 x infinity is NaN, as it is where p
+        // itself is below 2^-126).
         constexpr float above = 1.f + 0x1p-23f;
         f32x2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
@@ -946,6 +950,9 @@ __device__ __forceinline__ int32_t share(int32_t n, uint32_t rank, uint32_t ctas
 }
 
 // TOGETHER: a cluster of CTAs per segment, which share its steps; otherwise equal parts of the list.
+// The registers do not hold all (52 .. 140 bytes are spilled, 180 .. 308 for e4m3), but the
+// steps hardly notice: a softmax warp reads one to three of them a step, all warps together 8 and 12
+// of a step's 3800 and 1900 instructions (PAIR and not; e4m3 16 of 3100 and 20 of 1900), and writes none.
 template <class C, bool TOGETHER>
 __global__ void __launch_bounds__(C::THREADS, 1) tree_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                                                                   const __grid_constant__ CUtensorMap map_v, const Params p) {
